@@ -13,11 +13,12 @@ from . import _lib
 from ._lib import (SAR_EPI_F32, SAR_EPI_RESIDUAL, SAR_EPI_STORE, SAR_EPI_SWIGLU, SAR_GEMM_AUTO,
                    SAR_GEMM_PAIR_N128, SAR_GEMM_PAIR_N192,
                    SAR_GEMM_PAIR_N256, SAR_GEMM_STREAM_K, SAR_GEMM_TWO_CTAS,
-                   SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
+                   SAR_FP4_MX, SAR_FP4_NV, SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
                    SAR_IN_HIDDEN, SAR_IN_TOKENS, SAR_STORAGE_BF16, SAR_STORAGE_F16, KERNEL_KINDS,
                    SarError, check, lib)
 
 __all__ = ["Model", "KVCache", "Scheduler", "Batch", "StepGraph", "SarError", "lib", "check", "gemm", "rmsnorm",
+           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "SAR_FP4_NV", "SAR_FP4_MX",
            "op_sync_status", "op_wait_check",
            "launch_count", "KERNEL_KINDS", "SAR_IN_HIDDEN", "SAR_IN_TOKENS", "SAR_STORAGE_F16",
            "SAR_STORAGE_BF16", "storage_dtype"]
@@ -366,3 +367,69 @@ def rmsnorm(x, gain, y, eps: float, stream=None) -> None:
     """y (fp16/bf16) = rmsnorm of fp32 rows x with fp32 gain."""
     check(lib().sar_op_rmsnorm(_ptr(x), _ptr(gain), _ptr(y), x.shape[0], x.shape[1], eps,
                                _storage_of(y), _stream(stream)))
+
+
+# ---- 4-bit rows ----------------------------------------------------------------
+
+
+def _device_check(what: str, *tensors) -> None:
+    """Every tensor is on the current device (the library launches there)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != dev):
+            raise ValueError(f"{what}: tensors must be on the current CUDA device")
+
+
+def _rows_type(what: str, t) -> int:
+    import torch
+    types = {torch.float16: _lib.SAR_TYPE_F16, torch.bfloat16: _lib.SAR_TYPE_BF16, torch.float32: _lib.SAR_TYPE_F32}
+    if t.dtype not in types:
+        raise ValueError(f"{what}: rows must be float16, bfloat16 or float32")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: rows must be two-dimensional with adjacent columns")
+    return types[t.dtype]
+
+
+def _row_stride(t) -> int:
+    """Elements from row to row (a single row's own length: its stride means nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def fp4_scale_bytes(rows: int, cols: int, format: int = SAR_FP4_NV) -> int:
+    """Length in bytes of the scales of a 4-bit [rows, cols] matrix."""
+    n = ctypes.c_int64()
+    check(lib().sar_op_fp4_scale_bytes(rows, cols, format, ctypes.byref(n)))
+    return n.value
+
+
+def _fp4_check(what: str, codes, scales, rows: int, cols: int, format: int) -> None:
+    import torch
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise ValueError(f"{what}: codes and scales must be uint8")
+    if tuple(codes.shape) != (rows, cols // 2) or not codes.is_contiguous():
+        raise ValueError(f"{what}: codes must be contiguous [{rows}, {cols // 2}]")
+    if not scales.is_contiguous() or scales.numel() < fp4_scale_bytes(rows, cols, format):
+        raise ValueError(f"{what}: scales must be contiguous and hold {fp4_scale_bytes(rows, cols, format)} bytes")
+
+
+def fp4_quantize(x, codes, scales, format: int = SAR_FP4_NV, tensor_scale: float = 1.0, stream=None) -> None:
+    """codes (uint8 [rows, cols / 2]) and scales (uint8 [fp4_scale_bytes]) = the
+    microscaled 4-bit form of the rows of ``x`` (fp16, bf16 or fp32, any row
+    stride); see ``sar_op_fp4_quantize``."""
+    kind = _rows_type("fp4_quantize", x)
+    rows, cols = x.shape
+    _fp4_check("fp4_quantize", codes, scales, rows, cols, format)
+    _device_check("fp4_quantize", x, codes, scales)
+    check(lib().sar_op_fp4_quantize(_ptr(x), _row_stride(x), rows, cols, kind, format, tensor_scale, _ptr(codes),
+                                    _ptr(scales), _stream(stream)))
+
+
+def fp4_dequantize(codes, scales, y, format: int = SAR_FP4_NV, tensor_scale: float = 1.0, stream=None) -> None:
+    """y (fp16, bf16 or fp32 rows, any row stride) = what 4-bit rows stand for."""
+    kind = _rows_type("fp4_dequantize", y)
+    rows, cols = y.shape
+    _fp4_check("fp4_dequantize", codes, scales, rows, cols, format)
+    _device_check("fp4_dequantize", codes, scales, y)
+    check(lib().sar_op_fp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, format, tensor_scale, _ptr(y),
+                                      _row_stride(y), kind, _stream(stream)))

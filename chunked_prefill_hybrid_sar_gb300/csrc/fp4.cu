@@ -1,0 +1,320 @@
+// Microscaled 4-bit rows: quantisation and its inverse.
+//
+// A row is cut into blocks of B columns; block b of row r keeps one scale byte
+// s and B e2m1 codes q (0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign), and stands for
+// q * s * tensor_scale.  Two formats: NV (B = 16, s an e4m3 number) and MX
+// (B = 32, s = 2^(byte - 127)).
+//
+// Codes lie two to a byte, [rows][cols / 2].  Scales lie in tiles of 128 rows x
+// 4 blocks, 512 bytes each, in the order in which the 4-bit product's tensor
+// cores take them (see include/sar_ops.h), so that the product copies a tile
+// from global memory to tensor memory without touching it.
+#include <cuda_fp4.h>
+#include <cuda_fp8.h>
+
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace sar {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kSeg = 16;  // columns per thread: an NV block, half an MX block
+
+template <typename X>
+__device__ __forceinline__ float to_f32(X v) {
+  if constexpr (sizeof(X) == 4)
+    return v;
+  else
+    return Elem<X>::to(v);
+}
+
+// 16 consecutive values as fp32; vec: the address is 16-byte aligned.
+template <typename X>
+__device__ __forceinline__ void load16(const X* p, bool vec, float (&v)[16]) {
+  if (vec) {
+    const uint4* p4 = reinterpret_cast<const uint4*>(p);
+    if constexpr (sizeof(X) == 4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 u = __ldg(p4 + i);
+        v[4 * i] = __uint_as_float(u.x);
+        v[4 * i + 1] = __uint_as_float(u.y);
+        v[4 * i + 2] = __uint_as_float(u.z);
+        v[4 * i + 3] = __uint_as_float(u.w);
+      }
+    } else {
+      const uint4 a = __ldg(p4), b = __ldg(p4 + 1);
+      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[2 * i] = Elem<X>::lo(u[i]);
+        v[2 * i + 1] = Elem<X>::hi(u[i]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = to_f32<X>(p[i]);
+  }
+}
+
+// Byte offset of the scale tile of (row, tile column) plus the row's place in it.
+__device__ __forceinline__ size_t scale_offset(uint32_t row, uint32_t tile, uint32_t tiles) {
+  return ((size_t)(row >> 7) * tiles + tile) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+}
+
+// Each thread quantises 16 columns.  With t = x * inv_g and a = max |t| over
+// the block:
+//   NV  s = e4m3(min(a / 6, 448)),           q = e2m1(t / s)  (0 where s = 0)
+//   MX  s = 2^max(floor(log2 a) - 2, -127),  q = e2m1(t / s)
+// both roundings to nearest even, e2m1 saturating at 6 (a scale that was
+// rounded down leaves t / s up to 6.4, MX's floor up to 8).  A block with a NaN
+// or an infinity gets a NaN scale and zero codes.
+//
+// t / s has to fall on the right side of e2m1's seven borders.  For MX the
+// factor is a power of two.  For NV the quotient is formed as q0 = t * r with
+// r = 1 / s correctly rounded, and corrected once by its exact remainder
+// (Markstein 1990: the result is the correctly rounded t / s).  A correctly
+// rounded quotient never rounds onto a border b it does not equal: b * s has 7
+// significant bits at most, so a different t is at least one of its own units
+// away from it, which is more than half a unit of b after the division.  Two
+// fused multiply-adds per element instead of a division (~10 instructions).
+//
+// The 4 scale bytes that neighbour in a tile's row are gathered from the lanes
+// and stored as one word.  Columns are padded to whole tiles: the padding
+// blocks' scales are written as zero, as the product reads them.
+template <typename X, bool NV>
+__global__ void __launch_bounds__(kThreads)
+    fp4_quantize_kernel(const X* __restrict__ x, int64_t ldx, uint32_t rows, uint32_t cols, uint32_t tiles, float inv_g,
+                        uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int vec) {
+  constexpr uint32_t kSegsPerTile = NV ? 4 : 8;
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t segs = tiles * kSegsPerTile;
+  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  const bool live = i < (uint64_t)rows * segs;  // (whole groups of kSegsPerTile lanes)
+  const uint32_t row = live ? (uint32_t)i / segs : 0;
+  const uint32_t seg = live ? (uint32_t)i - row * segs : 0;
+  const uint32_t col = seg * kSeg;
+  const bool has = live && col < cols;
+  float v[16];
+  uint32_t ab = 0;
+  if (has) {
+    load16<X>(x + (int64_t)row * ldx + col, vec != 0, v);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      v[k] *= inv_g;
+      // as whole numbers: a NaN is larger than an infinity, which is larger than any number
+      ab = max(ab, __float_as_uint(v[k]) & 0x7fffffffu);
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = 0.f;
+  }
+  if constexpr (!NV) ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 1));
+  const bool bad = ab >= 0x7f800000u;
+  uint32_t byte;
+  if constexpr (NV) {
+    const __nv_fp8_storage_t s8 =
+        __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(ab), 6.f), __NV_SATFINITE, __NV_E4M3);
+    byte = bad ? 0x7Fu : (uint32_t)s8;
+    const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
+    const bool zero = bad || s == 0.f;
+    const float r = zero ? 0.f : __frcp_rn(s);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float q0 = v[k] * r;
+      // (the remainder's sign as written keeps a negative zero negative)
+      v[k] = zero ? 0.f : fmaf(-fmaf(q0, s, -v[k]), r, q0);
+    }
+  } else {
+    const uint32_t e = ab >> 23;  // biased exponent (0: zero or subnormal)
+    byte = bad ? 0xFFu : e >= 2 ? e - 2 : 0u;
+    const float r = __uint_as_float((254u - (bad ? 127u : byte)) << 23);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = bad ? 0.f : v[k] * r;
+  }
+  if (!has) byte = 0;
+  if (has) {
+    uint32_t w[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      w[h] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        w[h] |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(v[8 * h + 2 * k], v[8 * h + 2 * k + 1]), __NV_E2M1,
+                                                   cudaRoundNearest)
+                << (8 * k);
+    }
+    *reinterpret_cast<uint2*>(codes + (size_t)row * (cols / 2) + col / 2) = make_uint2(w[0], w[1]);
+  }
+  const uint32_t lane = threadIdx.x & 31;
+  uint32_t word;
+  if constexpr (NV) {
+    word = byte << (8 * (lane & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 1);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+  } else {
+    word = (lane & 1) ? 0u : byte << (8 * ((lane >> 1) & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, 2);
+    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+  }
+  if (live && (lane & (kSegsPerTile - 1)) == 0)
+    *reinterpret_cast<uint32_t*>(scales + scale_offset(row, seg / kSegsPerTile, tiles)) = word;
+}
+
+// y = code * s * g: the product of a code and its scale is exact in fp32 (3 and
+// 4 significant bits); * g rounds once, the conversion to Y once more.
+template <typename Y, bool NV>
+__global__ void __launch_bounds__(kThreads)
+    fp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint32_t rows,
+                          uint32_t cols, uint32_t tiles, float g, Y* __restrict__ y, int64_t ldy, int vec) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const uint32_t segs = cols / kSeg;
+  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= (uint64_t)rows * segs) return;
+  const uint32_t row = (uint32_t)i / segs;
+  const uint32_t seg = (uint32_t)i - row * segs;
+  const uint32_t block = NV ? seg : seg >> 1;
+  const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + (size_t)row * (cols / 2) + seg * 8));
+  const uint8_t b = __ldg(scales + scale_offset(row, block >> 2, tiles) + (block & 3));
+  float s;
+  if constexpr (NV)
+    s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
+  else  // 2^(b - 127); 2^-127 is a subnormal
+    s = __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : (uint32_t)b << 23);
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t w = k < 4 ? c.x : c.y;
+    const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * (k & 3))) & 0xffu), __NV_E2M1));
+    v[2 * k] = __low2float(h) * s * g;
+    v[2 * k + 1] = __high2float(h) * s * g;
+  }
+  Y* dst = y + (int64_t)row * ldy + seg * kSeg;
+  if constexpr (sizeof(Y) == 4) {
+    if (vec) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        reinterpret_cast<float4*>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) dst[k] = v[k];
+    }
+  } else {
+    if (vec) {
+      uint32_t w[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) w[k] = Elem<Y>::pack(v[2 * k], v[2 * k + 1]);
+      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) dst[k] = Elem<Y>::from(v[k]);
+    }
+  }
+}
+
+bool good_format(int format) { return format == SAR_FP4_NV || format == SAR_FP4_MX; }
+bool good_type(int type) { return type == SAR_TYPE_F16 || type == SAR_TYPE_BF16 || type == SAR_TYPE_F32; }
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The checks that both directions share; *blocks receives the launch's size.
+int check_rows(const char* what, const void* x, int64_t ld, int rows, int cols, int type, int format, float scale,
+               const void* codes, const void* scales, uint32_t* blocks) {
+  const std::string w(what);
+  if (rows < 0 || cols <= 0) return set_error(SAR_ERR_INVALID_ARG, w + ": bad shape");
+  if (!good_format(format)) return set_error(SAR_ERR_INVALID_ARG, w + ": bad format");
+  if (!good_type(type)) return set_error(SAR_ERR_INVALID_ARG, w + ": bad element type");
+  if (cols % 32) return set_error(SAR_ERR_UNSUPPORTED, w + ": columns must be a multiple of 32");
+  if (ld < cols) return set_error(SAR_ERR_INVALID_ARG, w + ": row stride below the row's length");
+  if (!(scale > 0.f) || !std::isfinite(scale) || !std::isfinite(1.f / scale))
+    return set_error(SAR_ERR_INVALID_ARG, w + ": the tensor scale must be positive and finite, as its inverse");
+  *blocks = 0;
+  if (rows == 0) return SAR_OK;
+  if (!x || !codes || !scales) return set_error(SAR_ERR_INVALID_ARG, w + ": null pointer");
+  if (reinterpret_cast<uintptr_t>(x) & (type == SAR_TYPE_F32 ? 3 : 1))
+    return set_error(SAR_ERR_INVALID_ARG, w + ": rows not aligned to their element");
+  if (!aligned16(codes) || !aligned16(scales))
+    return set_error(SAR_ERR_INVALID_ARG, w + ": codes and scales must be 16-byte aligned");
+  const uint64_t items = (uint64_t)rows * fp4_tiles(cols, format) * (format == SAR_FP4_NV ? 4 : 8);
+  if (items > 0xffffff00ull) return set_error(SAR_ERR_UNSUPPORTED, w + ": more than 2^32 groups of 16 columns");
+  *blocks = (uint32_t)((items + kThreads - 1) / kThreads);
+  return SAR_OK;
+}
+
+template <typename X>
+int quantize(const void* x, int64_t ldx, int rows, int cols, int format, float inv_g, void* codes, void* scales,
+             uint32_t blocks, cudaStream_t s) {
+  const int vec = aligned16(x) && (ldx * (int64_t)sizeof(X)) % 16 == 0;
+  const uint32_t tiles = (uint32_t)fp4_tiles(cols, format);
+  auto fn = format == SAR_FP4_NV ? fp4_quantize_kernel<X, true> : fp4_quantize_kernel<X, false>;
+  const cudaError_t e = launch_pdl(fn, dim3(blocks), dim3(kThreads), 0, s, static_cast<const X*>(x), ldx, (uint32_t)rows,
+                                   (uint32_t)cols, tiles, inv_g, static_cast<uint8_t*>(codes),
+                                   static_cast<uint8_t*>(scales), vec);
+  if (e != cudaSuccess) return cuda_error(e, "fp4 quantise launch");
+  count_launches(1);
+  return SAR_OK;
+}
+
+template <typename Y>
+int dequantize(const void* codes, const void* scales, int rows, int cols, int format, float g, void* y, int64_t ldy,
+               uint32_t blocks, cudaStream_t s) {
+  const int vec = aligned16(y) && (ldy * (int64_t)sizeof(Y)) % 16 == 0;
+  const uint32_t tiles = (uint32_t)fp4_tiles(cols, format);
+  auto fn = format == SAR_FP4_NV ? fp4_dequantize_kernel<Y, true> : fp4_dequantize_kernel<Y, false>;
+  const cudaError_t e =
+      launch_pdl(fn, dim3(blocks), dim3(kThreads), 0, s, static_cast<const uint8_t*>(codes),
+                 static_cast<const uint8_t*>(scales), (uint32_t)rows, (uint32_t)cols, tiles, g, static_cast<Y*>(y), ldy, vec);
+  if (e != cudaSuccess) return cuda_error(e, "fp4 dequantise launch");
+  count_launches(1);
+  return SAR_OK;
+}
+
+}  // namespace
+
+}  // namespace sar
+
+using sar::set_error;
+
+extern "C" {
+
+int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* out) {
+  if (!out || rows < 0 || cols <= 0 || !sar::good_format(format))
+    return set_error(SAR_ERR_INVALID_ARG, "fp4_scale_bytes: bad argument");
+  if (cols % 32) return set_error(SAR_ERR_UNSUPPORTED, "fp4_scale_bytes: columns must be a multiple of 32");
+  *out = ((int64_t)rows + 127) / 128 * sar::fp4_tiles(cols, format) * 512;
+  return SAR_OK;
+}
+
+int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_t type, int32_t format,
+                        float tensor_scale, void* codes, void* scales, void* stream) {
+  uint32_t blocks = 0;
+  SAR_TRY(sar::check_rows("fp4_quantize", x, ldx, rows, cols, type, format, tensor_scale, codes, scales, &blocks));
+  if (blocks == 0) return SAR_OK;
+  const float inv = 1.f / tensor_scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (type == SAR_TYPE_F32) return sar::quantize<float>(x, ldx, rows, cols, format, inv, codes, scales, blocks, s);
+  if (type == SAR_TYPE_BF16)
+    return sar::quantize<__nv_bfloat16>(x, ldx, rows, cols, format, inv, codes, scales, blocks, s);
+  return sar::quantize<__half>(x, ldx, rows, cols, format, inv, codes, scales, blocks, s);
+}
+
+int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, int32_t format,
+                          float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream) {
+  uint32_t blocks = 0;
+  SAR_TRY(sar::check_rows("fp4_dequantize", y, ldy, rows, cols, type, format, tensor_scale, codes, scales, &blocks));
+  if (blocks == 0) return SAR_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (type == SAR_TYPE_F32)
+    return sar::dequantize<float>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, s);
+  if (type == SAR_TYPE_BF16)
+    return sar::dequantize<__nv_bfloat16>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, s);
+  return sar::dequantize<__half>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, s);
+}
+
+}  // extern "C"

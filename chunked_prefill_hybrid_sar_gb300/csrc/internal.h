@@ -59,6 +59,18 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// The device error record [code, site, detail, 0] of the single-kernel entry
+// points on the current device (model.cu).
+int op_flags(int** out);
+
+// ---- 4-bit rows (fp4.cu) ---------------------------------------------------
+
+// Scale tiles (4 blocks wide) per row block of 128 rows.
+inline int fp4_tiles(int cols, int format) {
+  const int w = format == SAR_FP4_NV ? 64 : 128;
+  return (cols + w - 1) / w;
+}
+
 // ---- GEMM (gemm_tc.cu) -----------------------------------------------------
 
 // Encodes a 2D 16-bit (storage type) tensor map over row-major [rows, cols]

@@ -111,19 +111,32 @@ namespace {
 
 int check(cudaError_t e, const char* what) { return cuda_error(e, what); }
 
+}  // namespace
+
+namespace sar {
+
 // The device error record [code, site, detail, 0] of the single-kernel entry
-// points on the current device, allocated (and zeroed) at its first use there.
-std::mutex g_op_flags_mu;
-std::map<int, int*> g_op_flags;
+// points on the current device, allocated (and zeroed) at its first use there,
+// which may be while a stream is being captured: the allocation and the clear,
+// on a stream of their own, are no part of the captured work.
+static std::mutex g_op_flags_mu;
+static std::map<int, int*> g_op_flags;
 int op_flags(int** out) {
   int dev = 0;
   SAR_TRY(check(cudaGetDevice(&dev), "op flags: current device"));
   std::lock_guard<std::mutex> lk(g_op_flags_mu);
   int*& f = g_op_flags[dev];
   if (!f) {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    SAR_TRY(check(cudaThreadExchangeStreamCaptureMode(&mode), "op flags: capture mode"));
     int* p = nullptr;
-    SAR_TRY(check(cudaMalloc(&p, 16), "op flags: allocate"));
-    const int rc = check(cudaMemset(p, 0, 16), "op flags: clear");
+    cudaStream_t s = nullptr;
+    int rc = check(cudaMalloc(&p, 16), "op flags: allocate");
+    if (rc == SAR_OK) rc = check(cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking), "op flags: stream");
+    if (rc == SAR_OK) rc = check(cudaMemsetAsync(p, 0, 16, s), "op flags: clear");
+    if (rc == SAR_OK) rc = check(cudaStreamSynchronize(s), "op flags: synchronise");
+    if (s) cudaStreamDestroy(s);
+    cudaThreadExchangeStreamCaptureMode(&mode);
     if (rc != SAR_OK) {
       cudaFree(p);
       return rc;
@@ -133,6 +146,10 @@ int op_flags(int** out) {
   *out = f;
   return SAR_OK;
 }
+
+}  // namespace sar
+
+namespace {
 
 // ---- profiling helpers -----------------------------------------------------
 EventPair* prof_begin(sar_model* m, int kind, cudaStream_t s) {
@@ -1167,7 +1184,7 @@ int sar_op_gemm(const void* a, const void* w, void* c, const void* residual, int
   if (epilogue < SAR_EPI_STORE || epilogue > SAR_EPI_F32) return set_error(SAR_ERR_INVALID_ARG, "op_gemm: bad epilogue");
   if (storage != SAR_STORAGE_F16 && storage != SAR_STORAGE_BF16) return set_error(SAR_ERR_INVALID_ARG, "op_gemm: bad storage");
   int* err = nullptr;
-  SAR_TRY(op_flags(&err));
+  SAR_TRY(sar::op_flags(&err));
   sar::GemmCfg cfg;
   SAR_TRY(sar::gemm_config(M, N, K, epilogue, variant, &cfg, epilogue == SAR_EPI_RESIDUAL && c == residual));
   CUtensorMap amap, wmap;
@@ -1179,13 +1196,13 @@ int sar_op_gemm(const void* a, const void* w, void* c, const void* residual, int
 int sar_op_wait_check(int64_t limit_ns, int32_t arrivals, void* stream) {
   if (limit_ns <= 0 || arrivals < 0 || arrivals > 2) return set_error(SAR_ERR_INVALID_ARG, "op_wait_check: bad argument");
   int* err = nullptr;
-  SAR_TRY(op_flags(&err));
+  SAR_TRY(sar::op_flags(&err));
   return sar::launch_wait_check((uint64_t)limit_ns, arrivals, err, static_cast<cudaStream_t>(stream));
 }
 
 int sar_op_sync_status(void) {
   int* err = nullptr;
-  SAR_TRY(op_flags(&err));
+  SAR_TRY(sar::op_flags(&err));
   int h[4] = {0, 0, 0, 0};
   SAR_TRY(check(cudaDeviceSynchronize(), "op_sync_status: device synchronise"));
   SAR_TRY(check(cudaMemcpy(h, err, 16, cudaMemcpyDeviceToHost), "op_sync_status: read flags"));

@@ -175,4 +175,57 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo, 
   return d;
 }
 
+// ---- block-scaled 4-bit MMA (kind::mxf4nvf4 / kind::mxf4) --------------------
+
+// Copies one 512-byte scale tile (32 rows of 16 bytes, contiguous in shared
+// memory) into 4 tensor-memory columns, repeated for the four lane quarters:
+// byte 4 j + b of row l is the scale of operand row 32 j + l, K block b.
+// Executes in issue order ahead of the same thread's later MMAs.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+// Descriptor of such a tile: no swizzle, 8-row groups of 128 bytes.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(128 >> 4) << 16;
+  d |= (uint64_t)(128 >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  return d;
+}
+
+// D (128 x N fp32, tensor memory) (+)= (A . SA) . (B . SB)^T over K = 64: A and
+// B e2m1, two to a byte, K-major in 128-byte-swizzled shared memory.  NV: e4m3
+// scales of 16-element blocks, four per row; else e8m0 scales of 32-element
+// blocks, two per row (the descriptor's scale ids pick the pair).
+template <bool NV>
+__device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                        uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
+  if constexpr (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of mma_fp4: e2m1 operands (1), both K-major, scale
+// type e4m3 (0) or e8m0 (1), M = 128, N = n, K = 64; scale_id (0 or 2) is the
+// first of an e8m0 row's two scales within its 32-bit column, for A and B.
+__device__ __forceinline__ uint32_t idesc_fp4(int n, bool nv, uint32_t scale_id) {
+  return (scale_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((nv ? 0u : 1u) << 23) |
+         ((uint32_t)(128 >> 7) << 27) | (scale_id << 29);
+}
+
 }  // namespace sar

@@ -93,6 +93,50 @@ int sar_op_wait_check(int64_t limit_ns, int32_t arrivals, void* stream);
 int sar_op_rmsnorm(const void* x, const void* gain, void* y, int32_t rows, int32_t hidden,
                    float eps, int32_t storage, void* stream);
 
+/* ---- 4-bit rows --------------------------------------------------------- */
+
+/* Microscaled 4-bit floating point (no counterpart in the pages, which serve
+ * 16-bit weights): a matrix [rows, cols] is kept as e2m1 codes q (0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6 with a sign) with one scale s per block of columns of a row,
+ * and stands for q * s * tensor_scale.
+ *   SAR_FP4_NV  blocks of 16, s an e4m3 number (sign bit clear)
+ *   SAR_FP4_MX  blocks of 32, s = 2^(byte - 127); byte 255 is NaN
+ * cols is a multiple of 32.
+ *   codes   uint8 [rows][cols / 2], contiguous, 16-byte aligned: column 2i in
+ *           byte i's low four bits (bit 3 the sign), column 2i + 1 in its high ones
+ *   scales  uint8, 16-byte aligned, sar_op_fp4_scale_bytes() long.  Tiles of 128
+ *           rows x 4 blocks hold 512 bytes: row r and block b of the tile at
+ *           (r % 32) * 16 + (r / 32) * 4 + b.  The tiles of 128 rows follow one
+ *           another along the columns (the last one padded to 4 blocks), then
+ *           come those of the next 128 rows.  This is the order the product's
+ *           tensor cores take them in.  Padding blocks hold zero; the bytes of
+ *           rows behind the last are neither written nor used. */
+enum { SAR_FP4_NV = 0, SAR_FP4_MX = 1 };
+
+/* Element types of rows (the storage types, and fp32). */
+enum { SAR_TYPE_F16 = 0, SAR_TYPE_BF16 = 1, SAR_TYPE_F32 = 2 };
+
+/* Length of a matrix's scales in bytes. */
+int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* out);
+
+/* codes, scales = x: x device rows of `type`, row r at x + r * ldx elements
+ * (ldx >= cols; any alignment of the element, 16 bytes are faster).  With
+ * t = x * (1 / tensor_scale) in fp32 and a = max |t| over a block,
+ *   NV  s = a / 6 rounded to e4m3 (at most 448);    q = t / s rounded to e2m1
+ *   MX  s = 2^(floor(log2 a) - 2), at least 2^-127;  q = t / s rounded to e2m1
+ * to nearest even, q at most 6 in magnitude; a block whose scale rounds to zero
+ * is zero.  A block that holds a NaN or an infinity (in t) gets a NaN scale and
+ * zero codes.  tensor_scale > 0, finite, with a finite inverse.  rows = 0 does
+ * nothing; rows * cols / 16 (cols padded to whole scale tiles) stays below 2^32.
+ * Async on `stream`. */
+int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_t type, int32_t format,
+                        float tensor_scale, void* codes, void* scales, void* stream);
+
+/* y = the rows that codes and scales stand for: q * s (exact) * tensor_scale in
+ * fp32, rounded to `type`.  y rows as x above.  Async on `stream`. */
+int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, int32_t format,
+                          float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream);
+
 /* Device address of a step workspace buffer, valid until sar_model_destroy;
  * after a step on a one-layer model it holds that layer's intermediates.
  *   0: normed rows     [max_tokens, hidden] (storage type)
