@@ -13,12 +13,12 @@ from . import _lib
 from ._lib import (SAR_EPI_F32, SAR_EPI_RESIDUAL, SAR_EPI_STORE, SAR_EPI_SWIGLU, SAR_GEMM_AUTO,
                    SAR_GEMM_PAIR_N128, SAR_GEMM_PAIR_N192,
                    SAR_GEMM_PAIR_N256, SAR_GEMM_STREAM_K, SAR_GEMM_TWO_CTAS,
-                   SAR_FP4_MX, SAR_FP4_NV, SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
+                   SAR_FP4_GEMM_AUTO, SAR_FP4_GEMM_SPLIT, SAR_FP4_MX, SAR_FP4_NV, SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
                    SAR_IN_HIDDEN, SAR_IN_TOKENS, SAR_STORAGE_BF16, SAR_STORAGE_F16, KERNEL_KINDS,
                    SarError, check, lib)
 
 __all__ = ["Model", "KVCache", "Scheduler", "Batch", "StepGraph", "SarError", "lib", "check", "gemm", "rmsnorm",
-           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "SAR_FP4_NV", "SAR_FP4_MX",
+           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "gemm_fp4", "SAR_FP4_NV", "SAR_FP4_MX",
            "op_sync_status", "op_wait_check",
            "launch_count", "KERNEL_KINDS", "SAR_IN_HIDDEN", "SAR_IN_TOKENS", "SAR_STORAGE_F16",
            "SAR_STORAGE_BF16", "storage_dtype"]
@@ -433,3 +433,27 @@ def fp4_dequantize(codes, scales, y, format: int = SAR_FP4_NV, tensor_scale: flo
     _device_check("fp4_dequantize", codes, scales, y)
     check(lib().sar_op_fp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, format, tensor_scale, _ptr(y),
                                       _row_stride(y), kind, _stream(stream)))
+
+
+def gemm_fp4(a, a_scales, w, w_scales, c, residual=None, alpha: float = 1.0, epilogue=SAR_EPI_STORE,
+             format: int = SAR_FP4_NV, variant=SAR_FP4_GEMM_AUTO, stream=None) -> None:
+    """c = epilogue(alpha * a . w^T) of 4-bit rows (codes uint8 [rows, K / 2] and
+    their scales); 16-bit ``c`` for STORE and SWIGLU, fp32 for RESIDUAL and F32;
+    see ``sar_op_gemm_fp4``."""
+    import torch
+    M, N, K = a.shape[0], w.shape[0], 2 * a.shape[1]
+    _fp4_check("gemm_fp4", a, a_scales, M, K, format)
+    _fp4_check("gemm_fp4", w, w_scales, N, K, format)
+    wide = epilogue in (SAR_EPI_F32, SAR_EPI_RESIDUAL)
+    if c.dtype not in ((torch.float32,) if wide else (torch.float16, torch.bfloat16)):
+        raise ValueError("gemm_fp4: c must be fp32 for RESIDUAL and F32, fp16 or bf16 otherwise")
+    if tuple(c.shape) != (M, N // 2 if epilogue == SAR_EPI_SWIGLU else N) or not c.is_contiguous():
+        raise ValueError("gemm_fp4: c has another shape, or is not contiguous")
+    if (residual is None) != (epilogue != SAR_EPI_RESIDUAL):
+        raise ValueError("gemm_fp4: the residual goes with the RESIDUAL epilogue")
+    if residual is not None and (residual.dtype != torch.float32 or residual.shape != c.shape
+                                 or not residual.is_contiguous()):
+        raise ValueError("gemm_fp4: residual must be contiguous fp32 of c's shape")
+    _device_check("gemm_fp4", a, a_scales, w, w_scales, c, residual)
+    check(lib().sar_op_gemm_fp4(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(c), _ptr(residual), M, N, K,
+                                alpha, epilogue, format, variant, _storage_of(c), _stream(stream)))

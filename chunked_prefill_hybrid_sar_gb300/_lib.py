@@ -34,6 +34,7 @@ SAR_GEMM_TWO_CTAS = 0x1000
 SAR_Q_F32 = 0x100
 SAR_GEMM_STREAM_K = 0x2000
 SAR_FP4_NV, SAR_FP4_MX = 0, 1
+SAR_FP4_GEMM_AUTO, SAR_FP4_GEMM_SPLIT = 0, 1
 SAR_TYPE_F16, SAR_TYPE_BF16, SAR_TYPE_F32 = 0, 1, 2
 
 KERNEL_KINDS = ("embed", "rmsnorm", "gemm_qkv", "rope_append", "chunk_attn", "decode_attn", "gemm_o",
@@ -117,6 +118,7 @@ SIGNATURES = {
     "sar_op_fp4_scale_bytes": (i32, [i32, i32, i32, ctypes.POINTER(i64)]),
     "sar_op_fp4_quantize": (i32, [vp, i64, i32, i32, i32, i32, f32, vp, vp, vp]),
     "sar_op_fp4_dequantize": (i32, [vp, vp, i32, i32, i32, f32, vp, i64, i32, vp]),
+    "sar_op_gemm_fp4": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, f32, i32, i32, i32, i32, vp]),
     "sar_plan_inspect": (i32, [ctypes.POINTER(sar_dims), i32, i32, i32, i32, ctypes.POINTER(sar_batch), P_i32,
                                P_i32, i64, ctypes.POINTER(i64)]),
     "sar_model_debug_buffer": (i32, [vp, i32, ctypes.POINTER(vp)]),

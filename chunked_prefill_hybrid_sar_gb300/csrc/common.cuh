@@ -27,6 +27,9 @@ enum ErrSite {
   SITE_ROPE_BOUNDS = 30,
   SITE_EMBED_BOUNDS = 40,
   SITE_WAIT_CHECK = 50,
+  SITE_FP4_PRODUCER = 60,
+  SITE_FP4_MMA = 61,
+  SITE_FP4_EPILOGUE = 62,
 };
 
 // A wait that has not finished after this long gives up (normal waits take

@@ -1,0 +1,388 @@
+// Product of two microscaled 4-bit matrices on the 5th-generation tensor cores.
+//
+// C = epilogue(alpha * A . W^T), A = token rows [M, K], W = weight rows [N, K],
+// both e2m1 codes with block scales (fp4.cu).  kind::mxf4nvf4 / kind::mxf4 MMAs
+// take K = 64 codes a row from shared memory and the scales from tensor memory
+// and accumulate in fp32; the scales never meet the codes in a register.
+#include <cuda.h>
+
+#include <algorithm>
+#include <string>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc05.cuh"
+
+namespace sar {
+
+namespace {
+
+constexpr int kSlab = 256;                 // codes of a row per pipeline stage: 128 bytes, one swizzle span
+constexpr int kOpTile = 128 * 128;         // 128 rows of a slab
+constexpr int kTileBytes = 512;            // one scale tile
+constexpr int kSmemPerSm = 233472;         // 228 KB
+constexpr int kSmemLimit = 232448;         // 227 KB
+constexpr int kBarBytes = 256;
+
+template <bool NV>
+struct Fmt {
+  static constexpr int kTiles = NV ? 4 : 2;  // scale tiles of a row block in a slab (64 or 128 columns each)
+  static constexpr int kScaleBytes = kTiles * kTileBytes;
+};
+
+struct Params {
+  int M, N, K;
+  int slabs;      // of 256 columns
+  int tiles;      // scale tiles per row block
+  int bn;         // token rows per tile
+  int splits, slabs_per_split;
+  int stages, stage_bytes, tmem_cols;
+  const uint8_t* sa;
+  const uint8_t* sw;
+  void* c;
+  const float* r;
+  float alpha;
+  int vec;        // rows of c (and r) can be written four columns at a time
+  int* err;
+};
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
+// Writes four neighbouring results of row m from column n on.
+template <typename T, int EPI>
+__device__ __forceinline__ void put4(const Params& p, size_t m, int n, int ncols, const float (&x)[4]) {
+  const size_t at = m * (size_t)ncols + n;
+  if constexpr (EPI == SAR_EPI_F32 || EPI == SAR_EPI_RESIDUAL) {
+    float* c = reinterpret_cast<float*>(p.c) + at;
+    if (p.vec) {
+      float4 v = make_float4(x[0], x[1], x[2], x[3]);
+      if constexpr (EPI == SAR_EPI_RESIDUAL) {
+        const float4 r = *reinterpret_cast<const float4*>(p.r + at);
+        v = make_float4(v.x + r.x, v.y + r.y, v.z + r.z, v.w + r.w);
+      }
+      *reinterpret_cast<float4*>(c) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < ncols) c[i] = EPI == SAR_EPI_RESIDUAL ? x[i] + p.r[at + i] : x[i];
+    }
+  } else {
+    T* c = reinterpret_cast<T*>(p.c) + at;
+    if (p.vec) {
+      *reinterpret_cast<uint2*>(c) = make_uint2(Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < ncols) c[i] = Elem<T>::from(x[i]);
+    }
+  }
+}
+
+// Split tiling: 128 weight rows on the MMA's M side x bn <= 128 tokens on its N
+// side, the K range cut over the `splits` CTAs of a cluster.  Each CTA leaves
+// its fp32 partial tile in its own shared memory; after a cluster barrier each
+// adds up every CTA's partials (in rank order) for its share of the tokens and
+// writes them: no workspace, no atomics, one launch, the same sums each time.
+//   warp 0      TMA producer: 256-code slabs of both operands and their scale tiles
+//   warp 1      tensor memory; lane 0 copies scale tiles there and issues the MMAs
+//   warps 2..5  partial tile to shared memory, join, epilogue
+template <typename T, int EPI, bool NV>
+__global__ void __launch_bounds__(192)
+    gemm_fp4_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a, const Params p) {
+  using F = Fmt<NV>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + p.stages * p.stage_bytes);
+  uint64_t* empty_bar = full_bar + p.stages;
+  uint64_t* acc_bar = empty_bar + p.stages;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_bar + 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    mbar_init(smem_u32(acc_bar), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<false>(smem_u32(tmem_slot), (uint32_t)p.tmem_cols);
+    tmem_relinquish<false>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
+  const int mt = blockIdx.y, nt = blockIdx.z;
+  const int kb0 = rank * p.slabs_per_split;
+  const int n_slabs = min(p.slabs - kb0, p.slabs_per_split);
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_a);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      int i = 0;
+      const uint8_t* sw = p.sw + (size_t)nt * p.tiles * kTileBytes;
+      const uint8_t* sa = p.sa + (size_t)mt * p.tiles * kTileBytes;  // (several token tiles: bn = 128)
+      for (; i < n_slabs; ++i) {
+        const int s = i % p.stages;
+        if (!mbar_wait(smem_u32(&empty_bar[s]), ((uint32_t)(i / p.stages) & 1u) ^ 1u, p.err, SITE_FP4_PRODUCER)) {
+          ok = false;
+          break;
+        }
+        const int kb = kb0 + i;
+        const uint32_t st = smem_u32(smem + s * p.stage_bytes);
+        const uint32_t fb = smem_u32(&full_bar[s]);
+        const uint32_t tile0 = (uint32_t)kb * F::kTiles;
+        const uint32_t sb = (uint32_t)min(F::kTiles, p.tiles - (int)tile0) * kTileBytes;
+        const uint32_t a_at = st + kOpTile, s_at = a_at + (uint32_t)p.bn * 128;
+        mbar_expect_tx(fb, (uint32_t)kOpTile + (uint32_t)p.bn * 128 + 2 * sb);
+        tma_load_2d(st, &tm_w, kb * 128, nt * 128, fb);
+        tma_load_2d(a_at, &tm_a, kb * 128, mt * p.bn, fb);
+        bulk_g2s(s_at, sw + (size_t)tile0 * kTileBytes, sb, fb);
+        bulk_g2s(s_at + F::kScaleBytes, sa + (size_t)tile0 * kTileBytes, sb, fb);
+      }
+      // after a failure: no copy is in flight when the CTA leaves
+      for (int j = max(0, i - p.stages); !ok && j < i; ++j)
+        mbar_wait(smem_u32(&full_bar[j % p.stages]), (uint32_t)(j / p.stages) & 1u, p.err, SITE_FP4_PRODUCER);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      bool ok = true;
+      const uint32_t sf0 = tmem + (uint32_t)p.tmem_cols - 64;  // two buffers: 16 columns of W, 16 of A
+      for (int i = 0; ok && i < n_slabs; ++i) {
+        const int s = i % p.stages;
+        const uint32_t st = smem_u32(smem + s * p.stage_bytes);
+        const uint64_t wd = sw128_desc(st), ad = sw128_desc(st + kOpTile);
+        const uint32_t s_at = st + kOpTile + (uint32_t)p.bn * 128;
+        const uint64_t swd = scale_desc(s_at), sad = scale_desc(s_at + F::kScaleBytes);
+        const uint32_t sf = sf0 + (uint32_t)(i & 1) * 32;
+        // the MMAs that read this scale buffer (two slabs ago) have completed
+        if (i >= 2) ok = mbar_wait(smem_u32(&empty_bar[(i - 2) % p.stages]), (uint32_t)((i - 2) / p.stages) & 1u, p.err, SITE_FP4_MMA);
+        ok = ok && mbar_wait(smem_u32(&full_bar[s]), (uint32_t)(i / p.stages) & 1u, p.err, SITE_FP4_MMA);
+        if (!ok) break;
+        tc_fence_after();
+        const int nt_s = min(F::kTiles, p.tiles - (kb0 + i) * F::kTiles);
+        const int n_mma = min(4, (p.K - (kb0 + i) * kSlab + 63) >> 6);
+#pragma unroll
+        for (int t = 0; t < F::kTiles; ++t) {
+          if (t < nt_s) {
+            tmem_cp_scales(sf + 4 * t, swd + (uint64_t)(t * (kTileBytes >> 4)));
+            tmem_cp_scales(sf + 16 + 4 * t, sad + (uint64_t)(t * (kTileBytes >> 4)));
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j < n_mma) {
+            const int t = NV ? j : j >> 1;
+            mma_fp4<NV>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), idesc_fp4(p.bn, NV, NV ? 0u : 2u * (j & 1)),
+                        sf + 4 * t, sf + 16 + 4 * t, (i | j) != 0 ? 1u : 0u);
+          }
+        }
+        mma_commit(smem_u32(&empty_bar[s]));
+      }
+      if (ok) mma_commit(smem_u32(acc_bar));
+    }
+    __syncwarp();
+  } else {
+    int ok = 0;
+    if (lane == 0) ok = mbar_wait(smem_u32(acc_bar), 0, p.err, SITE_FP4_EPILOGUE) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    tc_fence_after();
+    // every MMA has completed, and with it every copy into the stages: they hold
+    // the partial tile now, [token][128 weight rows]
+    const int q = warp & 3;
+    float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
+    const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16);
+    for (int j = 0; ok && j < p.bn / 16; ++j) {
+      uint32_t v[16];
+      tmem_ld16(t0 + j * 16, v);
+      tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) part[(j * 16 + e) * 128] = __uint_as_float(v[e]);
+    }
+    tc_fence_before();
+  }
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+
+  if (warp >= 2) {
+    const int t = threadIdx.x - 64;
+    constexpr int kLanes = EPI == SAR_EPI_SWIGLU ? 16 : 32;  // four columns each
+    const int n4 = (t % kLanes) * 4;
+    const int m0 = mt * p.bn, rows = min(p.bn, p.M - m0);
+    const uint32_t part = smem_u32(smem);
+    auto joined = [&](int tok, int n, float (&x)[4]) {
+      const uint32_t at = part + (uint32_t)(tok * 128 + n) * 4;
+      x[0] = x[1] = x[2] = x[3] = 0.f;
+      for (int s = 0; s < p.splits; ++s) {
+        const float4 v = ld_cluster_f4(cluster_addr(at, (uint32_t)s));
+        x[0] += v.x;
+        x[1] += v.y;
+        x[2] += v.z;
+        x[3] += v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= p.alpha;
+    };
+    for (int tok = (t / kLanes) * p.splits + rank; tok < rows; tok += (128 / kLanes) * p.splits) {
+      float x[4];
+      joined(tok, n4, x);
+      if constexpr (EPI == SAR_EPI_SWIGLU) {
+        float u[4];
+        joined(tok, 64 + n4, u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = silu(x[i]) * u[i];
+        put4<T, EPI>(p, (size_t)(m0 + tok), nt * 64 + n4, p.N >> 1, x);
+      } else if (nt * 128 + n4 < p.N) {
+        put4<T, EPI>(p, (size_t)(m0 + tok), nt * 128 + n4, p.N, x);
+      }
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1)
+    cluster_sync();  // the partials are read by the whole cluster
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<false>(tmem, (uint32_t)p.tmem_cols);
+  }
+}
+
+template <typename T, bool NV>
+const void* pick_split(int epi) {
+  switch (epi) {
+    case SAR_EPI_STORE: return reinterpret_cast<const void*>(&gemm_fp4_split_kernel<T, SAR_EPI_STORE, NV>);
+    case SAR_EPI_RESIDUAL: return reinterpret_cast<const void*>(&gemm_fp4_split_kernel<T, SAR_EPI_RESIDUAL, NV>);
+    case SAR_EPI_SWIGLU: return reinterpret_cast<const void*>(&gemm_fp4_split_kernel<T, SAR_EPI_SWIGLU, NV>);
+    default: return reinterpret_cast<const void*>(&gemm_fp4_split_kernel<T, SAR_EPI_F32, NV>);
+  }
+}
+
+struct Call {
+  const void *a, *w;
+  int epi, format, storage, variant;
+  cudaStream_t s;
+};
+
+int launch_split(const Call& g, Params p) {
+  const bool nv = g.format == SAR_FP4_NV;
+  const int m_tiles = (p.M + 127) / 128, n_tiles = (p.N + 127) / 128;
+  if (m_tiles > 65535 || n_tiles > 65535) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many tiles");
+  p.bn = m_tiles > 1 ? 128 : (p.M + 15) / 16 * 16;
+  int splits = g.variant >> 8 & 0xff;
+  if (!splits) {
+    const long tiles = (long)m_tiles * n_tiles;
+    splits = (int)std::max<long>(1, std::min<long>(8, 2L * num_sms() / tiles));
+    splits = std::min(splits, std::max(1, p.slabs / 2));
+  }
+  if (splits > 8 || splits > p.slabs) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many K ranges");
+  p.slabs_per_split = (p.slabs + splits - 1) / splits;
+  p.splits = (p.slabs + p.slabs_per_split - 1) / p.slabs_per_split;  // no empty range
+  p.stage_bytes = kOpTile + p.bn * 128 + 2 * (nv ? Fmt<true>::kScaleBytes : Fmt<false>::kScaleBytes);
+  p.tmem_cols = p.bn <= 64 ? 128 : 256;
+  // two CTAs to an SM, each with half of its shared memory
+  const int extra = kBarBytes + 1024;
+  p.stages = std::min(8, (kSmemPerSm / 2 - 1024 - extra) / p.stage_bytes);
+  const int smem = p.stages * p.stage_bytes + extra;
+  const bool bf = g.storage == SAR_STORAGE_BF16;
+  const void* fn = nv ? (bf ? pick_split<__nv_bfloat16, true>(g.epi) : pick_split<__half, true>(g.epi))
+                      : (bf ? pick_split<__nv_bfloat16, false>(g.epi) : pick_split<__half, false>(g.epi));
+  CUtensorMap tw, ta;
+  SAR_TRY(make_tmap_bytes(&tw, g.w, (uint64_t)p.N, (uint64_t)p.K / 2, 128));
+  SAR_TRY(make_tmap_bytes(&ta, g.a, (uint64_t)p.M, (uint64_t)p.K / 2, (uint32_t)p.bn));
+  SAR_TRY(ensure_smem_attr(fn, kSmemLimit, "gemm_fp4: set smem attribute"));
+  void* args[] = {&tw, &ta, &p};
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[2];
+  lc.gridDim = dim3((unsigned)p.splits, (unsigned)m_tiles, (unsigned)n_tiles);
+  lc.blockDim = dim3(192);
+  lc.dynamicSmemBytes = (size_t)smem;
+  lc.stream = g.s;
+  lc.attrs = attr;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  lc.numAttrs = 1;
+  if (p.splits > 1) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    lc.numAttrs = 2;
+  }
+  const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
+  if (e != cudaSuccess) return cuda_error(e, "gemm_fp4 launch");
+  count_launches(1);
+  return SAR_OK;
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+}  // namespace sar
+
+using sar::set_error;
+
+extern "C" {
+
+int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const void* w_scales, void* c,
+                    const void* residual, int32_t M, int32_t N, int32_t K, float alpha, int32_t epilogue, int32_t format,
+                    int32_t variant, int32_t storage, void* stream) {
+  if (M < 0 || N < 1 || K < 1) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad shape");
+  if (epilogue < SAR_EPI_STORE || epilogue > SAR_EPI_F32) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad epilogue");
+  if (format != SAR_FP4_NV && format != SAR_FP4_MX) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad format");
+  if (storage != SAR_STORAGE_F16 && storage != SAR_STORAGE_BF16) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad storage");
+  if (variant < 0 || (variant & 0xff) > SAR_FP4_GEMM_SPLIT || variant > 0xffff)
+    return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: unknown variant");
+  if (K % 32) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: K must be a multiple of 32");
+  if (epilogue == SAR_EPI_SWIGLU && N % 128)
+    return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: SwiGLU needs whole 64-row gate/up block pairs");
+  if (M == 0) return SAR_OK;
+  if (!a || !a_scales || !w || !w_scales || !c) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: null pointer");
+  if (epilogue == SAR_EPI_RESIDUAL && !residual)
+    return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: residual epilogue without residual");
+  if (!sar::aligned(a, 16) || !sar::aligned(a_scales, 16) || !sar::aligned(w, 16) || !sar::aligned(w_scales, 16))
+    return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: codes and scales must be 16-byte aligned");
+  const bool wide_out = epilogue == SAR_EPI_F32 || epilogue == SAR_EPI_RESIDUAL;
+  const uintptr_t elem = wide_out ? 4 : 2;
+  if (!sar::aligned(c, elem) || (epilogue == SAR_EPI_RESIDUAL && !sar::aligned(residual, 4)))
+    return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: output not aligned to its element");
+  sar::Params p = {};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.slabs = (K + sar::kSlab - 1) / sar::kSlab;
+  p.tiles = sar::fp4_tiles(K, format);
+  p.sa = static_cast<const uint8_t*>(a_scales);
+  p.sw = static_cast<const uint8_t*>(w_scales);
+  p.c = c;
+  p.r = static_cast<const float*>(residual);
+  p.alpha = alpha;
+  p.vec = N % 4 == 0 && sar::aligned(c, 4 * elem) && (epilogue != SAR_EPI_RESIDUAL || sar::aligned(residual, 16));
+  SAR_TRY(sar::op_flags(&p.err));
+  const sar::Call g = {a, w, epilogue, format, storage, variant, static_cast<cudaStream_t>(stream)};
+  return sar::launch_split(g, p);
+}
+
+}  // extern "C"

@@ -78,6 +78,10 @@ inline int fp4_tiles(int cols, int format) {
 int make_tmap_16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,
                  int storage);
 
+// Encodes a 2D byte tensor map over row-major [rows, row_bytes] with a
+// 128-byte x box_rows box and 128-byte swizzle; bytes behind a row read zero.
+int make_tmap_bytes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
+
 struct GemmCfg {
   int swap = 0;     // weights on the MMA M side
   int msub = 1;     // 128-row A sub-tiles per tile (non-swap only)

@@ -137,6 +137,29 @@ int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, 
 int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, int32_t format,
                           float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream);
 
+/* Tilings of the 4-bit product. */
+enum {
+  SAR_FP4_GEMM_AUTO = 0,  /* the library's choice for (M, N, K)                        */
+  SAR_FP4_GEMM_SPLIT = 1  /* 128 weight rows x up to 128 token rows per tile, the K
+                             range cut over a cluster's CTAs; | (count << 8) asks for
+                             that many ranges (1..8, at most one per 256 columns)     */
+};
+
+/* C = epilogue(alpha * A . W^T) of 4-bit rows of one format: A [M, K] and W [N, K]
+ * as codes and scales laid out as above, each without its tensor scale (alpha
+ * holds their product).  K a multiple of 32, any M >= 0 and N >= 1.
+ *   SAR_EPI_STORE     C [M, N] in the 16-bit type `storage`
+ *   SAR_EPI_RESIDUAL  C fp32 [M, N] = alpha * A . W^T + R (R may equal C)
+ *   SAR_EPI_SWIGLU    W's rows gate/up interleaved in 64-row blocks (N a multiple
+ *                     of 128); C [M, N / 2] = silu(gate) * up in `storage`
+ *   SAR_EPI_F32       C fp32 [M, N]
+ * C and R are contiguous; N a multiple of 4 and 16-byte aligned rows are faster.
+ * Sums are fp32; the result does not depend on timing.  Async on `stream`;
+ * device-side failures are read with sar_op_sync_status(). */
+int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const void* w_scales, void* c,
+                    const void* residual, int32_t M, int32_t N, int32_t K, float alpha, int32_t epilogue, int32_t format,
+                    int32_t variant, int32_t storage, void* stream);
+
 /* Device address of a step workspace buffer, valid until sar_model_destroy;
  * after a step on a one-layer model it holds that layer's intermediates.
  *   0: normed rows     [max_tokens, hidden] (storage type)

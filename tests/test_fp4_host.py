@@ -76,3 +76,23 @@ def test_no_rows_is_no_work():
     assert lib.sar_op_fp4_dequantize(None, None, 0, 32, 0, 1.0, None, 32, 0, None) == _lib.SAR_OK
     n = ctypes.c_int64()
     assert lib.sar_op_fp4_scale_bytes(1, 33, 0, ctypes.byref(n)) == _lib.SAR_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("change,code", [
+    (dict(a=None), "INVALID"), (dict(sa=None), "INVALID"), (dict(w=None), "INVALID"), (dict(sw=None), "INVALID"),
+    (dict(c=None), "INVALID"), (dict(M=-1), "INVALID"), (dict(N=0), "INVALID"), (dict(K=0), "INVALID"),
+    (dict(K=48), "UNSUPPORTED"), (dict(epi=4), "INVALID"), (dict(epi=-1), "INVALID"), (dict(fmt=2), "INVALID"),
+    (dict(storage=2), "INVALID"), (dict(variant=0xff), "INVALID"), (dict(variant=-1), "INVALID"),
+    (dict(variant=1 << 16), "INVALID"), (dict(epi=2, N=192), "UNSUPPORTED"), (dict(epi=1), "INVALID"),
+    (dict(a=P + 8), "INVALID"), (dict(w=P + 8), "INVALID"), (dict(sa=P + 1), "INVALID"), (dict(sw=P + 4), "INVALID"),
+    (dict(c=P + 1), "INVALID"), (dict(epi=3, c=P + 2), "INVALID"), (dict(epi=1, r=P + 2), "INVALID"),
+])
+def test_product_is_refused(change, code):
+    a = dict(a=P, sa=P, w=P, sw=P, c=P, r=None, M=4, N=128, K=64, alpha=1.0, epi=0, fmt=0, variant=0, storage=0) | change
+    rc = sar.lib().sar_op_gemm_fp4(a["a"], a["sa"], a["w"], a["sw"], a["c"], a["r"], a["M"], a["N"], a["K"], a["alpha"],
+                                   a["epi"], a["fmt"], a["variant"], a["storage"], None)
+    assert rc == {"INVALID": _lib.SAR_ERR_INVALID_ARG, "UNSUPPORTED": _lib.SAR_ERR_UNSUPPORTED}[code]
+
+
+def test_product_of_no_tokens_is_no_work():
+    assert sar.lib().sar_op_gemm_fp4(None, None, None, None, None, None, 0, 64, 64, 1.0, 0, 0, 0, 0, None) == _lib.SAR_OK
