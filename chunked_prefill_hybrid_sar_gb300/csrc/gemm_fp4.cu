@@ -46,6 +46,11 @@ struct Params {
   int* err;
 };
 
+// The whole warp waits; all its lanes get the same answer.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, site)) != 0;
+}
+
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -134,52 +139,55 @@ __global__ void __launch_bounds__(192)
   pdl_launch_dependents();
 
   if (warp == 0) {
-    if (lane == 0) {
-      bool ok = true;
-      int i = 0;
-      const uint8_t* sw = p.sw + (size_t)nt * p.tiles * kTileBytes;
-      const uint8_t* sa = p.sa + (size_t)mt * p.tiles * kTileBytes;  // (several token tiles: bn = 128)
-      for (; i < n_slabs; ++i) {
-        const int s = i % p.stages;
-        if (!mbar_wait(smem_u32(&empty_bar[s]), ((uint32_t)(i / p.stages) & 1u) ^ 1u, p.err, SITE_FP4_PRODUCER)) {
-          ok = false;
-          break;
-        }
-        const int kb = kb0 + i;
-        const uint32_t st = smem_u32(smem + s * p.stage_bytes);
-        const uint32_t fb = smem_u32(&full_bar[s]);
-        const uint32_t tile0 = (uint32_t)kb * F::kTiles;
-        const uint32_t sb = (uint32_t)min(F::kTiles, p.tiles - (int)tile0) * kTileBytes;
-        const uint32_t a_at = st + kOpTile, s_at = a_at + (uint32_t)p.bn * 128;
+    bool ok = true;
+    int i = 0, s = 0;
+    uint32_t ph = 0;
+    const uint8_t* sw = p.sw + (size_t)nt * p.tiles * kTileBytes;
+    const uint8_t* sa = p.sa + (size_t)mt * p.tiles * kTileBytes;  // (several token tiles: bn = 128)
+    for (; i < n_slabs; ++i) {
+      ok = warp_wait(smem_u32(&empty_bar[s]), ph ^ 1u, p.err, SITE_FP4_PRODUCER);
+      if (!ok) break;
+      const int kb = kb0 + i;
+      const uint32_t st = smem_u32(smem + s * p.stage_bytes);
+      const uint32_t fb = smem_u32(&full_bar[s]);
+      const uint32_t tile0 = (uint32_t)kb * F::kTiles;
+      const uint32_t sb = (uint32_t)min(F::kTiles, p.tiles - (int)tile0) * kTileBytes;
+      const uint32_t a_at = st + kOpTile, s_at = a_at + (uint32_t)p.bn * 128;
+      if (elect_one()) {
         mbar_expect_tx(fb, (uint32_t)kOpTile + (uint32_t)p.bn * 128 + 2 * sb);
         tma_load_2d(st, &tm_w, kb * 128, nt * 128, fb);
         tma_load_2d(a_at, &tm_a, kb * 128, mt * p.bn, fb);
         bulk_g2s(s_at, sw + (size_t)tile0 * kTileBytes, sb, fb);
         bulk_g2s(s_at + F::kScaleBytes, sa + (size_t)tile0 * kTileBytes, sb, fb);
       }
-      // after a failure: no copy is in flight when the CTA leaves
-      for (int j = max(0, i - p.stages); !ok && j < i; ++j)
-        mbar_wait(smem_u32(&full_bar[j % p.stages]), (uint32_t)(j / p.stages) & 1u, p.err, SITE_FP4_PRODUCER);
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
+    // after a failure: no copy is in flight when the CTA leaves
+    for (int j = max(0, i - p.stages); !ok && j < i; ++j)
+      mbar_wait(smem_u32(&full_bar[j % p.stages]), (uint32_t)(j / p.stages) & 1u, p.err, SITE_FP4_PRODUCER);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      bool ok = true;
-      const uint32_t sf0 = tmem + (uint32_t)p.tmem_cols - 64;  // two buffers: 16 columns of W, 16 of A
-      for (int i = 0; ok && i < n_slabs; ++i) {
-        const int s = i % p.stages;
-        const uint32_t st = smem_u32(smem + s * p.stage_bytes);
-        const uint64_t wd = sw128_desc(st), ad = sw128_desc(st + kOpTile);
-        const uint32_t s_at = st + kOpTile + (uint32_t)p.bn * 128;
-        const uint64_t swd = scale_desc(s_at), sad = scale_desc(s_at + F::kScaleBytes);
-        const uint32_t sf = sf0 + (uint32_t)(i & 1) * 32;
-        // the MMAs that read this scale buffer (two slabs ago) have completed
-        if (i >= 2) ok = mbar_wait(smem_u32(&empty_bar[(i - 2) % p.stages]), (uint32_t)((i - 2) / p.stages) & 1u, p.err, SITE_FP4_MMA);
-        ok = ok && mbar_wait(smem_u32(&full_bar[s]), (uint32_t)(i / p.stages) & 1u, p.err, SITE_FP4_MMA);
-        if (!ok) break;
-        tc_fence_after();
-        const int nt_s = min(F::kTiles, p.tiles - (kb0 + i) * F::kTiles);
-        const int n_mma = min(4, (p.K - (kb0 + i) * kSlab + 63) >> 6);
+    bool ok = true;
+    // a scale buffer per stage (16 columns of W, 16 of A): a stage that is full
+    // was emptied, so the MMAs that read its scale buffer before have completed
+    const uint32_t sf0 = tmem + (uint32_t)p.tmem_cols - (uint32_t)p.stages * 32;
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n_slabs; ++i) {
+      const uint32_t st = smem_u32(smem + s * p.stage_bytes);
+      const uint64_t wd = sw128_desc(st), ad = sw128_desc(st + kOpTile);
+      const uint32_t s_at = st + kOpTile + (uint32_t)p.bn * 128;
+      const uint64_t swd = scale_desc(s_at), sad = scale_desc(s_at + F::kScaleBytes);
+      const uint32_t sf = sf0 + (uint32_t)s * 32;
+      const int nt_s = min(F::kTiles, p.tiles - (kb0 + i) * F::kTiles);
+      const int n_mma = min(4, (p.K - (kb0 + i) * kSlab + 63) >> 6);
+      ok = warp_wait(smem_u32(&full_bar[s]), ph, p.err, SITE_FP4_MMA);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int t = 0; t < F::kTiles; ++t) {
           if (t < nt_s) {
@@ -196,15 +204,16 @@ __global__ void __launch_bounds__(192)
           }
         }
         mma_commit(smem_u32(&empty_bar[s]));
+        if (i == n_slabs - 1) mma_commit(smem_u32(acc_bar));
       }
-      if (ok) mma_commit(smem_u32(acc_bar));
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1u;
+      }
     }
     __syncwarp();
   } else {
-    int ok = 0;
-    if (lane == 0) ok = mbar_wait(smem_u32(acc_bar), 0, p.err, SITE_FP4_EPILOGUE) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
+    const bool ok = warp_wait(smem_u32(acc_bar), 0, p.err, SITE_FP4_EPILOGUE);
     tc_fence_after();
     // every MMA has completed, and with it every copy into the stages: they hold
     // the partial tile now, [token][128 weight rows]
@@ -231,30 +240,45 @@ __global__ void __launch_bounds__(192)
     const int n4 = (t % kLanes) * 4;
     const int m0 = mt * p.bn, rows = min(p.bn, p.M - m0);
     const uint32_t part = smem_u32(smem);
-    auto joined = [&](int tok, int n, float (&x)[4]) {
-      const uint32_t at = part + (uint32_t)(tok * 128 + n) * 4;
-      x[0] = x[1] = x[2] = x[3] = 0.f;
+    // four tokens' partials are read at a time, rank by rank, so that their
+    // latency is paid once for all of them
+    constexpr int kU = 4;
+    const int step = (128 / kLanes) * p.splits;
+    auto joined = [&](int tok0, int n, float4 (&x)[kU]) {
+#pragma unroll
+      for (int u = 0; u < kU; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int s = 0; s < p.splits; ++s) {
-        const float4 v = ld_cluster_f4(cluster_addr(at, (uint32_t)s));
-        x[0] += v.x;
-        x[1] += v.y;
-        x[2] += v.z;
-        x[3] += v.w;
+        const uint32_t at = cluster_addr(part, (uint32_t)s) + (uint32_t)n * 4;
+        float4 v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) v[u] = ld_cluster_f4(at + (uint32_t)min(tok0 + u * step, p.bn - 1) * 512);
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          x[u].x += v[u].x;
+          x[u].y += v[u].y;
+          x[u].z += v[u].z;
+          x[u].w += v[u].w;
+        }
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] *= p.alpha;
     };
-    for (int tok = (t / kLanes) * p.splits + rank; tok < rows; tok += (128 / kLanes) * p.splits) {
-      float x[4];
-      joined(tok, n4, x);
-      if constexpr (EPI == SAR_EPI_SWIGLU) {
-        float u[4];
-        joined(tok, 64 + n4, u);
+    for (int tok0 = (t / kLanes) * p.splits + rank; tok0 < rows; tok0 += kU * step) {
+      float4 x[kU], y[kU];
+      joined(tok0, n4, x);
+      if constexpr (EPI == SAR_EPI_SWIGLU) joined(tok0, 64 + n4, y);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = silu(x[i]) * u[i];
-        put4<T, EPI>(p, (size_t)(m0 + tok), nt * 64 + n4, p.N >> 1, x);
-      } else if (nt * 128 + n4 < p.N) {
-        put4<T, EPI>(p, (size_t)(m0 + tok), nt * 128 + n4, p.N, x);
+      for (int u = 0; u < kU; ++u) {
+        const int tok = tok0 + u * step;
+        if (tok >= rows) continue;
+        float o[4] = {x[u].x * p.alpha, x[u].y * p.alpha, x[u].z * p.alpha, x[u].w * p.alpha};
+        if constexpr (EPI == SAR_EPI_SWIGLU) {
+          o[0] = silu(o[0]) * (y[u].x * p.alpha);
+          o[1] = silu(o[1]) * (y[u].y * p.alpha);
+          o[2] = silu(o[2]) * (y[u].z * p.alpha);
+          o[3] = silu(o[3]) * (y[u].w * p.alpha);
+          put4<T, EPI>(p, (size_t)(m0 + tok), nt * 64 + n4, p.N >> 1, o);
+        } else if (nt * 128 + n4 < p.N) {
+          put4<T, EPI>(p, (size_t)(m0 + tok), nt * 128 + n4, p.N, o);
+        }
       }
     }
   }
@@ -300,10 +324,10 @@ int launch_split(const Call& g, Params p) {
   p.slabs_per_split = (p.slabs + splits - 1) / splits;
   p.splits = (p.slabs + p.slabs_per_split - 1) / p.slabs_per_split;  // no empty range
   p.stage_bytes = kOpTile + p.bn * 128 + 2 * (nv ? Fmt<true>::kScaleBytes : Fmt<false>::kScaleBytes);
-  p.tmem_cols = p.bn <= 64 ? 128 : 256;
+  p.tmem_cols = 256;  // two CTAs to an SM share its 512 columns
   // two CTAs to an SM, each with half of its shared memory
   const int extra = kBarBytes + 1024;
-  p.stages = std::min(8, (kSmemPerSm / 2 - 1024 - extra) / p.stage_bytes);
+  p.stages = std::min((p.tmem_cols - p.bn) / 32, (kSmemPerSm / 2 - 1024 - extra) / p.stage_bytes);
   const int smem = p.stages * p.stage_bytes + extra;
   const bool bf = g.storage == SAR_STORAGE_BF16;
   const void* fn = nv ? (bf ? pick_split<__nv_bfloat16, true>(g.epi) : pick_split<__half, true>(g.epi))
