@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(192)
   using F = Fmt<NV>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + p.stages * p.stage_bytes);
   uint64_t* empty_bar = full_bar + p.stages;
   uint64_t* acc_bar = empty_bar + p.stages;
@@ -125,7 +125,12 @@ __global__ void __launch_bounds__(192)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  // (addresses that the compiler cannot tell to be the same in all lanes are made
+  // so by a shuffle: the MMA loop then runs on uniform registers, without a move
+  // per operand and instruction)
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+  const uint32_t bars = __shfl_sync(0xffffffffu, smem_u32(full_bar), 0);
 
   const int rank = p.splits > 1 ? (int)cluster_ctarank() : 0;
   const int mt = blockIdx.y, nt = blockIdx.z;
@@ -145,11 +150,11 @@ __global__ void __launch_bounds__(192)
     const uint8_t* sw = p.sw + (size_t)nt * p.tiles * kTileBytes;
     const uint8_t* sa = p.sa + (size_t)mt * p.tiles * kTileBytes;  // (several token tiles: bn = 128)
     for (; i < n_slabs; ++i) {
-      ok = warp_wait(smem_u32(&empty_bar[s]), ph ^ 1u, p.err, SITE_FP4_PRODUCER);
+      ok = warp_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER);
       if (!ok) break;
       const int kb = kb0 + i;
-      const uint32_t st = smem_u32(smem + s * p.stage_bytes);
-      const uint32_t fb = smem_u32(&full_bar[s]);
+      const uint32_t st = base + (uint32_t)(s * p.stage_bytes);
+      const uint32_t fb = bars + (uint32_t)s * 8;
       const uint32_t tile0 = (uint32_t)kb * F::kTiles;
       const uint32_t sb = (uint32_t)min(F::kTiles, p.tiles - (int)tile0) * kTileBytes;
       const uint32_t a_at = st + kOpTile, s_at = a_at + (uint32_t)p.bn * 128;
@@ -170,47 +175,53 @@ __global__ void __launch_bounds__(192)
       mbar_wait(smem_u32(&full_bar[j % p.stages]), (uint32_t)(j / p.stages) & 1u, p.err, SITE_FP4_PRODUCER);
     __syncwarp();
   } else if (warp == 1) {
-    bool ok = true;
     // a scale buffer per stage (16 columns of W, 16 of A): a stage that is full
     // was emptied, so the MMAs that read its scale buffer before have completed
     const uint32_t sf0 = tmem + (uint32_t)p.tmem_cols - (uint32_t)p.stages * 32;
+    const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;  // in a descriptor's 16-byte units
+    const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
+    const uint64_t swd0 = scale_desc(base + kOpTile + (uint32_t)p.bn * 128);
+    const uint32_t idesc0 = idesc_fp4(p.bn, NV, 0), idesc1 = idesc_fp4(p.bn, NV, NV ? 0 : 2);
     int s = 0;
     uint32_t ph = 0;
-    for (int i = 0; i < n_slabs; ++i) {
-      const uint32_t st = smem_u32(smem + s * p.stage_bytes);
-      const uint64_t wd = sw128_desc(st), ad = sw128_desc(st + kOpTile);
-      const uint32_t s_at = st + kOpTile + (uint32_t)p.bn * 128;
-      const uint64_t swd = scale_desc(s_at), sad = scale_desc(s_at + F::kScaleBytes);
+    // one slab: nt_s scale tiles of each operand to tensor memory, n_mma MMAs
+    auto slab = [&](uint32_t acc, int nt_s, int n_mma) {
+      const uint32_t off = (uint32_t)s * stage_step;
+      const uint64_t wd = wd0 + off, ad = ad0 + off, swd = swd0 + off;
       const uint32_t sf = sf0 + (uint32_t)s * 32;
-      const int nt_s = min(F::kTiles, p.tiles - (kb0 + i) * F::kTiles);
-      const int n_mma = min(4, (p.K - (kb0 + i) * kSlab + 63) >> 6);
-      ok = warp_wait(smem_u32(&full_bar[s]), ph, p.err, SITE_FP4_MMA);
-      if (!ok) break;
+      if (!warp_wait(bars + (uint32_t)s * 8, ph, p.err, SITE_FP4_MMA)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
         for (int t = 0; t < F::kTiles; ++t) {
           if (t < nt_s) {
             tmem_cp_scales(sf + 4 * t, swd + (uint64_t)(t * (kTileBytes >> 4)));
-            tmem_cp_scales(sf + 16 + 4 * t, sad + (uint64_t)(t * (kTileBytes >> 4)));
+            tmem_cp_scales(sf + 16 + 4 * t, swd + (uint64_t)((F::kScaleBytes + t * kTileBytes) >> 4));
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j < n_mma) {
             const int t = NV ? j : j >> 1;
-            mma_fp4<NV>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), idesc_fp4(p.bn, NV, NV ? 0u : 2u * (j & 1)),
-                        sf + 4 * t, sf + 16 + 4 * t, (i | j) != 0 ? 1u : 0u);
+            mma_fp4<NV>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), (j & 1) ? idesc1 : idesc0, sf + 4 * t,
+                        sf + 16 + 4 * t, j != 0 ? 1u : acc);
           }
         }
-        mma_commit(smem_u32(&empty_bar[s]));
-        if (i == n_slabs - 1) mma_commit(smem_u32(acc_bar));
+        mma_commit(bars + (uint32_t)(p.stages + s) * 8);
       }
       if (++s == p.stages) {
         s = 0;
         ph ^= 1u;
       }
-    }
+      return true;
+    };
+    // whole slabs, then the row's ragged end
+    const int whole = min(n_slabs, p.K / kSlab - kb0);
+    bool ok = true;
+    for (int i = 0; ok && i < whole; ++i) ok = slab(i != 0 ? 1u : 0u, F::kTiles, 4);
+    if (ok && whole < n_slabs)
+      ok = slab(whole != 0 ? 1u : 0u, p.tiles - (kb0 + whole) * F::kTiles, (p.K - (kb0 + whole) * kSlab + 63) >> 6);
+    if (ok && elect_one()) mma_commit(smem_u32(acc_bar));
     __syncwarp();
   } else {
     const bool ok = warp_wait(smem_u32(acc_bar), 0, p.err, SITE_FP4_EPILOGUE);
