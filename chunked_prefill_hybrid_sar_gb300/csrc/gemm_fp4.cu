@@ -23,6 +23,8 @@ constexpr int kTileBytes = 512;            // one scale tile
 constexpr int kSmemPerSm = 233472;         // 228 KB
 constexpr int kSmemLimit = 232448;         // 227 KB
 constexpr int kBarBytes = 256;
+constexpr int kPairThreads = 320;
+constexpr int kXchgBytes = 2 * 2 * 64 * 17 * 4;  // pair SwiGLU: per token half two buffers of 64 rows x 16 tokens
 
 template <bool NV>
 struct Fmt {
@@ -42,9 +44,35 @@ struct Params {
   void* c;
   const float* r;
   float alpha;
+  // pair tiling
+  int m_full, n_tiles, last_bn, group, units;
   int vec;        // rows of c (and r) can be written four columns at a time
   int* err;
 };
+
+// Work unit u of the pair tiling.  Whole token tiles come first, in groups of
+// `group` token tiles that share a weight tile one after the other (the pairs
+// running at one time then cover a block of tiles, and what they fetch meets in
+// L2); the narrow last token tile of each weight tile comes last.
+struct Tile {
+  int mt, nt, bn;
+};
+__device__ __forceinline__ Tile tile_of(const Params& p, int u) {
+  Tile t;
+  const int n_full = p.m_full * p.n_tiles;
+  if (u < n_full) {
+    const int g = u / (p.group * p.n_tiles), m0 = g * p.group;
+    const int gs = min(p.group, p.m_full - m0), r = u - m0 * p.n_tiles;
+    t.nt = r / gs;
+    t.mt = m0 + r - t.nt * gs;
+    t.bn = 256;
+  } else {
+    t.nt = u - n_full;
+    t.mt = p.m_full;
+    t.bn = p.last_bn;
+  }
+  return t;
+}
 
 // The whole warp waits; all its lanes get the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, int site) {
@@ -181,7 +209,7 @@ __global__ void __launch_bounds__(192)
     const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;  // in a descriptor's 16-byte units
     const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
     const uint64_t swd0 = scale_desc(base + kOpTile + (uint32_t)p.bn * 128);
-    const uint32_t idesc0 = idesc_fp4(p.bn, NV, 0), idesc1 = idesc_fp4(p.bn, NV, NV ? 0 : 2);
+    const uint32_t idesc0 = idesc_fp4(128, p.bn, NV, 0), idesc1 = idesc_fp4(128, p.bn, NV, NV ? 0 : 2);
     int s = 0;
     uint32_t ph = 0;
     // one slab: nt_s scale tiles of each operand to tensor memory, n_mma MMAs
@@ -195,15 +223,15 @@ __global__ void __launch_bounds__(192)
 #pragma unroll
         for (int t = 0; t < F::kTiles; ++t) {
           if (t < nt_s) {
-            tmem_cp_scales(sf + 4 * t, swd + (uint64_t)(t * (kTileBytes >> 4)));
-            tmem_cp_scales(sf + 16 + 4 * t, swd + (uint64_t)((F::kScaleBytes + t * kTileBytes) >> 4));
+            tmem_cp_scales<false>(sf + 4 * t, swd + (uint64_t)(t * (kTileBytes >> 4)));
+            tmem_cp_scales<false>(sf + 16 + 4 * t, swd + (uint64_t)((F::kScaleBytes + t * kTileBytes) >> 4));
           }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j < n_mma) {
             const int t = NV ? j : j >> 1;
-            mma_fp4<NV>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), (j & 1) ? idesc1 : idesc0, sf + 4 * t,
+            mma_fp4<NV, false>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), (j & 1) ? idesc1 : idesc0, sf + 4 * t,
                         sf + 16 + 4 * t, j != 0 ? 1u : acc);
           }
         }
@@ -304,6 +332,239 @@ __global__ void __launch_bounds__(192)
   }
 }
 
+// Pair tiling: 256 weight rows x up to 256 tokens per tile over a CTA pair
+// (cta_group::2).  Each CTA of the pair holds 128 weight rows and half of the
+// tile's tokens in shared memory; the leader's MMAs (M = 256) read both, so an
+// SM fetches (128 + 128) rows per 128 x 256 results where one CTA alone would
+// fetch (128 + 256).  Tokens lie on the MMA's N side, so the last token tile is
+// as narrow as the batch leaves it (multiples of 16), not a whole tile.
+// Persistent: the pairs walk the tiles, whole ones first.
+//   warp 0      TMA producer (both CTAs), completion counted on the leader's barrier
+//   warp 1      tensor memory; the leader's copies the scale tiles and issues the MMAs
+//   warps 2..9  epilogue: a lane quarter (32 weight rows) x half of the tokens each,
+//               held in registers, so that the next tile's MMAs start once the
+//               accumulator has been read and run under the stores
+// Tensor memory: 256 accumulator columns, then a scale buffer of 48 (NV; 24)
+// columns per stage.
+template <typename T, int EPI, bool NV>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                         const __grid_constant__ CUtensorMap tm_last, const __grid_constant__ CUtensorMap tm_sw,
+                         const __grid_constant__ CUtensorMap tm_sa, const Params p) {
+  using F = Fmt<NV>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + p.stages * p.stage_bytes);
+  uint64_t* empty_bar = full_bar + p.stages;
+  uint64_t* acc_bar = empty_bar + p.stages;  // [0] full, [1] empty
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_bar + 2);
+  float* xchg = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes + kBarBytes);  // SwiGLU
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(smem_u32(&full_bar[s]), 1);
+      mbar_init(smem_u32(&empty_bar[s]), 1);
+    }
+    mbar_init(smem_u32(&acc_bar[0]), 1);
+    mbar_init(smem_u32(&acc_bar[1]), 16);  // the epilogue warps of both CTAs
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc<true>(smem_u32(tmem_slot), 512);
+    tmem_relinquish<true>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
+  const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+  const uint32_t bars = __shfl_sync(0xffffffffu, smem_u32(full_bar), 0);
+  const uint32_t accb = __shfl_sync(0xffffffffu, smem_u32(acc_bar), 0);
+  const int rank = (int)cluster_ctarank();
+  const int cid = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (warp == 0 && elect_one()) {
+    tma_prefetch_desc(&tm_w);
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_sw);
+    tma_prefetch_desc(&tm_sa);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (warp == 0) {
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int u = cid; ok && u < p.units; u += pairs) {
+      const Tile w = tile_of(p, u);
+      const int blocks = w.bn > 128 ? 2 : 1;
+      const uint32_t bytes = (uint32_t)(kOpTile + (w.bn >> 1) * 128 + (1 + blocks) * F::kScaleBytes);
+      const void* ma = w.bn == 256 ? &tm_a : &tm_last;
+      const int w_row = w.nt * 256 + rank * 128, a_row = w.mt * 256 + rank * (w.bn >> 1);
+      const int sw_row = (w.nt * 2 + rank) * p.tiles, sa_row = w.mt * 2 * p.tiles;
+      for (int kb = 0; kb < p.slabs; ++kb) {
+        ok = warp_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER);
+        if (!ok) break;
+        const uint32_t st = base + (uint32_t)(s * p.stage_bytes);
+        if (elect_one()) {
+          const uint32_t fb = bars + (uint32_t)s * 8, lead = cluster_addr(fb, 0);
+          if (rank == 0) mbar_expect_tx(fb, 2 * bytes);
+          tma_load_2d_pair(st, &tm_w, kb * 128, w_row, lead);
+          tma_load_2d_pair(st + kOpTile, ma, kb * 128, a_row, lead);
+          tma_load_2d_pair(st + 2 * kOpTile, &tm_sw, 0, sw_row + kb * F::kTiles, lead);
+          tma_load_2d_pair(st + 2 * kOpTile + F::kScaleBytes, &tm_sa, 0, sa_row + kb * F::kTiles, lead);
+          if (blocks == 2)
+            tma_load_2d_pair(st + 2 * kOpTile + 2 * F::kScaleBytes, &tm_sa, 0, sa_row + p.tiles + kb * F::kTiles, lead);
+        }
+        if (++s == p.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // the leader's MMAs have released every fill, so that neither a copy nor a
+    // commit is still on its way to this CTA when it leaves (after a failure:
+    // waited for once more, for a shorter time)
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER, ok ? kWaitLimitNs : kWaitLimitNs / 16);
+      if (++s == p.stages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      constexpr uint32_t kScaleCols = NV ? 48 : 24;
+      const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
+      const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
+      const uint64_t sd0 = scale_desc(base + 2 * kOpTile);
+      int s = 0, n = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = cid; ok && u < p.units; u += pairs, ++n) {
+        const Tile w = tile_of(p, u);
+        const bool two = w.bn > 128;
+        const uint32_t idesc0 = idesc_fp4(256, w.bn, NV, 0), idesc1 = idesc_fp4(256, w.bn, NV, NV ? 0 : 2);
+        // the accumulator has been read (by both CTAs' epilogues)
+        if (n > 0) ok = warp_wait(accb + 8, (uint32_t)(n - 1) & 1u, p.err, SITE_FP4_MMA);
+        if (!ok) break;
+        tc_fence_after();
+        auto slab = [&](uint32_t acc, int nt_s, int n_mma) {
+          const uint32_t off = (uint32_t)s * stage_step;
+          const uint64_t wd = wd0 + off, ad = ad0 + off, sd = sd0 + off;
+          const uint32_t sf = tmem + 256 + (uint32_t)s * kScaleCols;
+          if (!warp_wait(bars + (uint32_t)s * 8, ph, p.err, SITE_FP4_MMA)) return false;
+          tc_fence_after();
+          if (elect_one()) {
+            // columns: W tile t at 4 t; token tile t at 4 kTiles + 8 t, its two row blocks side by side
+#pragma unroll
+            for (int t = 0; t < F::kTiles; ++t) {
+              if (t < nt_s) {
+                tmem_cp_scales<true>(sf + 4 * t, sd + (uint64_t)(t * (kTileBytes >> 4)));
+                tmem_cp_scales<true>(sf + 4 * F::kTiles + 8 * t, sd + (uint64_t)((F::kScaleBytes + t * kTileBytes) >> 4));
+                if (two)
+                  tmem_cp_scales<true>(sf + 4 * F::kTiles + 8 * t + 4,
+                                       sd + (uint64_t)((2 * F::kScaleBytes + t * kTileBytes) >> 4));
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (j < n_mma) {
+                const int t = NV ? j : j >> 1;
+                mma_fp4<NV, true>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), (j & 1) ? idesc1 : idesc0,
+                                  sf + 4 * t, sf + 4 * F::kTiles + 8 * t, j != 0 ? 1u : acc);
+              }
+            }
+            mma_commit_pair(bars + (uint32_t)(p.stages + s) * 8);
+          }
+          if (++s == p.stages) {
+            s = 0;
+            ph ^= 1u;
+          }
+          return true;
+        };
+        const int whole = p.K / kSlab;
+        for (int i = 0; ok && i < whole; ++i) ok = slab(i != 0 ? 1u : 0u, F::kTiles, 4);
+        if (ok && whole < p.slabs)
+          ok = slab(whole != 0 ? 1u : 0u, p.tiles - whole * F::kTiles, (p.K - whole * kSlab + 63) >> 6);
+        if (ok && elect_one()) mma_commit_pair(accb);
+        __syncwarp();
+      }
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, h = (warp - 2) >> 2;
+    int n = 0;
+    bool alive = true;  // false once a wait gave up: no more loads and stores, but the named barriers stay matched
+    for (int u = cid; u < p.units; u += pairs, ++n) {
+      const Tile w = tile_of(p, u);
+      if (alive) alive = warp_wait(accb, (uint32_t)n & 1u, p.err, SITE_FP4_EPILOGUE);
+      if (!alive && EPI != SAR_EPI_SWIGLU) break;
+      tc_fence_after();
+      uint32_t v[128];
+      const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_ld32(t0 + j * 32, v + j * 32);
+      tmem_wait_ld();
+      tc_fence_before();
+      __syncwarp();
+      if (alive && elect_one()) mbar_arrive_cluster(cluster_addr(accb + 8, 0));
+      const int m0 = w.mt * 256 + h * 128;
+      const int rows = alive ? min(128, p.M - m0) : 0;  // (may be negative: the half is empty)
+      const int row = w.nt * 256 + rank * 128 + q * 32 + lane;  // weight row
+      if constexpr (EPI == SAR_EPI_SWIGLU) {
+        // lanes 0..63 of the CTA's 128 hold gate rows, 64..127 the matching up
+        // rows: these go over through shared memory, 16 tokens at a time
+        float* xb = xchg + h * (2 * 64 * 17);
+        const int F2 = p.N >> 1;
+        const int col = (w.nt * 2 + rank) * 64 + (q & 1) * 32 + lane;
+        T* c = reinterpret_cast<T*>(p.c) + (size_t)m0 * F2 + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float* xj = xb + (j & 1) * (64 * 17) + ((q & 1) * 32 + lane) * 17;
+          if (q >= 2) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) xj[e] = __uint_as_float(v[j * 16 + e]);
+          }
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
+          if (q < 2 && col < F2) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (j * 16 + e < rows)
+                c[(size_t)(j * 16 + e) * F2] =
+                    Elem<T>::from(silu(__uint_as_float(v[j * 16 + e]) * p.alpha) * (xj[e] * p.alpha));
+          }
+        }
+      } else if (row < p.N) {
+        const size_t at = (size_t)m0 * p.N + row;
+#pragma unroll
+        for (int e = 0; e < 128; ++e) {
+          if (e < rows) {
+            const float x = __uint_as_float(v[e]) * p.alpha;
+            const size_t i = at + (size_t)e * p.N;
+            if constexpr (EPI == SAR_EPI_F32)
+              reinterpret_cast<float*>(p.c)[i] = x;
+            else if constexpr (EPI == SAR_EPI_RESIDUAL)
+              reinterpret_cast<float*>(p.c)[i] = x + p.r[i];
+            else
+              reinterpret_cast<T*>(p.c)[i] = Elem<T>::from(x);
+          }
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA of a pair leaves while the other may still address it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<true>(tmem, 512);
+  }
+}
+
 template <typename T, bool NV>
 const void* pick_split(int epi) {
   switch (epi) {
@@ -371,6 +632,73 @@ int launch_split(const Call& g, Params p) {
   return SAR_OK;
 }
 
+template <typename T, bool NV>
+const void* pick_pair(int epi) {
+  switch (epi) {
+    case SAR_EPI_STORE: return reinterpret_cast<const void*>(&gemm_fp4_pair_kernel<T, SAR_EPI_STORE, NV>);
+    case SAR_EPI_RESIDUAL: return reinterpret_cast<const void*>(&gemm_fp4_pair_kernel<T, SAR_EPI_RESIDUAL, NV>);
+    case SAR_EPI_SWIGLU: return reinterpret_cast<const void*>(&gemm_fp4_pair_kernel<T, SAR_EPI_SWIGLU, NV>);
+    default: return reinterpret_cast<const void*>(&gemm_fp4_pair_kernel<T, SAR_EPI_F32, NV>);
+  }
+}
+
+int launch_pair(const Call& g, Params p) {
+  const bool nv = g.format == SAR_FP4_NV;
+  const int rem = p.M % 256;
+  p.m_full = p.M / 256;
+  p.last_bn = (rem + 15) / 16 * 16;
+  if (p.last_bn == 256) {  // the last tile is as good as whole
+    ++p.m_full;
+    p.last_bn = 0;
+  }
+  p.n_tiles = (p.N + 255) / 256;
+  p.group = std::max(1, std::min(8, p.m_full));
+  const long units = (long)p.n_tiles * (p.m_full + (p.last_bn ? 1 : 0));
+  if (units > (1l << 30)) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many tiles");
+  p.units = (int)units;
+  const int sb = nv ? Fmt<true>::kScaleBytes : Fmt<false>::kScaleBytes;
+  p.stage_bytes = 2 * kOpTile + 3 * sb;  // (a multiple of 1024)
+  const int extra = kBarBytes + 1024 + (g.epi == SAR_EPI_SWIGLU ? kXchgBytes : 0);
+  p.stages = std::min(256 / (nv ? 48 : 24), (kSmemLimit - extra) / p.stage_bytes);
+  const int smem = p.stages * p.stage_bytes + extra;
+  const bool bf = g.storage == SAR_STORAGE_BF16;
+  const void* fn = nv ? (bf ? pick_pair<__nv_bfloat16, true>(g.epi) : pick_pair<__half, true>(g.epi))
+                      : (bf ? pick_pair<__nv_bfloat16, false>(g.epi) : pick_pair<__half, false>(g.epi));
+  CUtensorMap tw, ta, tl, tsw, tsa;
+  const uint64_t kb = (uint64_t)p.K / 2;
+  SAR_TRY(make_tmap_bytes(&tw, g.w, (uint64_t)p.N, kb, 128));
+  SAR_TRY(make_tmap_bytes(&ta, g.a, (uint64_t)p.M, kb, 128));
+  SAR_TRY(make_tmap_bytes(&tl, g.a, (uint64_t)p.M, kb, p.last_bn ? (uint32_t)p.last_bn / 2 : 128));
+  SAR_TRY(make_tmap_words(&tsw, p.sw, (uint64_t)((p.N + 127) / 128) * p.tiles, kTileBytes / 4, sb / kTileBytes));
+  SAR_TRY(make_tmap_words(&tsa, p.sa, (uint64_t)((p.M + 127) / 128) * p.tiles, kTileBytes / 4, sb / kTileBytes));
+  SAR_TRY(ensure_smem_attr(fn, kSmemLimit, "gemm_fp4: set smem attribute"));
+  void* args[] = {&tw, &ta, &tl, &tsw, &tsa, &p};
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[2];
+  lc.blockDim = dim3(kPairThreads);
+  lc.dynamicSmemBytes = (size_t)smem;
+  lc.stream = g.s;
+  lc.attrs = attr;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t qc = lc;  // the cluster shape alone
+  qc.gridDim = dim3(128);
+  qc.attrs = &attr[1];
+  qc.numAttrs = 1;
+  int pairs = 0;
+  SAR_TRY(max_active_clusters(fn, qc, 2, &pairs, "gemm_fp4: cluster occupancy"));
+  lc.numAttrs = 2;
+  lc.gridDim = dim3(2u * (unsigned)std::min(pairs, p.units));
+  const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
+  if (e != cudaSuccess) return cuda_error(e, "gemm_fp4 launch");
+  count_launches(1);
+  return SAR_OK;
+}
+
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
@@ -388,7 +716,8 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
   if (epilogue < SAR_EPI_STORE || epilogue > SAR_EPI_F32) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad epilogue");
   if (format != SAR_FP4_NV && format != SAR_FP4_MX) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad format");
   if (storage != SAR_STORAGE_F16 && storage != SAR_STORAGE_BF16) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad storage");
-  if (variant < 0 || (variant & 0xff) > SAR_FP4_GEMM_SPLIT || variant > 0xffff)
+  if (variant < 0 || (variant & 0xff) > SAR_FP4_GEMM_PAIR || variant > 0xffff ||
+      (variant > 0xff && (variant & 0xff) != SAR_FP4_GEMM_SPLIT))
     return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: unknown variant");
   if (K % 32) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: K must be a multiple of 32");
   if (epilogue == SAR_EPI_SWIGLU && N % 128)
@@ -417,7 +746,7 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
   p.vec = N % 4 == 0 && sar::aligned(c, 4 * elem) && (epilogue != SAR_EPI_RESIDUAL || sar::aligned(residual, 16));
   SAR_TRY(sar::op_flags(&p.err));
   const sar::Call g = {a, w, epilogue, format, storage, variant, static_cast<cudaStream_t>(stream)};
-  return sar::launch_split(g, p);
+  return (variant & 0xff) == SAR_FP4_GEMM_PAIR ? sar::launch_pair(g, p) : sar::launch_split(g, p);
 }
 
 }  // extern "C"

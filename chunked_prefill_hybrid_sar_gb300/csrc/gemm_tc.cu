@@ -1084,6 +1084,22 @@ int make_tmap_bytes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t r
   return SAR_OK;
 }
 
+int make_tmap_words(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  if ((reinterpret_cast<uintptr_t>(ptr) & 15) || cols % 4 || cols > 256 || rows == 0 || box_rows == 0 || box_rows > 256)
+    return set_error(SAR_ERR_INVALID_ARG, "tensor map (words): pointer/stride not 16-byte aligned or bad box");
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {(cuuint64_t)cols * 4};
+  cuuint32_t box[2] = {cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_INT32, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+  return SAR_OK;
+}
+
 // fp32 [rows, cols] row-major, boxes of box_rows x box_cols (box_cols * 4 =
 // 128 bytes: 128-byte swizzle), for the epilogue's TMA reductions.
 int make_tmap_f32_box(CUtensorMap* map, void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,

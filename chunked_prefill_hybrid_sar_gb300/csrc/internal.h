@@ -82,6 +82,10 @@ int make_tmap_16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols
 // 128-byte x box_rows box and 128-byte swizzle; bytes behind a row read zero.
 int make_tmap_bytes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
 
+// A 2D map of 32-bit words over row-major [rows, cols], boxes of box_rows whole
+// rows (cols <= 256), no swizzle; rows behind the last read zero.
+int make_tmap_words(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows);
+
 struct GemmCfg {
   int swap = 0;     // weights on the MMA M side
   int msub = 1;     // 128-row A sub-tiles per tile (non-swap only)

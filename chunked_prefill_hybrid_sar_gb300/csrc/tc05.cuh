@@ -194,9 +194,14 @@ __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t saddr, uint32_t lbo, 
 // Copies one 512-byte scale tile (32 rows of 16 bytes, contiguous in shared
 // memory) into 4 tensor-memory columns, repeated for the four lane quarters:
 // byte 4 j + b of row l is the scale of operand row 32 j + l, K block b.
-// Executes in issue order ahead of the same thread's later MMAs.
+// Executes in issue order ahead of the same thread's later MMAs.  PAIR: in both
+// CTAs of a pair, each from its own shared memory.
+template <bool PAIR>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
 // Descriptor of such a tile: no swizzle, 8-row groups of 128 bytes.
@@ -209,18 +214,36 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t saddr) {
   return d;
 }
 
-// D (128 x N fp32, tensor memory) (+)= (A . SA) . (B . SB)^T over K = 64: A and
+// D (M x N fp32, tensor memory) (+)= (A . SA) . (B . SB)^T over K = 64: A and
 // B e2m1, two to a byte, K-major in 128-byte-swizzled shared memory.  NV: e4m3
 // scales of 16-element blocks, four per row; else e8m0 scales of 32-element
-// blocks, two per row (the descriptor's scale ids pick the pair).
-template <bool NV>
+// blocks, two per row (the descriptor's scale ids pick the pair).  M = 128;
+// PAIR: M = 256 over a CTA pair, split as in mma_f16, each CTA's tensor memory
+// holding the scales of its own 128 rows of A and of all N rows of B.
+template <bool NV, bool PAIR>
 __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                         uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate) {
-  if constexpr (NV)
+  if constexpr (NV && PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else if constexpr (NV)
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
+            d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+        : "memory");
+  else if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(
             d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
         : "memory");
@@ -235,11 +258,25 @@ __device__ __forceinline__ void mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_
 }
 
 // Instruction descriptor of mma_fp4: e2m1 operands (1), both K-major, scale
-// type e4m3 (0) or e8m0 (1), M = 128, N = n, K = 64; scale_id (0 or 2) is the
+// type e4m3 (0) or e8m0 (1), M = m, N = n, K = 64; scale_id (0 or 2) is the
 // first of an e8m0 row's two scales within its 32-bit column, for A and B.
-__device__ __forceinline__ uint32_t idesc_fp4(int n, bool nv, uint32_t scale_id) {
+__device__ __forceinline__ uint32_t idesc_fp4(int m, int n, bool nv, uint32_t scale_id) {
   return (scale_id << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((nv ? 0u : 1u) << 23) |
-         ((uint32_t)(128 >> 7) << 27) | (scale_id << 29);
+         ((uint32_t)(m >> 7) << 27) | (scale_id << 29);
+}
+
+// tmem_ld16 with 32 columns.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
 }
 
 }  // namespace sar

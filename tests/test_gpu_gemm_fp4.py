@@ -60,7 +60,7 @@ def run(a, w, fmt, epi="f32", dtype=torch.float16, alpha=1.0, residual=None, var
 
 
 def variants(M, N, K):
-    v = {"auto": sar.SAR_FP4_GEMM_AUTO, "split": sar.SAR_FP4_GEMM_SPLIT}
+    v = {"auto": sar.SAR_FP4_GEMM_AUTO, "split": sar.SAR_FP4_GEMM_SPLIT, "pair": sar.SAR_FP4_GEMM_PAIR}
     for n in (1, 2, 3, 8):
         if n <= (K + 255) // 256:
             v[f"split{n}"] = sar.SAR_FP4_GEMM_SPLIT | n << 8
@@ -69,7 +69,8 @@ def variants(M, N, K):
 
 SHAPES = [(1, 1, 32), (1, 128, 64), (2, 130, 96), (16, 256, 256), (17, 64, 288), (33, 200, 512), (48, 129, 800),
           (64, 512, 1024), (65, 384, 2080), (127, 127, 160), (128, 128, 2304), (129, 256, 256), (200, 1000, 544),
-          (257, 300, 1088), (513, 640, 320)]
+          (257, 300, 1088), (513, 640, 320),
+          (256, 256, 1024), (512, 512, 96), (384, 700, 4384), (770, 20000, 288), (2048, 5632, 256)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)
