@@ -7,6 +7,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstring>
 #include <string>
 
 #include "common.cuh"
@@ -24,7 +25,9 @@ constexpr int kSmemPerSm = 233472;         // 228 KB
 constexpr int kSmemLimit = 232448;         // 227 KB
 constexpr int kBarBytes = 256;
 constexpr int kPairThreads = 320;
-constexpr int kXchgBytes = 2 * 2 * 64 * 17 * 4;  // pair SwiGLU: per token half two buffers of 64 rows x 16 tokens
+// Staging of one epilogue warp of the pair tiling: two boxes of 2 KB, or (SwiGLU)
+// 16 tokens x 32 columns of fp32 from its partner and two boxes of 1 KB.
+constexpr int kWarpOut = 4096;
 
 template <bool NV>
 struct Fmt {
@@ -46,6 +49,7 @@ struct Params {
   float alpha;
   // pair tiling
   int m_full, n_tiles, last_bn, group, units;
+  int tma_out;    // c is written (or, where it is r, added to) through a tensor map
   int vec;        // rows of c (and r) can be written four columns at a time
   int* err;
 };
@@ -77,6 +81,19 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int u) {
 // The whole warp waits; all its lanes get the same answer.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* err, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, site)) != 0;
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void st_shared16(uint32_t addr, T v) {
+  asm volatile("st.shared.b16 [%0], %1;" ::"r"(addr), "h"(*reinterpret_cast<const unsigned short*>(&v)) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
@@ -350,7 +367,8 @@ template <typename T, int EPI, bool NV>
 __global__ void __launch_bounds__(kPairThreads, 1)
     gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                          const __grid_constant__ CUtensorMap tm_last, const __grid_constant__ CUtensorMap tm_sw,
-                         const __grid_constant__ CUtensorMap tm_sa, const Params p) {
+                         const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_c,
+                         const Params p) {
   using F = Fmt<NV>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -359,7 +377,6 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   uint64_t* empty_bar = full_bar + p.stages;
   uint64_t* acc_bar = empty_bar + p.stages;  // [0] full, [1] empty
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_bar + 2);
-  float* xchg = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes + kBarBytes);  // SwiGLU
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -382,6 +399,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
   const uint32_t bars = __shfl_sync(0xffffffffu, smem_u32(full_bar), 0);
   const uint32_t accb = __shfl_sync(0xffffffffu, smem_u32(acc_bar), 0);
+  const uint32_t stage_end = base + (uint32_t)(p.stages * p.stage_bytes + kBarBytes);  // the epilogue's staging
   const int rank = (int)cluster_ctarank();
   const int cid = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (warp == 0 && elect_one()) {
@@ -448,17 +466,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         const Tile w = tile_of(p, u);
         const bool two = w.bn > 128;
         const uint32_t idesc0 = idesc_fp4(256, w.bn, NV, 0), idesc1 = idesc_fp4(256, w.bn, NV, NV ? 0 : 2);
-        // the accumulator has been read (by both CTAs' epilogues)
-        if (n > 0) ok = warp_wait(accb + 8, (uint32_t)(n - 1) & 1u, p.err, SITE_FP4_MMA);
-        if (!ok) break;
-        tc_fence_after();
-        auto slab = [&](uint32_t acc, int nt_s, int n_mma) {
+        // The accumulator has to have been read (by both CTAs' epilogues) before
+        // the tile's first MMA; its first scale tiles are copied ahead of that wait
+        auto slab = [&](bool first, int nt_s, int n_mma) {
           const uint32_t off = (uint32_t)s * stage_step;
           const uint64_t wd = wd0 + off, ad = ad0 + off, sd = sd0 + off;
           const uint32_t sf = tmem + 256 + (uint32_t)s * kScaleCols;
           if (!warp_wait(bars + (uint32_t)s * 8, ph, p.err, SITE_FP4_MMA)) return false;
           tc_fence_after();
-          if (elect_one()) {
+          auto scales = [&]() {
             // columns: W tile t at 4 t; token tile t at 4 kTiles + 8 t, its two row blocks side by side
 #pragma unroll
             for (int t = 0; t < F::kTiles; ++t) {
@@ -470,12 +486,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                        sd + (uint64_t)((2 * F::kScaleBytes + t * kTileBytes) >> 4));
               }
             }
+          };
+          if (first) {
+            if (elect_one()) scales();
+            __syncwarp();
+            if (n > 0 && !warp_wait(accb + 8, (uint32_t)(n - 1) & 1u, p.err, SITE_FP4_MMA)) return false;
+            tc_fence_after();
+          }
+          if (elect_one()) {
+            if (!first) scales();
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               if (j < n_mma) {
                 const int t = NV ? j : j >> 1;
                 mma_fp4<NV, true>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), (j & 1) ? idesc1 : idesc0,
-                                  sf + 4 * t, sf + 4 * F::kTiles + 8 * t, j != 0 ? 1u : acc);
+                                  sf + 4 * t, sf + 4 * F::kTiles + 8 * t, (j != 0 || !first) ? 1u : 0u);
               }
             }
             mma_commit_pair(bars + (uint32_t)(p.stages + s) * 8);
@@ -487,9 +512,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           return true;
         };
         const int whole = p.K / kSlab;
-        for (int i = 0; ok && i < whole; ++i) ok = slab(i != 0 ? 1u : 0u, F::kTiles, 4);
+        if (whole > 0) ok = slab(true, F::kTiles, 4);
+        for (int i = 1; ok && i < whole; ++i) ok = slab(false, F::kTiles, 4);
         if (ok && whole < p.slabs)
-          ok = slab(whole != 0 ? 1u : 0u, p.tiles - whole * F::kTiles, (p.K - whole * kSlab + 63) >> 6);
+          ok = slab(whole == 0, p.tiles - whole * F::kTiles, (p.K - whole * kSlab + 63) >> 6);
         if (ok && elect_one()) mma_commit_pair(accb);
         __syncwarp();
       }
@@ -497,10 +523,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3, h = (warp - 2) >> 2;
-    int n = 0;
+    const uint32_t mine = stage_end + (uint32_t)(warp - 2) * kWarpOut;  // this warp's staging
+    int n = 0, boxes = 0;
     bool alive = true;  // false once a wait gave up: no more loads and stores, but the named barriers stay matched
     for (int u = cid; u < p.units; u += pairs, ++n) {
       const Tile w = tile_of(p, u);
+      const int m0 = w.mt * 256 + h * 128;
+      const int n0 = w.nt * 256 + rank * 128 + q * 32;  // this warp's first weight row
+      const int row = n0 + lane;
+      const bool adds = EPI == SAR_EPI_RESIDUAL && p.tma_out && p.c == p.r;  // added in L2
+      if (EPI == SAR_EPI_RESIDUAL && !adds) {
+        // the residual's lines are on their way to L2 while the MMAs run
+        for (int e = lane; e < min(128, p.M - m0); e += 32)
+          if (n0 < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.r + (size_t)(m0 + e) * p.N + n0));
+      }
       if (alive) alive = warp_wait(accb, (uint32_t)n & 1u, p.err, SITE_FP4_EPILOGUE);
       if (!alive && EPI != SAR_EPI_SWIGLU) break;
       tc_fence_after();
@@ -512,49 +548,104 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (alive && elect_one()) mbar_arrive_cluster(cluster_addr(accb + 8, 0));
-      const int m0 = w.mt * 256 + h * 128;
       const int rows = alive ? min(128, p.M - m0) : 0;  // (may be negative: the half is empty)
-      const int row = w.nt * 256 + rank * 128 + q * 32 + lane;  // weight row
+      // One box of `cnt` tokens x 32 columns leaves from the warp's staging
+      // (rows behind M and columns behind N are clipped); the other box of the two
+      // may still be read meanwhile.
+      auto box_begin = [&](uint32_t bytes) {
+        if (lane == 0) bulk_wait_read_all_but_one();
+        __syncwarp();
+        return mine + (EPI == SAR_EPI_SWIGLU ? kWarpOut / 2 : 0) + (uint32_t)(boxes & 1) * bytes;
+      };
+      auto box_end = [&](uint32_t at, int col, int m) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the TMA unit
+        __syncwarp();
+        if (lane == 0) {
+          if (adds)
+            tma_reduce_add_2d(&tm_c, col, m, at);
+          else
+            tma_store_2d(&tm_c, col, m, at);
+          bulk_commit();
+        }
+        ++boxes;
+      };
       if constexpr (EPI == SAR_EPI_SWIGLU) {
-        // lanes 0..63 of the CTA's 128 hold gate rows, 64..127 the matching up
-        // rows: these go over through shared memory, 16 tokens at a time
-        float* xb = xchg + h * (2 * 64 * 17);
+        // The CTA's lanes 0..63 hold gate rows, 64..127 the matching up rows.  Of
+        // every 32 tokens the gate warp finishes the first 16 and the warp with
+        // its up rows the others: each hands over the half that the other needs.
         const int F2 = p.N >> 1;
-        const int col = (w.nt * 2 + rank) * 64 + (q & 1) * 32 + lane;
-        T* c = reinterpret_cast<T*>(p.c) + (size_t)m0 * F2 + col;
+        const int col0 = (w.nt * 2 + rank) * 64 + (q & 1) * 32;
+        const bool gate = q < 2;
+        const uint32_t theirs = stage_end + (uint32_t)((warp - 2) ^ 2) * kWarpOut;
+        const int bar = 1 + h * 2 + (q & 1);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float* xj = xb + (j & 1) * (64 * 17) + ((q & 1) * 32 + lane) * 17;
-          if (q >= 2) {
+        for (int g = 0; g < 4; ++g) {
+          asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");  // the partner has read the last ones
 #pragma unroll
-            for (int e = 0; e < 16; ++e) xj[e] = __uint_as_float(v[j * 16 + e]);
+          for (int e = 0; e < 16; ++e)
+            st_shared(theirs + (uint32_t)(e * 32 + lane) * 4, gate ? v[32 * g + 16 + e] : v[32 * g + e]);
+          asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+          const int m = m0 + 32 * g + (gate ? 0 : 16), cnt = m0 + rows - m;
+          if (cnt <= 0 || col0 >= F2) continue;
+          const uint32_t at = p.tma_out ? box_begin(1024) : 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float mineval = __uint_as_float(gate ? v[32 * g + e] : v[32 * g + 16 + e]) * p.alpha;
+            const float other = __uint_as_float(ld_shared(mine + (uint32_t)(e * 32 + lane) * 4)) * p.alpha;
+            const T o = Elem<T>::from(gate ? silu(mineval) * other : silu(other) * mineval);
+            if (p.tma_out)
+              st_shared16(at + (uint32_t)(e * 32 + lane) * 2, o);
+            else if (e < cnt)
+              reinterpret_cast<T*>(p.c)[(size_t)(m + e) * F2 + col0 + lane] = o;
           }
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + h) : "memory");
-          if (q < 2 && col < F2) {
+          if (p.tma_out) box_end(at, col0, m);
+        }
+      } else if constexpr (EPI == SAR_EPI_STORE) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (32 * g >= rows || n0 >= p.N) continue;
+          const uint32_t at = p.tma_out ? box_begin(2048) : 0;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const T o = Elem<T>::from(__uint_as_float(v[32 * g + e]) * p.alpha);
+            if (p.tma_out)
+              st_shared16(at + (uint32_t)(e * 32 + lane) * 2, o);
+            else if (32 * g + e < rows && row < p.N)
+              reinterpret_cast<T*>(p.c)[(size_t)(m0 + 32 * g + e) * p.N + row] = o;
+          }
+          if (p.tma_out) box_end(at, n0, m0 + 32 * g);
+        }
+      } else {
+#pragma unroll
+        for (int g = 0; g < 8; ++g) {
+          if (16 * g >= rows || n0 >= p.N) continue;
+          float x[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(v[16 * g + e]) * p.alpha;
+          if (EPI == SAR_EPI_RESIDUAL && !adds) {
+            // (all loads first: C may be R)
+            float r[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e)
-              if (j * 16 + e < rows)
-                c[(size_t)(j * 16 + e) * F2] =
-                    Elem<T>::from(silu(__uint_as_float(v[j * 16 + e]) * p.alpha) * (xj[e] * p.alpha));
-          }
-        }
-      } else if (row < p.N) {
-        const size_t at = (size_t)m0 * p.N + row;
+              r[e] = 16 * g + e < rows && row < p.N ? p.r[(size_t)(m0 + 16 * g + e) * p.N + row] : 0.f;
 #pragma unroll
-        for (int e = 0; e < 128; ++e) {
-          if (e < rows) {
-            const float x = __uint_as_float(v[e]) * p.alpha;
-            const size_t i = at + (size_t)e * p.N;
-            if constexpr (EPI == SAR_EPI_F32)
-              reinterpret_cast<float*>(p.c)[i] = x;
-            else if constexpr (EPI == SAR_EPI_RESIDUAL)
-              reinterpret_cast<float*>(p.c)[i] = x + p.r[i];
-            else
-              reinterpret_cast<T*>(p.c)[i] = Elem<T>::from(x);
+            for (int e = 0; e < 16; ++e) x[e] += r[e];
           }
+          const uint32_t at = p.tma_out ? box_begin(2048) : 0;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            if (p.tma_out)
+              st_shared(at + (uint32_t)(e * 32 + lane) * 4, __float_as_uint(x[e]));
+            else if (16 * g + e < rows && row < p.N)
+              reinterpret_cast<float*>(p.c)[(size_t)(m0 + 16 * g + e) * p.N + row] = x[e];
+          }
+          if (p.tma_out) box_end(at, n0, m0 + 16 * g);
         }
       }
     }
+    // the boxes are in C before the CTA (and its shared memory) goes
+    if (lane == 0 && boxes > 0) bulk_wait_all();
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -574,6 +665,8 @@ const void* pick_split(int epi) {
     default: return reinterpret_cast<const void*>(&gemm_fp4_split_kernel<T, SAR_EPI_F32, NV>);
   }
 }
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 struct Call {
   const void *a, *w;
@@ -658,21 +751,28 @@ int launch_pair(const Call& g, Params p) {
   p.units = (int)units;
   const int sb = nv ? Fmt<true>::kScaleBytes : Fmt<false>::kScaleBytes;
   p.stage_bytes = 2 * kOpTile + 3 * sb;  // (a multiple of 1024)
-  const int extra = kBarBytes + 1024 + (g.epi == SAR_EPI_SWIGLU ? kXchgBytes : 0);
+  const int extra = kBarBytes + 1024 + 8 * kWarpOut;
   p.stages = std::min(256 / (nv ? 48 : 24), (kSmemLimit - extra) / p.stage_bytes);
   const int smem = p.stages * p.stage_bytes + extra;
   const bool bf = g.storage == SAR_STORAGE_BF16;
   const void* fn = nv ? (bf ? pick_pair<__nv_bfloat16, true>(g.epi) : pick_pair<__half, true>(g.epi))
                       : (bf ? pick_pair<__nv_bfloat16, false>(g.epi) : pick_pair<__half, false>(g.epi));
-  CUtensorMap tw, ta, tl, tsw, tsa;
+  CUtensorMap tw, ta, tl, tsw, tsa, tc;
+  std::memset(&tc, 0, sizeof(tc));
   const uint64_t kb = (uint64_t)p.K / 2;
   SAR_TRY(make_tmap_bytes(&tw, g.w, (uint64_t)p.N, kb, 128));
   SAR_TRY(make_tmap_bytes(&ta, g.a, (uint64_t)p.M, kb, 128));
   SAR_TRY(make_tmap_bytes(&tl, g.a, (uint64_t)p.M, kb, p.last_bn ? (uint32_t)p.last_bn / 2 : 128));
   SAR_TRY(make_tmap_words(&tsw, p.sw, (uint64_t)((p.N + 127) / 128) * p.tiles, kTileBytes / 4, sb / kTileBytes));
   SAR_TRY(make_tmap_words(&tsa, p.sa, (uint64_t)((p.M + 127) / 128) * p.tiles, kTileBytes / 4, sb / kTileBytes));
+  const bool wide = g.epi == SAR_EPI_F32 || g.epi == SAR_EPI_RESIDUAL;
+  const int cols = g.epi == SAR_EPI_SWIGLU ? p.N / 2 : p.N;
+  p.tma_out = cols % (wide ? 4 : 8) == 0 && aligned(p.c, 16);
+  if (p.tma_out)
+    SAR_TRY(make_tmap_out(&tc, p.c, (uint64_t)p.M, (uint64_t)cols, g.epi == SAR_EPI_STORE ? 32 : 16, 32,
+                          wide ? SAR_TYPE_F32 : g.storage));
   SAR_TRY(ensure_smem_attr(fn, kSmemLimit, "gemm_fp4: set smem attribute"));
-  void* args[] = {&tw, &ta, &tl, &tsw, &tsa, &p};
+  void* args[] = {&tw, &ta, &tl, &tsw, &tsa, &tc, &p};
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   lc.blockDim = dim3(kPairThreads);
@@ -698,8 +798,6 @@ int launch_pair(const Call& g, Params p) {
   count_launches(1);
   return SAR_OK;
 }
-
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
 

@@ -1100,6 +1100,26 @@ int make_tmap_words(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t c
   return SAR_OK;
 }
 
+int make_tmap_out(CUtensorMap* map, void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows, uint32_t box_cols,
+                  int type) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  const uint64_t elem = type == SAR_TYPE_F32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(ptr) & 15) || cols * elem % 16 || rows == 0 || box_rows > 256 || box_cols * elem % 16)
+    return set_error(SAR_ERR_INVALID_ARG, "tensor map (output): pointer/stride not 16-byte aligned or bad box");
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * elem};
+  cuuint32_t box[2] = {box_cols, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapDataType dt = type == SAR_TYPE_F32    ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                 : type == SAR_TYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUresult r = fn(map, dt, 2, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+  return SAR_OK;
+}
+
 // fp32 [rows, cols] row-major, boxes of box_rows x box_cols (box_cols * 4 =
 // 128 bytes: 128-byte swizzle), for the epilogue's TMA reductions.
 int make_tmap_f32_box(CUtensorMap* map, void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows,

@@ -86,6 +86,11 @@ int make_tmap_bytes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t r
 // rows (cols <= 256), no swizzle; rows behind the last read zero.
 int make_tmap_words(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows);
 
+// A 2D map over an output [rows, cols] of SAR_TYPE_* elements, boxes of box_rows x
+// box_cols, no swizzle.
+int make_tmap_out(CUtensorMap* map, void* ptr, uint64_t rows, uint64_t cols, uint32_t box_rows, uint32_t box_cols,
+                  int type);
+
 struct GemmCfg {
   int swap = 0;     // weights on the MMA M side
   int msub = 1;     // 128-row A sub-tiles per tile (non-swap only)
