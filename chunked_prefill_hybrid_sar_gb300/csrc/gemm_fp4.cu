@@ -83,6 +83,36 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, int* er
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, err, site)) != 0;
 }
 
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ uint32_t mbar_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+
+// A ring's next full stage for the issuing warp.  The barrier is asked one slab
+// ahead, before that slab's instructions are issued, so that its answer's
+// latency (about 100 clocks of the 430 that a slab took to issue) runs under them.
+struct Ring {
+  uint32_t bars, stages, s = 0, ph = 0, peek = 0;
+  __device__ __forceinline__ bool next_full(int* err, uint32_t& stage) {
+    if (!__all_sync(0xffffffffu, peek) && !warp_wait(bars + s * 8, ph, err, SITE_FP4_MMA)) return false;
+    stage = s;
+    if (++s == stages) {
+      s = 0;
+      ph ^= 1u;
+    }
+    peek = mbar_done(bars + s * 8, ph);
+    return true;
+  }
+};
+
 __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
@@ -227,14 +257,14 @@ __global__ void __launch_bounds__(192)
     const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
     const uint64_t swd0 = scale_desc(base + kOpTile + (uint32_t)p.bn * 128);
     const uint32_t idesc0 = idesc_fp4(128, p.bn, NV, 0), idesc1 = idesc_fp4(128, p.bn, NV, NV ? 0 : 2);
-    int s = 0;
-    uint32_t ph = 0;
+    Ring ring{bars, (uint32_t)p.stages};
     // one slab: nt_s scale tiles of each operand to tensor memory, n_mma MMAs
     auto slab = [&](uint32_t acc, int nt_s, int n_mma) {
-      const uint32_t off = (uint32_t)s * stage_step;
+      uint32_t s;
+      if (!ring.next_full(p.err, s)) return false;
+      const uint32_t off = s * stage_step;
       const uint64_t wd = wd0 + off, ad = ad0 + off, swd = swd0 + off;
-      const uint32_t sf = sf0 + (uint32_t)s * 32;
-      if (!warp_wait(bars + (uint32_t)s * 8, ph, p.err, SITE_FP4_MMA)) return false;
+      const uint32_t sf = sf0 + s * 32;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -252,11 +282,7 @@ __global__ void __launch_bounds__(192)
                         sf + 16 + 4 * t, j != 0 ? 1u : acc);
           }
         }
-        mma_commit(bars + (uint32_t)(p.stages + s) * 8);
-      }
-      if (++s == p.stages) {
-        s = 0;
-        ph ^= 1u;
+        mma_commit(bars + (p.stages + s) * 8);
       }
       return true;
     };
@@ -459,8 +485,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
       const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
       const uint64_t sd0 = scale_desc(base + 2 * kOpTile);
-      int s = 0, n = 0;
-      uint32_t ph = 0;
+      Ring ring{bars, (uint32_t)p.stages};
+      int n = 0;
       bool ok = true;
       for (int u = cid; ok && u < p.units; u += pairs, ++n) {
         const Tile w = tile_of(p, u);
@@ -469,10 +495,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // The accumulator has to have been read (by both CTAs' epilogues) before
         // the tile's first MMA; its first scale tiles are copied ahead of that wait
         auto slab = [&](bool first, int nt_s, int n_mma) {
-          const uint32_t off = (uint32_t)s * stage_step;
+          uint32_t s;
+          if (!ring.next_full(p.err, s)) return false;
+          const uint32_t off = s * stage_step;
           const uint64_t wd = wd0 + off, ad = ad0 + off, sd = sd0 + off;
-          const uint32_t sf = tmem + 256 + (uint32_t)s * kScaleCols;
-          if (!warp_wait(bars + (uint32_t)s * 8, ph, p.err, SITE_FP4_MMA)) return false;
+          const uint32_t sf = tmem + 256 + s * kScaleCols;
           tc_fence_after();
           auto scales = [&]() {
             // columns: W tile t at 4 t; token tile t at 4 kTiles + 8 t, its two row blocks side by side
@@ -503,11 +530,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                   sf + 4 * t, sf + 4 * F::kTiles + 8 * t, (j != 0 || !first) ? 1u : 0u);
               }
             }
-            mma_commit_pair(bars + (uint32_t)(p.stages + s) * 8);
-          }
-          if (++s == p.stages) {
-            s = 0;
-            ph ^= 1u;
+            mma_commit_pair(bars + (p.stages + s) * 8);
           }
           return true;
         };
@@ -547,7 +570,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (alive && elect_one()) mbar_arrive_cluster(cluster_addr(accb + 8, 0));
+      if (alive && elect_one()) mbar_arrive_cluster_relaxed(cluster_addr(accb + 8, 0));
       const int rows = alive ? min(128, p.M - m0) : 0;  // (may be negative: the half is empty)
       // One box of `cnt` tokens x 32 columns leaves from the warp's staging
       // (rows behind M and columns behind N are clipped); the other box of the two
