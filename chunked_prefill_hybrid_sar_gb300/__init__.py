@@ -13,7 +13,8 @@ from . import _lib
 from ._lib import (SAR_EPI_F32, SAR_EPI_RESIDUAL, SAR_EPI_STORE, SAR_EPI_SWIGLU, SAR_GEMM_AUTO,
                    SAR_GEMM_PAIR_N128, SAR_GEMM_PAIR_N192,
                    SAR_GEMM_PAIR_N256, SAR_GEMM_STREAM_K, SAR_GEMM_TWO_CTAS,
-                   SAR_FP4_GEMM_AUTO, SAR_FP4_GEMM_PAIR, SAR_FP4_GEMM_SPLIT, SAR_FP4_MX, SAR_FP4_NV, SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
+                   SAR_FP4_GEMM_AUTO, SAR_FP4_GEMM_PAIR, SAR_FP4_GEMM_SPLIT,
+                   SAR_FP4_GEMM_TOKENS64, SAR_FP4_MX, SAR_FP4_NV, SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
                    SAR_IN_HIDDEN, SAR_IN_TOKENS, SAR_STORAGE_BF16, SAR_STORAGE_F16, KERNEL_KINDS,
                    SarError, check, lib)
 

@@ -35,6 +35,7 @@ SAR_Q_F32 = 0x100
 SAR_GEMM_STREAM_K = 0x2000
 SAR_FP4_NV, SAR_FP4_MX = 0, 1
 SAR_FP4_GEMM_AUTO, SAR_FP4_GEMM_SPLIT, SAR_FP4_GEMM_PAIR = 0, 1, 2
+SAR_FP4_GEMM_TOKENS64 = 0x1000
 SAR_TYPE_F16, SAR_TYPE_BF16, SAR_TYPE_F32 = 0, 1, 2
 
 KERNEL_KINDS = ("embed", "rmsnorm", "gemm_qkv", "rope_append", "chunk_attn", "decode_attn", "gemm_o",

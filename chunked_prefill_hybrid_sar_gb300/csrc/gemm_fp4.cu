@@ -7,6 +7,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <string>
 
@@ -166,7 +167,7 @@ __device__ __forceinline__ void put4(const Params& p, size_t m, int n, int ncols
 }
 
 // Split tiling: 128 weight rows on the MMA's M side x bn <= 128 tokens on its N
-// side, the K range cut over the `splits` CTAs of a cluster.  Each CTA leaves
+// side (one tile of all tokens, or tiles of 64 or 128), the K range cut over the `splits` CTAs of a cluster.  Each CTA leaves
 // its fp32 partial tile in its own shared memory; after a cluster barrier each
 // adds up every CTA's partials (in rank order) for its share of the tokens and
 // writes them: no workspace, no atomics, one launch, the same sums each time.
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(192)
     int i = 0, s = 0;
     uint32_t ph = 0;
     const uint8_t* sw = p.sw + (size_t)nt * p.tiles * kTileBytes;
-    const uint8_t* sa = p.sa + (size_t)mt * p.tiles * kTileBytes;  // (several token tiles: bn = 128)
+    const uint8_t* sa = p.sa + (size_t)(mt * p.bn >> 7) * p.tiles * kTileBytes;
     for (; i < n_slabs; ++i) {
       ok = warp_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER);
       if (!ok) break;
@@ -256,6 +257,8 @@ __global__ void __launch_bounds__(192)
     const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;  // in a descriptor's 16-byte units
     const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
     const uint64_t swd0 = scale_desc(base + kOpTile + (uint32_t)p.bn * 128);
+    // the odd 64-token tiles' scales are the last two of their row block's four columns
+    const uint32_t half = (uint32_t)(mt * p.bn >> 5) & 2u;
     const uint32_t idesc0 = idesc_fp4(128, p.bn, NV, 0), idesc1 = idesc_fp4(128, p.bn, NV, NV ? 0 : 2);
     Ring ring{bars, (uint32_t)p.stages};
     // one slab: nt_s scale tiles of each operand to tensor memory, n_mma MMAs
@@ -279,7 +282,7 @@ __global__ void __launch_bounds__(192)
           if (j < n_mma) {
             const int t = NV ? j : j >> 1;
             mma_fp4<NV, false>(tmem, wd + (uint64_t)(2 * j), ad + (uint64_t)(2 * j), (j & 1) ? idesc1 : idesc0, sf + 4 * t,
-                        sf + 16 + 4 * t, j != 0 ? 1u : acc);
+                        sf + 16 + 4 * t + half, j != 0 ? 1u : acc);
           }
         }
         mma_commit(bars + (p.stages + s) * 8);
@@ -302,12 +305,13 @@ __global__ void __launch_bounds__(192)
     const int q = warp & 3;
     float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
     const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16);
-    for (int j = 0; ok && j < p.bn / 16; ++j) {
-      uint32_t v[16];
-      tmem_ld16(t0 + j * 16, v);
+    for (int j = 0; ok && j < p.bn; j += 32) {
+      uint32_t v[32];
+      tmem_ld32(t0 + j, v);  // (past bn: columns of the tile's own allocation)
       tmem_wait_ld();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) part[(j * 16 + e) * 128] = __uint_as_float(v[e]);
+      for (int e = 0; e < 32; ++e)
+        if (j + e < p.bn) part[(j + e) * 128] = __uint_as_float(v[e]);
     }
     tc_fence_before();
   }
@@ -322,9 +326,9 @@ __global__ void __launch_bounds__(192)
     const int n4 = (t % kLanes) * 4;
     const int m0 = mt * p.bn, rows = min(p.bn, p.M - m0);
     const uint32_t part = smem_u32(smem);
-    // four tokens' partials are read at a time, rank by rank, so that their
+    // eight tokens' partials are read at a time, rank by rank, so that their
     // latency is paid once for all of them
-    constexpr int kU = 4;
+    constexpr int kU = 8;
     const int step = (128 / kLanes) * p.splits;
     auto joined = [&](int tok0, int n, float4 (&x)[kU]) {
 #pragma unroll
@@ -333,7 +337,8 @@ __global__ void __launch_bounds__(192)
         const uint32_t at = cluster_addr(part, (uint32_t)s) + (uint32_t)n * 4;
         float4 v[kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u) v[u] = ld_cluster_f4(at + (uint32_t)min(tok0 + u * step, p.bn - 1) * 512);
+        for (int u = 0; u < kU; ++u)
+          v[u] = tok0 + u * step < rows ? ld_cluster_f4(at + (uint32_t)(tok0 + u * step) * 512) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           x[u].x += v[u].x;
@@ -555,8 +560,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int n0 = w.nt * 256 + rank * 128 + q * 32;  // this warp's first weight row
       const int row = n0 + lane;
       const bool adds = EPI == SAR_EPI_RESIDUAL && p.tma_out && p.c == p.r;  // added in L2
-      if (EPI == SAR_EPI_RESIDUAL && !adds) {
-        // the residual's lines are on their way to L2 while the MMAs run
+      if (EPI == SAR_EPI_RESIDUAL && !adds && p.slabs <= 32) {
+        // the residual's lines are on their way to L2 while the MMAs run (8192 x
+        // 14336, K = 4096: 304 -> 262 us; at K = 20480 they came so early that some
+        // had left L2 again: 8192 x 7168 372 -> 391 us, hence the limit)
         for (int e = lane; e < min(128, p.M - m0); e += 32)
           if (n0 < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.r + (size_t)(m0 + e) * p.N + n0));
       }
@@ -697,17 +704,64 @@ struct Call {
   cudaStream_t s;
 };
 
+// ---- choice of the tiling ----------------------------------------------------
+//
+// Microseconds of a launch, from its tiles: fitted to 1400 timed runs (1 to 2048
+// tokens, N 1024 to 28672, K 1024 to 14336, every tiling and number of K ranges).
+// Taking the smallest estimate costs 1.2% over the fastest measured tiling on
+// average and 16% at worst.  What it weighs: few tokens want many CTAs on the
+// weight (K ranges, until their join costs more than the shorter ranges save: 16
+// x 4096 x 14336 15.8 us as one range, 10.1 as four, 12.4 as eight); a middling
+// number wants 64-token tiles (128 x 4096 x 4096: 7.5 us, against 9.2 with 128);
+// many want the pair tiling (2048 x 28672 x 4096: 85 us, against 147).
+constexpr double kSlabOne = 0.276, kSlabOneToken = 0.0006;  // a slab of a CTA alone on its SM; per token of the tile
+constexpr double kSlabTwo = 0.448, kSlabTwoToken = 0.0001;  // of a CTA that shares its SM
+constexpr double kSplitBase = -1.7, kSplitWave = 3.8, kSplitToken = 0.025, kSplitJoin = 0.55;
+constexpr double kPairSlab = 0.338, kPairSlabMin = 0.27, kPairBase = 2.5, kPairTile = 2.1;
+
+double split_us(const Params& p, int width, int splits, int sms) {
+  const int m_tiles = (p.M + width - 1) / width, per = (p.slabs + splits - 1) / splits;
+  const int ranges = (p.slabs + per - 1) / per;
+  const int bn = m_tiles > 1 ? width : (p.M + 15) / 16 * 16;
+  const double ctas = (double)m_tiles * ((p.N + 127) / 128) * ranges;
+  const double slab = ctas <= sms ? kSlabOne + kSlabOneToken * bn : kSlabTwo + kSlabTwoToken * bn;
+  return kSplitBase + std::ceil(ctas / (2.0 * sms)) * (per * slab + kSplitWave + kSplitToken * bn) +
+         kSplitJoin * (ranges - 1) * std::cbrt(bn / 16.0);
+}
+
+double pair_us(const Params& p, int sms) {
+  const int last = (p.M % 256 + 15) / 16 * 16, full = p.M / 256 + (last == 256), pairs = std::max(1, sms / 2);
+  const long n_tiles = (p.N + 255) / 256, units = n_tiles * (full + (last != 0 && last != 256));
+  const long whole = (full * n_tiles + pairs - 1) / pairs, narrow = std::max(0l, (units + pairs - 1) / pairs - whole);
+  return kPairBase + whole * (p.slabs * kPairSlab + kPairTile) +
+         narrow * (p.slabs * std::max(kPairSlabMin, kPairSlab * last / 256) + kPairTile);
+}
+
+int pick_variant(const Params& p) {
+  const int sms = num_sms();
+  int best = SAR_FP4_GEMM_PAIR;
+  double us = pair_us(p, sms);
+  for (int width : {128, 64}) {
+    if (width == 64 && p.M <= 64) break;  // one tile either way
+    for (int splits : {1, 2, 3, 4, 6, 8}) {
+      if (splits > p.slabs) break;
+      const double t = split_us(p, width, splits, sms);
+      if (t < us) {
+        us = t;
+        best = SAR_FP4_GEMM_SPLIT | splits << 8 | (width == 64 ? SAR_FP4_GEMM_TOKENS64 : 0);
+      }
+    }
+  }
+  return best;
+}
+
 int launch_split(const Call& g, Params p) {
   const bool nv = g.format == SAR_FP4_NV;
-  const int m_tiles = (p.M + 127) / 128, n_tiles = (p.N + 127) / 128;
+  const int width = g.variant & SAR_FP4_GEMM_TOKENS64 ? 64 : 128;
+  const int m_tiles = (p.M + width - 1) / width, n_tiles = (p.N + 127) / 128;
   if (m_tiles > 65535 || n_tiles > 65535) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many tiles");
-  p.bn = m_tiles > 1 ? 128 : (p.M + 15) / 16 * 16;
-  int splits = g.variant >> 8 & 0xff;
-  if (!splits) {
-    const long tiles = (long)m_tiles * n_tiles;
-    splits = (int)std::max<long>(1, std::min<long>(8, 2L * num_sms() / tiles));
-    splits = std::min(splits, std::max(1, p.slabs / 2));
-  }
+  p.bn = m_tiles > 1 ? width : (p.M + 15) / 16 * 16;
+  const int splits = std::max(1, g.variant >> 8 & 0xf);
   if (splits > 8 || splits > p.slabs) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many K ranges");
   p.slabs_per_split = (p.slabs + splits - 1) / splits;
   p.splits = (p.slabs + p.slabs_per_split - 1) / p.slabs_per_split;  // no empty range
@@ -837,7 +891,7 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
   if (epilogue < SAR_EPI_STORE || epilogue > SAR_EPI_F32) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad epilogue");
   if (format != SAR_FP4_NV && format != SAR_FP4_MX) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad format");
   if (storage != SAR_STORAGE_F16 && storage != SAR_STORAGE_BF16) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad storage");
-  if (variant < 0 || (variant & 0xff) > SAR_FP4_GEMM_PAIR || variant > 0xffff ||
+  if (variant < 0 || (variant & 0xff) > SAR_FP4_GEMM_PAIR || variant > 0x1fff ||
       (variant > 0xff && (variant & 0xff) != SAR_FP4_GEMM_SPLIT))
     return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: unknown variant");
   if (K % 32) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: K must be a multiple of 32");
@@ -866,6 +920,7 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
   p.alpha = alpha;
   p.vec = N % 4 == 0 && sar::aligned(c, 4 * elem) && (epilogue != SAR_EPI_RESIDUAL || sar::aligned(residual, 16));
   SAR_TRY(sar::op_flags(&p.err));
+  if (variant == SAR_FP4_GEMM_AUTO) variant = sar::pick_variant(p);
   const sar::Call g = {a, w, epilogue, format, storage, variant, static_cast<cudaStream_t>(stream)};
   return (variant & 0xff) == SAR_FP4_GEMM_PAIR ? sar::launch_pair(g, p) : sar::launch_split(g, p);
 }

@@ -141,10 +141,11 @@ int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, i
 enum {
   SAR_FP4_GEMM_AUTO = 0,  /* the library's choice for (M, N, K)                        */
   SAR_FP4_GEMM_SPLIT = 1, /* 128 weight rows x up to 128 token rows per tile, the K
-                             range cut over a cluster's CTAs; | (count << 8) asks for
-                             that many ranges (1..8, at most one per 256 columns)     */
-  SAR_FP4_GEMM_PAIR = 2   /* 256 weight rows x up to 256 token rows per tile over a
+                             range cut over a cluster's CTAs: | (count << 8) for that
+                             many ranges (up to 8, one per 256 columns; else one)     */
+  SAR_FP4_GEMM_PAIR = 2,  /* 256 weight rows x up to 256 token rows per tile over a
                              pair of CTAs (2-CTA cluster), persistent               */
+  SAR_FP4_GEMM_TOKENS64 = 0x1000 /* flag for SPLIT: tiles of 64 token rows             */
 };
 
 /* C = epilogue(alpha * A . W^T) of 4-bit rows of one format: A [M, K] and W [N, K]

@@ -64,6 +64,7 @@ def variants(M, N, K):
     for n in (1, 2, 3, 8):
         if n <= (K + 255) // 256:
             v[f"split{n}"] = sar.SAR_FP4_GEMM_SPLIT | n << 8
+            v[f"split{n}x64"] = v[f"split{n}"] | sar.SAR_FP4_GEMM_TOKENS64
     return v
 
 
