@@ -371,30 +371,46 @@ def rmsnorm(x, gain, y, eps: float, stream=None) -> None:
 
 
 # ---- 4-bit rows ----------------------------------------------------------------
+#
+# The checks below run in a decode loop, in front of kernels of a few
+# microseconds: they read each attribute once and make no call into the library.
+
+_ROW_TYPES: dict = {}  # torch dtype -> SAR_TYPE_*, filled at the first call
 
 
-def _device_check(what: str, *tensors) -> None:
-    """Every tensor is on the current device (the library launches there)."""
+def _row_types() -> dict:
+    if not _ROW_TYPES:
+        import torch
+        _ROW_TYPES.update({torch.float16: _lib.SAR_TYPE_F16, torch.bfloat16: _lib.SAR_TYPE_BF16,
+                           torch.float32: _lib.SAR_TYPE_F32})
+    return _ROW_TYPES
+
+
+def _launch_stream(what: str, stream, *tensors) -> int | None:
+    """Checks that every tensor is on the current device, where the library
+    launches, and returns the stream's address (None: the current stream's)."""
     import torch
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != dev):
+        if t is not None and not (t.is_cuda and t.get_device() == dev):
             raise ValueError(f"{what}: tensors must be on the current CUDA device")
+    # (the stream's address alone: a torch.cuda.Stream object takes 3 us to make)
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
-def _rows_type(what: str, t) -> int:
-    import torch
-    types = {torch.float16: _lib.SAR_TYPE_F16, torch.bfloat16: _lib.SAR_TYPE_BF16, torch.float32: _lib.SAR_TYPE_F32}
-    if t.dtype not in types:
+def _rows(what: str, t):
+    """(rows, columns, row stride, SAR_TYPE_*) of a two-dimensional tensor with
+    adjacent columns; a single row's stride, which means nothing, is its length."""
+    kind = _row_types().get(t.dtype)
+    if kind is None:
         raise ValueError(f"{what}: rows must be float16, bfloat16 or float32")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: rows must be two-dimensional with adjacent columns")
-    return types[t.dtype]
-
-
-def _row_stride(t) -> int:
-    """Elements from row to row (a single row's own length: its stride means nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.dim() != 2:
+        raise ValueError(f"{what}: rows must be two-dimensional")
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError(f"{what}: a row's columns must be adjacent")
+    return rows, cols, (ld if rows > 1 else cols), kind
 
 
 def fp4_scale_bytes(rows: int, cols: int, format: int = SAR_FP4_NV) -> int:
@@ -406,34 +422,34 @@ def fp4_scale_bytes(rows: int, cols: int, format: int = SAR_FP4_NV) -> int:
 
 def _fp4_check(what: str, codes, scales, rows: int, cols: int, format: int) -> None:
     import torch
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
         raise ValueError(f"{what}: codes and scales must be uint8")
-    if tuple(codes.shape) != (rows, cols // 2) or not codes.is_contiguous():
-        raise ValueError(f"{what}: codes must be contiguous [{rows}, {cols // 2}]")
-    if not scales.is_contiguous() or scales.numel() < fp4_scale_bytes(rows, cols, format):
-        raise ValueError(f"{what}: scales must be contiguous and hold {fp4_scale_bytes(rows, cols, format)} bytes")
+    if codes.dim() != 2 or codes.shape[0] != rows or 2 * codes.shape[1] != cols or not codes.is_contiguous():
+        raise ValueError(f"{what}: codes must be contiguous, two to a byte: {rows} rows of {cols}")
+    # fp4_scale_bytes, for the formats and columns that the library takes
+    width = 64 if format == SAR_FP4_NV else 128
+    if not scales.is_contiguous() or scales.numel() < (rows + 127) // 128 * ((cols + width - 1) // width) * 512:
+        raise ValueError(f"{what}: scales must be contiguous and as long as fp4_scale_bytes says")
 
 
 def fp4_quantize(x, codes, scales, format: int = SAR_FP4_NV, tensor_scale: float = 1.0, stream=None) -> None:
     """codes (uint8 [rows, cols / 2]) and scales (uint8 [fp4_scale_bytes]) = the
     microscaled 4-bit form of the rows of ``x`` (fp16, bf16 or fp32, any row
     stride); see ``sar_op_fp4_quantize``."""
-    kind = _rows_type("fp4_quantize", x)
-    rows, cols = x.shape
+    rows, cols, ld, kind = _rows("fp4_quantize", x)
     _fp4_check("fp4_quantize", codes, scales, rows, cols, format)
-    _device_check("fp4_quantize", x, codes, scales)
-    check(lib().sar_op_fp4_quantize(_ptr(x), _row_stride(x), rows, cols, kind, format, tensor_scale, _ptr(codes),
-                                    _ptr(scales), _stream(stream)))
+    st = _launch_stream("fp4_quantize", stream, x, codes, scales)
+    check(lib().sar_op_fp4_quantize(x.data_ptr(), ld, rows, cols, kind, format, tensor_scale, codes.data_ptr(),
+                                    scales.data_ptr(), st))
 
 
 def fp4_dequantize(codes, scales, y, format: int = SAR_FP4_NV, tensor_scale: float = 1.0, stream=None) -> None:
     """y (fp16, bf16 or fp32 rows, any row stride) = what 4-bit rows stand for."""
-    kind = _rows_type("fp4_dequantize", y)
-    rows, cols = y.shape
+    rows, cols, ld, kind = _rows("fp4_dequantize", y)
     _fp4_check("fp4_dequantize", codes, scales, rows, cols, format)
-    _device_check("fp4_dequantize", codes, scales, y)
-    check(lib().sar_op_fp4_dequantize(_ptr(codes), _ptr(scales), rows, cols, format, tensor_scale, _ptr(y),
-                                      _row_stride(y), kind, _stream(stream)))
+    st = _launch_stream("fp4_dequantize", stream, codes, scales, y)
+    check(lib().sar_op_fp4_dequantize(codes.data_ptr(), scales.data_ptr(), rows, cols, format, tensor_scale, y.data_ptr(),
+                                      ld, kind, st))
 
 
 def gemm_fp4(a, a_scales, w, w_scales, c, residual=None, alpha: float = 1.0, epilogue=SAR_EPI_STORE,
@@ -441,20 +457,22 @@ def gemm_fp4(a, a_scales, w, w_scales, c, residual=None, alpha: float = 1.0, epi
     """c = epilogue(alpha * a . w^T) of 4-bit rows (codes uint8 [rows, K / 2] and
     their scales); 16-bit ``c`` for STORE and SWIGLU, fp32 for RESIDUAL and F32;
     see ``sar_op_gemm_fp4``."""
-    import torch
-    M, N, K = a.shape[0], w.shape[0], 2 * a.shape[1]
+    if a.dim() != 2 or w.dim() != 2:
+        raise ValueError("gemm_fp4: codes must be two-dimensional")
+    M, K = a.shape
+    N, K = w.shape[0], 2 * K
     _fp4_check("gemm_fp4", a, a_scales, M, K, format)
     _fp4_check("gemm_fp4", w, w_scales, N, K, format)
+    rows, cols, _, kind = _rows("gemm_fp4", c)
     wide = epilogue in (SAR_EPI_F32, SAR_EPI_RESIDUAL)
-    if c.dtype not in ((torch.float32,) if wide else (torch.float16, torch.bfloat16)):
+    if wide != (kind == _lib.SAR_TYPE_F32):
         raise ValueError("gemm_fp4: c must be fp32 for RESIDUAL and F32, fp16 or bf16 otherwise")
-    if tuple(c.shape) != (M, N // 2 if epilogue == SAR_EPI_SWIGLU else N) or not c.is_contiguous():
+    if rows != M or cols != (N // 2 if epilogue == SAR_EPI_SWIGLU else N) or not c.is_contiguous():
         raise ValueError("gemm_fp4: c has another shape, or is not contiguous")
     if (residual is None) != (epilogue != SAR_EPI_RESIDUAL):
         raise ValueError("gemm_fp4: the residual goes with the RESIDUAL epilogue")
-    if residual is not None and (residual.dtype != torch.float32 or residual.shape != c.shape
-                                 or not residual.is_contiguous()):
+    if residual is not None and (residual.dtype != c.dtype or residual.shape != c.shape or not residual.is_contiguous()):
         raise ValueError("gemm_fp4: residual must be contiguous fp32 of c's shape")
-    _device_check("gemm_fp4", a, a_scales, w, w_scales, c, residual)
-    check(lib().sar_op_gemm_fp4(_ptr(a), _ptr(a_scales), _ptr(w), _ptr(w_scales), _ptr(c), _ptr(residual), M, N, K,
-                                alpha, epilogue, format, variant, _storage_of(c), _stream(stream)))
+    st = _launch_stream("gemm_fp4", stream, a, a_scales, w, w_scales, c, residual)
+    check(lib().sar_op_gemm_fp4(a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), c.data_ptr(),
+                                _ptr(residual), M, N, K, alpha, epilogue, format, variant, 0 if wide else kind, st))

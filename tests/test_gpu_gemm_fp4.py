@@ -160,6 +160,7 @@ def test_nan_scale_poisons_its_row_alone(fmt, M):
 def test_no_tokens():
     w = Rows(np.random.default_rng(0), 64, 64, "nv")
     a = torch.empty(0, 32, dtype=torch.uint8, device="cuda")
+    a = a.view(0, 32)
     n = sar.launch_count()
     sar.gemm_fp4(a, torch.empty(0, dtype=torch.uint8, device="cuda"), w.codes, w.scales,
                  torch.empty(0, 64, dtype=torch.float16, device="cuda"))
