@@ -19,7 +19,7 @@ from ._lib import (SAR_EPI_F32, SAR_EPI_RESIDUAL, SAR_EPI_STORE, SAR_EPI_SWIGLU,
                    SarError, check, lib)
 
 __all__ = ["Model", "KVCache", "Scheduler", "Batch", "StepGraph", "SarError", "lib", "check", "gemm", "rmsnorm",
-           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "gemm_fp4", "SAR_FP4_NV", "SAR_FP4_MX",
+           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "gemm_fp4", "LogitControls", "logits_control", "token_state_add", "SAR_FP4_NV", "SAR_FP4_MX",
            "op_sync_status", "op_wait_check",
            "launch_count", "KERNEL_KINDS", "SAR_IN_HIDDEN", "SAR_IN_TOKENS", "SAR_STORAGE_F16",
            "SAR_STORAGE_BF16", "storage_dtype"]
@@ -211,6 +211,14 @@ class StepGraph:
         check(lib().sar_graph_enqueue_host_tokens(self.h, _ptr(inp), ctypes.cast(_ptr(tokens_out), _lib.P_i32),
                                                   _stream(stream)))
         self._pending = (inp, tokens_out)
+
+    def set_controls(self, controls: "LogitControls | None") -> None:
+        """The token launches pick under ``controls`` (a row per logits row)
+        from now on; None: greedily again."""
+        if controls is not None and controls.rows is not None and controls.rows < self._keep[0].logit_rows:
+            raise ValueError("set_controls: an array is shorter than the logits' rows")
+        check(lib().sar_graph_set_controls(self.h, None if controls is None else ctypes.byref(controls.c)))
+        self._controls = controls
 
     def wait(self) -> None:
         """Waits for the last enqueue_host_tokens step of this graph."""
@@ -476,3 +484,118 @@ def gemm_fp4(a, a_scales, w, w_scales, c, residual=None, alpha: float = 1.0, epi
     st = _launch_stream("gemm_fp4", stream, a, a_scales, w, w_scales, c, residual)
     check(lib().sar_op_gemm_fp4(a.data_ptr(), a_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr(), c.data_ptr(),
                                 _ptr(residual), M, N, K, alpha, epilogue, format, variant, 0 if wide else kind, st))
+
+
+# ---- logits controls -------------------------------------------------------------
+
+
+class LogitControls:
+    """What a batch's requests ask of their logits (``sar_logit_controls``): a
+    handle over device tensors that the caller keeps filling; build it once.
+
+    state       int16 [slots, >= vocab]: bit 15 the token is in the prompt, the
+                low bits how often it was generated (``token_state_add``)
+    slots       int32 [rows], -1 for a row without
+    repetition, presence, frequency   fp32 [rows], each optional
+    bias_offsets int32 [rows + 1], bias_tokens int32, bias_values fp32
+    mask        int32 [masks, >= ceil(vocab / 32)], bit set = allowed
+    mask_rows   int32 [rows], -1 for a row without (None: row r takes mask r)
+    count_picks each pick is counted into its row's slot
+    """
+
+    def __init__(self, state=None, slots=None, repetition=None, presence=None, frequency=None, bias_offsets=None,
+                 bias_tokens=None, bias_values=None, mask=None, mask_rows=None, count_picks: bool = False):
+        import torch
+        what = "LogitControls"
+
+        def flat(t, dtype, name):
+            if t is None:
+                return None
+            if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous():
+                raise ValueError(f"{what}: {name} must be a contiguous one-dimensional {dtype} tensor")
+            return t.data_ptr()
+
+        def table(t, dtype, name):
+            if t.dtype != dtype or t.dim() != 2 or t.stride(1) != 1 or t.shape[0] < 1:
+                raise ValueError(f"{what}: {name} must be a two-dimensional {dtype} tensor with adjacent columns")
+            return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1]), t.shape[0]
+
+        c = _lib.sar_logit_controls()
+        self._keep = (state, slots, repetition, presence, frequency, bias_offsets, bias_tokens, bias_values, mask,
+                      mask_rows)
+        _launch_stream(what, 0, *self._keep)
+        if state is not None:
+            c.state, c.state_ld, c.n_slots = table(state, torch.int16, "state")
+        c.slots = flat(slots, torch.int32, "slots")
+        c.repetition = flat(repetition, torch.float32, "repetition")
+        c.presence = flat(presence, torch.float32, "presence")
+        c.frequency = flat(frequency, torch.float32, "frequency")
+        c.bias_offsets = flat(bias_offsets, torch.int32, "bias_offsets")
+        c.bias_tokens = flat(bias_tokens, torch.int32, "bias_tokens")
+        c.bias_values = flat(bias_values, torch.float32, "bias_values")
+        if len({t is None for t in (bias_offsets, bias_tokens, bias_values)}) > 1:
+            raise ValueError(f"{what}: biases need offsets, tokens and values")
+        if bias_tokens is not None:
+            if bias_tokens.numel() != bias_values.numel():
+                raise ValueError(f"{what}: bias_tokens and bias_values differ in length")
+            c.n_biases = bias_tokens.numel()
+            if c.n_biases == 0:  # (an empty tensor has no address)
+                c.bias_offsets = c.bias_tokens = c.bias_values = None
+        if mask is not None:
+            c.mask, c.mask_ld, c.n_masks = table(mask, torch.int32, "mask")
+        c.mask_rows = flat(mask_rows, torch.int32, "mask_rows")
+        c.count_picks = 1 if count_picks else 0
+        lens = [t.numel() for t in (slots, repetition, presence, frequency, mask_rows) if t is not None]
+        if bias_offsets is not None:
+            lens.append(bias_offsets.numel() - 1)
+        if mask is not None and mask_rows is None:
+            lens.append(mask.shape[0])
+        self.rows = min(lens) if lens else None  # the most rows and tokens a call may have
+        self.vocab = min([1 << 30] + ([] if state is None else [state.shape[1]]) + ([] if mask is None else [32 * mask.shape[1]]))
+        self.device = next((t.get_device() for t in self._keep if t is not None), None)
+        self.c = c
+
+
+def logits_control(logits, controls: LogitControls, out=None, tokens_out=None, stream=None) -> None:
+    """out (the logits' type; may be ``logits``) = the logits under ``controls``;
+    tokens_out (int32 [rows]) = each row's pick, -1 where no token is left; see
+    ``sar_logits_control``."""
+    import torch
+    rows, vocab, ld, kind = _rows("logits_control", logits)
+    ld_out = 0
+    if out is not None:
+        out_rows, out_cols, ld_out, out_kind = _rows("logits_control", out)
+        if (out_rows, out_cols, out_kind) != (rows, vocab, kind):
+            raise ValueError("logits_control: out must have the logits' shape and type")
+    if tokens_out is not None and (tokens_out.dtype is not torch.int32 or tokens_out.numel() < rows
+                                   or not tokens_out.is_contiguous()):
+        raise ValueError("logits_control: tokens_out must be contiguous int32, one per row")
+    if (controls.rows is not None and controls.rows < rows) or controls.vocab < vocab:
+        raise ValueError("logits_control: the controls hold fewer rows or tokens than the logits")
+    st = _launch_stream("logits_control", stream, logits, out, tokens_out)
+    if controls.device is not None and controls.device != logits.get_device():
+        raise ValueError("logits_control: the controls are on another device")
+    check(lib().sar_logits_control(logits.data_ptr(), ld, rows, vocab, kind, ctypes.byref(controls.c), _ptr(out), ld_out,
+                                   _ptr(tokens_out), st))
+
+
+def token_state_add(state, slots, offsets, tokens, vocab: int | None = None, prompt_lens=None, reset: bool = False,
+                    stream=None) -> None:
+    """Counts ``tokens[offsets[i]:offsets[i + 1]]`` into row ``slots[i]`` of the
+    int16 ``state`` [slots, >= vocab], the first ``prompt_lens[i]`` of them as
+    prompt tokens; ``reset``: the rows are made anew; see ``sar_token_state_add``."""
+    import torch
+    if state.dtype is not torch.int16 or state.dim() != 2 or (state.shape[1] > 1 and state.stride(1) != 1):
+        raise ValueError("token_state_add: state must be two-dimensional int16 with adjacent columns")
+    n_slots, cols = state.shape
+    vocab = cols if vocab is None else vocab
+    if vocab > cols:
+        raise ValueError("token_state_add: state is narrower than the vocabulary")
+    n = slots.numel()
+    for t, least in ((slots, 0), (offsets, n + 1), (tokens, 0), (prompt_lens, n)):
+        if t is not None and (t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < least):
+            raise ValueError("token_state_add: index arrays must be contiguous int32 and long enough")
+    st = _launch_stream("token_state_add", stream, state, slots, offsets, tokens, prompt_lens)
+    check(lib().sar_token_state_add(state.data_ptr(), state.stride(0) if n_slots > 1 else cols, n_slots, vocab,
+                                    slots.data_ptr(), n, offsets.data_ptr(), tokens.data_ptr(), tokens.numel(),
+                                    _ptr(prompt_lens), 1 if reset else 0, st))

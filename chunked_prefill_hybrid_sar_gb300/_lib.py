@@ -79,6 +79,13 @@ class sar_sched_cfg(ctypes.Structure):
                 ("max_batch", i32), ("max_chunks", i32)]
 
 
+class sar_logit_controls(ctypes.Structure):
+    _fields_ = [("state", vp), ("state_ld", i64), ("slots", vp), ("repetition", vp), ("presence", vp),
+                ("frequency", vp), ("bias_offsets", vp), ("bias_tokens", vp), ("bias_values", vp), ("mask", vp),
+                ("mask_ld", i64), ("mask_rows", vp), ("n_slots", i32), ("n_biases", i32), ("n_masks", i32),
+                ("count_picks", i32)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "sar_last_error": (ctypes.c_char_p, []),
@@ -116,6 +123,9 @@ SIGNATURES = {
     "sar_op_rmsnorm": (i32, [vp, vp, vp, i32, i32, ctypes.c_float, i32, vp]),
     "sar_op_sync_status": (i32, []),
     "sar_op_wait_check": (i32, [i64, i32, vp]),
+    "sar_logits_control": (i32, [vp, i64, i32, i32, i32, ctypes.POINTER(sar_logit_controls), vp, i64, vp, vp]),
+    "sar_token_state_add": (i32, [vp, i64, i32, i32, vp, i32, vp, vp, i32, vp, i32, vp]),
+    "sar_graph_set_controls": (i32, [vp, ctypes.POINTER(sar_logit_controls)]),
     "sar_op_fp4_scale_bytes": (i32, [i32, i32, i32, ctypes.POINTER(i64)]),
     "sar_op_fp4_quantize": (i32, [vp, i64, i32, i32, i32, i32, f32, vp, vp, vp]),
     "sar_op_fp4_dequantize": (i32, [vp, vp, i32, i32, i32, f32, vp, i64, i32, vp]),

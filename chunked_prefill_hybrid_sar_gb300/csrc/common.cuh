@@ -30,6 +30,12 @@ enum ErrSite {
   SITE_FP4_PRODUCER = 60,
   SITE_FP4_MMA = 61,
   SITE_FP4_EPILOGUE = 62,
+  SITE_STATE_SLOT = 70,
+  SITE_STATE_OFFSET = 71,
+  SITE_STATE_TOKEN = 72,
+  SITE_CONTROL_SLOT = 73,
+  SITE_CONTROL_MASK = 74,
+  SITE_CONTROL_BIAS = 75,
 };
 
 // A wait that has not finished after this long gives up (normal waits take

@@ -63,6 +63,11 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // points on the current device (model.cu).
 int op_flags(int** out);
 
+// ---- logits controls (logits.cu) -------------------------------------------
+int check_controls(const sar_logit_controls* c, int vocab);
+int launch_control(const void* x, int64_t ldx, int rows, int vocab, int type, const sar_logit_controls& c, void* y,
+                   int64_t ldy, int32_t* picks, cudaStream_t s);
+
 // ---- 4-bit rows (fp4.cu) ---------------------------------------------------
 
 // Scale tiles (4 blocks wide) per row block of 128 rows.

@@ -1265,7 +1265,9 @@ struct sar_graph {
   int32_t* md = nullptr;       // the graph's own device copy of the step metadata
   int32_t* md_host = nullptr;  // pinned staging for sar_graph_update
   float* partials = nullptr;   // the graph's own decode split partials
-  int32_t* tokens = nullptr;   // greedy picks of the captured logits rows
+  int32_t* tokens = nullptr;   // picks of the captured logits rows
+  bool controlled = false;     // picks under `controls` instead of greedily
+  sar_logit_controls controls = {};
   cudaEvent_t staged = nullptr;
   cudaGraph_t graph = nullptr;
   cudaGraphExec_t exec = nullptr;
@@ -1399,6 +1401,14 @@ int host_copy(void* dst, const void* src, size_t n, cudaStream_t s) {
   return check(cudaMemcpyAsync(dst, src, n, cudaMemcpyDefault, s), "host copy");
 }
 
+// Each captured logits row's token, greedily or under the graph's controls.
+int launch_pick(sar_graph* g, cudaStream_t s) {
+  const int R = g->p.R, V = g->m->d.vocab;
+  if (g->controlled)
+    return sar::launch_control(g->logits, V, R, V, SAR_TYPE_F32, g->controls, nullptr, 0, g->tokens, s);
+  return sar::launch_argmax(g->logits, R, V, g->tokens, s);
+}
+
 }  // namespace
 
 int sar_graph_launch_host(sar_graph* g, const void* in, float* logits_out, float* hidden_out, void* stream) {
@@ -1423,7 +1433,7 @@ int sar_graph_launch_host_tokens(sar_graph* g, const void* in, int32_t* tokens_o
   const size_t in_bytes = g->in_kind == SAR_IN_TOKENS ? M * 4 : M * H * 2;
   SAR_TRY(host_copy(g->in, in, in_bytes, s));
   SAR_TRY(check(cudaGraphLaunch(g->exec, s), "graph: launch"));
-  SAR_TRY(sar::launch_argmax(g->logits, g->p.R, g->m->d.vocab, g->tokens, s));
+  SAR_TRY(launch_pick(g, s));
   SAR_TRY(host_copy(tokens_out, g->tokens, (size_t)g->p.R * 4, s));
   return check(cudaStreamSynchronize(s), "graph: synchronise");
 }
@@ -1446,9 +1456,20 @@ int sar_graph_enqueue_host_tokens(sar_graph* g, const void* in, int32_t* tokens_
   SAR_TRY(check(cudaEventRecord(g->in_ready, g->copy), "graph: input copied"));
   SAR_TRY(check(cudaStreamWaitEvent(s, g->in_ready, 0), "graph: input wait"));
   SAR_TRY(check(cudaGraphLaunch(g->exec, s), "graph: launch"));
-  SAR_TRY(sar::launch_argmax(g->logits, g->p.R, g->m->d.vocab, g->tokens, s));
+  SAR_TRY(launch_pick(g, s));
   SAR_TRY(host_copy(tokens_out, g->tokens, (size_t)g->p.R * 4, s));
   return check(cudaEventRecord(g->done, s), "graph: step enqueued");
+}
+
+int sar_graph_set_controls(sar_graph* g, const sar_logit_controls* controls) {
+  if (!g) return set_error(SAR_ERR_INVALID_ARG, "graph: null graph");
+  if (!g->logits) return set_error(SAR_ERR_INVALID_ARG, "graph: logits not captured");
+  if (controls) {
+    SAR_TRY(sar::check_controls(controls, g->m->d.vocab));
+    g->controls = *controls;
+  }
+  g->controlled = controls != nullptr;
+  return SAR_OK;
 }
 
 int sar_graph_wait(sar_graph* g) {

@@ -275,6 +275,77 @@ int sar_graph_destroy(sar_graph* g);
 int sar_sample_greedy(sar_model* m, const float* logits, int32_t rows, int32_t* tokens_out,
                       void* stream);
 
+/* ---- logits controls ---------------------------------------------------- */
+
+/* Element types of rows (the storage types, and fp32). */
+enum { SAR_TYPE_F16 = 0, SAR_TYPE_BF16 = 1, SAR_TYPE_F32 = 2 };
+
+/* What requests ask of their logits before the pick (the pages' traces decode
+ * greedily to a fixed length and have no counterpart).  All arrays are device
+ * memory; each part is off where its pointer is NULL.  For token v of row r
+ * with logit x, in fp32, each operation rounded:
+ *   penalties  (row r's slot s = slots[r]; -1: none) with made = state[s][v] & 0x7fff:
+ *              if state[s][v] != 0: x = x > 0 ? x / repetition[r] : x * repetition[r]
+ *              x = x - frequency[r] * made;  if made > 0: x = x - presence[r]
+ *   biases     x = x + (the sum, in list order, of the biases that row r's list
+ *              bias_offsets[r] .. bias_offsets[r + 1] gives v)
+ *   mask       x = -inf unless bit v % 32 of word v / 32 of the mask row
+ *              mask_rows[r] (NULL: row r; -1: all allowed) is set
+ * state is uint16 [n_slots][state_ld]: bit 15 set where the token is in the
+ * request's prompt, the low bits how often the request has generated it.
+ * count_picks: each row's pick is counted into its slot (no slot then belongs to
+ * two rows of a call). */
+typedef struct sar_logit_controls {
+  uint16_t* state;
+  int64_t state_ld;
+  const int32_t* slots;
+  const float* repetition; /* [rows], > 0 */
+  const float* presence;   /* [rows] */
+  const float* frequency;  /* [rows] */
+  const int32_t* bias_offsets; /* [rows + 1] */
+  const int32_t* bias_tokens;  /* [n_biases] */
+  const float* bias_values;    /* [n_biases] */
+  const uint32_t* mask; /* [n_masks][mask_ld] words */
+  int64_t mask_ld;
+  const int32_t* mask_rows; /* [rows] */
+  int32_t n_slots;
+  int32_t n_biases;
+  int32_t n_masks;
+  int32_t count_picks;
+} sar_logit_controls;
+
+/* Applies the controls to `rows` rows of logits (device, SAR_TYPE_* `type`, row r
+ * at logits + r * ld elements) and writes the changed logits to `out` (the same
+ * type, rows at ld_out; may be the logits themselves; NULL: not written) and each
+ * row's pick to tokens_out (NULL: none): the lowest token among the largest
+ * changed logits before they are rounded to `type`; NaN is never picked; -1 where
+ * nothing is above -inf (a mask that leaves no token).  Index arrays are checked
+ * on the device: a slot, mask row, list or bias token out of range is passed over
+ * and reported by sar_op_sync_status().  16-byte aligned rows are faster.  Async
+ * on `stream`; allocates nothing after the first call on a device. */
+int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t vocab, int32_t type,
+                       const sar_logit_controls* controls, void* out, int64_t ld_out, int32_t* tokens_out, void* stream);
+
+/* Counts tokens into the token state.  Row i of the call (i < n) adds tokens
+ * offsets[i] .. offsets[i + 1] of `tokens` (device int32 [n_tokens]; offsets device
+ * int32 [n + 1]) to slot slots[i]: the first prompt_lens[i] (device, NULL: none) as
+ * prompt tokens, the others as generated ones, whose counts stop at 32767.  reset:
+ * each slot's first `vocab` entries are made anew from the row's tokens (a request
+ * admitted, or resumed with its history); a slot named again in the call is passed
+ * over.  Otherwise the tokens are added to what is there, also where two rows name
+ * one slot.  Slots, offsets and tokens out of range are passed over; these and a
+ * slot named again are reported by sar_op_sync_status().  Async on `stream`. */
+int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vocab, const int32_t* slots, int32_t n,
+                        const int32_t* offsets, const int32_t* tokens, int32_t n_tokens, const int32_t* prompt_lens,
+                        int32_t reset, void* stream);
+
+/* Makes sar_graph_launch_host_tokens and sar_graph_enqueue_host_tokens of this
+ * graph pick under `controls` (one entry per logits row; NULL: greedily again)
+ * instead of greedily; the captured logits stay as they are.  The struct is
+ * copied; its arrays are read at every launch and have to outlive the last one.
+ * Not to be called while an enqueued step has not been waited for. */
+int sar_graph_set_controls(sar_graph* g, const sar_logit_controls* controls);
+
 /* ---- decode attention without allocation ------------------------------- */
 
 /* Paged decode attention that allocates nothing.  The paper has no

@@ -113,9 +113,6 @@ int sar_op_rmsnorm(const void* x, const void* gain, void* y, int32_t rows, int32
  *           rows behind the last are neither written nor used. */
 enum { SAR_FP4_NV = 0, SAR_FP4_MX = 1 };
 
-/* Element types of rows (the storage types, and fp32). */
-enum { SAR_TYPE_F16 = 0, SAR_TYPE_BF16 = 1, SAR_TYPE_F32 = 2 };
-
 /* Length of a matrix's scales in bytes. */
 int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* out);
 
