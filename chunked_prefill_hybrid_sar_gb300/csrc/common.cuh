@@ -36,6 +36,7 @@ enum ErrSite {
   SITE_CONTROL_SLOT = 73,
   SITE_CONTROL_MASK = 74,
   SITE_CONTROL_BIAS = 75,
+  SITE_CONTROL_PIPE = 76,
 };
 
 // A wait that has not finished after this long gives up (normal waits take

@@ -13,6 +13,7 @@
 #include <cuda_fp8.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -22,7 +23,24 @@ namespace sar {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSeg = 16;  // columns per thread: an NV block, half an MX block
+constexpr int kSeg = 16;         // columns per quantising thread: an NV block, half an MX block
+constexpr int kDequantEach = 4;  // units of 16 output bytes per dequantising thread
+
+// n / d for n < 2^31 as a multiplication and a shift (Granlund and Montgomery
+// 1994: mul = ceil(2^(31 + l) / d) with 2^l >= d): the division of an item's
+// number into row and column would otherwise cost a thread as much as six of its
+// sixteen elements.
+struct Divisor {
+  uint32_t d, mul, shift;
+};
+Divisor divisor(uint32_t d) {
+  uint32_t l = 0;
+  while ((1ull << l) < d) ++l;
+  return {d, (uint32_t)(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+__device__ __forceinline__ uint32_t over(uint32_t n, const Divisor& v) {
+  return (uint32_t)(((uint64_t)n * v.mul) >> v.shift);
+}
 
 template <typename X>
 __device__ __forceinline__ float to_f32(X v) {
@@ -32,33 +50,52 @@ __device__ __forceinline__ float to_f32(X v) {
     return Elem<X>::to(v);
 }
 
-// 16 consecutive values as fp32; vec: the address is 16-byte aligned.
+// 16 consecutive values as fp32, and the largest of their magnitudes as a bit
+// pattern of their own type: patterns without the sign rise with the magnitude,
+// a NaN's is above infinity's, and two 16-bit ones are compared at a time.
+// vec: the address is 16-byte aligned.
 template <typename X>
-__device__ __forceinline__ void load16(const X* p, bool vec, float (&v)[16]) {
-  if (vec) {
-    const uint4* p4 = reinterpret_cast<const uint4*>(p);
-    if constexpr (sizeof(X) == 4) {
+__device__ __forceinline__ uint32_t load16(const X* p, bool vec, float (&v)[16]) {
+  uint32_t m = 0;
+  if constexpr (sizeof(X) == 4) {
+    uint32_t u[16];
+    if (vec) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 u = __ldg(p4 + i);
-        v[4 * i] = __uint_as_float(u.x);
-        v[4 * i + 1] = __uint_as_float(u.y);
-        v[4 * i + 2] = __uint_as_float(u.z);
-        v[4 * i + 3] = __uint_as_float(u.w);
-      }
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(u + 4 * i) = __ldg(reinterpret_cast<const uint4*>(p) + i);
     } else {
-      const uint4 a = __ldg(p4), b = __ldg(p4 + 1);
-      const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[2 * i] = Elem<X>::lo(u[i]);
-        v[2 * i + 1] = Elem<X>::hi(u[i]);
-      }
+      for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(p[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      m = max(m, u[i] & 0x7fffffffu);
+      v[i] = __uint_as_float(u[i]);
     }
   } else {
+    uint32_t u[8];
+    if (vec) {
+      *reinterpret_cast<uint4*>(u) = __ldg(reinterpret_cast<const uint4*>(p));
+      *reinterpret_cast<uint4*>(u + 4) = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = to_f32<X>(p[i]);
+      for (int i = 0; i < 8; ++i) u[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      m = __vmaxu2(m, u[i] & 0x7fff7fffu);
+      v[2 * i] = Elem<X>::lo(u[i]);
+      v[2 * i + 1] = Elem<X>::hi(u[i]);
+    }
+    m = max(m & 0xffffu, m >> 16);
   }
+  return m;
+}
+
+// The fp32 pattern of the magnitude that load16 returns.
+template <typename X>
+__device__ __forceinline__ uint32_t magnitude(uint32_t m) {
+  return sizeof(X) == 4 ? m : __float_as_uint(Elem<typename std::conditional<sizeof(X) == 4, __half, X>::type>::lo(m));
 }
 
 // Byte offset of the scale tile of (row, tile column) plus the row's place in it.
@@ -88,27 +125,27 @@ __device__ __forceinline__ size_t scale_offset(uint32_t row, uint32_t tile, uint
 // blocks' scales are written as zero, as the product reads them.
 template <typename X, bool NV>
 __global__ void __launch_bounds__(kThreads)
-    fp4_quantize_kernel(const X* __restrict__ x, int64_t ldx, uint32_t rows, uint32_t cols, uint32_t tiles, float inv_g,
+    fp4_quantize_kernel(const X* __restrict__ x, int64_t ldx, uint32_t rows, uint32_t cols, uint32_t tiles, Divisor segs,
+                        float inv_g,
                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int vec) {
   constexpr uint32_t kSegsPerTile = NV ? 4 : 8;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t segs = tiles * kSegsPerTile;
   const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  const bool live = i < (uint64_t)rows * segs;  // (whole groups of kSegsPerTile lanes)
-  const uint32_t row = live ? (uint32_t)i / segs : 0;
-  const uint32_t seg = live ? (uint32_t)i - row * segs : 0;
+  const bool live = i < (uint64_t)rows * segs.d;  // (whole groups of kSegsPerTile lanes)
+  const uint32_t row = live ? over((uint32_t)i, segs) : 0;
+  const uint32_t seg = live ? (uint32_t)i - row * segs.d : 0;
   const uint32_t col = seg * kSeg;
   const bool has = live && col < cols;
   float v[16];
-  uint32_t ab = 0;
+  uint32_t ab = 0;  // the block's max |t| as a pattern
   if (has) {
-    load16<X>(x + (int64_t)row * ldx + col, vec != 0, v);
+    // max |x| * inv_g is max |x * inv_g|: the rounding keeps the order
+    const float a = __uint_as_float(magnitude<X>(load16<X>(x + (int64_t)row * ldx + col, vec != 0, v)));
+    ab = __float_as_uint(a * inv_g);
+    if (inv_g != 1.f) {
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      v[k] *= inv_g;
-      // as whole numbers: a NaN is larger than an infinity, which is larger than any number
-      ab = max(ab, __float_as_uint(v[k]) & 0x7fffffffu);
+      for (int k = 0; k < 16; ++k) v[k] *= inv_g;
     }
   } else {
 #pragma unroll
@@ -116,26 +153,27 @@ __global__ void __launch_bounds__(kThreads)
   }
   if constexpr (!NV) ab = max(ab, __shfl_xor_sync(0xffffffffu, ab, 1));
   const bool bad = ab >= 0x7f800000u;
+  bool zero = bad;  // no codes
   uint32_t byte;
   if constexpr (NV) {
     const __nv_fp8_storage_t s8 =
         __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(ab), 6.f), __NV_SATFINITE, __NV_E4M3);
     byte = bad ? 0x7Fu : (uint32_t)s8;
     const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
-    const bool zero = bad || s == 0.f;
-    const float r = zero ? 0.f : __frcp_rn(s);
+    zero = bad || s == 0.f;
+    const float r = __frcp_rn(s);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const float q0 = v[k] * r;
       // (the remainder's sign as written keeps a negative zero negative)
-      v[k] = zero ? 0.f : fmaf(-fmaf(q0, s, -v[k]), r, q0);
+      v[k] = fmaf(-fmaf(q0, s, -v[k]), r, q0);
     }
   } else {
     const uint32_t e = ab >> 23;  // biased exponent (0: zero or subnormal)
     byte = bad ? 0xFFu : e >= 2 ? e - 2 : 0u;
     const float r = __uint_as_float((254u - (bad ? 127u : byte)) << 23);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = bad ? 0.f : v[k] * r;
+    for (int k = 0; k < 16; ++k) v[k] *= r;
   }
   if (!has) byte = 0;
   if (has) {
@@ -149,7 +187,7 @@ __global__ void __launch_bounds__(kThreads)
                                                    cudaRoundNearest)
                 << (8 * k);
     }
-    *reinterpret_cast<uint2*>(codes + (size_t)row * (cols / 2) + col / 2) = make_uint2(w[0], w[1]);
+    *reinterpret_cast<uint2*>(codes + (size_t)row * (cols / 2) + col / 2) = zero ? make_uint2(0, 0) : make_uint2(w[0], w[1]);
   }
   const uint32_t lane = threadIdx.x & 31;
   uint32_t word;
@@ -168,53 +206,64 @@ __global__ void __launch_bounds__(kThreads)
 
 // y = code * s * g: the product of a code and its scale is exact in fp32 (3 and
 // 4 significant bits); * g rounds once, the conversion to Y once more.
+//
+// A unit is 16 bytes of output (8 or 4 columns), neighbouring lanes take
+// neighbouring units and a thread takes 32 bytes' worth kThreads units apart, so
+// that a warp's store covers 512 whole bytes (a thread's 16 columns as two
+// stores: 69.0 us for 20480 x 7168 bf16, every sector written in two halves).
 template <typename Y, bool NV>
 __global__ void __launch_bounds__(kThreads)
     fp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint32_t rows,
-                          uint32_t cols, uint32_t tiles, float g, Y* __restrict__ y, int64_t ldy, int vec) {
+                          uint32_t cols, uint32_t tiles, Divisor units, float g, Y* __restrict__ y, int64_t ldy, int vec) {
+  constexpr uint32_t kCols = 16 / sizeof(Y);
+  constexpr int kEach = kDequantEach;
   pdl_wait();
   pdl_launch_dependents();
-  const uint32_t segs = cols / kSeg;
-  const uint64_t i = (uint64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (i >= (uint64_t)rows * segs) return;
-  const uint32_t row = (uint32_t)i / segs;
-  const uint32_t seg = (uint32_t)i - row * segs;
-  const uint32_t block = NV ? seg : seg >> 1;
-  const uint2 c = __ldg(reinterpret_cast<const uint2*>(codes + (size_t)row * (cols / 2) + seg * 8));
-  const uint8_t b = __ldg(scales + scale_offset(row, block >> 2, tiles) + (block & 3));
-  float s;
-  if constexpr (NV)
-    s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3)));
-  else  // 2^(b - 127); 2^-127 is a subnormal
-    s = __uint_as_float(b == 255 ? 0x7fc00000u : b == 0 ? 0x00400000u : (uint32_t)b << 23);
-  float v[16];
+  const uint64_t n = (uint64_t)rows * units.d;
+  uint32_t c[kEach], b[kEach], row[kEach], col[kEach];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t w = k < 4 ? c.x : c.y;
-    const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * (k & 3))) & 0xffu), __NV_E2M1));
-    v[2 * k] = __low2float(h) * s * g;
-    v[2 * k + 1] = __high2float(h) * s * g;
+  for (int u = 0; u < kEach; ++u) {
+    const uint64_t i = ((uint64_t)blockIdx.x * kEach + u) * kThreads + threadIdx.x;
+    if (i >= n) break;
+    row[u] = over((uint32_t)i, units);
+    const uint32_t unit = (uint32_t)i - row[u] * units.d;
+    col[u] = unit * kCols;
+    const uint32_t block = col[u] / (NV ? 16 : 32);
+    const uint8_t* at = codes + (size_t)row[u] * (cols / 2) + unit * (kCols / 2);
+    c[u] = sizeof(Y) == 4 ? (uint32_t)__ldg(reinterpret_cast<const unsigned short*>(at))
+                          : __ldg(reinterpret_cast<const uint32_t*>(at));
+    b[u] = __ldg(scales + scale_offset(row[u], block >> 2, tiles) + (block & 3));
   }
-  Y* dst = y + (int64_t)row * ldy + seg * kSeg;
-  if constexpr (sizeof(Y) == 4) {
-    if (vec) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        reinterpret_cast<float4*>(dst)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-    } else {
+  for (int u = 0; u < kEach; ++u) {
+    const uint64_t i = ((uint64_t)blockIdx.x * kEach + u) * kThreads + threadIdx.x;
+    if (i >= n) break;
+    float s;
+    if constexpr (NV)
+      s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b[u], __NV_E4M3)));
+    else  // 2^(b - 127); 2^-127 is a subnormal
+      s = __uint_as_float(b[u] == 255 ? 0x7fc00000u : b[u] == 0 ? 0x00400000u : b[u] << 23);
+    float v[kCols];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) dst[k] = v[k];
+    for (int k = 0; k < (int)kCols / 2; ++k) {
+      const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((c[u] >> (8 * k)) & 0xffu), __NV_E2M1));
+      v[2 * k] = __low2float(h) * s * g;
+      v[2 * k + 1] = __high2float(h) * s * g;
     }
-  } else {
-    if (vec) {
-      uint32_t w[8];
+    Y* dst = y + (int64_t)row[u] * ldy + col[u];
+    if (!vec) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) w[k] = Elem<Y>::pack(v[2 * k], v[2 * k + 1]);
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      for (int k = 0; k < (int)kCols; ++k) {
+        if constexpr (sizeof(Y) == 4)
+          dst[k] = v[k];
+        else
+          dst[k] = Elem<Y>::from(v[k]);
+      }
+    } else if constexpr (sizeof(Y) == 4) {
+      *reinterpret_cast<float4*>(dst) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
-#pragma unroll
-      for (int k = 0; k < 16; ++k) dst[k] = Elem<Y>::from(v[k]);
+      *reinterpret_cast<uint4*>(dst) = make_uint4(Elem<Y>::pack(v[0], v[1]), Elem<Y>::pack(v[2], v[3]),
+                                                  Elem<Y>::pack(v[4], v[5]), Elem<Y>::pack(v[6], v[7]));
     }
   }
 }
@@ -223,9 +272,10 @@ bool good_format(int format) { return format == SAR_FP4_NV || format == SAR_FP4_
 bool good_type(int type) { return type == SAR_TYPE_F16 || type == SAR_TYPE_BF16 || type == SAR_TYPE_F32; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// The checks that both directions share; *blocks receives the launch's size.
-int check_rows(const char* what, const void* x, int64_t ld, int rows, int cols, int type, int format, float scale,
-               const void* codes, const void* scales, uint32_t* blocks) {
+// The checks that both directions share; *blocks and *div receive the launch's
+// size and work items per row.
+int check_rows(const char* what, bool quantising, const void* x, int64_t ld, int rows, int cols, int type, int format,
+               float scale, const void* codes, const void* scales, uint32_t* blocks, Divisor* div) {
   const std::string w(what);
   if (rows < 0 || cols <= 0) return set_error(SAR_ERR_INVALID_ARG, w + ": bad shape");
   if (!good_format(format)) return set_error(SAR_ERR_INVALID_ARG, w + ": bad format");
@@ -241,20 +291,26 @@ int check_rows(const char* what, const void* x, int64_t ld, int rows, int cols, 
     return set_error(SAR_ERR_INVALID_ARG, w + ": rows not aligned to their element");
   if (!aligned16(codes) || !aligned16(scales))
     return set_error(SAR_ERR_INVALID_ARG, w + ": codes and scales must be 16-byte aligned");
-  const uint64_t items = (uint64_t)rows * fp4_tiles(cols, format) * (format == SAR_FP4_NV ? 4 : 8);
-  if (items > 0xffffff00ull) return set_error(SAR_ERR_UNSUPPORTED, w + ": more than 2^32 groups of 16 columns");
-  *blocks = (uint32_t)((items + kThreads - 1) / kThreads);
+  // work items: 16 columns of a row padded to whole scale tiles (quantising), 16
+  // bytes of output (dequantising)
+  const uint64_t per_row = quantising ? (uint64_t)fp4_tiles(cols, format) * (format == SAR_FP4_NV ? 4 : 8)
+                                      : (uint64_t)cols * (type == SAR_TYPE_F32 ? 4 : 2) / 16;
+  const uint64_t items = rows * per_row;
+  if (items >= 1ull << 31) return set_error(SAR_ERR_UNSUPPORTED, w + ": more than 2^31 work items");
+  const int per_block = kThreads * (quantising ? 1 : kDequantEach);
+  *blocks = (uint32_t)((items + per_block - 1) / per_block);
+  *div = divisor((uint32_t)per_row);
   return SAR_OK;
 }
 
 template <typename X>
 int quantize(const void* x, int64_t ldx, int rows, int cols, int format, float inv_g, void* codes, void* scales,
-             uint32_t blocks, cudaStream_t s) {
+             uint32_t blocks, Divisor div, cudaStream_t s) {
   const int vec = aligned16(x) && (ldx * (int64_t)sizeof(X)) % 16 == 0;
   const uint32_t tiles = (uint32_t)fp4_tiles(cols, format);
   auto fn = format == SAR_FP4_NV ? fp4_quantize_kernel<X, true> : fp4_quantize_kernel<X, false>;
   const cudaError_t e = launch_pdl(fn, dim3(blocks), dim3(kThreads), 0, s, static_cast<const X*>(x), ldx, (uint32_t)rows,
-                                   (uint32_t)cols, tiles, inv_g, static_cast<uint8_t*>(codes),
+                                   (uint32_t)cols, tiles, div, inv_g, static_cast<uint8_t*>(codes),
                                    static_cast<uint8_t*>(scales), vec);
   if (e != cudaSuccess) return cuda_error(e, "fp4 quantise launch");
   count_launches(1);
@@ -263,13 +319,13 @@ int quantize(const void* x, int64_t ldx, int rows, int cols, int format, float i
 
 template <typename Y>
 int dequantize(const void* codes, const void* scales, int rows, int cols, int format, float g, void* y, int64_t ldy,
-               uint32_t blocks, cudaStream_t s) {
+               uint32_t blocks, Divisor div, cudaStream_t s) {
   const int vec = aligned16(y) && (ldy * (int64_t)sizeof(Y)) % 16 == 0;
   const uint32_t tiles = (uint32_t)fp4_tiles(cols, format);
   auto fn = format == SAR_FP4_NV ? fp4_dequantize_kernel<Y, true> : fp4_dequantize_kernel<Y, false>;
   const cudaError_t e =
       launch_pdl(fn, dim3(blocks), dim3(kThreads), 0, s, static_cast<const uint8_t*>(codes),
-                 static_cast<const uint8_t*>(scales), (uint32_t)rows, (uint32_t)cols, tiles, g, static_cast<Y*>(y), ldy, vec);
+                 static_cast<const uint8_t*>(scales), (uint32_t)rows, (uint32_t)cols, tiles, div, g, static_cast<Y*>(y), ldy, vec);
   if (e != cudaSuccess) return cuda_error(e, "fp4 dequantise launch");
   count_launches(1);
   return SAR_OK;
@@ -294,27 +350,31 @@ int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* 
 int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_t type, int32_t format,
                         float tensor_scale, void* codes, void* scales, void* stream) {
   uint32_t blocks = 0;
-  SAR_TRY(sar::check_rows("fp4_quantize", x, ldx, rows, cols, type, format, tensor_scale, codes, scales, &blocks));
+  sar::Divisor div;
+  SAR_TRY(sar::check_rows("fp4_quantize", true, x, ldx, rows, cols, type, format, tensor_scale, codes, scales, &blocks,
+                          &div));
   if (blocks == 0) return SAR_OK;
   const float inv = 1.f / tensor_scale;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (type == SAR_TYPE_F32) return sar::quantize<float>(x, ldx, rows, cols, format, inv, codes, scales, blocks, s);
+  if (type == SAR_TYPE_F32) return sar::quantize<float>(x, ldx, rows, cols, format, inv, codes, scales, blocks, div, s);
   if (type == SAR_TYPE_BF16)
-    return sar::quantize<__nv_bfloat16>(x, ldx, rows, cols, format, inv, codes, scales, blocks, s);
-  return sar::quantize<__half>(x, ldx, rows, cols, format, inv, codes, scales, blocks, s);
+    return sar::quantize<__nv_bfloat16>(x, ldx, rows, cols, format, inv, codes, scales, blocks, div, s);
+  return sar::quantize<__half>(x, ldx, rows, cols, format, inv, codes, scales, blocks, div, s);
 }
 
 int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, int32_t format,
                           float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream) {
   uint32_t blocks = 0;
-  SAR_TRY(sar::check_rows("fp4_dequantize", y, ldy, rows, cols, type, format, tensor_scale, codes, scales, &blocks));
+  sar::Divisor div;
+  SAR_TRY(sar::check_rows("fp4_dequantize", false, y, ldy, rows, cols, type, format, tensor_scale, codes, scales, &blocks,
+                          &div));
   if (blocks == 0) return SAR_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (type == SAR_TYPE_F32)
-    return sar::dequantize<float>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, s);
+    return sar::dequantize<float>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, div, s);
   if (type == SAR_TYPE_BF16)
-    return sar::dequantize<__nv_bfloat16>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, s);
-  return sar::dequantize<__half>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, s);
+    return sar::dequantize<__nv_bfloat16>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, div, s);
+  return sar::dequantize<__half>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, div, s);
 }
 
 }  // extern "C"

@@ -134,9 +134,11 @@ __global__ void __launch_bounds__(256) state_append_kernel(const StateArgs a) {
 
 // ---- logits --------------------------------------------------------------------
 
-constexpr int kCtlThreads = 512;
-constexpr int kCtlSpan = 32768;              // tokens per pass: two bitmaps of 4 KB
-constexpr int kCtlTile = 8 * kCtlThreads;    // tokens per CTA and step
+constexpr int kCtlThreads = 256;
+constexpr int kCtlTile = 4096;    // tokens per CTA and step
+constexpr int kCtlStages = 3;     // steps on their way
+constexpr int kCtlSpan = 32768;   // tokens per pass over a row's biases: two bitmaps of 4 KB
+constexpr long kCtlPerSm = 3;     // CTAs that fit an SM's shared memory
 
 struct CtlArgs {
   const void* x;
@@ -170,6 +172,22 @@ __device__ __forceinline__ float penalised(float x, uint32_t s, const RowCtl& w)
 struct Best {
   float v = -INFINITY;
   int i = 0x7fffffff;
+  // (of tokens that come in rising order only a larger one counts)
+  __device__ __forceinline__ void take_later(float x, int t) {
+    if (x > v) {
+      v = x;
+      i = t;
+    }
+  }
+  // the best of the warp's lanes, in all of them
+  __device__ __forceinline__ void warp() {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float x = __shfl_xor_sync(0xffffffffu, v, o);
+      const int t = __shfl_xor_sync(0xffffffffu, i, o);
+      take(x, t);
+    }
+  }
   __device__ __forceinline__ void take(float x, int t) {
     if (x > v || (x == v && t < i && x > -INFINITY)) {
       v = x;
@@ -177,6 +195,20 @@ struct Best {
     }
   }
 };
+
+// The part of a tile's array that a bulk copy can bring to shared memory: the
+// elements [lo, hi) of [t0, t1) that lie in whole 16-byte pieces.  The few others
+// (rows at odd addresses) are read where they are.
+struct Window {
+  int lo, hi;
+};
+__device__ __forceinline__ Window window(const void* base, int t0, int t1, int size) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(base) + (uintptr_t)t0 * size;
+  const uintptr_t e = reinterpret_cast<uintptr_t>(base) + (uintptr_t)t1 * size;
+  Window w = {t0 + (int)((0 - p) & 15) / size, t1 - (int)(e & 15) / size};
+  if (w.hi <= w.lo) w.lo = w.hi = t0;
+  return w;
+}
 
 template <typename T>
 __device__ __forceinline__ float ctl_load(const T* p) {
@@ -199,63 +231,100 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
 // cluster has CTAs, and one launch without a workspace does penalties, biases,
 // mask, store and pick.
 //
+// Logits, token state and mask words come in tiles of 4096 tokens by bulk copies,
+// three tiles ahead: with ordinary loads a thread's registers hold too little of
+// what has to be on its way (256 x 64000 fp32, pick only: 30 us with one step of
+// loads in flight at 16 warps an SM, 28 us with two).
+//
 // Biases come as a list per row.  Their tokens are marked in a bitmap of the
 // stretch; the dense pass leaves marked tokens as they are, and the list's
 // threads then finish one each: penalties from the original logit, the token's
 // biases added up in list order (a second bitmap marks tokens that are listed
 // again: only those search the list), mask.
 //
-// VEC: a thread takes 8 neighbouring tokens with 16-byte accesses; otherwise
-// (rows at odd addresses) 8 tokens kCtlThreads apart, a warp's still adjacent.
+// VEC: rows at 16-byte boundaries; a thread takes 4 neighbouring tokens at a
+// time, otherwise single ones.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlArgs a) {
+  extern __shared__ __align__(16) uint8_t stage_mem[];  // [stages] logits, state, mask words of a tile
   __shared__ uint32_t listed[kCtlSpan / 32], twice[kCtlSpan / 32];
+  __shared__ __align__(8) uint64_t full[kCtlStages];
   __shared__ float best_v[kCtlThreads / 32];
   __shared__ int best_i[kCtlThreads / 32];
   __shared__ Best cta_best;
-  pdl_wait();
-  pdl_launch_dependents();
+  constexpr uint32_t kState = kCtlTile * sizeof(T), kMask = kState + kCtlTile * 2, kStage = kMask + kCtlTile / 8;
   const int r = blockIdx.y, rank = blockIdx.x, tid = threadIdx.x;
   const bool tells = rank == 0 && tid == 0;
+  if (tid == 0) {
+    for (int i = 0; i < kCtlStages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_launch_dependents();
   const sar_logit_controls& c = a.c;
-  RowCtl w;
-  int slot = -1;
-  if (c.state) {
-    slot = c.slots[r];
-    if (slot >= c.n_slots || slot < -1) {
-      if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_SLOT, r);
-      slot = -1;
-    }
-    if (slot >= 0 && (c.repetition || c.presence || c.frequency)) {
-      w.state = c.state + (int64_t)slot * c.state_ld;
-      if (c.repetition) w.rep = c.repetition[r];
-      if (c.presence) w.pres = c.presence[r];
-      if (c.frequency) w.freq = c.frequency[r];
-    }
-  }
-  if (c.mask) {
-    const int m = c.mask_rows ? c.mask_rows[r] : r;
-    if (m >= c.n_masks || m < -1) {
-      if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_MASK, r);
-    } else if (m >= 0) {
-      w.mask = c.mask + (int64_t)m * c.mask_ld;
-    }
-  }
-  int b0 = 0, b1 = 0;
-  if (c.bias_offsets) {
-    b0 = c.bias_offsets[r];
-    b1 = c.bias_offsets[r + 1];
-    if (b0 < 0 || b1 < b0 || b1 > c.n_biases) {
-      if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, r);
-      b0 = b1 = 0;
-    }
-  }
   const T* x = static_cast<const T*>(a.x) + (int64_t)r * a.ldx;
   T* y = a.y ? static_cast<T*>(a.y) + (int64_t)r * a.ldy : nullptr;
   const int lo = rank * a.chunk, hi = min(a.vocab, lo + a.chunk);
+  const int tiles = hi > lo ? (hi - lo + kCtlTile - 1) / kCtlTile : 0;
+  RowCtl w;
+
+  // tile i to its stage (one thread): the logits, which wait for no index, and
+  // then the rest
+  auto fetch_x = [&](int i) {
+    const int t0 = lo + i * kCtlTile, t1 = min(hi, t0 + kCtlTile);
+    const uint32_t st = smem_u32(stage_mem) + (uint32_t)(i % kCtlStages) * kStage, bar = smem_u32(&full[i % kCtlStages]);
+    const Window wx = window(x, t0, t1, sizeof(T));
+    if (wx.hi > wx.lo) {
+      const uint32_t bytes = (uint32_t)((wx.hi - wx.lo) * sizeof(T));
+      asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+      bulk_g2s(st, x + wx.lo, bytes, bar);
+    }
+  };
+  auto fetch_rest = [&](int i) {
+    const int t0 = lo + i * kCtlTile, t1 = min(hi, t0 + kCtlTile);
+    const uint32_t st = smem_u32(stage_mem) + (uint32_t)(i % kCtlStages) * kStage, bar = smem_u32(&full[i % kCtlStages]);
+    const Window ws = w.state ? window(w.state, t0, t1, 2) : Window{0, 0};
+    const Window wm = w.mask ? window(w.mask, t0 >> 5, (t1 + 31) >> 5, 4) : Window{0, 0};
+    mbar_expect_tx(bar, (uint32_t)((ws.hi - ws.lo) * 2 + (wm.hi - wm.lo) * 4));
+    if (ws.hi > ws.lo) bulk_g2s(st + kState, w.state + ws.lo, (uint32_t)(ws.hi - ws.lo) * 2, bar);
+    if (wm.hi > wm.lo) bulk_g2s(st + kMask, w.mask + wm.lo, (uint32_t)(wm.hi - wm.lo) * 4, bar);
+  };
+  if (tid == 0)
+    for (int i = 0; i < min(tiles, kCtlStages); ++i) fetch_x(i);
+
+  // the row's indexes and factors, all on their way at once
+  int slot = c.state ? c.slots[r] : -1;
+  int m = !c.mask ? -1 : c.mask_rows ? c.mask_rows[r] : r;
+  int b0 = c.bias_offsets ? c.bias_offsets[r] : 0, b1 = c.bias_offsets ? c.bias_offsets[r + 1] : 0;
+  if (c.repetition) w.rep = c.repetition[r];
+  if (c.presence) w.pres = c.presence[r];
+  if (c.frequency) w.freq = c.frequency[r];
+  if (c.state && (slot >= c.n_slots || slot < -1)) {
+    if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_SLOT, r);
+    slot = -1;
+  }
+  if (slot >= 0 && (c.repetition || c.presence || c.frequency)) w.state = c.state + (int64_t)slot * c.state_ld;
+  if (c.mask && (m >= c.n_masks || m < -1)) {
+    if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_MASK, r);
+    m = -1;
+  }
+  if (m >= 0) w.mask = c.mask + (int64_t)m * c.mask_ld;
+  if (b0 < 0 || b1 < b0 || b1 > c.n_biases) {
+    if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, r);
+    b0 = b1 = 0;
+  }
+  if (tid == 0)
+    for (int i = 0; i < min(tiles, kCtlStages); ++i) fetch_rest(i);
+
   Best best;
   for (int s0 = lo; s0 < hi; s0 += kCtlSpan) {
     const int s1 = min(hi, s0 + kCtlSpan);
+    // this thread's first listed token of the span, with what finishing it reads
+    // loaded ahead of the dense pass (which leaves it as it is)
+    int et = -1;
+    float ev = 0.f, ex = 0.f;
+    uint32_t es = 0, em = 1;
     if (b1 > b0) {
       __syncthreads();  // the last span's bitmaps are done with
       for (int i = tid; i < kCtlSpan / 32; i += kCtlThreads) listed[i] = twice[i] = 0;
@@ -265,92 +334,110 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
         if (t >= s0 && t < s1) {
           const uint32_t bit = 1u << (t & 31);
           if (atomicOr(&listed[(t - s0) >> 5], bit) & bit) atomicOr(&twice[(t - s0) >> 5], bit);
+          if (e < b0 + kCtlThreads) {
+            et = t;
+            ev = __ldg(c.bias_values + e);
+            ex = ctl_load<T>(x + t);
+            if (w.state) es = w.state[t];
+            if (w.mask) em = __ldg(w.mask + (t >> 5)) >> (t & 31) & 1;
+          }
         } else if (rank == 0 && s0 == lo && (t < 0 || t >= a.vocab)) {
           report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, e);
         }
       }
       __syncthreads();
     }
-    // (s0 and every tile start are multiples of 32)
+    // (spans and tiles start at multiples of 32 tokens)
     for (int t0 = s0; t0 < s1; t0 += kCtlTile) {
-      auto token = [&](int k) { return VEC ? t0 + tid * 8 + k : t0 + k * kCtlThreads + tid; };
-      float v[8];
-      uint32_t s[8];
-      uint32_t on = 0, raw = 0;  // bit k: allowed; left to the list
-      const bool full = VEC && token(7) < s1;
-      if (full) {
-        const int t = token(0);
-        if constexpr (sizeof(T) == 4) {
-          const float4 p = __ldcs(reinterpret_cast<const float4*>(x + t)), q = __ldcs(reinterpret_cast<const float4*>(x + t) + 1);
-          v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w, v[4] = q.x, v[5] = q.y, v[6] = q.z, v[7] = q.w;
-        } else {
-          const uint4 p = __ldcs(reinterpret_cast<const uint4*>(x + t));
-          const uint32_t u[4] = {p.x, p.y, p.z, p.w};
+      const int i = (t0 - lo) / kCtlTile, t1 = min(s1, t0 + kCtlTile);
+      mbar_wait(smem_u32(&full[i % kCtlStages]), (uint32_t)(i / kCtlStages) & 1u, a.err, SITE_CONTROL_PIPE);
+      const uint8_t* st = stage_mem + (i % kCtlStages) * kStage;
+      const T* xs = reinterpret_cast<const T*>(st);
+      const uint16_t* ss = reinterpret_cast<const uint16_t*>(st + kState);
+      const uint32_t* ms = reinterpret_cast<const uint32_t*>(st + kMask);
+      const Window wm = w.mask ? window(w.mask, t0 >> 5, (t1 + 31) >> 5, 4) : Window{0, 0};
+      auto allowed = [&](int t) {  // the mask word of token t, bit t % 32 first
+        if (!w.mask) return 0xffffffffu;
+        const int q = t >> 5;
+        return (q >= wm.lo && q < wm.hi ? ms[q - wm.lo] : __ldg(w.mask + q)) >> (t & 31);
+      };
+      if (VEC) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[2 * k] = Elem<T>::lo(u[k]);
-            v[2 * k + 1] = Elem<T>::hi(u[k]);
+        for (int g = 0; g < kCtlTile / (4 * kCtlThreads); ++g) {
+          const int at = (g * kCtlThreads + tid) * 4, t = t0 + at;
+          if (t + 4 > t1) {
+            for (int k = 0; k < 4 && t + k < t1; ++k) {  // (the vocabulary's last tokens)
+              float v = ctl_load<T>(x + t + k);
+              if (!(b1 > b0 && (listed[(t + k - s0) >> 5] >> ((t + k) & 31) & 1))) {
+                if (w.state) v = penalised(v, w.state[t + k], w);
+                if (!(allowed(t + k) & 1)) v = -INFINITY;
+                best.take_later(v, t + k);
+              }
+              if (y) ctl_store<T>(y + t + k, v);
+            }
+            continue;
           }
-        }
-        if (w.state) {
-          const uint4 p = *reinterpret_cast<const uint4*>(w.state + t);
-          const uint32_t u[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            s[2 * k] = u[k] & 0xffffu;
-            s[2 * k + 1] = u[k] >> 16;
-          }
-        }
-        on = w.mask ? __ldg(w.mask + (t >> 5)) >> (t & 31) & 0xffu : 0xffu;
-        if (b1 > b0) raw = listed[(t - s0) >> 5] >> (t & 31) & 0xffu;
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int t = token(k);
-          if (t < s1) {
-            v[k] = ctl_load<T>(x + t);
-            if (w.state) s[k] = w.state[t];
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int t = token(k);
-          if (t < s1) {
-            on |= (w.mask ? __ldg(w.mask + (t >> 5)) >> (t & 31) & 1u : 1u) << k;
-            if (b1 > b0) raw |= (listed[(t - s0) >> 5] >> (t & 31) & 1u) << k;
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (raw >> k & 1) continue;
-        if (w.state && (full || token(k) < s1)) v[k] = penalised(v[k], s[k], w);
-        if (!(on >> k & 1)) v[k] = -INFINITY;
-        if (full || token(k) < s1) best.take(v[k], token(k));
-      }
-      if (y) {
-        if (full) {
-          T* d = y + token(0);
+          float v[4];
           if constexpr (sizeof(T) == 4) {
-            __stcs(reinterpret_cast<float4*>(d), make_float4(v[0], v[1], v[2], v[3]));
-            __stcs(reinterpret_cast<float4*>(d) + 1, make_float4(v[4], v[5], v[6], v[7]));
+            const float4 p = *reinterpret_cast<const float4*>(xs + at);
+            v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
           } else {
-            __stcs(reinterpret_cast<uint4*>(d), make_uint4(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3]),
-                                                           Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7])));
+            const uint2 p = *reinterpret_cast<const uint2*>(xs + at);
+            v[0] = Elem<T>::lo(p.x), v[1] = Elem<T>::hi(p.x), v[2] = Elem<T>::lo(p.y), v[3] = Elem<T>::hi(p.y);
           }
-        } else {
+          uint2 u = make_uint2(0, 0);
+          if (w.state) u = *reinterpret_cast<const uint2*>(ss + at);
+          uint32_t raw = 0;  // bit k: left to the list
+          if (b1 > b0) raw = listed[(t - s0) >> 5] >> (t & 31) & 0xfu;
+          if (u.x | u.y) {  // (most of a vocabulary is unseen)
+            const uint32_t s[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (token(k) < s1) ctl_store<T>(y + token(k), v[k]);
+            for (int k = 0; k < 4; ++k)
+              if (!(raw >> k & 1)) v[k] = penalised(v[k], s[k], w);
+          }
+          const uint32_t off = ~allowed(t) & ~raw & 0xfu;
+          if (off) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (off >> k & 1) v[k] = -INFINITY;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (!(raw >> k & 1)) best.take_later(v[k], t + k);
+          if (y) {
+            if constexpr (sizeof(T) == 4)
+              __stcs(reinterpret_cast<float4*>(y + t), make_float4(v[0], v[1], v[2], v[3]));
+            else
+              __stcs(reinterpret_cast<uint2*>(y + t), make_uint2(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3])));
+          }
         }
+      } else {
+        const Window wx = window(x, t0, t1, sizeof(T));
+        const Window ws = w.state ? window(w.state, t0, t1, 2) : Window{0, 0};
+#pragma unroll 4
+        for (int t = t0 + tid; t < t1; t += kCtlThreads) {
+          float v = t >= wx.lo && t < wx.hi ? ctl_load<T>(xs + (t - wx.lo)) : ctl_load<T>(x + t);
+          if (!(b1 > b0 && (listed[(t - s0) >> 5] >> (t & 31) & 1))) {
+            if (w.state) v = penalised(v, t >= ws.lo && t < ws.hi ? ss[t - ws.lo] : w.state[t], w);
+            if (!(allowed(t) & 1)) v = -INFINITY;
+            best.take_later(v, t);
+          }
+          if (y) ctl_store<T>(y + t, v);
+        }
+      }
+      __syncthreads();  // the stage is read
+      if (tid == 0 && i + kCtlStages < tiles) {
+        fetch_x(i + kCtlStages);
+        fetch_rest(i + kCtlStages);
       }
     }
     if (b1 > b0) {
-      __syncthreads();  // y's marked tokens hold the logits (y may be x)
+      // (where y is x its marked tokens still hold the logits)
       for (int e = b0 + tid; e < b1; e += kCtlThreads) {
-        const int t = __ldg(c.bias_tokens + e);
+        const bool kept = e < b0 + kCtlThreads;
+        const int t = kept ? et : __ldg(c.bias_tokens + e);
         if (t < s0 || t >= s1) continue;
-        float sum = __ldg(c.bias_values + e);
+        float sum = kept ? ev : __ldg(c.bias_values + e);
         if (twice[(t - s0) >> 5] >> (t & 31) & 1) {
           bool first = true;
           for (int f = b0; f < e; ++f) first = first && __ldg(c.bias_tokens + f) != t;
@@ -358,46 +445,48 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
           for (int f = e + 1; f < b1; ++f)
             if (__ldg(c.bias_tokens + f) == t) sum = __fadd_rn(sum, __ldg(c.bias_values + f));
         }
-        float v = ctl_load<T>(x + t);
-        if (w.state) v = penalised(v, w.state[t], w);
-        v = __fadd_rn(v, sum);
-        if (w.mask && !(__ldg(w.mask + (t >> 5)) >> (t & 31) & 1)) v = -INFINITY;
+        if (!kept) {
+          ex = ctl_load<T>(x + t);
+          es = w.state ? w.state[t] : 0;
+          em = w.mask ? __ldg(w.mask + (t >> 5)) >> (t & 31) & 1 : 1;
+        }
+        const float v = em ? __fadd_rn(penalised(ex, es, w), sum) : -INFINITY;
         best.take(v, t);
         if (y) ctl_store<T>(y + t, v);
       }
     }
   }
   if (!a.picks) return;  // (every CTA of the cluster alike)
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float v = __shfl_xor_sync(0xffffffffu, best.v, o);
-    const int i = __shfl_xor_sync(0xffffffffu, best.i, o);
-    best.take(v, i);
-  }
+  best.warp();
   if ((tid & 31) == 0) {
     best_v[tid >> 5] = best.v;
     best_i[tid >> 5] = best.i;
   }
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 1; i < kCtlThreads / 32; ++i) best.take(best_v[i], best_i[i]);
-    cta_best = best;
+  if (tid < 32) {
+    best = Best();
+    if (tid < kCtlThreads / 32) best.take(best_v[tid], best_i[tid]);
+    best.warp();
+    if (tid == 0) cta_best = best;
   }
   __syncwarp();
   cluster_sync();
-  if (tells) {
-    for (int k = 1; k < (int)gridDim.x; ++k) {
-      const uint32_t at = cluster_addr(smem_u32(&cta_best), (uint32_t)k);
+  if (rank == 0 && tid < 32) {
+    if (tid > 0 && tid < (int)gridDim.x) {
+      const uint32_t at = cluster_addr(smem_u32(&cta_best), (uint32_t)tid);
       float v;
       int i;
       asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at + (uint32_t)offsetof(Best, v)) : "memory");
       asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(i) : "r"(at + (uint32_t)offsetof(Best, i)) : "memory");
       best.take(v, i);
     }
-    const bool any = best.i != 0x7fffffff;
-    a.picks[r] = any ? best.i : -1;
-    // (every CTA of the row has read its state)
-    if (any && c.count_picks && slot >= 0) state_count(c.state + (int64_t)slot * c.state_ld + best.i, false);
+    best.warp();
+    if (tid == 0) {
+      const bool any = best.i != 0x7fffffff;
+      a.picks[r] = any ? best.i : -1;
+      // (every CTA of the row has read its state)
+      if (any && c.count_picks && slot >= 0) state_count(c.state + (int64_t)slot * c.state_ld + best.i, false);
+    }
   }
   __syncwarp();
   cluster_sync();  // rank 0 has read the others' shared memory
@@ -410,6 +499,8 @@ int launch_control_t(const CtlArgs& a, int rows, int ctas, bool vec, cudaStream_
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)ctas, (unsigned)rows);
   lc.blockDim = dim3(kCtlThreads);
+  lc.dynamicSmemBytes = kCtlStages * (kCtlTile * sizeof(T) + kCtlTile * 2 + kCtlTile / 8);
+  SAR_TRY(ensure_smem_attr(reinterpret_cast<const void*>(fn), (int)lc.dynamicSmemBytes, "logits control: set smem attribute"));
   lc.stream = s;
   lc.attrs = attr;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -464,9 +555,11 @@ int launch_control(const void* x, int64_t ldx, int rows, int vocab, int type, co
   const int64_t size = type == SAR_TYPE_F32 ? 4 : 2;
   const bool vec = aligned(x, 16) && ldx * size % 16 == 0 && aligned(y, 16) && (!y || ldy * size % 16 == 0) &&
                    (!c.state || (aligned(c.state, 16) && c.state_ld % 8 == 0));
-  // CTAs to a row: enough to fill the SMs twice, at least one tile of tokens each
+  // CTAs to a row: as many as stay resident at once (three to an SM), at least one
+  // tile of tokens each.  Beyond one wave every further CTA costs its start: 256
+  // rows of 64000 with two to a row took longer than with one (see the kernel)
   int ctas = 1;
-  while (ctas < 8 && (long)rows * ctas < 2l * num_sms() && vocab > ctas * kCtlTile) ctas *= 2;
+  while (ctas < 8 && 2l * rows * ctas <= kCtlPerSm * num_sms() && vocab > ctas * kCtlTile) ctas *= 2;
   a.chunk = (int)((((int64_t)vocab + ctas - 1) / ctas + kCtlTile - 1) / kCtlTile * kCtlTile);
   // (65535 rows to a launch)
   for (int r0 = 0; r0 < rows; r0 += 65535) {

@@ -124,13 +124,14 @@ int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* 
  * to nearest even, q at most 6 in magnitude; a block whose scale rounds to zero
  * is zero.  A block that holds a NaN or an infinity (in t) gets a NaN scale and
  * zero codes.  tensor_scale > 0, finite, with a finite inverse.  rows = 0 does
- * nothing; rows * cols / 16 (cols padded to whole scale tiles) stays below 2^32.
+ * nothing; rows * cols / 16 (cols padded to whole scale tiles) stays below 2^31.
  * Async on `stream`. */
 int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_t type, int32_t format,
                         float tensor_scale, void* codes, void* scales, void* stream);
 
 /* y = the rows that codes and scales stand for: q * s (exact) * tensor_scale in
- * fp32, rounded to `type`.  y rows as x above.  Async on `stream`. */
+ * fp32, rounded to `type`.  y rows as x above, below 2^31 times 16 bytes in all.
+ * Async on `stream`. */
 int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, int32_t format,
                           float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream);
 
