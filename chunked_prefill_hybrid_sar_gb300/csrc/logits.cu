@@ -134,11 +134,11 @@ __global__ void __launch_bounds__(256) state_append_kernel(const StateArgs a) {
 
 // ---- logits --------------------------------------------------------------------
 
-constexpr int kCtlThreads = 256;
+constexpr int kCtlThreads = 512;  // that work on tokens; one more warp fetches
 constexpr int kCtlTile = 4096;    // tokens per CTA and step
-constexpr int kCtlStages = 3;     // steps on their way
+constexpr int kCtlStages = 4;     // steps on their way
 constexpr int kCtlSpan = 32768;   // tokens per pass over a row's biases: two bitmaps of 4 KB
-constexpr long kCtlPerSm = 3;     // CTAs that fit an SM's shared memory
+constexpr long kCtlPerSm = 2;     // CTAs that fit an SM's shared memory
 
 struct CtlArgs {
   const void* x;
@@ -245,10 +245,10 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
 // VEC: rows at 16-byte boundaries; a thread takes 4 neighbouring tokens at a
 // time, otherwise single ones.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlArgs a) {
+__global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_kernel(const CtlArgs a) {
   extern __shared__ __align__(16) uint8_t stage_mem[];  // [stages] logits, state, mask words of a tile
   __shared__ uint32_t listed[kCtlSpan / 32], twice[kCtlSpan / 32];
-  __shared__ __align__(8) uint64_t full[kCtlStages];
+  __shared__ __align__(8) uint64_t full[kCtlStages], empty[kCtlStages];
   __shared__ float best_v[kCtlThreads / 32];
   __shared__ int best_i[kCtlThreads / 32];
   __shared__ Best cta_best;
@@ -256,7 +256,10 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
   const int r = blockIdx.y, rank = blockIdx.x, tid = threadIdx.x;
   const bool tells = rank == 0 && tid == 0;
   if (tid == 0) {
-    for (int i = 0; i < kCtlStages; ++i) mbar_init(smem_u32(&full[i]), 1);
+    for (int i = 0; i < kCtlStages; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), kCtlThreads / 32);
+    }
     fence_mbar_init();
   }
   __syncthreads();
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
   const int tiles = hi > lo ? (hi - lo + kCtlTile - 1) / kCtlTile : 0;
   RowCtl w;
 
-  // tile i to its stage (one thread): the logits, which wait for no index, and
+  // tile i to its stage (the fetching thread): the logits, which wait for no index, and
   // then the rest
   auto fetch_x = [&](int i) {
     const int t0 = lo + i * kCtlTile, t1 = min(hi, t0 + kCtlTile);
@@ -290,7 +293,8 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
     if (ws.hi > ws.lo) bulk_g2s(st + kState, w.state + ws.lo, (uint32_t)(ws.hi - ws.lo) * 2, bar);
     if (wm.hi > wm.lo) bulk_g2s(st + kMask, w.mask + wm.lo, (uint32_t)(wm.hi - wm.lo) * 4, bar);
   };
-  if (tid == 0)
+  const bool fetches = tid == kCtlThreads;
+  if (fetches)
     for (int i = 0; i < min(tiles, kCtlStages); ++i) fetch_x(i);
 
   // the row's indexes and factors, all on their way at once
@@ -314,11 +318,20 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
     if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, r);
     b0 = b1 = 0;
   }
-  if (tid == 0)
+  if (fetches) {
     for (int i = 0; i < min(tiles, kCtlStages); ++i) fetch_rest(i);
+    for (int i = kCtlStages; i < tiles; ++i) {
+      // (a wait that gave up is reported; the copies go on, so that the others' waits end)
+      mbar_wait(smem_u32(&empty[i % kCtlStages]), (uint32_t)(i / kCtlStages - 1) & 1u, a.err, SITE_CONTROL_PIPE);
+      fetch_x(i);
+      fetch_rest(i);
+    }
+  }
+  // the working threads alone
+  auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kCtlThreads) : "memory"); };
 
   Best best;
-  for (int s0 = lo; s0 < hi; s0 += kCtlSpan) {
+  for (int s0 = lo; s0 < hi && tid < kCtlThreads; s0 += kCtlSpan) {
     const int s1 = min(hi, s0 + kCtlSpan);
     // this thread's first listed token of the span, with what finishing it reads
     // loaded ahead of the dense pass (which leaves it as it is)
@@ -326,9 +339,9 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
     float ev = 0.f, ex = 0.f;
     uint32_t es = 0, em = 1;
     if (b1 > b0) {
-      __syncthreads();  // the last span's bitmaps are done with
+      sync();  // the last span's bitmaps are done with
       for (int i = tid; i < kCtlSpan / 32; i += kCtlThreads) listed[i] = twice[i] = 0;
-      __syncthreads();
+      sync();
       for (int e = b0 + tid; e < b1; e += kCtlThreads) {
         const int t = __ldg(c.bias_tokens + e);
         if (t >= s0 && t < s1) {
@@ -345,7 +358,7 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
           report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, e);
         }
       }
-      __syncthreads();
+      sync();
     }
     // (spans and tiles start at multiples of 32 tokens)
     for (int t0 = s0; t0 < s1; t0 += kCtlTile) {
@@ -413,25 +426,29 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
         }
       } else {
         const Window wx = window(x, t0, t1, sizeof(T));
-        const Window ws = w.state ? window(w.state, t0, t1, 2) : Window{0, 0};
-#pragma unroll 4
-        for (int t = t0 + tid; t < t1; t += kCtlThreads) {
-          float v = t >= wx.lo && t < wx.hi ? ctl_load<T>(xs + (t - wx.lo)) : ctl_load<T>(x + t);
+        const Window ws = w.state ? window(w.state, t0, t1, 2) : wx;
+        const int i0 = max(wx.lo, ws.lo), i1 = max(i0, min(wx.hi, ws.hi));  // in shared memory, both
+        auto one = [&](int t, float v, uint32_t seen) {
           if (!(b1 > b0 && (listed[(t - s0) >> 5] >> (t & 31) & 1))) {
-            if (w.state) v = penalised(v, t >= ws.lo && t < ws.hi ? ss[t - ws.lo] : w.state[t], w);
+            v = penalised(v, seen, w);
             if (!(allowed(t) & 1)) v = -INFINITY;
             best.take_later(v, t);
           }
           if (y) ctl_store<T>(y + t, v);
-        }
+        };
+        // (the few tokens at the tile's ends first or last, as their numbers rise)
+        if (t0 + tid < min(i0, t1)) one(t0 + tid, ctl_load<T>(x + t0 + tid), w.state ? w.state[t0 + tid] : 0);
+        const T* xi = xs - wx.lo;
+        const uint16_t* si = ss - ws.lo;
+#pragma unroll 4
+        for (int t = i0 + tid; t < i1; t += kCtlThreads) one(t, ctl_load<T>(xi + t), w.state ? si[t] : 0);
+        if (i1 + tid < t1) one(i1 + tid, ctl_load<T>(x + i1 + tid), w.state ? w.state[i1 + tid] : 0);
       }
-      __syncthreads();  // the stage is read
-      if (tid == 0 && i + kCtlStages < tiles) {
-        fetch_x(i + kCtlStages);
-        fetch_rest(i + kCtlStages);
-      }
+      __syncwarp();
+      if ((tid & 31) == 0) mbar_arrive(smem_u32(&empty[i % kCtlStages]));  // the warp has read the stage
     }
     if (b1 > b0) {
+      if (y) sync();  // y's listed tokens are written last
       // (where y is x its marked tokens still hold the logits)
       for (int e = b0 + tid; e < b1; e += kCtlThreads) {
         const bool kept = e < b0 + kCtlThreads;
@@ -458,7 +475,7 @@ __global__ void __launch_bounds__(kCtlThreads) logits_control_kernel(const CtlAr
   }
   if (!a.picks) return;  // (every CTA of the cluster alike)
   best.warp();
-  if ((tid & 31) == 0) {
+  if (tid < kCtlThreads && (tid & 31) == 0) {
     best_v[tid >> 5] = best.v;
     best_i[tid >> 5] = best.i;
   }
@@ -498,7 +515,7 @@ int launch_control_t(const CtlArgs& a, int rows, int ctas, bool vec, cudaStream_
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   lc.gridDim = dim3((unsigned)ctas, (unsigned)rows);
-  lc.blockDim = dim3(kCtlThreads);
+  lc.blockDim = dim3(kCtlThreads + 32);
   lc.dynamicSmemBytes = kCtlStages * (kCtlTile * sizeof(T) + kCtlTile * 2 + kCtlTile / 8);
   SAR_TRY(ensure_smem_attr(reinterpret_cast<const void*>(fn), (int)lc.dynamicSmemBytes, "logits control: set smem attribute"));
   lc.stream = s;
@@ -555,7 +572,7 @@ int launch_control(const void* x, int64_t ldx, int rows, int vocab, int type, co
   const int64_t size = type == SAR_TYPE_F32 ? 4 : 2;
   const bool vec = aligned(x, 16) && ldx * size % 16 == 0 && aligned(y, 16) && (!y || ldy * size % 16 == 0) &&
                    (!c.state || (aligned(c.state, 16) && c.state_ld % 8 == 0));
-  // CTAs to a row: as many as stay resident at once (three to an SM), at least one
+  // CTAs to a row: as many as stay resident at once (two to an SM), at least one
   // tile of tokens each.  Beyond one wave every further CTA costs its start: 256
   // rows of 64000 with two to a row took longer than with one (see the kernel)
   int ctas = 1;
