@@ -97,19 +97,20 @@ __device__ __forceinline__ uint32_t mbar_done(uint32_t bar, uint32_t parity) {
   return ok;
 }
 
-// A ring's next full stage for the issuing warp.  The barrier is asked one slab
-// ahead, before that slab's instructions are issued, so that its answer's
-// latency (about 100 clocks of the 430 that a slab took to issue) runs under them.
+// A warp's walk over the stages of a ring.  The barrier is asked one slab ahead,
+// before the slab's instructions are issued, so that its answer's latency (about
+// 100 clocks of the 430 that a slab took to issue) runs under them.
+// flip: 1 for the warp that fills (a fresh barrier counts as passed).
 struct Ring {
-  uint32_t bars, stages, s = 0, ph = 0, peek = 0;
-  __device__ __forceinline__ bool next_full(int* err, uint32_t& stage) {
-    if (!__all_sync(0xffffffffu, peek) && !warp_wait(bars + s * 8, ph, err, SITE_FP4_MMA)) return false;
+  uint32_t bars, stages, flip, s = 0, ph = 0, peek = 0;
+  __device__ __forceinline__ bool next(int* err, int site, uint32_t& stage) {
+    if (!__all_sync(0xffffffffu, peek) && !warp_wait(bars + s * 8, ph ^ flip, err, site)) return false;
     stage = s;
     if (++s == stages) {
       s = 0;
       ph ^= 1u;
     }
-    peek = mbar_done(bars + s * 8, ph);
+    peek = mbar_done(bars + s * 8, ph ^ flip);
     return true;
   }
 };
@@ -221,16 +222,17 @@ __global__ void __launch_bounds__(192)
 
   if (warp == 0) {
     bool ok = true;
-    int i = 0, s = 0;
-    uint32_t ph = 0;
+    int i = 0;
+    Ring ring{bars + (uint32_t)p.stages * 8, (uint32_t)p.stages, 1};
     const uint8_t* sw = p.sw + (size_t)nt * p.tiles * kTileBytes;
     const uint8_t* sa = p.sa + (size_t)(mt * p.bn >> 7) * p.tiles * kTileBytes;
     for (; i < n_slabs; ++i) {
-      ok = warp_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER);
+      uint32_t s;
+      ok = ring.next(p.err, SITE_FP4_PRODUCER, s);
       if (!ok) break;
       const int kb = kb0 + i;
-      const uint32_t st = base + (uint32_t)(s * p.stage_bytes);
-      const uint32_t fb = bars + (uint32_t)s * 8;
+      const uint32_t st = base + s * (uint32_t)p.stage_bytes;
+      const uint32_t fb = bars + s * 8;
       const uint32_t tile0 = (uint32_t)kb * F::kTiles;
       const uint32_t sb = (uint32_t)min(F::kTiles, p.tiles - (int)tile0) * kTileBytes;
       const uint32_t a_at = st + kOpTile, s_at = a_at + (uint32_t)p.bn * 128;
@@ -240,10 +242,6 @@ __global__ void __launch_bounds__(192)
         tma_load_2d(a_at, &tm_a, kb * 128, mt * p.bn, fb);
         bulk_g2s(s_at, sw + (size_t)tile0 * kTileBytes, sb, fb);
         bulk_g2s(s_at + F::kScaleBytes, sa + (size_t)tile0 * kTileBytes, sb, fb);
-      }
-      if (++s == p.stages) {
-        s = 0;
-        ph ^= 1u;
       }
     }
     // after a failure: no copy is in flight when the CTA leaves
@@ -260,11 +258,11 @@ __global__ void __launch_bounds__(192)
     // the odd 64-token tiles' scales are the last two of their row block's four columns
     const uint32_t half = (uint32_t)(mt * p.bn >> 5) & 2u;
     const uint32_t idesc0 = idesc_fp4(128, p.bn, NV, 0), idesc1 = idesc_fp4(128, p.bn, NV, NV ? 0 : 2);
-    Ring ring{bars, (uint32_t)p.stages};
+    Ring ring{bars, (uint32_t)p.stages, 0};
     // one slab: nt_s scale tiles of each operand to tensor memory, n_mma MMAs
     auto slab = [&](uint32_t acc, int nt_s, int n_mma) {
       uint32_t s;
-      if (!ring.next_full(p.err, s)) return false;
+      if (!ring.next(p.err, SITE_FP4_MMA, s)) return false;
       const uint32_t off = s * stage_step;
       const uint64_t wd = wd0 + off, ad = ad0 + off, swd = swd0 + off;
       const uint32_t sf = sf0 + s * 32;
@@ -443,8 +441,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   pdl_launch_dependents();
 
   if (warp == 0) {
-    int s = 0;
-    uint32_t ph = 0;
+    Ring ring{bars + (uint32_t)p.stages * 8, (uint32_t)p.stages, 1};
     bool ok = true;
     for (int u = cid; ok && u < p.units; u += pairs) {
       const Tile w = tile_of(p, u);
@@ -454,11 +451,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int w_row = w.nt * 256 + rank * 128, a_row = w.mt * 256 + rank * (w.bn >> 1);
       const int sw_row = (w.nt * 2 + rank) * p.tiles, sa_row = w.mt * 2 * p.tiles;
       for (int kb = 0; kb < p.slabs; ++kb) {
-        ok = warp_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER);
+        uint32_t s;
+        ok = ring.next(p.err, SITE_FP4_PRODUCER, s);
         if (!ok) break;
-        const uint32_t st = base + (uint32_t)(s * p.stage_bytes);
+        const uint32_t st = base + s * (uint32_t)p.stage_bytes;
         if (elect_one()) {
-          const uint32_t fb = bars + (uint32_t)s * 8, lead = cluster_addr(fb, 0);
+          const uint32_t fb = bars + s * 8, lead = cluster_addr(fb, 0);
           if (rank == 0) mbar_expect_tx(fb, 2 * bytes);
           tma_load_2d_pair(st, &tm_w, kb * 128, w_row, lead);
           tma_load_2d_pair(st + kOpTile, ma, kb * 128, a_row, lead);
@@ -467,20 +465,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (blocks == 2)
             tma_load_2d_pair(st + 2 * kOpTile + 2 * F::kScaleBytes, &tm_sa, 0, sa_row + p.tiles + kb * F::kTiles, lead);
         }
-        if (++s == p.stages) {
-          s = 0;
-          ph ^= 1u;
-        }
       }
     }
     // the leader's MMAs have released every fill, so that neither a copy nor a
     // commit is still on its way to this CTA when it leaves (after a failure:
     // waited for once more, for a shorter time)
     for (int i = 0; i < p.stages; ++i) {
-      mbar_wait(bars + (uint32_t)(p.stages + s) * 8, ph ^ 1u, p.err, SITE_FP4_PRODUCER, ok ? kWaitLimitNs : kWaitLimitNs / 16);
-      if (++s == p.stages) {
-        s = 0;
-        ph ^= 1u;
+      mbar_wait(ring.bars + ring.s * 8, ring.ph ^ 1u, p.err, SITE_FP4_PRODUCER, ok ? kWaitLimitNs : kWaitLimitNs / 16);
+      if (++ring.s == ring.stages) {
+        ring.s = 0;
+        ring.ph ^= 1u;
       }
     }
     __syncwarp();
@@ -490,7 +484,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
       const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
       const uint64_t sd0 = scale_desc(base + 2 * kOpTile);
-      Ring ring{bars, (uint32_t)p.stages};
+      Ring ring{bars, (uint32_t)p.stages, 0};
       int n = 0;
       bool ok = true;
       for (int u = cid; ok && u < p.units; u += pairs, ++n) {
@@ -501,7 +495,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         // the tile's first MMA; its first scale tiles are copied ahead of that wait
         auto slab = [&](bool first, int nt_s, int n_mma) {
           uint32_t s;
-          if (!ring.next_full(p.err, s)) return false;
+          if (!ring.next(p.err, SITE_FP4_MMA, s)) return false;
           const uint32_t off = s * stage_step;
           const uint64_t wd = wd0 + off, ad = ad0 + off, sd = sd0 + off;
           const uint32_t sf = tmem + 256 + s * kScaleCols;
