@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       fetch_rest(i);
     }
   }
+  const bool mask_whole = (reinterpret_cast<uintptr_t>(w.mask) & 15) == 0;
   // the working threads alone
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kCtlThreads) : "memory"); };
 
@@ -368,7 +369,9 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       const T* xs = reinterpret_cast<const T*>(st);
       const uint16_t* ss = reinterpret_cast<const uint16_t*>(st + kState);
       const uint32_t* ms = reinterpret_cast<const uint32_t*>(st + kMask);
-      const Window wm = w.mask ? window(w.mask, t0 >> 5, (t1 + 31) >> 5, 4) : Window{0, 0};
+      // (a row of whole 16-byte pieces: all of a tile's words but the last piece's rest)
+      Window wm = {t0 >> 5, max(t0 >> 5, (t1 + 31) >> 5 & ~3)};
+      if (w.mask && !mask_whole) wm = window(w.mask, t0 >> 5, (t1 + 31) >> 5, 4);
       auto allowed = [&](int t) {  // the mask word of token t, bit t % 32 first
         if (!w.mask) return 0xffffffffu;
         const int q = t >> 5;
@@ -414,9 +417,20 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
             for (int k = 0; k < 4; ++k)
               if (off >> k & 1) v[k] = -INFINITY;
           }
+          // the four's largest (NaN loses); which one it is matters only where it leads
+          float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          if (raw) {
+            top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (!(raw >> k & 1)) best.take_later(v[k], t + k);
+            for (int k = 0; k < 4; ++k)
+              if (!(raw >> k & 1)) top = fmaxf(top, v[k]);
+          }
+          if (top > best.v) {
+            best.v = top;
+#pragma unroll
+            for (int k = 3; k >= 0; --k)
+              if (v[k] == top && !(raw >> k & 1)) best.i = t + k;
+          }
           if (y) {
             if constexpr (sizeof(T) == 4)
               __stcs(reinterpret_cast<float4*>(y + t), make_float4(v[0], v[1], v[2], v[3]));
@@ -456,11 +470,16 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
         if (t < s0 || t >= s1) continue;
         float sum = kept ? ev : __ldg(c.bias_values + e);
         if (twice[(t - s0) >> 5] >> (t & 31) & 1) {
+          // (no early end: a step then waits for no load but its own eighth)
           bool first = true;
-          for (int f = b0; f < e; ++f) first = first && __ldg(c.bias_tokens + f) != t;
+#pragma unroll 8
+          for (int f = b0; f < e; ++f) first &= __ldg(c.bias_tokens + f) != t;
           if (!first) continue;  // its first entry's thread adds it
-          for (int f = e + 1; f < b1; ++f)
-            if (__ldg(c.bias_tokens + f) == t) sum = __fadd_rn(sum, __ldg(c.bias_values + f));
+#pragma unroll 8
+          for (int f = e + 1; f < b1; ++f) {
+            const float more = __fadd_rn(sum, __ldg(c.bias_values + f));
+            sum = __ldg(c.bias_tokens + f) == t ? more : sum;
+          }
         }
         if (!kept) {
           ex = ctl_load<T>(x + t);
