@@ -135,8 +135,9 @@ __global__ void __launch_bounds__(256) state_append_kernel(const StateArgs a) {
 // ---- logits --------------------------------------------------------------------
 
 constexpr int kCtlThreads = 512;  // that work on tokens; one more warp fetches
-constexpr int kCtlTile = 4096;    // tokens per CTA and step
-constexpr int kCtlStages = 4;     // steps on their way
+constexpr int kCtlTile = 8192;    // tokens per CTA and step
+constexpr int kCtlStages = 2;     // steps on their way
+constexpr int kCtlLeast = 4096;   // tokens that a CTA is started for
 constexpr int kCtlSpan = 32768;   // tokens per pass over a row's biases: two bitmaps of 4 KB
 constexpr long kCtlPerSm = 2;     // CTAs that fit an SM's shared memory
 
@@ -156,14 +157,24 @@ struct RowCtl {
   const uint16_t* state = nullptr;  // null: no penalties
   const uint32_t* mask = nullptr;   // null: every token allowed
   float rep = 1.f, pres = 0.f, freq = 0.f;
+  float inv_rep = 1.f;     // correctly rounded
+  bool plain_rep = true;   // of ordinary size
 };
 
 // The penalties, in the order and with the roundings the header gives (no fused
-// multiply-add: f * count is rounded before it is taken off).
+// multiply-add: f * count is rounded before it is taken off).  x / rep is formed
+// with the row's 1 / rep and corrected by its exact remainder, which rounds it
+// correctly (Markstein 1990) while nothing on the way over- or underflows;
+// otherwise it is divided.
 __device__ __forceinline__ float penalised(float x, uint32_t s, const RowCtl& w) {
-  if (s == 0) return x;
+  if (__builtin_expect(s == 0, 1)) return x;  // (a branch: few tokens are seen)
   const uint32_t made = s & 0x7fffu;
-  x = x > 0.f ? __fdiv_rn(x, w.rep) : __fmul_rn(x, w.rep);
+  if (x > 0.f) {
+    const float q = __fmul_rn(x, w.inv_rep);
+    x = w.plain_rep && x > 1e-20f && x < 1e20f ? __fmaf_rn(-__fmaf_rn(q, w.rep, -x), w.inv_rep, q) : __fdiv_rn(x, w.rep);
+  } else {
+    x = __fmul_rn(x, w.rep);
+  }
   x = __fsub_rn(x, __fmul_rn(w.freq, (float)made));
   return made ? __fsub_rn(x, w.pres) : x;
 }
@@ -210,6 +221,32 @@ __device__ __forceinline__ Window window(const void* base, int t0, int t1, int s
   return w;
 }
 
+// Where a stage's arrays begin and end.
+struct Placed {
+  Window x, s, m;  // logits and token state by token, mask by word
+};
+
+// Masks K tokens (bit k of `on`: allowed) and takes the largest into `best`, those
+// of `raw` left out of both.  A NaN loses; which token leads is looked up only
+// where one of them does.
+template <int K, typename Token>
+__device__ __forceinline__ void lead(float (&v)[K], uint32_t on, uint32_t raw, Best& best, const Token& token) {
+  const uint32_t off = ~on & ~raw & ((1u << K) - 1);
+  if (off) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (off >> k & 1) v[k] = -INFINITY;
+  }
+  float top = v[0];
+#pragma unroll
+  for (int k = 1; k < K; ++k) top = fmaxf(top, v[k]);
+  if (top > best.v) {  // (also where a token left out has the largest)
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (!(raw >> k & 1)) best.take_later(v[k], token(k));
+  }
+}
+
 template <typename T>
 __device__ __forceinline__ float ctl_load(const T* p) {
   if constexpr (sizeof(T) == 4)
@@ -231,8 +268,8 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
 // cluster has CTAs, and one launch without a workspace does penalties, biases,
 // mask, store and pick.
 //
-// Logits, token state and mask words come in tiles of 4096 tokens by bulk copies,
-// three tiles ahead: with ordinary loads a thread's registers hold too little of
+// Logits, token state and mask words come in tiles of 8192 tokens by bulk copies,
+// two tiles at a time: with ordinary loads a thread's registers hold too little of
 // what has to be on its way (256 x 64000 fp32, pick only: 30 us with one step of
 // loads in flight at 16 warps an SM, 28 us with two).
 //
@@ -248,12 +285,16 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_kernel(const CtlArgs a) {
   extern __shared__ __align__(16) uint8_t stage_mem[];  // [stages] logits, state, mask words of a tile
   __shared__ uint32_t listed[kCtlSpan / 32], twice[kCtlSpan / 32];
+  __shared__ int list_t[kCtlThreads];  // the list's first entries
+  __shared__ float list_v[kCtlThreads];
   __shared__ __align__(8) uint64_t full[kCtlStages], empty[kCtlStages];
+  __shared__ Placed placed[kCtlStages];
   __shared__ float best_v[kCtlThreads / 32];
   __shared__ int best_i[kCtlThreads / 32];
   __shared__ Best cta_best;
   constexpr uint32_t kState = kCtlTile * sizeof(T), kMask = kState + kCtlTile * 2, kStage = kMask + kCtlTile / 8;
   const int r = blockIdx.y, rank = blockIdx.x, tid = threadIdx.x;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const bool tells = rank == 0 && tid == 0;
   if (tid == 0) {
     for (int i = 0; i < kCtlStages; ++i) {
@@ -272,28 +313,38 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
   const int tiles = hi > lo ? (hi - lo + kCtlTile - 1) / kCtlTile : 0;
   RowCtl w;
 
-  // tile i to its stage (the fetching thread): the logits, which wait for no index, and
-  // then the rest
+  // The fetching warp brings tile i to its stage: the logits, which wait for no
+  // index, and then the rest.
+  const bool fetches = warp == kCtlThreads / 32;
+  const uint32_t stage0 = __shfl_sync(0xffffffffu, smem_u32(stage_mem), 0), full0 = __shfl_sync(0xffffffffu, smem_u32(full), 0);
   auto fetch_x = [&](int i) {
     const int t0 = lo + i * kCtlTile, t1 = min(hi, t0 + kCtlTile);
-    const uint32_t st = smem_u32(stage_mem) + (uint32_t)(i % kCtlStages) * kStage, bar = smem_u32(&full[i % kCtlStages]);
+    const uint32_t st = stage0 + (uint32_t)(i % kCtlStages) * kStage, bar = full0 + (uint32_t)(i % kCtlStages) * 8;
     const Window wx = window(x, t0, t1, sizeof(T));
-    if (wx.hi > wx.lo) {
-      const uint32_t bytes = (uint32_t)((wx.hi - wx.lo) * sizeof(T));
-      asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-      bulk_g2s(st, x + wx.lo, bytes, bar);
+    const uint32_t bytes = (uint32_t)((wx.hi - wx.lo) * sizeof(T));
+    if (elect_one()) {
+      placed[i % kCtlStages].x = wx;
+      if (bytes > 0) {
+        asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+        bulk_g2s(st, x + wx.lo, bytes, bar);
+      }
     }
+    __syncwarp();
   };
   auto fetch_rest = [&](int i) {
     const int t0 = lo + i * kCtlTile, t1 = min(hi, t0 + kCtlTile);
-    const uint32_t st = smem_u32(stage_mem) + (uint32_t)(i % kCtlStages) * kStage, bar = smem_u32(&full[i % kCtlStages]);
+    const uint32_t st = stage0 + (uint32_t)(i % kCtlStages) * kStage, bar = full0 + (uint32_t)(i % kCtlStages) * 8;
     const Window ws = w.state ? window(w.state, t0, t1, 2) : Window{0, 0};
     const Window wm = w.mask ? window(w.mask, t0 >> 5, (t1 + 31) >> 5, 4) : Window{0, 0};
-    mbar_expect_tx(bar, (uint32_t)((ws.hi - ws.lo) * 2 + (wm.hi - wm.lo) * 4));
-    if (ws.hi > ws.lo) bulk_g2s(st + kState, w.state + ws.lo, (uint32_t)(ws.hi - ws.lo) * 2, bar);
-    if (wm.hi > wm.lo) bulk_g2s(st + kMask, w.mask + wm.lo, (uint32_t)(wm.hi - wm.lo) * 4, bar);
+    if (elect_one()) {
+      placed[i % kCtlStages].s = ws;
+      placed[i % kCtlStages].m = wm;
+      mbar_expect_tx(bar, (uint32_t)((ws.hi - ws.lo) * 2 + (wm.hi - wm.lo) * 4));
+      if (ws.hi > ws.lo) bulk_g2s(st + kState, w.state + ws.lo, (uint32_t)(ws.hi - ws.lo) * 2, bar);
+      if (wm.hi > wm.lo) bulk_g2s(st + kMask, w.mask + wm.lo, (uint32_t)(wm.hi - wm.lo) * 4, bar);
+    }
+    __syncwarp();
   };
-  const bool fetches = tid == kCtlThreads;
   if (fetches)
     for (int i = 0; i < min(tiles, kCtlStages); ++i) fetch_x(i);
 
@@ -313,6 +364,8 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
     if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_MASK, r);
     m = -1;
   }
+  w.inv_rep = __frcp_rn(w.rep);
+  w.plain_rep = w.rep > 1e-10f && w.rep < 1e10f;
   if (m >= 0) w.mask = c.mask + (int64_t)m * c.mask_ld;
   if (b0 < 0 || b1 < b0 || b1 > c.n_biases) {
     if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, r);
@@ -327,7 +380,6 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       fetch_rest(i);
     }
   }
-  const bool mask_whole = (reinterpret_cast<uintptr_t>(w.mask) & 15) == 0;
   // the working threads alone
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kCtlThreads) : "memory"); };
 
@@ -345,12 +397,16 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       sync();
       for (int e = b0 + tid; e < b1; e += kCtlThreads) {
         const int t = __ldg(c.bias_tokens + e);
+        if (e < b0 + kCtlThreads) {
+          ev = __ldg(c.bias_values + e);
+          list_t[tid] = t;
+          list_v[tid] = ev;
+        }
         if (t >= s0 && t < s1) {
           const uint32_t bit = 1u << (t & 31);
           if (atomicOr(&listed[(t - s0) >> 5], bit) & bit) atomicOr(&twice[(t - s0) >> 5], bit);
           if (e < b0 + kCtlThreads) {
             et = t;
-            ev = __ldg(c.bias_values + e);
             ex = ctl_load<T>(x + t);
             if (w.state) es = w.state[t];
             if (w.mask) em = __ldg(w.mask + (t >> 5)) >> (t & 31) & 1;
@@ -369,94 +425,103 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       const T* xs = reinterpret_cast<const T*>(st);
       const uint16_t* ss = reinterpret_cast<const uint16_t*>(st + kState);
       const uint32_t* ms = reinterpret_cast<const uint32_t*>(st + kMask);
-      // (a row of whole 16-byte pieces: all of a tile's words but the last piece's rest)
-      Window wm = {t0 >> 5, max(t0 >> 5, (t1 + 31) >> 5 & ~3)};
-      if (w.mask && !mask_whole) wm = window(w.mask, t0 >> 5, (t1 + 31) >> 5, 4);
-      auto allowed = [&](int t) {  // the mask word of token t, bit t % 32 first
-        if (!w.mask) return 0xffffffffu;
+      const Placed at = placed[i % kCtlStages];
+      auto mask_bits = [&](int t) {  // the mask from token t on, bit 0 first
         const int q = t >> 5;
-        return (q >= wm.lo && q < wm.hi ? ms[q - wm.lo] : __ldg(w.mask + q)) >> (t & 31);
+        return (q >= at.m.lo && q < at.m.hi ? ms[q - at.m.lo] : __ldg(w.mask + q)) >> (t & 31);
       };
-      if (VEC) {
+      auto listed_bits = [&](int t) { return listed[(t - s0) >> 5] >> (t & 31); };
+      // a lone token (at a row's or a tile's ends)
+      auto one = [&](int t) {
+        float v = ctl_load<T>(x + t);
+        if (!(b1 > b0 && (listed_bits(t) & 1))) {
+          if (w.state) v = penalised(v, w.state[t], w);
+          if (w.mask && !(mask_bits(t) & 1)) v = -INFINITY;
+          best.take_later(v, t);
+        }
+        if (y) ctl_store<T>(y + t, v);
+      };
+      // Eight tokens at once: the row's switches and the lead are looked at once for
+      // all of them (a token alone: 25 instructions each, which was the limit).
+      int done = t0;  // tokens before it are worked on
+      constexpr int kHalf = 4 * kCtlThreads;  // two groups of four to a thread
+      for (; VEC && done + 2 * kHalf <= t1; done += 2 * kHalf) {
+        const int p = done - t0 + tid * 4, t = t0 + p;
+        float v[8];
+        if constexpr (sizeof(T) == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(xs + p), g = *reinterpret_cast<const float4*>(xs + kHalf + p);
+          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w, v[4] = g.x, v[5] = g.y, v[6] = g.z, v[7] = g.w;
+        } else {
+          const uint2 f = *reinterpret_cast<const uint2*>(xs + p), g = *reinterpret_cast<const uint2*>(xs + kHalf + p);
+          v[0] = Elem<T>::lo(f.x), v[1] = Elem<T>::hi(f.x), v[2] = Elem<T>::lo(f.y), v[3] = Elem<T>::hi(f.y);
+          v[4] = Elem<T>::lo(g.x), v[5] = Elem<T>::hi(g.x), v[6] = Elem<T>::lo(g.y), v[7] = Elem<T>::hi(g.y);
+        }
+        uint32_t raw = 0, on = 0xffu;  // bit k: left to the list; allowed
+        if (b1 > b0) raw = (listed_bits(t) & 0xfu) | (listed_bits(t + kHalf) & 0xfu) << 4;
+        if (w.mask) on = (mask_bits(t) & 0xfu) | (mask_bits(t + kHalf) & 0xfu) << 4;
+        if (w.state) {
+          const uint2 f = *reinterpret_cast<const uint2*>(ss + p), g = *reinterpret_cast<const uint2*>(ss + kHalf + p);
+          if (f.x | f.y | g.x | g.y) {  // (most of a vocabulary is unseen)
+            const uint32_t s[4] = {f.x, f.y, g.x, g.y};
 #pragma unroll
-        for (int g = 0; g < kCtlTile / (4 * kCtlThreads); ++g) {
-          const int at = (g * kCtlThreads + tid) * 4, t = t0 + at;
-          if (t + 4 > t1) {
-            for (int k = 0; k < 4 && t + k < t1; ++k) {  // (the vocabulary's last tokens)
-              float v = ctl_load<T>(x + t + k);
-              if (!(b1 > b0 && (listed[(t + k - s0) >> 5] >> ((t + k) & 31) & 1))) {
-                if (w.state) v = penalised(v, w.state[t + k], w);
-                if (!(allowed(t + k) & 1)) v = -INFINITY;
-                best.take_later(v, t + k);
-              }
-              if (y) ctl_store<T>(y + t + k, v);
-            }
-            continue;
-          }
-          float v[4];
-          if constexpr (sizeof(T) == 4) {
-            const float4 p = *reinterpret_cast<const float4*>(xs + at);
-            v[0] = p.x, v[1] = p.y, v[2] = p.z, v[3] = p.w;
-          } else {
-            const uint2 p = *reinterpret_cast<const uint2*>(xs + at);
-            v[0] = Elem<T>::lo(p.x), v[1] = Elem<T>::hi(p.x), v[2] = Elem<T>::lo(p.y), v[3] = Elem<T>::hi(p.y);
-          }
-          uint2 u = make_uint2(0, 0);
-          if (w.state) u = *reinterpret_cast<const uint2*>(ss + at);
-          uint32_t raw = 0;  // bit k: left to the list
-          if (b1 > b0) raw = listed[(t - s0) >> 5] >> (t & 31) & 0xfu;
-          if (u.x | u.y) {  // (most of a vocabulary is unseen)
-            const uint32_t s[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!(raw >> k & 1)) v[k] = penalised(v[k], s[k], w);
-          }
-          const uint32_t off = ~allowed(t) & ~raw & 0xfu;
-          if (off) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (off >> k & 1) v[k] = -INFINITY;
-          }
-          // the four's largest (NaN loses); which one it is matters only where it leads
-          float top = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
-          if (raw) {
-            top = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!(raw >> k & 1)) top = fmaxf(top, v[k]);
-          }
-          if (top > best.v) {
-            best.v = top;
-#pragma unroll
-            for (int k = 3; k >= 0; --k)
-              if (v[k] == top && !(raw >> k & 1)) best.i = t + k;
-          }
-          if (y) {
-            if constexpr (sizeof(T) == 4)
-              __stcs(reinterpret_cast<float4*>(y + t), make_float4(v[0], v[1], v[2], v[3]));
-            else
-              __stcs(reinterpret_cast<uint2*>(y + t), make_uint2(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3])));
+            for (int k = 0; k < 8; ++k)
+              if (!(raw >> k & 1)) v[k] = penalised(v[k], k & 1 ? s[k / 2] >> 16 : s[k / 2] & 0xffffu, w);
           }
         }
-      } else {
-        const Window wx = window(x, t0, t1, sizeof(T));
-        const Window ws = w.state ? window(w.state, t0, t1, 2) : wx;
-        const int i0 = max(wx.lo, ws.lo), i1 = max(i0, min(wx.hi, ws.hi));  // in shared memory, both
-        auto one = [&](int t, float v, uint32_t seen) {
-          if (!(b1 > b0 && (listed[(t - s0) >> 5] >> (t & 31) & 1))) {
-            v = penalised(v, seen, w);
-            if (!(allowed(t) & 1)) v = -INFINITY;
-            best.take_later(v, t);
+        lead(v, on, raw, best, [&](int k) { return t + (k & 3) + (k >> 2) * kHalf; });
+        if (y) {
+          if constexpr (sizeof(T) == 4) {
+            __stcs(reinterpret_cast<float4*>(y + t), make_float4(v[0], v[1], v[2], v[3]));
+            __stcs(reinterpret_cast<float4*>(y + t + kHalf), make_float4(v[4], v[5], v[6], v[7]));
+          } else {
+            __stcs(reinterpret_cast<uint2*>(y + t), make_uint2(Elem<T>::pack(v[0], v[1]), Elem<T>::pack(v[2], v[3])));
+            __stcs(reinterpret_cast<uint2*>(y + t + kHalf), make_uint2(Elem<T>::pack(v[4], v[5]), Elem<T>::pack(v[6], v[7])));
           }
-          if (y) ctl_store<T>(y + t, v);
-        };
-        // (the few tokens at the tile's ends first or last, as their numbers rise)
-        if (t0 + tid < min(i0, t1)) one(t0 + tid, ctl_load<T>(x + t0 + tid), w.state ? w.state[t0 + tid] : 0);
-        const T* xi = xs - wx.lo;
-        const uint16_t* si = ss - ws.lo;
-#pragma unroll 4
-        for (int t = i0 + tid; t < i1; t += kCtlThreads) one(t, ctl_load<T>(xi + t), w.state ? si[t] : 0);
-        if (i1 + tid < t1) one(i1 + tid, ctl_load<T>(x + i1 + tid), w.state ? w.state[i1 + tid] : 0);
+        }
+      }
+      if (done < t1) {
+        constexpr int kU = 4;
+        // what is in shared memory of both arrays; the few others, at the ends, one by one
+        const int i0 = max(done, w.state ? max(at.x.lo, at.s.lo) : at.x.lo);
+        const int i1 = max(i0, w.state ? min(at.x.hi, at.s.hi) : at.x.hi);
+        if (done + tid < min(i0, t1)) one(done + tid);
+        const T* xi = xs - at.x.lo;
+        const uint16_t* si = ss - at.s.lo;
+        for (int t = i0 + tid; t < i1; t += kU * kCtlThreads) {
+          float v[kU];
+          uint32_t s[kU], raw = 0, on = (1u << kU) - 1;
+#pragma unroll
+          for (int k = 0; k < kU; ++k) {
+            const int tk = t + k * kCtlThreads;
+            const bool in = tk < i1;
+            v[k] = in ? ctl_load<T>(xi + tk) : -INFINITY;
+            s[k] = in && w.state ? si[tk] : 0;
+            if (!in) raw |= 1u << k;
+          }
+          if (b1 > b0) {
+#pragma unroll
+            for (int k = 0; k < kU; ++k)
+              if (t + k * kCtlThreads < i1) raw |= (listed_bits(t + k * kCtlThreads) & 1) << k;
+          }
+          if (w.mask) {
+            on = 0;
+#pragma unroll
+            for (int k = 0; k < kU; ++k)
+              if (t + k * kCtlThreads < i1) on |= (mask_bits(t + k * kCtlThreads) & 1) << k;
+          }
+          if (s[0] | s[1] | s[2] | s[3]) {
+#pragma unroll
+            for (int k = 0; k < kU; ++k)
+              if (!(raw >> k & 1)) v[k] = penalised(v[k], s[k], w);
+          }
+          lead(v, on, raw, best, [&](int k) { return t + k * kCtlThreads; });
+          if (y) {
+#pragma unroll
+            for (int k = 0; k < kU; ++k)
+              if (t + k * kCtlThreads < i1) ctl_store<T>(y + t + k * kCtlThreads, v[k]);
+          }
+        }
+        if (i1 + tid < t1) one(i1 + tid);
       }
       __syncwarp();
       if ((tid & 31) == 0) mbar_arrive(smem_u32(&empty[i % kCtlStages]));  // the warp has read the stage
@@ -470,16 +535,21 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
         if (t < s0 || t >= s1) continue;
         float sum = kept ? ev : __ldg(c.bias_values + e);
         if (twice[(t - s0) >> 5] >> (t & 31) & 1) {
-          // (no early end: a step then waits for no load but its own eighth)
+          // its first entry's thread adds up the token's biases (no early end: the
+          // loads of eight steps are under way together)
           bool first = true;
+          const int n = b1 - b0, head = min(n, kCtlThreads), me = e - b0;
 #pragma unroll 8
-          for (int f = b0; f < e; ++f) first &= __ldg(c.bias_tokens + f) != t;
-          if (!first) continue;  // its first entry's thread adds it
+          for (int f = 0; f < min(me, head); ++f) first &= list_t[f] != t;
+          for (int f = head; f < me; ++f) first &= __ldg(c.bias_tokens + b0 + f) != t;
+          if (!first) continue;
 #pragma unroll 8
-          for (int f = e + 1; f < b1; ++f) {
-            const float more = __fadd_rn(sum, __ldg(c.bias_values + f));
-            sum = __ldg(c.bias_tokens + f) == t ? more : sum;
+          for (int f = me + 1; f < head; ++f) {
+            const float more = __fadd_rn(sum, list_v[f]);
+            sum = list_t[f] == t ? more : sum;
           }
+          for (int f = max(head, me + 1); f < n; ++f)
+            if (__ldg(c.bias_tokens + b0 + f) == t) sum = __fadd_rn(sum, __ldg(c.bias_values + b0 + f));
         }
         if (!kept) {
           ex = ctl_load<T>(x + t);
@@ -591,12 +661,12 @@ int launch_control(const void* x, int64_t ldx, int rows, int vocab, int type, co
   const int64_t size = type == SAR_TYPE_F32 ? 4 : 2;
   const bool vec = aligned(x, 16) && ldx * size % 16 == 0 && aligned(y, 16) && (!y || ldy * size % 16 == 0) &&
                    (!c.state || (aligned(c.state, 16) && c.state_ld % 8 == 0));
-  // CTAs to a row: as many as stay resident at once (two to an SM), at least one
-  // tile of tokens each.  Beyond one wave every further CTA costs its start: 256
+  // CTAs to a row: as many as stay resident at once (two to an SM), at least 4096
+  // tokens each.  Beyond one wave every further CTA costs its start: 256
   // rows of 64000 with two to a row took longer than with one (see the kernel)
   int ctas = 1;
-  while (ctas < 8 && 2l * rows * ctas <= kCtlPerSm * num_sms() && vocab > ctas * kCtlTile) ctas *= 2;
-  a.chunk = (int)((((int64_t)vocab + ctas - 1) / ctas + kCtlTile - 1) / kCtlTile * kCtlTile);
+  while (ctas < 8 && 2l * rows * ctas <= kCtlPerSm * num_sms() && vocab > ctas * kCtlLeast) ctas *= 2;
+  a.chunk = (int)((((int64_t)vocab + ctas - 1) / ctas + kCtlLeast - 1) / kCtlLeast * kCtlLeast);
   // (65535 rows to a launch)
   for (int r0 = 0; r0 < rows; r0 += 65535) {
     const int n = std::min(rows - r0, 65535);

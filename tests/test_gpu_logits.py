@@ -442,3 +442,17 @@ def test_head_in_four_bits_to_the_pick():
     exact = hq @ wq.T
     bound = (hidden / 64 + 10) * 2.0 ** -23 * (np.abs(hq) @ np.abs(wq).T)
     assert (np.abs(c.x.numpy() - exact) <= bound).all()
+
+
+@pytest.mark.parametrize("vocab", [50, 9000, 70000])
+def test_long_bias_lists_with_repeats(vocab):
+    """Lists beyond what one look at them holds (512), most tokens more than once."""
+    c = Case(2, vocab, "f32", biases=0)
+    rng = np.random.default_rng(vocab)
+    few = rng.integers(0, vocab, 400)
+    c.lists = [[(int(few[i]), float(v)) for i, v in zip(rng.integers(0, 400, 1300), rng.standard_normal(1300).astype(np.float32))],
+               [(int(t), float(np.float32(0.1))) for t in np.repeat(few[:40], 13)]]
+    x = c.x.cuda()
+    y, picks = torch.empty_like(x), torch.empty(2, dtype=torch.int32, device="cuda")
+    sar.logits_control(x, c.controls(), out=y, tokens_out=picks)
+    c.check(y, picks)
