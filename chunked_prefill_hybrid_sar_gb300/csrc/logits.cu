@@ -39,41 +39,47 @@ struct StateArgs {
 // A resetting call: CTA (span, row) counts the row's tokens that fall into its
 // span of the vocabulary in shared memory and writes the span whole, so the row
 // is neither cleared nor read first.  Every span's CTA reads the row's list
-// (from L2 after the first).  Shared-memory atomics on whole numbers: the result
+// (from L2 after the first), eight tokens of a thread at a time.  Bound by the
+// latency of that chain of loads, not by bytes.  Shared-memory atomics on whole numbers: the result
 // does not depend on their order.
 __global__ void __launch_bounds__(kStateThreads) state_reset_kernel(const StateArgs a) {
-  __shared__ uint32_t cnt[kStateSpan];
-  __shared__ int again;
+  __shared__ __align__(16) uint32_t cnt[kStateSpan];
   pdl_wait();
   pdl_launch_dependents();
   const int r = blockIdx.y, lo = blockIdx.x * kStateSpan, hi = min(a.vocab, lo + kStateSpan);
-  const int slot = a.slots[r];
   const bool first_cta = blockIdx.x == 0;
-  if (threadIdx.x == 0) again = 0;
-  for (int i = threadIdx.x; i < kStateSpan; i += kStateThreads) cnt[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < r; i += kStateThreads)
-    if (a.slots[i] == slot) again = 1;
-  __syncthreads();
+  // (all on their way at once)
+  const int slot = a.slots[r], b = a.offsets[r], e = a.offsets[r + 1], prompt = a.prompt_lens ? a.prompt_lens[r] : 0;
+  int again = 0;
+  for (int i = threadIdx.x; i < r; i += kStateThreads) again |= a.slots[i] == slot;
+  for (int i = threadIdx.x; i < kStateSpan / 4; i += kStateThreads) reinterpret_cast<uint4*>(cnt)[i] = make_uint4(0, 0, 0, 0);
+  again = __syncthreads_or(again);
   if (slot < 0 || slot >= a.n_slots || again) {
     if (first_cta && threadIdx.x == 0) report(a.err, SAR_ERR_BOUNDS, SITE_STATE_SLOT, r);
     return;
   }
-  const int b = a.offsets[r], e = a.offsets[r + 1];
   if (b < 0 || e < b || e > a.n_tokens) {
     if (first_cta && threadIdx.x == 0) report(a.err, SAR_ERR_BOUNDS, SITE_STATE_OFFSET, r);
     return;
   }
-  const int made = b + (a.prompt_lens ? max(0, a.prompt_lens[r]) : 0);  // (past e: a prompt only)
-  for (int i = b + (int)threadIdx.x; i < e; i += kStateThreads) {
-    const int t = __ldg(a.tokens + i);
-    if (t >= lo && t < hi) {
-      if (i < made || made < b)
-        atomicOr(&cnt[t - lo], 0x80000000u);
-      else
-        atomicAdd(&cnt[t - lo], 1u);
-    } else if (first_cta && (t < 0 || t >= a.vocab)) {
-      report(a.err, SAR_ERR_BOUNDS, SITE_STATE_TOKEN, i);
+  const int n_prompt = min(max(prompt, 0), e - b);
+  constexpr int kU = 8;  // tokens of a thread on their way at once
+  for (int i0 = b + (int)threadIdx.x; i0 < e; i0 += kU * kStateThreads) {
+    int t[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) t[u] = i0 + u * kStateThreads < e ? __ldg(a.tokens + i0 + u * kStateThreads) : lo;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = i0 + u * kStateThreads;
+      if (i >= e) break;
+      if (t[u] >= lo && t[u] < hi) {
+        if (i - b < n_prompt)
+          atomicOr(&cnt[t[u] - lo], 0x80000000u);
+        else
+          atomicAdd(&cnt[t[u] - lo], 1u);
+      } else if (first_cta && (t[u] < 0 || t[u] >= a.vocab)) {
+        report(a.err, SAR_ERR_BOUNDS, SITE_STATE_TOKEN, i);
+      }
     }
   }
   __syncthreads();
