@@ -13,13 +13,15 @@ from . import _lib
 from ._lib import (SAR_EPI_F32, SAR_EPI_RESIDUAL, SAR_EPI_STORE, SAR_EPI_SWIGLU, SAR_GEMM_AUTO,
                    SAR_GEMM_PAIR_N128, SAR_GEMM_PAIR_N192,
                    SAR_GEMM_PAIR_N256, SAR_GEMM_STREAM_K, SAR_GEMM_TWO_CTAS,
-                   SAR_FP4_GEMM_AUTO, SAR_FP4_GEMM_PAIR, SAR_FP4_GEMM_SPLIT,
-                   SAR_FP4_GEMM_TOKENS64, SAR_FP4_MX, SAR_FP4_NV, SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
+                   SAR_FP4_GEMM_AUTO,
+                   SAR_FP4_GEMM_PAIR, SAR_FP4_GEMM_SPLIT, SAR_FP4_GEMM_TOKENS64, SAR_FP4_MX, SAR_FP4_NV,
+                   SAR_GEMM_M128_N128, SAR_GEMM_M128_N256, SAR_GEMM_M256_N128, SAR_GEMM_SWAP,
                    SAR_IN_HIDDEN, SAR_IN_TOKENS, SAR_STORAGE_BF16, SAR_STORAGE_F16, KERNEL_KINDS,
                    SarError, check, lib)
 
 __all__ = ["Model", "KVCache", "Scheduler", "Batch", "StepGraph", "SarError", "lib", "check", "gemm", "rmsnorm",
-           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "gemm_fp4", "LogitControls", "logits_control", "token_state_add", "SAR_FP4_NV", "SAR_FP4_MX",
+           "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "gemm_fp4", "SAR_FP4_NV",
+           "SAR_FP4_MX", "LogitControls", "logits_control", "token_state_add",
            "op_sync_status", "op_wait_check",
            "launch_count", "KERNEL_KINDS", "SAR_IN_HIDDEN", "SAR_IN_TOKENS", "SAR_STORAGE_F16",
            "SAR_STORAGE_BF16", "storage_dtype"]

@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(kThreads)
 // A unit is 16 bytes of output (8 or 4 columns), neighbouring lanes take
 // neighbouring units and a thread takes 32 bytes' worth kThreads units apart, so
 // that a warp's store covers 512 whole bytes (a thread's 16 columns as two
-// stores: 69.0 us for 20480 x 7168 bf16, every sector written in two halves).
+// stores: 69.0 us for 20480 x 7168 bf16, every sector written in two halves; so
+// 60.0 us, 6.3 TB/s).  Bound by HBM.
 template <typename Y, bool NV>
 __global__ void __launch_bounds__(kThreads)
     fp4_dequantize_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, uint32_t rows,

@@ -4,6 +4,16 @@
 // both e2m1 codes with block scales (fp4.cu).  kind::mxf4nvf4 / kind::mxf4 MMAs
 // take K = 64 codes a row from shared memory and the scales from tensor memory
 // and accumulate in fp32; the scales never meet the codes in a register.
+//
+// Two tilings put the weight rows on the MMA's M side, so that a batch of any
+// number of tokens pads to 16: a split one for few tokens, bound by the weight's
+// bytes and, below about 30 MB, by the latencies of a launch; and a pair one for
+// many, bound by the tensor pipe and by what the SMs can fetch from L2.
+// pick_variant() chooses.
+//
+// Issuing is what both had to be made fast at: a 256-code slab is 8 to 12 scale
+// copies, 4 MMAs and a commit, and issued under a test of the lane's number it
+// took 910 clocks, under elect 344, from uniform registers 207.
 #include <cuda.h>
 
 #include <algorithm>
@@ -168,10 +178,17 @@ __device__ __forceinline__ void put4(const Params& p, size_t m, int n, int ncols
 }
 
 // Split tiling: 128 weight rows on the MMA's M side x bn <= 128 tokens on its N
-// side (one tile of all tokens, or tiles of 64 or 128), the K range cut over the `splits` CTAs of a cluster.  Each CTA leaves
-// its fp32 partial tile in its own shared memory; after a cluster barrier each
-// adds up every CTA's partials (in rank order) for its share of the tokens and
-// writes them: no workspace, no atomics, one launch, the same sums each time.
+// side (one tile of all tokens, or tiles of 64 or 128), the K range cut over the
+// `splits` CTAs of a cluster.  Each CTA leaves its fp32 partial tile in its own
+// shared memory; after a cluster barrier each adds up every CTA's partials (in
+// rank order) for its share of the tokens and writes them: no workspace, no
+// atomics, one launch, the same sums each time.  Two CTAs to an SM, each with
+// half of its shared memory and tensor memory: one starts or joins while the
+// other streams.
+//
+// 16 x 28672 x 4096 (66 MB): 13.1 us, 5.1 TB/s; 16 x 28672 x 14336: 36.8 us, 6.3
+// TB/s (93% of the copy rate): what is lost is about 3.3 us of launch, first
+// loads and join.  16 x 4096 x 4096 as four ranges 5.8 us, as one 6.6.
 //   warp 0      TMA producer: 256-code slabs of both operands and their scale tiles
 //   warp 1      tensor memory; lane 0 copies scale tiles there and issues the MMAs
 //   warps 2..5  partial tile to shared memory, join, epilogue
@@ -385,6 +402,12 @@ __global__ void __launch_bounds__(192)
 // fetch (128 + 256).  Tokens lie on the MMA's N side, so the last token tile is
 // as narrow as the batch leaves it (multiples of 16), not a whole tile.
 // Persistent: the pairs walk the tiles, whole ones first.
+//
+// 8192 x 7168 x 20480: 316 us, 7.6 PFLOP/s; the power cap leaves 1560 MHz there, at
+// which the MMAs alone take 309 us.  8192 x 14336 x 4096: 143 us, 6.7 PFLOP/s: a
+// slab takes 640 clocks instead of the MMAs' 512, as its 39 KB per SM come from L2
+// at 15.6 TB/s (asking for them earlier, by prefetches into L2, made it 157 us).
+// With 128 x 128 tiles of one CTA each it took 277 us.
 //   warp 0      TMA producer (both CTAs), completion counted on the leader's barrier
 //   warp 1      tensor memory; the leader's copies the scale tiles and issues the MMAs
 //   warps 2..9  epilogue: a lane quarter (32 weight rows) x half of the tokens each,

@@ -40,8 +40,9 @@ struct StateArgs {
 // span of the vocabulary in shared memory and writes the span whole, so the row
 // is neither cleared nor read first.  Every span's CTA reads the row's list
 // (from L2 after the first), eight tokens of a thread at a time.  Bound by the
-// latency of that chain of loads, not by bytes.  Shared-memory atomics on whole numbers: the result
-// does not depend on their order.
+// latency of that chain of loads, not by bytes (64 histories of up to 8192 tokens
+// over 64000: 7.1 us; 8.6 with one token at a time).  Shared-memory atomics on
+// whole numbers: the result does not depend on their order.
 __global__ void __launch_bounds__(kStateThreads) state_reset_kernel(const StateArgs a) {
   __shared__ __align__(16) uint32_t cnt[kStateSpan];
   pdl_wait();
@@ -274,10 +275,13 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
 // cluster has CTAs, and one launch without a workspace does penalties, biases,
 // mask, store and pick.
 //
-// Logits, token state and mask words come in tiles of 8192 tokens by bulk copies,
-// two tiles at a time: with ordinary loads a thread's registers hold too little of
-// what has to be on its way (256 x 64000 fp32, pick only: 30 us with one step of
-// loads in flight at 16 warps an SM, 28 us with two).
+// Logits, token state and mask words come in tiles of 8192 tokens by bulk copies
+// of a warp of its own, two tiles at a time: with ordinary loads a thread's
+// registers hold too little of what has to be on its way (256 x 64000 fp32, pick
+// only: 30 us, and 16.4 so).  With everything on and the logits written that size
+// takes 36 us, 4.5 TB/s: the 16 warps' instructions (about 12 a token) and 256
+// rows' CTAs on 304 places are what it waits for, not HBM alone.  One row of
+// 32000, eight CTAs: 6.1 us, the chain of one read, a cluster's join and a write.
 //
 // Biases come as a list per row.  Their tokens are marked in a bitmap of the
 // stretch; the dense pass leaves marked tokens as they are, and the list's
