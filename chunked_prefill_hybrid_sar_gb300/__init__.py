@@ -402,7 +402,7 @@ def _launch_stream(what: str, stream, *tensors) -> int | None:
     import torch
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.get_device() == dev):
+        if t is not None and t.get_device() != dev:  # (-1: not on a CUDA device)
             raise ValueError(f"{what}: tensors must be on the current CUDA device")
     # (the stream's address alone: a torch.cuda.Stream object takes 3 us to make)
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
@@ -411,12 +411,15 @@ def _launch_stream(what: str, stream, *tensors) -> int | None:
 def _rows(what: str, t):
     """(rows, columns, row stride, SAR_TYPE_*) of a two-dimensional tensor with
     adjacent columns; a single row's stride, which means nothing, is its length."""
-    kind = _row_types().get(t.dtype)
+    kind = _ROW_TYPES.get(t.dtype) if _ROW_TYPES else _row_types().get(t.dtype)
     if kind is None:
         raise ValueError(f"{what}: rows must be float16, bfloat16 or float32")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{what}: rows must be two-dimensional")
-    rows, cols = t.shape
+    rows, cols = shape
+    if t.is_contiguous():
+        return rows, cols, cols, kind
     ld, step = t.stride()
     if cols > 1 and step != 1:
         raise ValueError(f"{what}: a row's columns must be adjacent")
@@ -432,13 +435,14 @@ def fp4_scale_bytes(rows: int, cols: int, format: int = SAR_FP4_NV) -> int:
 
 def _fp4_check(what: str, codes, scales, rows: int, cols: int, format: int) -> None:
     import torch
-    if codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
+    byte = torch.uint8
+    if codes.dtype is not byte or scales.dtype is not byte:
         raise ValueError(f"{what}: codes and scales must be uint8")
-    if codes.dim() != 2 or codes.shape[0] != rows or 2 * codes.shape[1] != cols or not codes.is_contiguous():
+    if codes.shape != (rows, cols >> 1) or cols & 1 or not codes.is_contiguous():
         raise ValueError(f"{what}: codes must be contiguous, two to a byte: {rows} rows of {cols}")
     # fp4_scale_bytes, for the formats and columns that the library takes
     width = 64 if format == SAR_FP4_NV else 128
-    if not scales.is_contiguous() or scales.numel() < (rows + 127) // 128 * ((cols + width - 1) // width) * 512:
+    if scales.numel() < (rows + 127) // 128 * ((cols + width - 1) // width) * 512 or not scales.is_contiguous():
         raise ValueError(f"{what}: scales must be contiguous and as long as fp4_scale_bytes says")
 
 

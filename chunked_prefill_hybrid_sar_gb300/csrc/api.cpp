@@ -29,6 +29,14 @@ int cuda_error(cudaError_t e, const char* what) {
   return set_error(code, std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+int entry_failed(const char* what) noexcept {
+  try {
+    return set_error(SAR_ERR_OOM, std::string(what) + ": out of host memory");
+  } catch (...) {
+    return SAR_ERR_OOM;
+  }
+}
+
 void count_launches(int64_t n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 bool pdl_enabled() {

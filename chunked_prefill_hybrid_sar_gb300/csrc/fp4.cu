@@ -308,27 +308,27 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // size and work items per row.
 int check_rows(const char* what, bool quantising, const void* x, int64_t ld, int rows, int cols, int type, int format,
                float scale, const void* codes, const void* scales, uint32_t* blocks, Divisor* div) {
-  const std::string w(what);
-  if (rows < 0 || cols <= 0) return set_error(SAR_ERR_INVALID_ARG, w + ": bad shape");
-  if (!good_format(format)) return set_error(SAR_ERR_INVALID_ARG, w + ": bad format");
-  if (!good_type(type)) return set_error(SAR_ERR_INVALID_ARG, w + ": bad element type");
-  if (cols % 32) return set_error(SAR_ERR_UNSUPPORTED, w + ": columns must be a multiple of 32");
-  if (ld < cols) return set_error(SAR_ERR_INVALID_ARG, w + ": row stride below the row's length");
+  auto refuse = [what](int code, const char* why) { return set_error(code, std::string(what) + why); };
+  if (rows < 0 || cols <= 0) return refuse(SAR_ERR_INVALID_ARG, ": bad shape");
+  if (!good_format(format)) return refuse(SAR_ERR_INVALID_ARG, ": bad format");
+  if (!good_type(type)) return refuse(SAR_ERR_INVALID_ARG, ": bad element type");
+  if (cols % 32) return refuse(SAR_ERR_UNSUPPORTED, ": columns must be a multiple of 32");
+  if (ld < cols) return refuse(SAR_ERR_INVALID_ARG, ": row stride below the row's length");
   if (!(scale > 0.f) || !std::isfinite(scale) || !std::isfinite(1.f / scale))
-    return set_error(SAR_ERR_INVALID_ARG, w + ": the tensor scale must be positive and finite, as its inverse");
+    return refuse(SAR_ERR_INVALID_ARG, ": the tensor scale must be positive and finite, as its inverse");
   *blocks = 0;
   if (rows == 0) return SAR_OK;
-  if (!x || !codes || !scales) return set_error(SAR_ERR_INVALID_ARG, w + ": null pointer");
+  if (!x || !codes || !scales) return refuse(SAR_ERR_INVALID_ARG, ": null pointer");
   if (reinterpret_cast<uintptr_t>(x) & (type == SAR_TYPE_F32 ? 3 : 1))
-    return set_error(SAR_ERR_INVALID_ARG, w + ": rows not aligned to their element");
+    return refuse(SAR_ERR_INVALID_ARG, ": rows not aligned to their element");
   if (!aligned16(codes) || !aligned16(scales))
-    return set_error(SAR_ERR_INVALID_ARG, w + ": codes and scales must be 16-byte aligned");
+    return refuse(SAR_ERR_INVALID_ARG, ": codes and scales must be 16-byte aligned");
   // work items: 16 columns of a row padded to whole scale tiles (quantising), 16
   // bytes of output (dequantising)
   const uint64_t per_row = quantising ? (uint64_t)fp4_tiles(cols, format) * (format == SAR_FP4_NV ? 4 : 8)
                                       : (uint64_t)cols * (type == SAR_TYPE_F32 ? 4 : 2) / 16;
   const uint64_t items = rows * per_row;
-  if (items >= 1ull << 31) return set_error(SAR_ERR_UNSUPPORTED, w + ": more than 2^31 work items");
+  if (items >= 1ull << 31) return refuse(SAR_ERR_UNSUPPORTED, ": more than 2^31 work items");
   const int per_block = kThreads * (quantising ? 1 : kDequantEach);
   *blocks = (uint32_t)((items + per_block - 1) / per_block);
   if (quantising) *blocks = std::min<uint32_t>(*blocks, (uint32_t)num_sms() * kQuantPerSm);
@@ -372,16 +372,18 @@ using sar::set_error;
 
 extern "C" {
 
-int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* out) {
+int sar_op_fp4_scale_bytes(int32_t rows, int32_t cols, int32_t format, int64_t* out) try {
   if (!out || rows < 0 || cols <= 0 || !sar::good_format(format))
     return set_error(SAR_ERR_INVALID_ARG, "fp4_scale_bytes: bad argument");
   if (cols % 32) return set_error(SAR_ERR_UNSUPPORTED, "fp4_scale_bytes: columns must be a multiple of 32");
   *out = ((int64_t)rows + 127) / 128 * sar::fp4_tiles(cols, format) * 512;
   return SAR_OK;
+} catch (...) {
+  return sar::entry_failed("fp4_scale_bytes");
 }
 
 int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, int32_t type, int32_t format,
-                        float tensor_scale, void* codes, void* scales, void* stream) {
+                        float tensor_scale, void* codes, void* scales, void* stream) try {
   uint32_t blocks = 0;
   sar::Divisor div;
   SAR_TRY(sar::check_rows("fp4_quantize", true, x, ldx, rows, cols, type, format, tensor_scale, codes, scales, &blocks,
@@ -393,10 +395,12 @@ int sar_op_fp4_quantize(const void* x, int64_t ldx, int32_t rows, int32_t cols, 
   if (type == SAR_TYPE_BF16)
     return sar::quantize<__nv_bfloat16>(x, ldx, rows, cols, format, inv, codes, scales, blocks, div, s);
   return sar::quantize<__half>(x, ldx, rows, cols, format, inv, codes, scales, blocks, div, s);
+} catch (...) {
+  return sar::entry_failed("fp4_quantize");
 }
 
 int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, int32_t cols, int32_t format,
-                          float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream) {
+                          float tensor_scale, void* y, int64_t ldy, int32_t type, void* stream) try {
   uint32_t blocks = 0;
   sar::Divisor div;
   SAR_TRY(sar::check_rows("fp4_dequantize", false, y, ldy, rows, cols, type, format, tensor_scale, codes, scales, &blocks,
@@ -408,6 +412,8 @@ int sar_op_fp4_dequantize(const void* codes, const void* scales, int32_t rows, i
   if (type == SAR_TYPE_BF16)
     return sar::dequantize<__nv_bfloat16>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, div, s);
   return sar::dequantize<__half>(codes, scales, rows, cols, format, tensor_scale, y, ldy, blocks, div, s);
+} catch (...) {
+  return sar::entry_failed("fp4_dequantize");
 }
 
 }  // extern "C"

@@ -903,7 +903,7 @@ extern "C" {
 
 int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const void* w_scales, void* c,
                     const void* residual, int32_t M, int32_t N, int32_t K, float alpha, int32_t epilogue, int32_t format,
-                    int32_t variant, int32_t storage, void* stream) {
+                    int32_t variant, int32_t storage, void* stream) try {
   if (M < 0 || N < 1 || K < 1) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad shape");
   if (epilogue < SAR_EPI_STORE || epilogue > SAR_EPI_F32) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad epilogue");
   if (format != SAR_FP4_NV && format != SAR_FP4_MX) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad format");
@@ -940,6 +940,8 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
   if (variant == SAR_FP4_GEMM_AUTO) variant = sar::pick_variant(p);
   const sar::Call g = {a, w, epilogue, format, storage, variant, static_cast<cudaStream_t>(stream)};
   return (variant & 0xff) == SAR_FP4_GEMM_PAIR ? sar::launch_pair(g, p) : sar::launch_split(g, p);
+} catch (...) {
+  return sar::entry_failed("gemm_fp4");
 }
 
 }  // extern "C"

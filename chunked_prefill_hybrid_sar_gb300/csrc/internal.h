@@ -24,6 +24,9 @@ namespace sar {
 // ---- errors / bookkeeping (api.cpp) ----------------------------------------
 int set_error(int code, const std::string& msg);
 int cuda_error(cudaError_t e, const char* what);
+// For an entry's catch-all: no C++ exception (a failed host allocation) crosses
+// the C boundary.
+int entry_failed(const char* what) noexcept;
 void count_launches(int64_t n);
 int num_sms();
 // Raises kernel `fn`'s dynamic shared-memory limit to `bytes` on the current

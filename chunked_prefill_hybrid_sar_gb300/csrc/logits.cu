@@ -713,7 +713,7 @@ extern "C" {
 
 int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vocab, const int32_t* slots, int32_t n,
                         const int32_t* offsets, const int32_t* tokens, int32_t n_tokens, const int32_t* prompt_lens,
-                        int32_t reset, void* stream) {
+                        int32_t reset, void* stream) try {
   if (n_slots < 1 || vocab < 1 || ld < vocab || n < 0 || n_tokens < 0)
     return set_error(SAR_ERR_INVALID_ARG, "token_state_add: bad shape");
   if (n == 0 || (n_tokens == 0 && !reset)) return SAR_OK;
@@ -736,10 +736,12 @@ int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vo
   if (e != cudaSuccess) return sar::cuda_error(e, "token state launch");
   sar::count_launches(1);
   return SAR_OK;
+} catch (...) {
+  return sar::entry_failed("token_state_add");
 }
 
 int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t vocab, int32_t type,
-                       const sar_logit_controls* controls, void* out, int64_t ld_out, int32_t* tokens_out, void* stream) {
+                       const sar_logit_controls* controls, void* out, int64_t ld_out, int32_t* tokens_out, void* stream) try {
   if (!controls || rows < 0 || vocab < 1 || ld < vocab || (out && ld_out < vocab))
     return set_error(SAR_ERR_INVALID_ARG, "logits control: bad shape");
   if (type != SAR_TYPE_F16 && type != SAR_TYPE_BF16 && type != SAR_TYPE_F32)
@@ -756,6 +758,8 @@ int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t voc
     return set_error(SAR_ERR_INVALID_ARG, "logits control: buffer not aligned to its element");
   return sar::launch_control(logits, ld, rows, vocab, type, *controls, out, ld_out, tokens_out,
                              static_cast<cudaStream_t>(stream));
+} catch (...) {
+  return sar::entry_failed("logits_control");
 }
 
 }  // extern "C"
