@@ -60,6 +60,7 @@ struct Params {
   float alpha;
   // pair tiling
   int m_full, n_tiles, last_bn, group, units;
+  int pair_ranges;  // K ranges of a tile, a pair each (the pairs of a cluster)
   int tma_out;    // c is written (or, where it is r, added to) through a tensor map
   int vec;        // rows of c (and r) can be written four columns at a time
   int* err;
@@ -173,6 +174,58 @@ __device__ __forceinline__ void put4(const Params& p, size_t m, int n, int ncols
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (n + i < ncols) c[i] = Elem<T>::from(x[i]);
+    }
+  }
+}
+
+// Adds up a tile's partials, [token][128 weight rows] of fp32 at `part` in the
+// shared memory of `ranges` CTAs (range k in the cluster's CTA k * stride +
+// offset), for this CTA's share of the tokens (every ranges-th from `range` on),
+// in the ranges' order, and writes them through the epilogue.  kThreads threads, a
+// quarter warp's worth of columns each; block: which 128 weight rows.
+template <typename T, int EPI, int kThreads>
+__device__ __forceinline__ void join(const Params& p, uint32_t part, int ranges, int range, int stride, int offset, int t,
+                                     int block, int m0, int rows) {
+  constexpr int kLanes = EPI == SAR_EPI_SWIGLU ? 16 : 32;  // four columns each
+  constexpr int kU = 8;  // tokens read at a time, so that the latency is paid once for all of them
+  const int n4 = (t % kLanes) * 4;
+  const int step = (kThreads / kLanes) * ranges;
+  auto joined = [&](int tok0, int n, float4 (&x)[kU]) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < ranges; ++s) {
+      const uint32_t at = cluster_addr(part, (uint32_t)(s * stride + offset)) + (uint32_t)n * 4;
+      float4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        v[u] = tok0 + u * step < rows ? ld_cluster_f4(at + (uint32_t)(tok0 + u * step) * 512) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        x[u].x += v[u].x;
+        x[u].y += v[u].y;
+        x[u].z += v[u].z;
+        x[u].w += v[u].w;
+      }
+    }
+  };
+  for (int tok0 = (t / kLanes) * ranges + range; tok0 < rows; tok0 += kU * step) {
+    float4 x[kU], y[kU];
+    joined(tok0, n4, x);
+    if constexpr (EPI == SAR_EPI_SWIGLU) joined(tok0, 64 + n4, y);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int tok = tok0 + u * step;
+      if (tok >= rows) continue;
+      float o[4] = {x[u].x * p.alpha, x[u].y * p.alpha, x[u].z * p.alpha, x[u].w * p.alpha};
+      if constexpr (EPI == SAR_EPI_SWIGLU) {
+        o[0] = silu(o[0]) * (y[u].x * p.alpha);
+        o[1] = silu(o[1]) * (y[u].y * p.alpha);
+        o[2] = silu(o[2]) * (y[u].z * p.alpha);
+        o[3] = silu(o[3]) * (y[u].w * p.alpha);
+        if (block * 64 + n4 < p.N >> 1) put4<T, EPI>(p, (size_t)(m0 + tok), block * 64 + n4, p.N >> 1, o);
+      } else if (block * 128 + n4 < p.N) {
+        put4<T, EPI>(p, (size_t)(m0 + tok), block * 128 + n4, p.N, o);
+      }
     }
   }
 }
@@ -335,55 +388,8 @@ __global__ void __launch_bounds__(192)
   else
     __syncthreads();
 
-  if (warp >= 2) {
-    const int t = threadIdx.x - 64;
-    constexpr int kLanes = EPI == SAR_EPI_SWIGLU ? 16 : 32;  // four columns each
-    const int n4 = (t % kLanes) * 4;
-    const int m0 = mt * p.bn, rows = min(p.bn, p.M - m0);
-    const uint32_t part = smem_u32(smem);
-    // eight tokens' partials are read at a time, rank by rank, so that their
-    // latency is paid once for all of them
-    constexpr int kU = 8;
-    const int step = (128 / kLanes) * p.splits;
-    auto joined = [&](int tok0, int n, float4 (&x)[kU]) {
-#pragma unroll
-      for (int u = 0; u < kU; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int s = 0; s < p.splits; ++s) {
-        const uint32_t at = cluster_addr(part, (uint32_t)s) + (uint32_t)n * 4;
-        float4 v[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u)
-          v[u] = tok0 + u * step < rows ? ld_cluster_f4(at + (uint32_t)(tok0 + u * step) * 512) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          x[u].x += v[u].x;
-          x[u].y += v[u].y;
-          x[u].z += v[u].z;
-          x[u].w += v[u].w;
-        }
-      }
-    };
-    for (int tok0 = (t / kLanes) * p.splits + rank; tok0 < rows; tok0 += kU * step) {
-      float4 x[kU], y[kU];
-      joined(tok0, n4, x);
-      if constexpr (EPI == SAR_EPI_SWIGLU) joined(tok0, 64 + n4, y);
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int tok = tok0 + u * step;
-        if (tok >= rows) continue;
-        float o[4] = {x[u].x * p.alpha, x[u].y * p.alpha, x[u].z * p.alpha, x[u].w * p.alpha};
-        if constexpr (EPI == SAR_EPI_SWIGLU) {
-          o[0] = silu(o[0]) * (y[u].x * p.alpha);
-          o[1] = silu(o[1]) * (y[u].y * p.alpha);
-          o[2] = silu(o[2]) * (y[u].z * p.alpha);
-          o[3] = silu(o[3]) * (y[u].w * p.alpha);
-          put4<T, EPI>(p, (size_t)(m0 + tok), nt * 64 + n4, p.N >> 1, o);
-        } else if (nt * 128 + n4 < p.N) {
-          put4<T, EPI>(p, (size_t)(m0 + tok), nt * 128 + n4, p.N, o);
-        }
-      }
-    }
-  }
+  if (warp >= 2)
+    join<T, EPI, 128>(p, smem_u32(smem), p.splits, rank, 1, 0, threadIdx.x - 64, nt, mt * p.bn, min(p.bn, p.M - mt * p.bn));
   __syncwarp();
   if (p.splits > 1)
     cluster_sync();  // the partials are read by the whole cluster
@@ -402,6 +408,11 @@ __global__ void __launch_bounds__(192)
 // fetch (128 + 256).  Tokens lie on the MMA's N side, so the last token tile is
 // as narrow as the batch leaves it (multiples of 16), not a whole tile.
 // Persistent: the pairs walk the tiles, whole ones first.
+//
+// Where the tiles are too few for the SMs, a cluster of two pairs shares one: each
+// pair takes a K range, and the partial tiles are joined as in the split tiling
+// (512 x 4096 x 14336: 16.6 us, against 21.8 with one range; four ranges, in
+// clusters of 8 whole SMs of which few fit at a time, took 40.7).
 //
 // 8192 x 7168 x 20480: 316 us, 7.6 PFLOP/s; the power cap leaves 1560 MHz there, at
 // which the MMAs alone take 309 us.  8192 x 14336 x 4096: 143 us, 6.7 PFLOP/s: a
@@ -452,8 +463,11 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t bars = __shfl_sync(0xffffffffu, smem_u32(full_bar), 0);
   const uint32_t accb = __shfl_sync(0xffffffffu, smem_u32(acc_bar), 0);
   const uint32_t stage_end = base + (uint32_t)(p.stages * p.stage_bytes + kBarBytes);  // the epilogue's staging
-  const int rank = (int)cluster_ctarank();
-  const int cid = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  // this CTA's place in its pair, the pair's K range, the pair's leader
+  const int crank = (int)cluster_ctarank(), rank = crank & 1, kr = crank >> 1;
+  const uint32_t leader = (uint32_t)crank & ~1u;
+  const int cid = blockIdx.x / (2 * p.pair_ranges), pairs = gridDim.x / (2 * p.pair_ranges);
+  const int kb0 = kr * p.slabs_per_split, kb1 = min(p.slabs, kb0 + p.slabs_per_split);
   if (warp == 0 && elect_one()) {
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_a);
@@ -473,13 +487,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const void* ma = w.bn == 256 ? &tm_a : &tm_last;
       const int w_row = w.nt * 256 + rank * 128, a_row = w.mt * 256 + rank * (w.bn >> 1);
       const int sw_row = (w.nt * 2 + rank) * p.tiles, sa_row = w.mt * 2 * p.tiles;
-      for (int kb = 0; kb < p.slabs; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         uint32_t s;
         ok = ring.next(p.err, SITE_FP4_PRODUCER, s);
         if (!ok) break;
         const uint32_t st = base + s * (uint32_t)p.stage_bytes;
         if (elect_one()) {
-          const uint32_t fb = bars + s * 8, lead = cluster_addr(fb, 0);
+          const uint32_t fb = bars + s * 8, lead = cluster_addr(fb, leader);
           if (rank == 0) mbar_expect_tx(fb, 2 * bytes);
           tma_load_2d_pair(st, &tm_w, kb * 128, w_row, lead);
           tma_load_2d_pair(st + kOpTile, ma, kb * 128, a_row, lead);
@@ -507,6 +521,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const uint32_t stage_step = (uint32_t)p.stage_bytes >> 4;
       const uint64_t wd0 = sw128_desc(base), ad0 = sw128_desc(base + kOpTile);
       const uint64_t sd0 = scale_desc(base + 2 * kOpTile);
+      const uint16_t both = (uint16_t)(3u << leader);
       Ring ring{bars, (uint32_t)p.stages, 0};
       int n = 0;
       bool ok = true;
@@ -552,16 +567,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                                   sf + 4 * t, sf + 4 * F::kTiles + 8 * t, (j != 0 || !first) ? 1u : 0u);
               }
             }
-            mma_commit_pair(bars + (p.stages + s) * 8);
+            mma_commit_pair(bars + (p.stages + s) * 8, both);
           }
           return true;
         };
-        const int whole = p.K / kSlab;
-        if (whole > 0) ok = slab(true, F::kTiles, 4);
-        for (int i = 1; ok && i < whole; ++i) ok = slab(false, F::kTiles, 4);
-        if (ok && whole < p.slabs)
-          ok = slab(whole == 0, p.tiles - whole * F::kTiles, (p.K - whole * kSlab + 63) >> 6);
-        if (ok && elect_one()) mma_commit_pair(accb);
+        const int whole = min(kb1, p.K / kSlab);
+        if (whole > kb0) ok = slab(true, F::kTiles, 4);
+        for (int i = kb0 + 1; ok && i < whole; ++i) ok = slab(false, F::kTiles, 4);
+        if (ok && whole < kb1)
+          ok = slab(whole == kb0, p.tiles - whole * F::kTiles, (p.K - whole * kSlab + 63) >> 6);
+        if (ok && elect_one()) mma_commit_pair(accb, both);
         __syncwarp();
       }
     }
@@ -585,7 +600,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           if (n0 < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.r + (size_t)(m0 + e) * p.N + n0));
       }
       if (alive) alive = warp_wait(accb, (uint32_t)n & 1u, p.err, SITE_FP4_EPILOGUE);
-      if (!alive && EPI != SAR_EPI_SWIGLU) break;
+      if (!alive && EPI != SAR_EPI_SWIGLU && p.pair_ranges == 1) break;
       tc_fence_after();
       uint32_t v[128];
       const uint32_t t0 = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(h * 128);
@@ -594,8 +609,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tmem_wait_ld();
       tc_fence_before();
       __syncwarp();
-      if (alive && elect_one()) mbar_arrive_cluster_relaxed(cluster_addr(accb + 8, 0));
+      if (alive && elect_one()) mbar_arrive_cluster_relaxed(cluster_addr(accb + 8, leader));
       const int rows = alive ? min(128, p.M - m0) : 0;  // (may be negative: the half is empty)
+      if (p.pair_ranges > 1) {
+        // One tile to a cluster: this CTA's MMAs are done, its stages are free for
+        // the partial tile; every warp of the cluster passes this barrier once
+#pragma unroll
+        for (int e = 0; e < 128; ++e) st_shared(base + (uint32_t)((h * 128 + e) * 512 + (q * 32 + lane) * 4), v[e]);
+        __syncwarp();
+        cluster_sync();
+        if (alive)
+          join<T, EPI, 256>(p, base, p.pair_ranges, kr, 2, rank, threadIdx.x - 64, w.nt * 2 + rank, w.mt * 256,
+                            min(256, p.M - w.mt * 256));
+        break;
+      }
       // One box of `cnt` tokens x 32 columns leaves from the warp's staging
       // (rows behind M and columns behind N are clipped); the other box of the two
       // may still be read meanwhile.
@@ -694,6 +721,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     if (lane == 0 && boxes > 0) bulk_wait_all();
     __syncwarp();
   }
+  if (warp < 2 && p.pair_ranges > 1) cluster_sync();  // (the epilogue's)
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // neither CTA of a pair leaves while the other may still address it
@@ -723,18 +751,21 @@ struct Call {
 
 // ---- choice of the tiling ----------------------------------------------------
 //
-// Microseconds of a launch, from its tiles: fitted to 1400 timed runs (1 to 2048
+// Microseconds of a launch, from its tiles: fitted to 2300 timed runs (1 to 2048
 // tokens, N 1024 to 28672, K 1024 to 14336, every tiling and number of K ranges).
-// Taking the smallest estimate costs 1.2% over the fastest measured tiling on
-// average and 16% at worst.  What it weighs: few tokens want many CTAs on the
+// Taking the smallest estimate costs 1.3% over the fastest measured tiling on
+// average and 15% at worst.  What it weighs: few tokens want many CTAs on the
 // weight (K ranges, until their join costs more than the shorter ranges save: 16
 // x 4096 x 14336 15.8 us as one range, 10.1 as four, 12.4 as eight); a middling
 // number wants 64-token tiles (128 x 4096 x 4096: 7.5 us, against 9.2 with 128);
-// many want the pair tiling (2048 x 28672 x 4096: 85 us, against 147).
-constexpr double kSlabOne = 0.276, kSlabOneToken = 0.0006;  // a slab of a CTA alone on its SM; per token of the tile
-constexpr double kSlabTwo = 0.448, kSlabTwoToken = 0.0001;  // of a CTA that shares its SM
-constexpr double kSplitBase = -1.7, kSplitWave = 3.8, kSplitToken = 0.025, kSplitJoin = 0.55;
-constexpr double kPairSlab = 0.338, kPairSlabMin = 0.27, kPairBase = 2.5, kPairTile = 2.1;
+// many want the pair tiling (2048 x 28672 x 4096: 74 us, against 147), with two K
+// ranges where its tiles would leave half of the SMs idle (512 x 4096 x 14336: 16.6
+// us, against 21.8).
+constexpr double kSlabOne = 0.28, kSlabOneToken = 0.0006;  // a slab of a CTA alone on its SM; per token of the tile
+constexpr double kSlabTwo = 0.44, kSlabTwoToken = 0.0003;  // of a CTA that shares its SM
+constexpr double kSplitBase = -1.65, kSplitWave = 3.77, kSplitToken = 0.025, kSplitJoin = 0.54;
+constexpr double kPairSlab = 0.338, kPairSlabMin = 0.27, kPairBase = 2.6, kPairTile = 2.1;
+constexpr double kPairsSlab = 0.28, kPairsBase = 0.3, kPairsTile = 7.0;  // two K ranges to a tile
 
 double split_us(const Params& p, int width, int splits, int sms) {
   const int m_tiles = (p.M + width - 1) / width, per = (p.slabs + splits - 1) / splits;
@@ -754,10 +785,21 @@ double pair_us(const Params& p, int sms) {
          narrow * (p.slabs * std::max(kPairSlabMin, kPairSlab * last / 256) + kPairTile);
 }
 
+// Two K ranges: a cluster of four whole SMs to a tile (a GPC's SMs do not divide
+// into fours: about two clusters fewer than a quarter of the SMs fit).
+double pairs_us(const Params& p, int sms) {
+  const long units = (long)((p.N + 255) / 256) * ((p.M + 255) / 256), fit = std::max(1, sms / 4 - 2);
+  return kPairsBase + (units + fit - 1) / fit * ((p.slabs + 1) / 2 * kPairsSlab + kPairsTile);
+}
+
 int pick_variant(const Params& p) {
   const int sms = num_sms();
   int best = SAR_FP4_GEMM_PAIR;
   double us = pair_us(p, sms);
+  if (p.slabs > 1 && pairs_us(p, sms) < us) {
+    us = pairs_us(p, sms);
+    best = SAR_FP4_GEMM_PAIR | 2 << 8;
+  }
   for (int width : {128, 64}) {
     if (width == 64 && p.M <= 64) break;  // one tile either way
     for (int splits : {1, 2, 3, 4, 6, 8}) {
@@ -843,6 +885,13 @@ int launch_pair(const Call& g, Params p) {
   const long units = (long)p.n_tiles * (p.m_full + (p.last_bn ? 1 : 0));
   if (units > (1l << 30)) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many tiles");
   p.units = (int)units;
+  int ranges = std::max(1, g.variant >> 8 & 0xf);
+  if (ranges > 2) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: the pair tiling takes one or two K ranges");
+  if (ranges > p.slabs) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many K ranges");
+  p.slabs_per_split = (p.slabs + ranges - 1) / ranges;
+  if ((p.slabs + p.slabs_per_split - 1) / p.slabs_per_split != ranges)
+    return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: the K ranges leave one empty");
+  p.pair_ranges = ranges;
   const int sb = nv ? Fmt<true>::kScaleBytes : Fmt<false>::kScaleBytes;
   p.stage_bytes = 2 * kOpTile + 3 * sb;  // (a multiple of 1024)
   const int extra = kBarBytes + 1024 + 8 * kWarpOut;
@@ -876,17 +925,21 @@ int launch_pair(const Call& g, Params p) {
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = 2 * (unsigned)ranges;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
-  cudaLaunchConfig_t qc = lc;  // the cluster shape alone
-  qc.gridDim = dim3(128);
-  qc.attrs = &attr[1];
-  qc.numAttrs = 1;
-  int pairs = 0;
-  SAR_TRY(max_active_clusters(fn, qc, 2, &pairs, "gemm_fp4: cluster occupancy"));
+  int clusters = p.units;  // (several ranges: one tile to a cluster)
+  if (ranges == 1) {
+    cudaLaunchConfig_t qc = lc;  // the cluster shape alone
+    qc.gridDim = dim3(128);
+    qc.attrs = &attr[1];
+    qc.numAttrs = 1;
+    int pairs = 0;
+    SAR_TRY(max_active_clusters(fn, qc, 2, &pairs, "gemm_fp4: cluster occupancy"));
+    clusters = std::min(pairs, p.units);
+  }
   lc.numAttrs = 2;
-  lc.gridDim = dim3(2u * (unsigned)std::min(pairs, p.units));
+  lc.gridDim = dim3(2u * (unsigned)(ranges * clusters));
   const cudaError_t e = cudaLaunchKernelExC(&lc, fn, args);
   if (e != cudaSuccess) return cuda_error(e, "gemm_fp4 launch");
   count_launches(1);
@@ -909,7 +962,8 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
   if (format != SAR_FP4_NV && format != SAR_FP4_MX) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad format");
   if (storage != SAR_STORAGE_F16 && storage != SAR_STORAGE_BF16) return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: bad storage");
   if (variant < 0 || (variant & 0xff) > SAR_FP4_GEMM_PAIR || variant > 0x1fff ||
-      (variant > 0xff && (variant & 0xff) != SAR_FP4_GEMM_SPLIT))
+      ((variant & 0xf00) && (variant & 0xff) == SAR_FP4_GEMM_AUTO) ||
+      ((variant & SAR_FP4_GEMM_TOKENS64) && (variant & 0xff) != SAR_FP4_GEMM_SPLIT))
     return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: unknown variant");
   if (K % 32) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: K must be a multiple of 32");
   if (epilogue == SAR_EPI_SWIGLU && N % 128)

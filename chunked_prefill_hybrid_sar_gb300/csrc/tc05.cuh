@@ -107,11 +107,12 @@ __device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t adesc, uint64_
 }
 
 // Completion of the pair's MMAs so far, signalled on the same barrier offset
-// in both CTAs (mask 0b11).
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// in both CTAs (mask 0b11; the pair of ranks 2k and 2k + 1 in a larger cluster:
+// 0b11 << 2k).
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint16_t mask = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
+      "h"(mask)
       : "memory");
 }
 

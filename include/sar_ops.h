@@ -142,7 +142,8 @@ enum {
                              range cut over a cluster's CTAs: | (count << 8) for that
                              many ranges (up to 8, one per 256 columns; else one)     */
   SAR_FP4_GEMM_PAIR = 2,  /* 256 weight rows x up to 256 token rows per tile over a
-                             pair of CTAs (2-CTA cluster), persistent               */
+                             pair of CTAs (2-CTA cluster), persistent; | (2 << 8) for
+                             two K ranges per tile, a pair each                     */
   SAR_FP4_GEMM_TOKENS64 = 0x1000 /* flag for SPLIT: tiles of 64 token rows             */
 };
 

@@ -83,7 +83,7 @@ def test_no_rows_is_no_work():
     (dict(c=None), "INVALID"), (dict(M=-1), "INVALID"), (dict(N=0), "INVALID"), (dict(K=0), "INVALID"),
     (dict(K=48), "UNSUPPORTED"), (dict(epi=4), "INVALID"), (dict(epi=-1), "INVALID"), (dict(fmt=2), "INVALID"),
     (dict(storage=2), "INVALID"), (dict(variant=0xff), "INVALID"), (dict(variant=-1), "INVALID"),
-    (dict(variant=1 << 16), "INVALID"), (dict(variant=0x102), "INVALID"), (dict(variant=0x100), "INVALID"), (dict(variant=0x1002), "INVALID"), (dict(variant=0x2001), "INVALID"), (dict(epi=2, N=192), "UNSUPPORTED"), (dict(epi=1), "INVALID"),
+    (dict(variant=1 << 16), "INVALID"), (dict(variant=0x100), "INVALID"), (dict(variant=0x1002), "INVALID"), (dict(variant=0x2001), "INVALID"), (dict(epi=2, N=192), "UNSUPPORTED"), (dict(epi=1), "INVALID"),
     (dict(a=P + 8), "INVALID"), (dict(w=P + 8), "INVALID"), (dict(sa=P + 1), "INVALID"), (dict(sw=P + 4), "INVALID"),
     (dict(c=P + 1), "INVALID"), (dict(epi=3, c=P + 2), "INVALID"), (dict(epi=1, r=P + 2), "INVALID"),
 ])

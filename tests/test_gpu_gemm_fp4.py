@@ -65,6 +65,8 @@ def variants(M, N, K):
         if n <= (K + 255) // 256:
             v[f"split{n}"] = sar.SAR_FP4_GEMM_SPLIT | n << 8
             v[f"split{n}x64"] = v[f"split{n}"] | sar.SAR_FP4_GEMM_TOKENS64
+    if K > 256:
+        v["pair2"] = sar.SAR_FP4_GEMM_PAIR | 2 << 8
     return v
 
 
