@@ -164,26 +164,25 @@ struct RowCtl {
   const uint16_t* state = nullptr;  // null: no penalties
   const uint32_t* mask = nullptr;   // null: every token allowed
   float rep = 1.f, pres = 0.f, freq = 0.f;
-  float inv_rep = 1.f;     // correctly rounded
-  bool plain_rep = true;   // of ordinary size
+  float inv_rep = 1.f;               // correctly rounded
+  uint32_t ordinary = 0x40000000u;   // 2^64 over 2^-64 as bit patterns; 0: always divide
 };
 
 // The penalties, in the order and with the roundings the header gives (no fused
 // multiply-add: f * count is rounded before it is taken off).  x / rep is formed
 // with the row's 1 / rep and corrected by its exact remainder, which rounds it
 // correctly (Markstein 1990) while nothing on the way over- or underflows;
-// otherwise it is divided.
+// otherwise it is divided.  s != 0.
 __device__ __forceinline__ float penalised(float x, uint32_t s, const RowCtl& w) {
-  if (__builtin_expect(s == 0, 1)) return x;  // (a branch: few tokens are seen)
   const uint32_t made = s & 0x7fffu;
-  if (x > 0.f) {
-    const float q = __fmul_rn(x, w.inv_rep);
-    x = w.plain_rep && x > 1e-20f && x < 1e20f ? __fmaf_rn(-__fmaf_rn(q, w.rep, -x), w.inv_rep, q) : __fdiv_rn(x, w.rep);
-  } else {
-    x = __fmul_rn(x, w.rep);
-  }
-  x = __fsub_rn(x, __fmul_rn(w.freq, (float)made));
-  return made ? __fsub_rn(x, w.pres) : x;
+  const float q = __fmul_rn(x, w.inv_rep), less = __fmul_rn(x, w.rep);
+  const float div = __fmaf_rn(-__fmaf_rn(q, w.rep, -x), w.inv_rep, q);
+  // |x| outside [2^-64, 2^64), or a factor of unusual size
+  const bool odd = (__float_as_uint(x) & 0x7fffffffu) - 0x1f800000u >= w.ordinary;
+  float y = x > 0.f ? div : less;
+  if (__builtin_expect(odd, 0) && x > 0.f) y = __fdiv_rn(x, w.rep);
+  y = __fsub_rn(y, __fmul_rn(w.freq, (float)made));
+  return made ? __fsub_rn(y, w.pres) : y;
 }
 
 // The larger logit, then the lower token; NaN and -inf never come here.
@@ -235,9 +234,10 @@ struct Placed {
 
 // Masks K tokens (bit k of `on`: allowed) and takes the largest into `best`, those
 // of `raw` left out of both.  A NaN loses; which token leads is looked up only
-// where one of them does.
+// where one of them is above `bar`, what the warp had reached by the tile before
+// (a lane's own best would be passed by some lane of the warp at nearly every step).
 template <int K, typename Token>
-__device__ __forceinline__ void lead(float (&v)[K], uint32_t on, uint32_t raw, Best& best, const Token& token) {
+__device__ __forceinline__ void lead(float (&v)[K], uint32_t on, uint32_t raw, float bar, Best& best, const Token& token) {
   const uint32_t off = ~on & ~raw & ((1u << K) - 1);
   if (off) {
 #pragma unroll
@@ -247,7 +247,7 @@ __device__ __forceinline__ void lead(float (&v)[K], uint32_t on, uint32_t raw, B
   float top = v[0];
 #pragma unroll
   for (int k = 1; k < K; ++k) top = fmaxf(top, v[k]);
-  if (top > best.v) {  // (also where a token left out has the largest)
+  if (top > bar) {  // (also where a token left out has the largest)
 #pragma unroll
     for (int k = 0; k < K; ++k)
       if (!(raw >> k & 1)) best.take_later(v[k], token(k));
@@ -278,10 +278,11 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
 // Logits, token state and mask words come in tiles of 8192 tokens by bulk copies
 // of a warp of its own, two tiles at a time: with ordinary loads a thread's
 // registers hold too little of what has to be on its way (256 x 64000 fp32, pick
-// only: 30 us, and 16.4 so).  With everything on and the logits written that size
-// takes 36 us, 4.5 TB/s: the 16 warps' instructions (about 12 a token) and 256
-// rows' CTAs on 304 places are what it waits for, not HBM alone.  One row of
-// 32000, eight CTAs: 6.1 us, the chain of one read, a cluster's join and a write.
+// only: 30 us, and 15.5 so).  With everything on and the logits written that size
+// takes 36 us, 4.5 TB/s.  A further tile costs what HBM takes (7.0 TB/s from 32768
+// to 65536 tokens a row); a CTA's start, first loads and join cost about 6 us, and
+// 256 rows leave 104 SMs with two CTAs and 48 with one.  One row of 32000, eight
+// CTAs: 6.0 us, the chain of indexes, state, a cluster's join and a write.
 //
 // Biases come as a list per row.  Their tokens are marked in a bitmap of the
 // stretch; the dense pass leaves marked tokens as they are, and the list's
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
     m = -1;
   }
   w.inv_rep = __frcp_rn(w.rep);
-  w.plain_rep = w.rep > 1e-10f && w.rep < 1e10f;
+  if (!(w.rep > 1e-10f && w.rep < 1e10f)) w.ordinary = 0;
   if (m >= 0) w.mask = c.mask + (int64_t)m * c.mask_ld;
   if (b0 < 0 || b1 < b0 || b1 > c.n_biases) {
     if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, r);
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kCtlThreads) : "memory"); };
 
   Best best;
+  float bar = -INFINITY;  // the warp's best logit of the tiles before
   for (int s0 = lo; s0 < hi && tid < kCtlThreads; s0 += kCtlSpan) {
     const int s1 = min(hi, s0 + kCtlSpan);
     // this thread's first listed token of the span, with what finishing it reads
@@ -445,7 +447,8 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       auto one = [&](int t) {
         float v = ctl_load<T>(x + t);
         if (!(b1 > b0 && (listed_bits(t) & 1))) {
-          if (w.state) v = penalised(v, w.state[t], w);
+          const uint32_t seen = w.state ? w.state[t] : 0;
+          if (seen) v = penalised(v, seen, w);
           if (w.mask && !(mask_bits(t) & 1)) v = -INFINITY;
           best.take_later(v, t);
         }
@@ -474,11 +477,13 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
           if (f.x | f.y | g.x | g.y) {  // (most of a vocabulary is unseen)
             const uint32_t s[4] = {f.x, f.y, g.x, g.y};
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (!(raw >> k & 1)) v[k] = penalised(v[k], k & 1 ? s[k / 2] >> 16 : s[k / 2] & 0xffffu, w);
+            for (int k = 0; k < 8; ++k) {
+              const uint32_t seen = k & 1 ? s[k / 2] >> 16 : s[k / 2] & 0xffffu;
+              if (__builtin_expect(seen != 0, 0) && !(raw >> k & 1)) v[k] = penalised(v[k], seen, w);
+            }
           }
         }
-        lead(v, on, raw, best, [&](int k) { return t + (k & 3) + (k >> 2) * kHalf; });
+        lead(v, on, raw, bar, best, [&](int k) { return t + (k & 3) + (k >> 2) * kHalf; });
         if (y) {
           if constexpr (sizeof(T) == 4) {
             __stcs(reinterpret_cast<float4*>(y + t), make_float4(v[0], v[1], v[2], v[3]));
@@ -522,9 +527,9 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
           if (s[0] | s[1] | s[2] | s[3]) {
 #pragma unroll
             for (int k = 0; k < kU; ++k)
-              if (!(raw >> k & 1)) v[k] = penalised(v[k], s[k], w);
+              if (__builtin_expect(s[k] != 0, 0) && !(raw >> k & 1)) v[k] = penalised(v[k], s[k], w);
           }
-          lead(v, on, raw, best, [&](int k) { return t + k * kCtlThreads; });
+          lead(v, on, raw, bar, best, [&](int k) { return t + k * kCtlThreads; });
           if (y) {
 #pragma unroll
             for (int k = 0; k < kU; ++k)
@@ -534,6 +539,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
         if (i1 + tid < t1) one(i1 + tid);
       }
       __syncwarp();
+      bar = fmaxf(bar, warp_max(best.v));
       if ((tid & 31) == 0) mbar_arrive(smem_u32(&empty[i % kCtlStages]));  // the warp has read the stage
     }
     if (b1 > b0) {
@@ -566,7 +572,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
           es = w.state ? w.state[t] : 0;
           em = w.mask ? __ldg(w.mask + (t >> 5)) >> (t & 31) & 1 : 1;
         }
-        const float v = em ? __fadd_rn(penalised(ex, es, w), sum) : -INFINITY;
+        const float v = em ? __fadd_rn(es ? penalised(ex, es, w) : ex, sum) : -INFINITY;
         best.take(v, t);
         if (y) ctl_store<T>(y + t, v);
       }
