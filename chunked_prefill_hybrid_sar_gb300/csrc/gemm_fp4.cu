@@ -965,6 +965,8 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
       ((variant & 0xf00) && (variant & 0xff) == SAR_FP4_GEMM_AUTO) ||
       ((variant & SAR_FP4_GEMM_TOKENS64) && (variant & 0xff) != SAR_FP4_GEMM_SPLIT))
     return set_error(SAR_ERR_INVALID_ARG, "gemm_fp4: unknown variant");
+  // (sizes are rounded up to whole tiles in 32 bits)
+  if (M > 1 << 30 || N > 1 << 30 || K > 1 << 30) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: a side above 2^30");
   if (K % 32) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: K must be a multiple of 32");
   if (epilogue == SAR_EPI_SWIGLU && N % 128)
     return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: SwiGLU needs whole 64-row gate/up block pairs");

@@ -653,6 +653,8 @@ int check_controls(const sar_logit_controls* c, int vocab) {
   const int lists = (c->bias_offsets != nullptr) + (c->bias_tokens != nullptr) + (c->bias_values != nullptr);
   if ((lists != 0 && lists != 3) || c->n_biases < 0)
     return set_error(SAR_ERR_INVALID_ARG, "logits control: biases need offsets, tokens and values");
+  // (the kernel's steps past a list's end stay within 32 bits)
+  if (c->n_biases > 1 << 30) return set_error(SAR_ERR_UNSUPPORTED, "logits control: more than 2^30 biases");
   if (c->mask && (c->n_masks < 1 || c->mask_ld < ((int64_t)vocab + 31) / 32))
     return set_error(SAR_ERR_INVALID_ARG, "logits control: mask rows shorter than the vocabulary");
   if (!c->mask && c->mask_rows) return set_error(SAR_ERR_INVALID_ARG, "logits control: mask rows without a mask");
@@ -729,6 +731,9 @@ int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vo
       !sar::aligned(prompt_lens, 4))
     return set_error(SAR_ERR_INVALID_ARG, "token_state_add: array not aligned to its element");
   if (n > 65535) return set_error(SAR_ERR_UNSUPPORTED, "token_state_add: more than 65535 rows");
+  // (the kernels' steps past a list's end stay within 32 bits)
+  if (vocab > 1 << 30 || n_tokens > 1 << 30)
+    return set_error(SAR_ERR_UNSUPPORTED, "token_state_add: vocabulary or tokens above 2^30");
   sar::StateArgs a = {state, ld, n_slots, vocab, slots, n, offsets, tokens, n_tokens, prompt_lens, 0, nullptr};
   a.vec = sar::aligned(state, 16) && ld % 8 == 0;
   SAR_TRY(sar::op_flags(&a.err));
@@ -755,7 +760,8 @@ int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t voc
   if (!out && !tokens_out) return set_error(SAR_ERR_INVALID_ARG, "logits control: nothing to write");
   if (controls->count_picks && !tokens_out)
     return set_error(SAR_ERR_INVALID_ARG, "logits control: counted picks without picks");
-  if (vocab > (1 << 30)) return set_error(SAR_ERR_UNSUPPORTED, "logits control: vocabulary above 2^30");
+  if (vocab > (1 << 30) || rows > (1 << 30))
+    return set_error(SAR_ERR_UNSUPPORTED, "logits control: vocabulary or rows above 2^30");
   SAR_TRY(sar::check_controls(controls, vocab));
   if (rows == 0) return SAR_OK;
   if (!logits) return set_error(SAR_ERR_INVALID_ARG, "logits control: null logits");

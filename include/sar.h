@@ -321,8 +321,9 @@ typedef struct sar_logit_controls {
  * changed logits before they are rounded to `type`; NaN is never picked; -1 where
  * nothing is above -inf (a mask that leaves no token).  Index arrays are checked
  * on the device: a slot, mask row, list or bias token out of range is passed over
- * and reported by sar_op_sync_status().  16-byte aligned rows are faster.  Async
- * on `stream`; allocates nothing after the first call on a device. */
+ * and reported by sar_op_sync_status().  Rows, vocabulary and biases are at most
+ * 2^30 each.  16-byte aligned rows are faster.  Async on `stream`; allocates
+ * nothing after the first call on a device. */
 int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t vocab, int32_t type,
                        const sar_logit_controls* controls, void* out, int64_t ld_out, int32_t* tokens_out, void* stream);
 
@@ -334,7 +335,8 @@ int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t voc
  * admitted, or resumed with its history); a slot named again in the call is passed
  * over.  Otherwise the tokens are added to what is there, also where two rows name
  * one slot.  Slots, offsets and tokens out of range are passed over; these and a
- * slot named again are reported by sar_op_sync_status().  Async on `stream`. */
+ * slot named again are reported by sar_op_sync_status().  n is at most 65535,
+ * vocab and n_tokens at most 2^30.  Async on `stream`. */
 int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vocab, const int32_t* slots, int32_t n,
                         const int32_t* offsets, const int32_t* tokens, int32_t n_tokens, const int32_t* prompt_lens,
                         int32_t reset, void* stream);

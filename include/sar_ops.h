@@ -149,7 +149,8 @@ enum {
 
 /* C = epilogue(alpha * A . W^T) of 4-bit rows of one format: A [M, K] and W [N, K]
  * as codes and scales laid out as above, each without its tensor scale (alpha
- * holds their product).  K a multiple of 32, any M >= 0 and N >= 1.
+ * holds their product).  K a multiple of 32, any M >= 0 and N >= 1,
+ * each at most 2^30.
  *   SAR_EPI_STORE     C [M, N] in the 16-bit type `storage`
  *   SAR_EPI_RESIDUAL  C fp32 [M, N] = alpha * A . W^T + R (R may equal C)
  *   SAR_EPI_SWIGLU    W's rows gate/up interleaved in 64-row blocks (N a multiple

@@ -96,3 +96,10 @@ def test_product_is_refused(change, code):
 
 def test_product_of_no_tokens_is_no_work():
     assert sar.lib().sar_op_gemm_fp4(None, None, None, None, None, None, 0, 64, 64, 1.0, 0, 0, 0, 0, None) == _lib.SAR_OK
+
+
+@pytest.mark.parametrize("change", [dict(M=2 ** 31 - 1), dict(N=2 ** 31 - 1), dict(K=2 ** 31 - 32), dict(M=2 ** 30 + 1)])
+def test_sides_whose_tiles_pass_32_bits_are_refused(change):
+    a = dict(M=4, N=128, K=64) | change
+    rc = sar.lib().sar_op_gemm_fp4(P, P, P, P, P, None, a["M"], a["N"], a["K"], 1.0, 0, 0, 0, 0, None)
+    assert rc == _lib.SAR_ERR_UNSUPPORTED

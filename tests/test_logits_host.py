@@ -80,3 +80,22 @@ def test_state_calls_are_refused(change, code):
     rc = sar.lib().sar_token_state_add(a["state"], a["ld"], a["n_slots"], a["vocab"], a["slots"], a["n"], a["offsets"],
                                        a["tokens"], a["n_tokens"], a["prompt"], 0, None)
     assert rc == code
+
+
+# (a thread's next step past the end of such a list, or of such rows, would not fit 32 bits)
+@pytest.mark.parametrize("change,ctl", [
+    (dict(rows=2 ** 31 - 1), {}), (dict(vocab=2 ** 30 + 1, ld=2 ** 30 + 1, ld_out=2 ** 30 + 1), {}),
+    ({}, dict(bias_offsets=P, bias_tokens=P, bias_values=P, n_biases=2 ** 31 - 1)),
+])
+def test_controls_beyond_32_bits_are_refused(change, ctl):
+    a = GOOD | change
+    rc = sar.lib().sar_logits_control(a["logits"], a["ld"], a["rows"], a["vocab"], a["kind"], ctypes.byref(controls(**ctl)),
+                                      a["out"], a["ld_out"], a["tokens"], None)
+    assert rc == _lib.SAR_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("reset", [0, 1])
+@pytest.mark.parametrize("vocab,n_tokens", [(8, 2 ** 31 - 1), (2 ** 30 + 1, 4)])
+def test_state_calls_beyond_32_bits_are_refused(reset, vocab, n_tokens):
+    rc = sar.lib().sar_token_state_add(P, 2 ** 31, 2, vocab, P, 2, P, P, n_tokens, None, reset, None)
+    assert rc == _lib.SAR_ERR_UNSUPPORTED
