@@ -119,6 +119,36 @@ def test_epilogues(M, N, K, epi, dt, fmt):
         assert (off <= b).all(), (name, (off - b).max(), off.max())
 
 
+# The narrowest last token tile behind whole ones of 256: the fewest and the most
+# tokens in it, a ragged N and K, one weight tile and more tiles than pairs of SMs,
+# one and several whole token tiles.
+TAILS = [(257, 128, 32), (272, 130, 96), (258, 640, 1056), (517, 20736, 320), (1029, 6400, 544), (2049, 384, 2336)]
+
+
+@pytest.mark.parametrize("M,N,K", TAILS)
+@pytest.mark.parametrize("epi", ["store", "f32", "residual", "in place"])
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_a_few_tokens_behind_whole_tiles(M, N, K, epi, fmt):
+    rng = np.random.default_rng(M + K)
+    a, w = Rows(rng, M, K, fmt, plain=True), Rows(rng, N, K, fmt, plain=True)
+    in_place, epi = epi == "in place", "residual" if epi == "in place" else epi
+    dtype = torch.bfloat16 if epi == "store" else torch.float32
+    want = torch.from_numpy(2.0 ** -6 * (a.values @ w.values.T) + (epi == "residual")).to(dtype)
+    for offset in (0, 1):  # of C, in elements: written by tiles, and one by one
+        buf = torch.full((offset + M * N + 64,), 5.0, dtype=dtype, device="cuda")
+        c = buf[offset:offset + M * N].view(M, N)
+        r = None if epi != "residual" else c.fill_(1.0) if in_place else torch.ones(M, N, device="cuda")
+        run(a, w, fmt, epi, alpha=2.0 ** -6, residual=r, out=c, variant=sar.SAR_FP4_GEMM_PAIR)
+        assert torch.equal(c.cpu(), want)
+        assert (buf[:offset] == 5.0).all() and (buf[offset + M * N:] == 5.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(257, 128, 32), (264, 640, 1056), (528, 20736, 320), (1029, 6400, 544)])
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_swiglu_of_a_few_tokens_behind_whole_tiles(M, N, K, fmt):
+    test_epilogues(M, N, K, "swiglu", "bf16", fmt)
+
+
 def test_residual_in_place_and_repeated():
     rng = np.random.default_rng(4)
     a, w = Rows(rng, 70, 1024, "nv", plain=True), Rows(rng, 384, 1024, "nv", plain=True)
