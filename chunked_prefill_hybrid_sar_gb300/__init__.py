@@ -184,6 +184,7 @@ class StepGraph:
     def __init__(self, model: "Model", kv: "KVCache", batch: Batch, inp, hidden_out=None, logits_out=None,
                  layer_out=None, stream=None):
         self._keep = (batch, inp, hidden_out, logits_out, layer_out)
+        self._vocab = model.dims.vocab
         h = ctypes.c_void_p()
         check(lib().sar_graph_create(model.h, kv.h, ctypes.byref(batch.c), _ptr(inp), _ptr(hidden_out),
                                      _ptr(logits_out), _ptr(layer_out), _stream(stream), ctypes.byref(h)))
@@ -217,8 +218,15 @@ class StepGraph:
     def set_controls(self, controls: "LogitControls | None") -> None:
         """The token launches pick under ``controls`` (a row per logits row)
         from now on; None: greedily again."""
-        if controls is not None and controls.rows is not None and controls.rows < self._keep[0].logit_rows:
-            raise ValueError("set_controls: an array is shorter than the logits' rows")
+        if controls is not None:
+            # (the library sees strides alone: a table's columns may end before its stride does)
+            if controls.rows is not None and controls.rows < self._keep[0].logit_rows:
+                raise ValueError("set_controls: an array is shorter than the logits' rows")
+            if controls.vocab < self._vocab:
+                raise ValueError("set_controls: the token state or the mask is narrower than the vocabulary")
+            logits = self._keep[3]
+            if controls.device is not None and logits is not None and controls.device != logits.get_device():
+                raise ValueError("set_controls: the controls are on another device than the logits")
         check(lib().sar_graph_set_controls(self.h, None if controls is None else ctypes.byref(controls.c)))
         self._controls = controls
 
