@@ -113,11 +113,18 @@ __device__ __forceinline__ void state_count(uint16_t* at, bool prompt) {
   } while (old != was);
 }
 
-// An appending call: one thread per token, its row found by bisection.
+// An appending call: one thread per token, its row found by bisection, and one per
+// row that reports offsets which are out of range or fall (such a row may hold no
+// token that a thread could meet).  Where all offsets rise the bisection ends at
+// the token's row; where some fall it ends at one row at most.
 __global__ void __launch_bounds__(256) state_append_kernel(const StateArgs a) {
   pdl_wait();
   pdl_launch_dependents();
   const int i = blockIdx.x * 256 + threadIdx.x;
+  if (i < a.n) {
+    const int b = a.offsets[i], e = a.offsets[i + 1];
+    if (b < 0 || e < b || e > a.n_tokens) report(a.err, SAR_ERR_BOUNDS, SITE_STATE_OFFSET, i);
+  }
   if (i >= a.n_tokens) return;
   int lo = 0, hi = a.n;  // the last row that begins at or before i
   while (hi - lo > 1) {
@@ -127,8 +134,9 @@ __global__ void __launch_bounds__(256) state_append_kernel(const StateArgs a) {
     else
       hi = mid;
   }
-  const int b = a.offsets[lo];
-  if (i < b || i >= a.offsets[lo + 1]) return;  // a token of no row
+  const int b = a.offsets[lo], e = a.offsets[lo + 1];
+  if (i < b || i >= e) return;          // a token of no row
+  if (b < 0 || e > a.n_tokens) return;  // a row that is passed over (reported above)
   const int slot = a.slots[lo], t = a.tokens[i];
   if (slot < 0 || slot >= a.n_slots) {
     report(a.err, SAR_ERR_BOUNDS, SITE_STATE_SLOT, lo);
@@ -743,7 +751,7 @@ int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vo
     e = sar::launch_pdl(sar::state_reset_kernel, dim3((unsigned)((vocab + (int64_t)sar::kStateSpan - 1) / sar::kStateSpan), (unsigned)n),
                         dim3(sar::kStateThreads), 0, s, a);
   else
-    e = sar::launch_pdl(sar::state_append_kernel, dim3((unsigned)((n_tokens + 255ll) / 256)), dim3(256), 0, s, a);
+    e = sar::launch_pdl(sar::state_append_kernel, dim3((unsigned)((std::max(n_tokens, n) + 255ll) / 256)), dim3(256), 0, s, a);
   if (e != cudaSuccess) return sar::cuda_error(e, "token state launch");
   sar::count_launches(1);
   return SAR_OK;

@@ -334,9 +334,13 @@ int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t voc
  * each slot's first `vocab` entries are made anew from the row's tokens (a request
  * admitted, or resumed with its history); a slot named again in the call is passed
  * over.  Otherwise the tokens are added to what is there, also where two rows name
- * one slot.  Slots, offsets and tokens out of range are passed over; these and a
- * slot named again are reported by sar_op_sync_status().  n is at most 65535,
- * vocab and n_tokens at most 2^30.  Async on `stream`. */
+ * one slot.  Slots and tokens out of range are passed over, and so are rows whose
+ * offsets are out of range or fall; these and a slot named again are reported by
+ * sar_op_sync_status().  (Where offsets fall, an appending call counts each token
+ * once at most, and may leave out tokens of other rows; a resetting call counts
+ * every good row whole.)  A slot out of range is reported by an appending call where a
+ * token lands in its row; an appending call without tokens does nothing.  n is at
+ * most 65535, vocab and n_tokens at most 2^30.  Async on `stream`. */
 int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vocab, const int32_t* slots, int32_t n,
                         const int32_t* offsets, const int32_t* tokens, int32_t n_tokens, const int32_t* prompt_lens,
                         int32_t reset, void* stream);
