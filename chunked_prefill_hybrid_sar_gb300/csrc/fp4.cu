@@ -236,10 +236,13 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // y = code * s * g: the product of a code and its scale is exact in fp32 (3 and
-// 4 significant bits); * g rounds once, the conversion to Y once more.
+// 4 significant bits); * g rounds once, the conversion to Y once more.  MX's three
+// largest scales (2^125 and up) times a code can pass fp32 where the whole product
+// does not: they are taken 2^8 lower and g 2^8 higher, both exact.  (From g = 2^100
+// on such a block overflows whatever g is, but its zeros have to stay zeros.)
 //
 // A unit is 16 bytes of output (8 or 4 columns), neighbouring lanes take
-// neighbouring units and a thread takes 32 bytes' worth kThreads units apart, so
+// neighbouring units and a thread takes four of them kThreads units apart, so
 // that a warp's store covers 512 whole bytes (a thread's 16 columns as two
 // stores: 69.0 us for 20480 x 7168 bf16, every sector written in two halves; so
 // 60.0 us, 6.3 TB/s).  Bound by HBM.
@@ -270,17 +273,20 @@ __global__ void __launch_bounds__(kThreads)
   for (int u = 0; u < kEach; ++u) {
     const uint64_t i = ((uint64_t)blockIdx.x * kEach + u) * kThreads + threadIdx.x;
     if (i >= n) break;
-    float s;
-    if constexpr (NV)
+    float s, gs = g;
+    if constexpr (NV) {
       s = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b[u], __NV_E4M3)));
-    else  // 2^(b - 127); 2^-127 is a subnormal
-      s = __uint_as_float(b[u] == 255 ? 0x7fc00000u : b[u] == 0 ? 0x00400000u : b[u] << 23);
+    } else {  // 2^(b - 127); 2^-127 is a subnormal
+      const bool high = b[u] >= 252;
+      s = __uint_as_float(b[u] == 255 ? 0x7fc00000u : b[u] == 0 ? 0x00400000u : (high ? b[u] - 8 : b[u]) << 23);
+      if (high) gs = fminf(g, 0x1p100f) * 256.f;
+    }
     float v[kCols];
 #pragma unroll
     for (int k = 0; k < (int)kCols / 2; ++k) {
       const __half2 h(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((c[u] >> (8 * k)) & 0xffu), __NV_E2M1));
-      v[2 * k] = __low2float(h) * s * g;
-      v[2 * k + 1] = __high2float(h) * s * g;
+      v[2 * k] = __low2float(h) * s * gs;
+      v[2 * k + 1] = __high2float(h) * s * gs;
     }
     Y* dst = y + (int64_t)row[u] * ldy + col[u];
     if (!vec) {
