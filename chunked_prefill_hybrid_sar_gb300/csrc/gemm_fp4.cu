@@ -792,6 +792,12 @@ double pairs_us(const Params& p, int sms) {
   return kPairsBase + (units + fit - 1) / fit * ((p.slabs + 1) / 2 * kPairsSlab + kPairsTile);
 }
 
+// The split tiling's tiles lie on a grid's y and z (the pair tiling's on x).
+constexpr int kMaxGridYz = 65535;
+bool split_fits(const Params& p, int width) {
+  return (p.M + width - 1) / width <= kMaxGridYz && (p.N + 127) / 128 <= kMaxGridYz;
+}
+
 int pick_variant(const Params& p) {
   const int sms = num_sms();
   int best = SAR_FP4_GEMM_PAIR;
@@ -802,6 +808,7 @@ int pick_variant(const Params& p) {
   }
   for (int width : {128, 64}) {
     if (width == 64 && p.M <= 64) break;  // one tile either way
+    if (!split_fits(p, width)) continue;
     for (int splits : {1, 2, 3, 4, 6, 8}) {
       if (splits > p.slabs) break;
       const double t = split_us(p, width, splits, sms);
@@ -818,7 +825,7 @@ int launch_split(const Call& g, Params p) {
   const bool nv = g.format == SAR_FP4_NV;
   const int width = g.variant & SAR_FP4_GEMM_TOKENS64 ? 64 : 128;
   const int m_tiles = (p.M + width - 1) / width, n_tiles = (p.N + 127) / 128;
-  if (m_tiles > 65535 || n_tiles > 65535) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many tiles");
+  if (!split_fits(p, width)) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many tiles for the split tiling");
   p.bn = m_tiles > 1 ? width : (p.M + 15) / 16 * 16;
   const int splits = std::max(1, g.variant >> 8 & 0xf);
   if (splits > 8 || splits > p.slabs) return set_error(SAR_ERR_UNSUPPORTED, "gemm_fp4: too many K ranges");

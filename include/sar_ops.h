@@ -140,7 +140,8 @@ enum {
   SAR_FP4_GEMM_AUTO = 0,  /* the library's choice for (M, N, K)                        */
   SAR_FP4_GEMM_SPLIT = 1, /* 128 weight rows x up to 128 token rows per tile, the K
                              range cut over a cluster's CTAs: | (count << 8) for that
-                             many ranges (up to 8, one per 256 columns; else one)     */
+                             many ranges (up to 8, one per 256 columns; else one); up
+                             to 65535 tiles of either side's rows                     */
   SAR_FP4_GEMM_PAIR = 2,  /* 256 weight rows x up to 256 token rows per tile over a
                              pair of CTAs (2-CTA cluster), persistent; | (2 << 8) for
                              two K ranges per tile, a pair each                     */
