@@ -155,6 +155,8 @@ constexpr int kCtlStages = 2;     // steps on their way
 constexpr int kCtlLeast = 4096;   // tokens that a CTA is started for
 constexpr int kCtlSpan = 32768;   // tokens per pass over a row's biases: two bitmaps of 4 KB
 constexpr long kCtlPerSm = 2;     // CTAs that fit an SM's shared memory
+constexpr int kCtlMostBiases = 1 << 24;  // of a row (a span's work on them stays far below the waits' limit)
+constexpr int kCtlSlice = 64;     // tokens whose repeated biases a warp adds up at a time
 
 struct CtlArgs {
   const void* x;
@@ -277,6 +279,66 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
     *p = Elem<T>::from(v);
 }
 
+// Finishes the tokens of [s0, s1) that a long list names repeatedly (`twice`, in
+// shared memory): a warp takes a slice of 64 tokens that holds such, reads the list
+// once (its first 512 entries in shared memory) and adds up their biases in list
+// order; lane k holds the sums of the slice's tokens k and 32 + k.  Returns the best
+// of this lane's tokens.  256 x 64000 written, 1300 biases a row: 67 us (157 with a
+// search per entry; 513 a row 41 and 39).  Not inlined: inside the kernel it made
+// the dense pass spill (the same without a list 21.7 us, and 20.8 so).
+template <typename T>
+__device__ __noinline__ Best finish_repeated(const T* x, T* y, const int32_t* tokens, const float* values, int b0, int b1,
+                                             int s0, int s1, const uint32_t* twice, const int* list_t, const float* list_v,
+                                             const RowCtl w) {
+  Best best;
+  const int lane = threadIdx.x & 31;
+  for (int q = threadIdx.x >> 5; q * kCtlSlice < s1 - s0; q += kCtlThreads / 32) {
+    const uint32_t rep0 = twice[2 * q], rep1 = twice[2 * q + 1];
+    if (!(rep0 | rep1)) continue;
+    const int base = s0 + q * kCtlSlice;
+    float sum0 = -0.f, sum1 = -0.f;  // (what adding a first bias leaves as it is)
+    constexpr int kU = 8;            // loads of a lane under way at once
+    static_assert(kCtlThreads % (32 * kU) == 0, "the list's head is whole steps");
+    for (int e0 = b0; e0 < b1; e0 += 32 * kU) {
+      const bool head = e0 - b0 < kCtlThreads;  // (whole steps are)
+      const int* at_t = head ? list_t : tokens;
+      const float* at_v = head ? list_v : values;
+      const int first = head ? e0 - b0 : e0;
+      int t[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int e = 32 * u + lane;
+        t[u] = e0 + e < b1 ? at_t[first + e] : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const uint32_t at = (uint32_t)t[u] - (uint32_t)base;  // (beyond the slice also where t is out of range)
+        const bool in = at < kCtlSlice && ((at < 32 ? rep0 : rep1) >> (at & 31) & 1);
+        uint32_t hits = __ballot_sync(0xffffffffu, in);
+        if (!hits) continue;
+        const float v = in ? at_v[first + 32 * u + lane] : 0.f;
+        for (; hits; hits &= hits - 1) {  // in list order
+          const int from = __ffs(hits) - 1;
+          const uint32_t to = __shfl_sync(0xffffffffu, at, from);
+          const float more = __shfl_sync(0xffffffffu, v, from);
+          if (to == (uint32_t)lane) sum0 = __fadd_rn(sum0, more);
+          if (to == (uint32_t)lane + 32) sum1 = __fadd_rn(sum1, more);
+        }
+      }
+    }
+    for (int h = 0; h < 2; ++h) {
+      if (!((h ? rep1 : rep0) >> lane & 1)) continue;
+      const int t = base + 32 * h + lane;
+      const uint32_t seen = w.state ? w.state[t] : 0, on = w.mask ? __ldg(w.mask + (t >> 5)) >> (t & 31) & 1 : 1;
+      float v = ctl_load<T>(x + t);
+      v = on ? __fadd_rn(seen ? penalised(v, seen, w) : v, h ? sum1 : sum0) : -INFINITY;
+      best.take(v, t);
+      if (y) ctl_store<T>(y + t, v);
+    }
+  }
+  return best;
+}
+
 // One pass over the logits: a cluster of CTAs shares each row, every CTA takes
 // one stretch of the vocabulary and the stretches' best tokens meet through
 // distributed shared memory, so that a lone row is read by as many SMs as the
@@ -295,8 +357,11 @@ __device__ __forceinline__ void ctl_store(T* p, float v) {
 // Biases come as a list per row.  Their tokens are marked in a bitmap of the
 // stretch; the dense pass leaves marked tokens as they are, and the list's
 // threads then finish one each: penalties from the original logit, the token's
-// biases added up in list order (a second bitmap marks tokens that are listed
-// again: only those search the list), mask.
+// biases added up in list order, mask.  A second bitmap marks tokens that are
+// listed again.  In a list of up to 512 those alone search it, in shared memory;
+// in a longer one, where every such search would make the work grow with the
+// length's square, each warp takes slices of 64 tokens that hold a repeated one
+// and reads the list once for each.
 //
 // VEC: rows at 16-byte boundaries; a thread takes 4 neighbouring tokens at a
 // time, otherwise single ones.
@@ -386,7 +451,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
   w.inv_rep = __frcp_rn(w.rep);
   if (!(w.rep > 1e-10f && w.rep < 1e10f)) w.ordinary = 0;
   if (m >= 0) w.mask = c.mask + (int64_t)m * c.mask_ld;
-  if (b0 < 0 || b1 < b0 || b1 > c.n_biases) {
+  if (b0 < 0 || b1 < b0 || b1 > c.n_biases || b1 - b0 > kCtlMostBiases) {
     if (tells) report(a.err, SAR_ERR_BOUNDS, SITE_CONTROL_BIAS, r);
     b0 = b1 = 0;
   }
@@ -553,27 +618,26 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
     if (b1 > b0) {
       if (y) sync();  // y's listed tokens are written last
       // (where y is x its marked tokens still hold the logits)
+      const int n = b1 - b0;
       for (int e = b0 + tid; e < b1; e += kCtlThreads) {
         const bool kept = e < b0 + kCtlThreads;
         const int t = kept ? et : __ldg(c.bias_tokens + e);
         if (t < s0 || t >= s1) continue;
         float sum = kept ? ev : __ldg(c.bias_values + e);
         if (twice[(t - s0) >> 5] >> (t & 31) & 1) {
+          if (n > kCtlThreads) continue;  // (below)
           // its first entry's thread adds up the token's biases (no early end: the
           // loads of eight steps are under way together)
           bool first = true;
-          const int n = b1 - b0, head = min(n, kCtlThreads), me = e - b0;
+          const int me = e - b0;
 #pragma unroll 8
-          for (int f = 0; f < min(me, head); ++f) first &= list_t[f] != t;
-          for (int f = head; f < me; ++f) first &= __ldg(c.bias_tokens + b0 + f) != t;
+          for (int f = 0; f < me; ++f) first &= list_t[f] != t;
           if (!first) continue;
 #pragma unroll 8
-          for (int f = me + 1; f < head; ++f) {
+          for (int f = me + 1; f < n; ++f) {
             const float more = __fadd_rn(sum, list_v[f]);
             sum = list_t[f] == t ? more : sum;
           }
-          for (int f = max(head, me + 1); f < n; ++f)
-            if (__ldg(c.bias_tokens + b0 + f) == t) sum = __fadd_rn(sum, __ldg(c.bias_values + b0 + f));
         }
         if (!kept) {
           ex = ctl_load<T>(x + t);
@@ -583,6 +647,10 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
         const float v = em ? __fadd_rn(es ? penalised(ex, es, w) : ex, sum) : -INFINITY;
         best.take(v, t);
         if (y) ctl_store<T>(y + t, v);
+      }
+      if (n > kCtlThreads) {
+        const Best b = finish_repeated<T>(x, y, c.bias_tokens, c.bias_values, b0, b1, s0, s1, twice, list_t, list_v, w);
+        best.take(b.v, b.i);
       }
     }
   }
