@@ -155,7 +155,9 @@ constexpr int kCtlStages = 2;     // steps on their way
 constexpr int kCtlLeast = 4096;   // tokens that a CTA is started for
 constexpr int kCtlSpan = 32768;   // tokens per pass over a row's biases: two bitmaps of 4 KB
 constexpr long kCtlPerSm = 2;     // CTAs that fit an SM's shared memory
-constexpr int kCtlMostBiases = 1 << 24;  // of a row (a span's work on them stays far below the waits' limit)
+// Biases of a row.  A span's work on its list has to stay far below the waits' 2 s
+// (2^24 biases that repeat every token of a span: 1.6 s).
+constexpr int kCtlMostBiases = 1 << 21;
 constexpr int kCtlSlice = 64;     // tokens whose repeated biases a warp adds up at a time
 
 struct CtlArgs {
