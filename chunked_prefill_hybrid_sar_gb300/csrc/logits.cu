@@ -459,17 +459,24 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
   }
   if (fetches) {
     for (int i = 0; i < min(tiles, kCtlStages); ++i) fetch_rest(i);
-    for (int i = kCtlStages; i < tiles; ++i) {
-      // (a wait that gave up is reported; the copies go on, so that the others' waits end)
-      mbar_wait(smem_u32(&empty[i % kCtlStages]), (uint32_t)(i / kCtlStages - 1) & 1u, a.err, SITE_CONTROL_PIPE);
+    int i = kCtlStages;  // tiles before it are on their way
+    for (; i < tiles; ++i) {
+      // (a stage that was not given back stays as it is: no tile overwrites one that is being read)
+      if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[i % kCtlStages]), (uint32_t)(i / kCtlStages - 1) & 1u, a.err,
+                                             SITE_CONTROL_PIPE)))
+        break;
       fetch_x(i);
       fetch_rest(i);
     }
+    // whatever the working warps did, no copy is under way when the CTA leaves
+    for (int j = max(0, i - kCtlStages); j < min(i, tiles); ++j)
+      mbar_wait(smem_u32(&full[j % kCtlStages]), (uint32_t)(j / kCtlStages) & 1u, a.err, SITE_CONTROL_PIPE);
   }
   // the working threads alone
   auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(kCtlThreads) : "memory"); };
 
   Best best;
+  bool alive = true;      // false once a wait gave up: what this thread has read is not the row's
   float bar = -INFINITY;  // the warp's best logit of the tiles before
   for (int s0 = lo; s0 < hi && tid < kCtlThreads; s0 += kCtlSpan) {
     const int s1 = min(hi, s0 + kCtlSpan);
@@ -507,7 +514,8 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
     // (spans and tiles start at multiples of 32 tokens)
     for (int t0 = s0; t0 < s1; t0 += kCtlTile) {
       const int i = (t0 - lo) / kCtlTile, t1 = min(s1, t0 + kCtlTile);
-      mbar_wait(smem_u32(&full[i % kCtlStages]), (uint32_t)(i / kCtlStages) & 1u, a.err, SITE_CONTROL_PIPE);
+      alive &= mbar_wait(smem_u32(&full[i % kCtlStages]), (uint32_t)(i / kCtlStages) & 1u, a.err, SITE_CONTROL_PIPE,
+                         alive ? kWaitLimitNs : 0);  // (going on keeps the warp together and the barriers matched)
       const uint8_t* st = stage_mem + (i % kCtlStages) * kStage;
       const T* xs = reinterpret_cast<const T*>(st);
       const uint16_t* ss = reinterpret_cast<const uint16_t*>(st + kState);
@@ -657,6 +665,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
     }
   }
   if (!a.picks) return;  // (every CTA of the cluster alike)
+  if (!alive) best.v = INFINITY, best.i = -1;  // a row that was not read whole has no pick
   best.warp();
   if (tid < kCtlThreads && (tid & 31) == 0) {
     best_v[tid >> 5] = best.v;
@@ -685,7 +694,7 @@ __global__ void __launch_bounds__(kCtlThreads + 32, kCtlPerSm) logits_control_ke
       const bool any = best.i != 0x7fffffff;
       a.picks[r] = any ? best.i : -1;
       // (every CTA of the row has read its state)
-      if (any && c.count_picks && slot >= 0) state_count(c.state + (int64_t)slot * c.state_ld + best.i, false);
+      if (any && best.i >= 0 && c.count_picks && slot >= 0) state_count(c.state + (int64_t)slot * c.state_ld + best.i, false);
     }
   }
   __syncwarp();
