@@ -844,13 +844,13 @@ int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t voc
     return set_error(SAR_ERR_INVALID_ARG, "logits control: bad shape");
   if (type != SAR_TYPE_F16 && type != SAR_TYPE_BF16 && type != SAR_TYPE_F32)
     return set_error(SAR_ERR_INVALID_ARG, "logits control: bad element type");
+  if (rows == 0) return SAR_OK;  // (its slots and picks may be arrays without an address)
   if (!out && !tokens_out) return set_error(SAR_ERR_INVALID_ARG, "logits control: nothing to write");
   if (controls->count_picks && !tokens_out)
     return set_error(SAR_ERR_INVALID_ARG, "logits control: counted picks without picks");
   if (vocab > (1 << 30) || rows > (1 << 30))
     return set_error(SAR_ERR_UNSUPPORTED, "logits control: vocabulary or rows above 2^30");
   SAR_TRY(sar::check_controls(controls, vocab));
-  if (rows == 0) return SAR_OK;
   if (!logits) return set_error(SAR_ERR_INVALID_ARG, "logits control: null logits");
   const uintptr_t size = type == SAR_TYPE_F32 ? 4 : 2;
   if (!sar::aligned(logits, size) || !sar::aligned(out, size) || !sar::aligned(tokens_out, 4))

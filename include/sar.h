@@ -322,7 +322,8 @@ typedef struct sar_logit_controls {
  * nothing is above -inf (a mask that leaves no token).  Index arrays are checked
  * on the device: a slot, mask row, list or bias token out of range is passed over
  * and reported by sar_op_sync_status(), and so is a row's list of more than 2^21
- * biases.  Rows, vocabulary and biases are at most 2^30 each.  16-byte aligned rows are faster.  Async on `stream`; allocates
+ * biases.  rows = 0 does nothing.  Rows, vocabulary and biases are at most 2^30
+ * each.  16-byte aligned rows are faster.  Async on `stream`; allocates
  * nothing after the first call on a device. */
 int sar_logits_control(const void* logits, int64_t ld, int32_t rows, int32_t vocab, int32_t type,
                        const sar_logit_controls* controls, void* out, int64_t ld_out, int32_t* tokens_out, void* stream);
