@@ -185,6 +185,8 @@ class StepGraph:
                  layer_out=None, stream=None):
         self._keep = (batch, inp, hidden_out, logits_out, layer_out)
         self._vocab = model.dims.vocab
+        self._pending = self._controls = None
+        self._earlier = []  # controls that an enqueued step may still read
         h = ctypes.c_void_p()
         check(lib().sar_graph_create(model.h, kv.h, ctypes.byref(batch.c), _ptr(inp), _ptr(hidden_out),
                                      _ptr(logits_out), _ptr(layer_out), _stream(stream), ctypes.byref(h)))
@@ -217,7 +219,8 @@ class StepGraph:
 
     def set_controls(self, controls: "LogitControls | None") -> None:
         """The token launches pick under ``controls`` (a row per logits row)
-        from now on; None: greedily again."""
+        from now on; None: greedily again.  A step that is enqueued keeps the
+        controls that it was enqueued under."""
         if controls is not None:
             # (the library sees strides alone: a table's columns may end before its stride does)
             if controls.rows is not None and controls.rows < self._keep[0].logit_rows:
@@ -228,12 +231,15 @@ class StepGraph:
             if controls.device is not None and logits is not None and controls.device != logits.get_device():
                 raise ValueError("set_controls: the controls are on another device than the logits")
         check(lib().sar_graph_set_controls(self.h, None if controls is None else ctypes.byref(controls.c)))
+        if self._pending is not None:
+            self._earlier.append(self._controls)
         self._controls = controls
 
     def wait(self) -> None:
         """Waits for the last enqueue_host_tokens step of this graph."""
         check(lib().sar_graph_wait(self.h))
         self._pending = None
+        self._earlier.clear()
 
     def close(self) -> None:
         if self.h:

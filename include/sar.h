@@ -349,8 +349,8 @@ int sar_token_state_add(uint16_t* state, int64_t ld, int32_t n_slots, int32_t vo
 /* Makes sar_graph_launch_host_tokens and sar_graph_enqueue_host_tokens of this
  * graph pick under `controls` (one entry per logits row; NULL: greedily again)
  * instead of greedily; the captured logits stay as they are.  The struct is
- * copied; its arrays are read at every launch and have to outlive the last one.
- * Not to be called while an enqueued step has not been waited for. */
+ * copied; its arrays are read by every step launched under it and have to outlive
+ * the last of these.  A step that is enqueued already keeps its controls. */
 int sar_graph_set_controls(sar_graph* g, const sar_logit_controls* controls);
 
 /* ---- decode attention without allocation ------------------------------- */
