@@ -1461,7 +1461,7 @@ int sar_graph_enqueue_host_tokens(sar_graph* g, const void* in, int32_t* tokens_
   return check(cudaEventRecord(g->done, s), "graph: step enqueued");
 }
 
-int sar_graph_set_controls(sar_graph* g, const sar_logit_controls* controls) {
+int sar_graph_set_controls(sar_graph* g, const sar_logit_controls* controls) try {
   if (!g) return set_error(SAR_ERR_INVALID_ARG, "graph: null graph");
   if (!g->logits) return set_error(SAR_ERR_INVALID_ARG, "graph: logits not captured");
   if (controls) {
@@ -1470,6 +1470,8 @@ int sar_graph_set_controls(sar_graph* g, const sar_logit_controls* controls) {
   }
   g->controlled = controls != nullptr;
   return SAR_OK;
+} catch (...) {
+  return sar::entry_failed("graph_set_controls");
 }
 
 int sar_graph_wait(sar_graph* g) {
