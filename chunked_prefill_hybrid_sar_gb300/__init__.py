@@ -204,8 +204,9 @@ class StepGraph:
         check(lib().sar_graph_launch_host(self.h, _ptr(inp), _ptr(logits_out), _ptr(hidden_out), _stream(stream)))
 
     def launch_host_tokens(self, inp, tokens_out, stream=None) -> None:
-        """Host input in, the captured step, each logits row's greedy pick out
-        (host int32 [R], synchronous)."""
+        """Host input in, the captured step, each logits row's pick out (host
+        int32 [R], synchronous): greedy, or under ``set_controls``, where -1
+        stands for a row whose mask leaves no token."""
         check(lib().sar_graph_launch_host_tokens(self.h, _ptr(inp), ctypes.cast(_ptr(tokens_out), _lib.P_i32),
                                                  _stream(stream)))
 

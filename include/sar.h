@@ -243,12 +243,13 @@ int sar_graph_launch(sar_graph* g, void* stream);
  * Pinned host memory makes the copies asynchronous to the host. */
 int sar_graph_launch_host(sar_graph* g, const void* in, float* logits_out, float* hidden_out, void* stream);
 
-/* The captured step with HOST buffers, sampled greedily on the device: copies
- * `in` as sar_graph_launch_host does, runs the graph, picks each captured
- * logits row's argmax (as sar_sample_greedy: lowest index on ties) into the
- * graph's own device array and copies the R token ids to `tokens_out` (host
- * int32 [R], the rows of sar_batch's logits order); returns once they are in
- * host memory.  The logits must have been captured.  This is a serving step's
+/* The captured step with HOST buffers, sampled on the device: copies `in` as
+ * sar_graph_launch_host does, runs the graph, picks each captured logits row's
+ * token into the graph's own device array (its argmax as sar_sample_greedy,
+ * lowest index on ties; under sar_graph_set_controls as sar_logits_control, which
+ * gives -1 where a mask leaves no token) and copies the R token ids to
+ * `tokens_out` (host int32 [R], the rows of sar_batch's logits order); returns
+ * once they are in host memory.  The logits must have been captured.  This is a serving step's
  * round trip: the host needs the next tokens, not the logits. */
 int sar_graph_launch_host_tokens(sar_graph* g, const void* in, int32_t* tokens_out, void* stream);
 
@@ -257,7 +258,7 @@ int sar_graph_launch_host_tokens(sar_graph* g, const void* in, int32_t* tokens_o
  * on the graph's own copy stream (created on first use) once the graph's
  * previous enqueued step has ended, and can therefore run while other work
  * computes on `stream`; the captured step waits for it on `stream`, then the
- * greedy picks and their copy into `tokens_out` follow there.  Returns once
+ * picks and their copy into `tokens_out` follow there.  Returns once
  * everything is enqueued.  `in` must stay unchanged and `tokens_out` unread
  * until sar_graph_wait(g) returns.  Steps enqueued on one stream run in
  * order; a sar_graph_update of another graph may be called in between (its
