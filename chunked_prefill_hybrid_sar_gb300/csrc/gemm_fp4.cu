@@ -36,6 +36,12 @@ constexpr int kSmemPerSm = 233472;         // 228 KB
 constexpr int kSmemLimit = 232448;         // 227 KB
 constexpr int kBarBytes = 256;
 constexpr int kPairThreads = 320;
+// The pair tiling asks L2 for the residual ahead of the tile's MMAs up to this many
+// slabs.  With and without, in us: 8192 x 7168, K = 4096 141 and 157, 6144 148 and
+// 163, 7168 (28 slabs) 161 and 166, 7680 170 and 167, 8192 179 and 169, 20480 361
+// and 344; 8192 x 14336, K = 7168 304 and 314, 7680 324 and 319; 2048 x 4096 within
+// 3% either way from 6144 on.
+constexpr int kPrefetchSlabs = 28;
 // Staging of one epilogue warp of the pair tiling: two boxes of 2 KB, or (SwiGLU)
 // 16 tokens x 32 columns of fp32 from its partner and two boxes of 1 KB.
 constexpr int kWarpOut = 4096;
@@ -592,10 +598,9 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       const int n0 = w.nt * 256 + rank * 128 + q * 32;  // this warp's first weight row
       const int row = n0 + lane;
       const bool adds = EPI == SAR_EPI_RESIDUAL && p.tma_out && p.c == p.r;  // added in L2
-      if (EPI == SAR_EPI_RESIDUAL && !adds && p.slabs <= 32) {
-        // the residual's lines are on their way to L2 while the MMAs run (8192 x
-        // 14336, K = 4096: 304 -> 262 us; at K = 20480 they came so early that some
-        // had left L2 again: 8192 x 7168 372 -> 391 us, hence the limit)
+      if (EPI == SAR_EPI_RESIDUAL && !adds && p.slabs <= kPrefetchSlabs) {
+        // the residual's lines are on their way to L2 while the MMAs run; over a long
+        // K they come so early that some have left L2 again when they are read
         for (int e = lane; e < min(128, p.M - m0); e += 32)
           if (n0 < p.N) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.r + (size_t)(m0 + e) * p.N + n0));
       }
