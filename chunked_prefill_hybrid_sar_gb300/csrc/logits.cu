@@ -350,11 +350,13 @@ __device__ __noinline__ Best finish_repeated(const T* x, T* y, const int32_t* to
 // Logits, token state and mask words come in tiles of 8192 tokens by bulk copies
 // of a warp of its own, two tiles at a time: with ordinary loads a thread's
 // registers hold too little of what has to be on its way (256 x 64000 fp32, pick
-// only: 30 us, and 15.5 so).  With everything on and the logits written that size
-// takes 36 us, 4.5 TB/s.  A further tile costs what HBM takes (7.0 TB/s from 32768
-// to 65536 tokens a row); a CTA's start, first loads and join cost about 6 us, and
-// 256 rows leave 104 SMs with two CTAs and 48 with one.  One row of 32000, eight
-// CTAs: 6.0 us, the chain of indexes, state, a cluster's join and a write.
+// only: 30 us, and 15.4 so).  With everything on and the logits written that size
+// takes 36 us, 4.5 TB/s.  A further tile costs what reading HBM takes (256 rows,
+// penalties and pick, inputs that rotate through 400 MB and more: 15.9 us at 32768
+// tokens, 22.8 at 65536, so 7.2 TB/s of logits and state between them); a CTA's
+// start, first loads and join cost about 6 us, and 256 rows leave 104 SMs with two
+// CTAs and 48 with one.  One row of 32000, eight CTAs: 6.1 us, the chain of indexes,
+// state, a cluster's join and a write.
 //
 // Biases come as a list per row.  Their tokens are marked in a bitmap of the
 // stretch; the dense pass leaves marked tokens as they are, and the list's

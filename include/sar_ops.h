@@ -158,8 +158,11 @@ enum {
  *                     of 128); C [M, N / 2] = silu(gate) * up in `storage`
  *   SAR_EPI_F32       C fp32 [M, N]
  * C and R are contiguous; N a multiple of 4 and 16-byte aligned rows are faster.
- * Sums are fp32; the result does not depend on timing.  Async on `stream`;
- * device-side failures are read with sar_op_sync_status(). */
+ * Sums are fp32 as the tensor cores form them: where one does not fit 24 bits they
+ * cut it off instead of rounding it, which costs up to 2^-23 of the products'
+ * magnitudes per 64 columns; K ranges are then added in fp32.  The result does not
+ * depend on timing.  Async on `stream`; device-side failures are read with
+ * sar_op_sync_status(). */
 int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const void* w_scales, void* c,
                     const void* residual, int32_t M, int32_t N, int32_t K, float alpha, int32_t epilogue, int32_t format,
                     int32_t variant, int32_t storage, void* stream);
