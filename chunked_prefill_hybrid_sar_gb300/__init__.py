@@ -7,6 +7,7 @@ tensors (device memory and streams) and host lists into the C ABI of
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 from . import _lib
@@ -22,6 +23,7 @@ from ._lib import (SAR_EPI_F32, SAR_EPI_RESIDUAL, SAR_EPI_STORE, SAR_EPI_SWIGLU,
 __all__ = ["Model", "KVCache", "Scheduler", "Batch", "StepGraph", "SarError", "lib", "check", "gemm", "rmsnorm",
            "fp4_quantize", "fp4_dequantize", "fp4_scale_bytes", "gemm_fp4", "SAR_FP4_NV",
            "SAR_FP4_MX", "LogitControls", "logits_control", "token_state_add",
+           "KV8Cache", "page_map", "qk_norm_rope", "kv8_attention", "kv8_attention_workspace",
            "op_sync_status", "op_wait_check",
            "launch_count", "KERNEL_KINDS", "SAR_IN_HIDDEN", "SAR_IN_TOKENS", "SAR_STORAGE_F16",
            "SAR_STORAGE_BF16", "storage_dtype"]
@@ -620,3 +622,197 @@ def token_state_add(state, slots, offsets, tokens, vocab: int | None = None, pro
     check(lib().sar_token_state_add(state.data_ptr(), state.stride(0) if n_slots > 1 else cols, n_slots, vocab,
                                     slots.data_ptr(), n, offsets.data_ptr(), tokens.data_ptr(), tokens.numel(),
                                     _ptr(prompt_lens), 1 if reset else 0, st))
+
+
+# ---- KV cache in 8 bits ----------------------------------------------------------
+
+
+class KV8Cache:
+    """A layer's paged cache in 8 bits (``sar_kv8``): a handle over device tensors.
+
+    k_codes, v_codes    uint8 [pages, kv heads, page size, head_dim], e4m3 codes
+    k_scales, v_scales  fp32 [pages, kv heads], a scale for each page and head
+    """
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales):
+        import torch
+        for t, dtype in ((k_codes, torch.uint8), (v_codes, torch.uint8), (k_scales, torch.float32), (v_scales, torch.float32)):
+            if t.dtype is not dtype or not t.is_contiguous():
+                raise ValueError("KV8Cache: codes must be contiguous uint8, scales contiguous float32")
+        if k_codes.dim() != 4 or v_codes.shape != k_codes.shape:
+            raise ValueError("KV8Cache: codes must be [pages, kv heads, page size, head_dim], keys as values")
+        if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
+            raise ValueError("KV8Cache: scales must be [pages, kv heads]")
+        _launch_stream("KV8Cache", 0, k_codes, v_codes, k_scales, v_scales)
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
+        self.device = k_codes.get_device()
+        self.c = _lib.sar_kv8(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+                              *k_codes.shape)
+
+    @classmethod
+    def empty(cls, num_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KV8Cache":
+        """A cache of its own tensors, zeroed."""
+        import torch
+        codes = [torch.zeros(num_pages, n_kv_heads, page_size, head_dim, dtype=torch.uint8, device=device) for _ in range(2)]
+        scales = [torch.zeros(num_pages, n_kv_heads, dtype=torch.float32, device=device) for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def _int32(what: str, t, least: int, name: str) -> int:
+    import torch
+    if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < least:
+        raise ValueError(f"{what}: {name} must be contiguous int32, {least} long at least")
+    return t.data_ptr()
+
+
+def _tables(what: str, t, n: int) -> int:
+    """The row stride of block tables."""
+    import torch
+    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: block_tables must be two-dimensional int32 with adjacent columns, a row per request")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, positions, slots, page_size: int,
+             lens_out=None, free_count_out=None, stream=None) -> None:
+    """Block tables and slot maps from request lengths, on the device: pages for
+    ``new_lens`` more tokens of each request (-1: it has ended and gives its pages
+    back) from the stack ``free_pages`` [pages of the cache], whose first
+    ``free_count`` are free; ``row_offsets`` [n + 1], ``positions`` and ``slots``
+    [rows] of the step's rows.  ``lens_out`` and ``free_count_out`` default to ``lens``
+    and ``free_count``, in place; see ``sar_page_map``."""
+    what, n = "page_map", lens.numel()
+    lens_out = lens if lens_out is None else lens_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    stride = _tables(what, block_tables, n)
+    if block_tables.shape[0] > 1 and stride < block_tables.shape[1]:
+        raise ValueError("page_map: rows of block_tables overlap")
+    rows = positions.numel()
+    a = _lib.sar_page_map_args(
+        _int32(what, lens, n, "lens"), _int32(what, new_lens, n, "new_lens"), _int32(what, lens_out, n, "lens_out"),
+        block_tables.data_ptr(), _int32(what, free_pages, 1, "free_pages"), _int32(what, free_count, 1, "free_count"),
+        _int32(what, free_count_out, 1, "free_count_out"), _int32(what, row_offsets, n + 1, "row_offsets"),
+        _int32(what, positions, rows, "positions"), _int32(what, slots, rows, "slots"), n, stride, page_size,
+        free_pages.numel(), rows)
+    st = _launch_stream(what, stream, lens, new_lens, lens_out, block_tables, free_pages, free_count, free_count_out,
+                        row_offsets, positions, slots)
+    check(lib().sar_page_map(ctypes.byref(a), st))
+
+
+def qk_norm_rope(q, k, q_out, head_dim: int, positions=None, v=None, k_out=None, cache: "KV8Cache | None" = None,
+                 slots=None, q_gain=None, k_gain=None, eps: float = 1e-5, rope_base: float = 10000.0, stream=None) -> None:
+    """q_out (and k_out) = the heads of the rows q [rows, heads * head_dim] (and k),
+    normalised where there is a gain (fp32 [head_dim]) and rotated to ``positions``
+    (int32 [rows]); with a ``cache``, k and v also go into it at ``slots`` (int32
+    [rows], -1: not).  ``q`` and ``q_out`` may be None; see ``sar_qk_norm_rope``."""
+    import torch
+    what = "qk_norm_rope"
+    if q is None and k is None:
+        raise ValueError("qk_norm_rope: neither queries nor keys")
+    a = _lib.sar_qk_rows()
+    a.head_dim = head_dim
+    rows, cols, ld, kind = _rows(what, k if q is None else q)
+    a.rows, a.type = rows, kind
+    for name, t, out in (("q", q, q_out), ("k", k, k_out), ("v", v, None)):
+        if t is None:
+            if out is not None:
+                raise ValueError(f"qk_norm_rope: {name}_out without {name}")
+            continue
+        n, cols, ld, t_kind = _rows(what, t)
+        if n != rows or t_kind != kind or cols % head_dim:
+            raise ValueError("qk_norm_rope: q, k and v must have the same rows and type, and whole heads")
+        setattr(a, name, t.data_ptr())
+        setattr(a, "ld" + name, ld)
+        if name == "q":
+            a.n_q_heads = cols // head_dim
+        elif name == "k":
+            a.n_kv_heads = cols // head_dim
+        elif k is None or cols != k.shape[1]:
+            raise ValueError("qk_norm_rope: v must have k's heads")
+    a.out_type = kind if kind != _lib.SAR_TYPE_F32 else _lib.SAR_TYPE_BF16
+    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is None:
+            continue
+        n, cols, ld, a.out_type = _rows(what, t)
+        if (n, cols) != tuple(like.shape):
+            raise ValueError(f"qk_norm_rope: {name} must have its rows' shape")
+        setattr(a, name, t.data_ptr())
+        setattr(a, "ld" + name, ld)
+    if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
+        raise ValueError("qk_norm_rope: q_out and k_out must have one type")
+    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
+        if t is not None:
+            if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != head_dim:
+                raise ValueError("qk_norm_rope: gains must be contiguous float32, one per dim of a head")
+            setattr(a, name, t.data_ptr())
+    if positions is not None:
+        a.positions = _int32(what, positions, rows, "positions")
+    if cache is not None:
+        if slots is None or v is None or k is None:
+            raise ValueError("qk_norm_rope: a cache needs k, v and slots")
+        a.slots = _int32(what, slots, rows, "slots")
+    a.eps, a.rope_base = eps, rope_base
+    st = _launch_stream(what, stream, q, k, v, q_out, k_out, q_gain, k_gain, positions, slots)
+    if cache is not None and cache.device != (k if q is None else q).get_device():
+        raise ValueError("qk_norm_rope: the cache is on another device")
+    check(lib().sar_qk_norm_rope(ctypes.byref(a), ctypes.byref(cache.c) if cache is not None else None, st))
+
+
+def _kv8_batch(cache: KV8Cache, q, n: int, max_rows, max_len):
+    what = "kv8_attention"
+    rows, cols, ld, kind = _rows(what, q)
+    if kind == _lib.SAR_TYPE_F32 or cols % cache.head_dim:
+        raise ValueError("kv8_attention: q must be float16 or bfloat16, with whole heads of the cache's head_dim")
+    b = _lib.sar_kv8_batch()
+    b.q, b.ldq, b.rows, b.n, b.n_q_heads = q.data_ptr(), ld, rows, n, cols // cache.head_dim
+    b.storage = kind
+    b.max_rows = max(1, rows) if max_rows is None else max_rows
+    b.max_len = 0 if max_len is None else max_len
+    return b
+
+
+def kv8_attention_workspace(cache: KV8Cache, q, n: int, max_rows: int | None = None, max_len: int | None = None) -> int:
+    """Bytes of workspace of ``kv8_attention`` for rows like ``q`` of ``n`` sequences."""
+    out = ctypes.c_int64()
+    check(lib().sar_kv8_attention_workspace(ctypes.byref(_kv8_batch(cache, q, n, max_rows, max_len)),
+                                            ctypes.byref(cache.c), ctypes.byref(out)))
+    return out.value
+
+
+def kv8_attention(q, cache: KV8Cache, row_offsets, lens, block_tables, out, max_rows: int | None = None,
+                  max_len: int | None = None, window: int = 0, scale: float = 0.0, workspace=None, stream=None) -> None:
+    """out = attention of the rows q [rows, heads * head_dim] over the 8-bit cache:
+    sequence i's rows ``row_offsets[i] .. row_offsets[i + 1]`` are the last of its
+    ``lens[i]`` tokens, in the pages of ``block_tables[i]``.  ``max_rows`` bounds a
+    sequence's rows (1: single tokens alone), ``max_len`` is about the longest length.
+    ``workspace`` (uint8, ``kv8_attention_workspace`` bytes) belongs to one call at a
+    time; None: allocated for the call; see ``sar_kv8_attention``."""
+    import torch
+    what = "kv8_attention"
+    n = lens.numel()
+    b = _kv8_batch(cache, q, n, max_rows, max_len)
+    rows, cols, b.ldo, kind = _rows(what, out)
+    if (rows, cols, kind) != (b.rows, q.shape[1], b.storage):
+        raise ValueError("kv8_attention: out must have q's shape and type")
+    b.out = out.data_ptr()
+    b.row_offsets = _int32(what, row_offsets, n + 1, "row_offsets")
+    b.lens = _int32(what, lens, n, "lens")
+    b.bt_stride = _tables(what, block_tables, n)
+    b.block_tables = block_tables.data_ptr()
+    b.window, b.scale = window, scale
+    st = _launch_stream(what, stream, q, out, row_offsets, lens, block_tables, workspace)
+    if cache.device != q.get_device():
+        raise ValueError("kv8_attention: the cache is on another device")
+    if workspace is None and b.rows and n:
+        need = ctypes.c_int64()
+        check(lib().sar_kv8_attention_workspace(ctypes.byref(b), ctypes.byref(cache.c), ctypes.byref(need)))
+        # (allocated under the stream that it is used on, which the caching allocator ties it to)
+        with contextlib.nullcontext() if stream is None else torch.cuda.stream(
+                torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
+            workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
+    if workspace is not None:
+        if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("kv8_attention: workspace must be contiguous uint8")
+        b.workspace, b.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    check(lib().sar_kv8_attention(ctypes.byref(b), ctypes.byref(cache.c), st))

@@ -86,6 +86,32 @@ class sar_logit_controls(ctypes.Structure):
                 ("count_picks", i32)]
 
 
+class sar_kv8(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("k_codes", "v_codes", "k_scales", "v_scales")] + [
+        (n, i32) for n in ("num_pages", "n_kv_heads", "page_size", "head_dim")]
+
+
+class sar_page_map_args(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("lens", "new_lens", "lens_out", "block_tables", "free_pages", "free_count",
+                                  "free_count_out", "row_offsets", "positions", "slots")] + [
+        (n, i32) for n in ("n", "bt_stride", "page_size", "num_pages", "max_rows")]
+
+
+class sar_qk_rows(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("q", "k", "v", "q_out", "k_out")] + [
+        (n, i64) for n in ("ldq", "ldk", "ldv", "ldq_out", "ldk_out")] + [
+        (n, vp) for n in ("q_gain", "k_gain", "positions", "slots")] + [
+        (n, i32) for n in ("rows", "n_q_heads", "n_kv_heads", "head_dim", "type", "out_type")] + [
+        ("eps", f32), ("rope_base", f32)]
+
+
+class sar_kv8_batch(ctypes.Structure):
+    _fields_ = [(n, vp) for n in ("q", "out")] + [("ldq", i64), ("ldo", i64)] + [
+        (n, vp) for n in ("row_offsets", "lens", "block_tables", "workspace")] + [("workspace_bytes", i64)] + [
+        (n, i32) for n in ("rows", "n", "n_q_heads", "bt_stride", "storage", "max_rows", "max_len", "window")] + [
+        ("scale", f32)]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "sar_last_error": (ctypes.c_char_p, []),
@@ -130,6 +156,10 @@ SIGNATURES = {
     "sar_op_fp4_quantize": (i32, [vp, i64, i32, i32, i32, i32, f32, vp, vp, vp]),
     "sar_op_fp4_dequantize": (i32, [vp, vp, i32, i32, i32, f32, vp, i64, i32, vp]),
     "sar_op_gemm_fp4": (i32, [vp, vp, vp, vp, vp, vp, i32, i32, i32, f32, i32, i32, i32, i32, vp]),
+    "sar_page_map": (i32, [ctypes.POINTER(sar_page_map_args), vp]),
+    "sar_qk_norm_rope": (i32, [ctypes.POINTER(sar_qk_rows), ctypes.POINTER(sar_kv8), vp]),
+    "sar_kv8_attention_workspace": (i32, [ctypes.POINTER(sar_kv8_batch), ctypes.POINTER(sar_kv8), ctypes.POINTER(i64)]),
+    "sar_kv8_attention": (i32, [ctypes.POINTER(sar_kv8_batch), ctypes.POINTER(sar_kv8), vp]),
     "sar_plan_inspect": (i32, [ctypes.POINTER(sar_dims), i32, i32, i32, i32, ctypes.POINTER(sar_batch), P_i32,
                                P_i32, i64, ctypes.POINTER(i64)]),
     "sar_model_debug_buffer": (i32, [vp, i32, ctypes.POINTER(vp)]),

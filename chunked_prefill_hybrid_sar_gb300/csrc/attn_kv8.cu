@@ -1,0 +1,789 @@
+// Attention of single tokens over the 8-bit paged cache.
+//
+// Bound by the cache's bytes: 2 D of them per key and KV head, for 4 D G flops.
+//
+// All (sequence, KV head) units' keys, in blocks of 32, form one line, of which every
+// CTA takes an equal stretch, whatever the lengths.  Where a stretch begins or ends
+// inside a unit, the CTA writes that piece unnormalised, and a second kernel joins a
+// unit's pieces; so a call of a few long sequences and one of many short ones both
+// fill the machine.  The plan is three prefix sums' worth of arithmetic on the
+// lengths, formed by every CTA itself.
+//
+// Inside a CTA four warps take the stretch's blocks in turn, each with a ring of
+// blocks of its own, filled by TMA with the 128-byte swizzle across unit ends, so
+// the stream does not stop where a unit does.  Keys are the rows of the products:
+// S^T = K Q^T has 16 keys x 8 heads a tile and O^T = V^T P^T 16 dims x 8 heads, so a
+// group of up to eight heads wastes half as much as it would as the rows.  Codes
+// turn to fp16 in registers, exactly, on their way into the products; the order of
+// the dims inside a K = 16 step is free, and taken so that a lane's 16 bytes of a key
+// are its operands.  V's bytes are turned by ldmatrix over pairs of dims.
+//
+// Scales cost nothing: with t = S k_scale scale + log2(v_scale) in base 2 and m the
+// running maximum of t, 2^(t - m) weighs V's codes, and the sum takes it times
+// 1 / v_scale.
+#include <algorithm>
+
+#include "kv8.cuh"
+#include "tc05.cuh"
+
+namespace sar {
+
+namespace {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecKeys = 32;    // keys of a block
+constexpr int kDecStages = 3;   // blocks of a warp's ring
+constexpr int kDecHeads = 8;    // query heads of a KV head: the products' columns
+constexpr int kDecPerSm = 2;
+constexpr int kDecLeast = 8;    // blocks of a CTA's stretch at least, where there are so few
+
+struct DecArgs {
+  Kv8Attn a;
+  int64_t* before;   // [n + 1] blocks of a KV head before each sequence
+  float* parts;      // [2 * CTAs][8][D]: a CTA's first and last piece
+  float2* parts_ml;  // [2 * CTAs][8] maximum and sum
+  int vec_q, vec_o;
+};
+
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+// The transpose of an 8 x 8 matrix of 16-bit elements, a row's pair to a lane.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 2^x by the SFU (relative error 2^-22; 2^-inf = 0): a weight that is rounded to
+// fp16 next.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A sequence of one row, as the decode kernel sees it.
+struct DecSeq {
+  int row, len, lo;  // its row, its length, the oldest key it sees
+  int blocks;        // of 32 keys, from the one that holds lo; one (without keys) where it is empty; 0: not this kernel's
+};
+__device__ __forceinline__ DecSeq dec_sequence(const Kv8Attn& a, int i) {
+  DecSeq s;
+  int rows;
+  const bool ok = kv8_sequence(a, i, s.row, rows, s.len);
+  s.lo = a.window > 0 ? max(0, s.len - a.window) : 0;
+  s.blocks = ok && rows == 1 ? max(1, (s.len + kDecKeys - 1) / kDecKeys - s.lo / kDecKeys) : 0;
+  return s;
+}
+
+// The stretches: CTA c of C has blocks [T c / C, T (c + 1) / C).
+__device__ __forceinline__ int64_t dec_ctas(int64_t T, int64_t grid) {
+  return max((int64_t)1, min(grid, T / kDecLeast));
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
+    kv8_decode_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                      const __grid_constant__ DecArgs d) {
+  constexpr int BLK = kDecKeys * D;          // bytes of a block's keys
+  constexpr int STAGE = 2 * BLK;
+  constexpr int NT = D / 16;                 // tiles of 16 dims
+  constexpr int OWN = NT / kDecWarps;        // of which a warp joins so many
+  constexpr int HALVES = D / 64;
+  constexpr int kThreads = kDecWarps * 32;
+  const Kv8Attn& a = d.a;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ float rec[kDecWarps][NT - OWN][4][32];  // tiles for the other warps to join
+  __shared__ float ml_s[kDecWarps][kDecHeads][2];
+  __shared__ float scale_s[kDecWarps][kDecStages][2][2];  // a block's two pages: key, value scale; key < 0: no page
+  __shared__ uint64_t bars_s[kDecWarps][kDecStages];
+  __shared__ int64_t sums_s[kThreads];
+  __shared__ int64_t first_s[2];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c4 = lane & 3;
+  const uint32_t ring = smem_u32(smem) + warp * kDecStages * STAGE;
+  if (lane == 0) {
+    for (int s = 0; s < kDecStages; ++s) mbar_init(smem_u32(&bars_s[warp][s]), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmk);
+    tma_prefetch_desc(&tmv);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- this CTA's stretch ----
+  const int per = (a.n + kThreads - 1) / kThreads;
+  const int i0 = min(a.n, (int)threadIdx.x * per), i1 = min(a.n, i0 + per);
+  int64_t mine = 0;
+  for (int i = i0; i < i1; ++i) {
+    mine += dec_sequence(a, i).blocks;
+    if (blockIdx.x == 0) {  // (once for the call)
+      int r0, rows, len;
+      if (!kv8_sequence(a, i, r0, rows, len)) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SEQUENCE, i);
+    }
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) sums_s[warp] = incl;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) incl += sums_s[w];
+    total += sums_s[w];
+  }
+  const int64_t excl = incl - mine;
+  if (blockIdx.x == 0) {
+    int64_t at = excl;
+    for (int i = i0; i < i1; ++i) {
+      d.before[i] = at;
+      at += dec_sequence(a, i).blocks;
+    }
+    if (threadIdx.x == 0) d.before[a.n] = total;
+  }
+  const int64_t all = total * a.kvh;
+  const int64_t C = dec_ctas(all, gridDim.x);
+  if (all == 0 || blockIdx.x >= C) return;
+  const int64_t b0 = all * blockIdx.x / C, b1 = all * (blockIdx.x + 1) / C;
+  if (b0 >= excl * a.kvh && b0 < incl * a.kvh) {
+    int64_t at = excl;
+    int i = i0;
+    while (true) {
+      const int nb = dec_sequence(a, i).blocks;
+      if (b0 < (at + nb) * a.kvh) break;
+      at += nb;
+      ++i;
+    }
+    first_s[0] = i;
+    first_s[1] = at * a.kvh;
+  }
+  __syncthreads();
+
+  // A place on the line: block b of sequence seq, whose blocks begin at `start`.
+  struct Place {
+    int64_t b, start;
+    int seq;
+    DecSeq s;
+  };
+  auto settle = [&](Place& p) {  // to the sequence that holds p.b (p.b < b1)
+    while (p.b >= p.start + (int64_t)p.s.blocks * a.kvh) {
+      p.start += (int64_t)p.s.blocks * a.kvh;
+      p.s = dec_sequence(a, ++p.seq);
+    }
+  };
+  Place here;
+  here.b = b0;
+  here.start = first_s[1];
+  here.seq = (int)first_s[0];
+  here.s = dec_sequence(a, here.seq);
+
+  // ---- loads: a warp's blocks are b0 + warp, + 4, ... ----
+  Place ahead = here;
+  ahead.b += warp;
+  int kh_a = 0, key_a = 0, page_a = -1;
+  // the page of the next block's 16 keys (lane 0: the first, lane 1: the second)
+  auto look_up = [&]() {
+    if (ahead.b >= b1) return;
+    settle(ahead);
+    const int64_t j = ahead.b - ahead.start;
+    kh_a = (int)(j / ahead.s.blocks);
+    key_a = (ahead.s.lo / kDecKeys + (int)(j - (int64_t)kh_a * ahead.s.blocks)) * kDecKeys;
+    page_a = -1;
+    const int key = key_a + 16 * lane;
+    if (lane < 2 && key < ahead.s.len && key + (a.shift > 4 ? kDecKeys : 16) > ahead.s.lo) {  // (pages behind a window may be gone)
+      page_a = a.bt[(int64_t)ahead.seq * a.bt_stride + (key >> a.shift)];
+      if (page_a < 0 || page_a >= a.num_pages) {
+        report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page_a);
+        page_a = -1;
+      }
+    }
+  };
+  auto issue = [&](int s) {  // that block into stage s, and the look-up of the one after
+    const uint32_t bar = smem_u32(&bars_s[warp][s]), dst = ring + s * STAGE;
+    // pages of 32 keys and up: one box holds the block
+    const bool whole = a.shift > 4;
+    const int p0 = __shfl_sync(0xffffffffu, page_a, 0), p1 = __shfl_sync(0xffffffffu, page_a, 1);
+    const int boxes = whole ? (p0 >= 0) : (p0 >= 0) + (p1 >= 0);
+    const uint32_t box = whole ? BLK : BLK / 2;
+    if (lane < 2) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    if (lane == 0) {
+      if (boxes)
+        mbar_expect_tx(bar, 2 * boxes * box);
+      else
+        mbar_arrive(bar);
+    }
+    __syncwarp();
+    if (lane < 2) {
+      const int ps = 1 << a.shift;
+      if (page_a >= 0) {
+        const int64_t unit = (int64_t)page_a * a.kvh + kh_a;
+        if (lane == 0 || !whole) {
+          // (rows of the map are 128 bytes: one key, or two of 64 dims)
+          const int row = (int)((unit * ps + ((key_a + 16 * lane) & (ps - 1))) * D / 128);
+          tma_load_2d(dst + lane * (BLK / 2), &tmk, 0, row, bar);
+          tma_load_2d(dst + BLK + lane * (BLK / 2), &tmv, 0, row, bar);
+        }
+        const uint32_t to = smem_u32(&scale_s[warp][s][lane][0]);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(a.k_scales + unit) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + 4), "l"(a.v_scales + unit) : "memory");
+      } else {
+        scale_s[warp][s][lane][0] = -1.f;
+      }
+    }
+    ahead.b += kDecWarps;
+    look_up();
+  };
+  look_up();
+  int issued = 0, consumed = 0;
+#pragma unroll
+  for (int s = 0; s < kDecStages; ++s) {
+    if (ahead.b < b1) {
+      issue(s);
+      ++issued;
+    }
+    cp_async_commit();
+  }
+
+  bool alive = true;  // false once a wait gave up: the CTA's barriers stay matched
+  bool first_piece = true;
+  int64_t next = b0 + warp;  // this warp's next block
+  for (int64_t b = b0; b < b1;) {
+    // ---- one unit's piece: blocks [b, e) ----
+    here.b = b;
+    settle(here);
+    const DecSeq& sq = here.s;
+    const int kh = (int)((b - here.start) / sq.blocks);
+    const int64_t u0 = here.start + (int64_t)kh * sq.blocks, u1 = u0 + sq.blocks;
+    const int64_t e = min(b1, u1);
+
+    // queries: head g, its dims in the order of the products' steps, scaled by a power of
+    // two so that the largest lies in [1, 2): bf16's range goes into fp16's
+    uint32_t qf[HALVES * 4][2];
+    float fac;
+    {
+      uint32_t w[HALVES * 8];
+      const bool live = g < a.G;
+      const T* qp = static_cast<const T*>(a.q) + (int64_t)sq.row * a.ldq + (int64_t)(kh * a.G + (live ? g : 0)) * D;
+#pragma unroll
+      for (int h = 0; h < HALVES; ++h) {
+        const T* p = qp + 16 * (HALVES * c4 + h);
+        if (d.vec_q) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8);
+          w[8 * h] = x.x, w[8 * h + 1] = x.y, w[8 * h + 2] = x.z, w[8 * h + 3] = x.w;
+          w[8 * h + 4] = y.x, w[8 * h + 5] = y.y, w[8 * h + 6] = y.z, w[8 * h + 7] = y.w;
+        } else {
+          const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) w[8 * h + k] = u[2 * k] | (uint32_t)u[2 * k + 1] << 16;
+        }
+      }
+      float pow2 = 1.f;
+      if constexpr (Elem<T>::kMmaFormat == 1) {
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < HALVES * 8; ++k) m = fmaxf(m, fmaxf(fabsf(Elem<T>::lo(w[k])), fabsf(Elem<T>::hi(w[k]))));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        // (an exponent whose inverse is a normal number too; infinities stay what they are)
+        const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 253u);
+        pow2 = __uint_as_float(ex << 23);
+        const float inv = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+        for (int k = 0; k < HALVES * 8; ++k) w[k] = pack_f16(Elem<T>::lo(w[k]) * inv, Elem<T>::hi(w[k]) * inv);
+      }
+#pragma unroll
+      for (int k = 0; k < HALVES * 4; ++k) qf[k][0] = live ? w[2 * k] : 0u, qf[k][1] = live ? w[2 * k + 1] : 0u;
+      fac = pow2 * a.scale;
+    }
+    // of the columns' heads, 2 c4 and 2 c4 + 1
+    const float fac0 = __shfl_sync(0xffffffffu, fac, 8 * c4), fac1 = __shfl_sync(0xffffffffu, fac, 8 * c4 + 4);
+
+    float o[NT][4];
+#pragma unroll
+    for (int c = 0; c < NT; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    for (; next < e; next += kDecWarps) {
+      const int s = consumed % kDecStages;
+      cp_async_wait<kDecStages - 1>();
+      if (alive) {
+        int got = 0;
+        if (lane == 0)
+          got = mbar_wait(smem_u32(&bars_s[warp][s]), (uint32_t)((consumed / kDecStages) & 1), a.err, SITE_KV8_PIPE) ? 1 : 0;
+        alive = __shfl_sync(0xffffffffu, got, 0) != 0;
+      }
+      __syncwarp();
+      ++consumed;
+      if (alive && sq.len > 0) {
+        const int key0 = (sq.lo / kDecKeys + (int)(next - u0)) * kDecKeys;
+        const uint32_t kb = ring + s * STAGE, vb = kb + BLK;
+        float ks[2], lv[2], iv[2];
+        bool page[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          ks[t] = scale_s[warp][s][t][0];
+          const float v = scale_s[warp][s][t][1];
+          page[t] = ks[t] >= 0.f;
+          lv[t] = page[t] ? log2f(v) : 0.f;
+          iv[t] = page[t] ? 1.f / v : 0.f;
+        }
+        const bool edge = key0 < sq.lo || key0 + kDecKeys > sq.len || !page[0] || !page[1];
+        // ---- S^T = K Q^T ----
+        float sc[2][4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+          for (int h = 0; h < HALVES; ++h) {
+            uint4 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              // key k's 16-byte chunk c: rows of 128 bytes hold one key, or two
+              const int k = t * 16 + u * 8 + g;
+              const int row = D == 128 ? k : k >> 1, chunk = D == 128 ? 2 * c4 + h : (k & 1) * 4 + c4;
+              x[u] = lds_u4(kb + row * 128 + ((chunk ^ (row & 7)) << 4));
+            }
+            const uint32_t lo[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, hi[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+              mma_f16(sc[t], from_e4m3x2(lo[w]), from_e4m3x2(hi[w]), from_e4m3x2(lo[w] >> 16), from_e4m3x2(hi[w] >> 16),
+                      qf[4 * h + w][0], qf[4 * h + w][1]);
+          }
+        }
+        // ---- softmax over keys t * 16 + 8 u + g, of heads 2 c4 (even) and 2 c4 + 1 ----
+        float mx0 = m0, mx1 = m1;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float f0 = fac0 * ks[t], f1 = fac1 * ks[t];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            sc[t][2 * u] = fmaf(sc[t][2 * u], f0, lv[t]);
+            sc[t][2 * u + 1] = fmaf(sc[t][2 * u + 1], f1, lv[t]);
+            if (edge) {
+              const int key = key0 + t * 16 + u * 8 + g;
+              if (key < sq.lo || key >= sq.len || !page[t]) sc[t][2 * u] = sc[t][2 * u + 1] = -INFINITY;
+            }
+            mx0 = fmaxf(mx0, sc[t][2 * u]);
+            mx1 = fmaxf(mx1, sc[t][2 * u + 1]);
+          }
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
+        }
+        if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
+          const float r0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - mx0), r1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - mx1);
+#pragma unroll
+          for (int c = 0; c < NT; ++c) o[c][0] *= r0, o[c][1] *= r1, o[c][2] *= r0, o[c][3] *= r1;
+          l0 *= r0;
+          l1 *= r1;
+          m0 = mx0;
+          m1 = mx1;
+        }
+        const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
+        uint32_t pb[2][2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const float p0 = exp2_fast(sc[t][0] - ref0), p1 = exp2_fast(sc[t][1] - ref1);
+          const float p2 = exp2_fast(sc[t][2] - ref0), p3 = exp2_fast(sc[t][3] - ref1);
+          l0 = fmaf(p0 + p2, iv[t], l0);
+          l1 = fmaf(p1 + p3, iv[t], l1);
+          pb[t][0] = transposed(pack_f16(p0, p1));
+          pb[t][1] = transposed(pack_f16(p2, p3));
+        }
+        // ---- O^T += V^T P^T; codes of keys that are not seen count as zero ----
+        uint32_t keep[4];
+        if (edge) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = key0 + 8 * q + 2 * c4;
+            keep[q] = (key >= sq.lo && key < sq.len && page[q >> 1] ? 0xffffu : 0u) |
+                      (key + 1 >= sq.lo && key + 1 < sq.len && page[q >> 1] ? 0xffff0000u : 0u);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          uint32_t v[4];
+          const int row = D == 128 ? lane : lane >> 1, chunk = D == 128 ? c : (lane & 1) * 4 + c;
+          ldsm_x4_t(vb + row * 128 + ((chunk ^ (row & 7)) << 4), v);
+          if (edge) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] &= keep[q];
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = __byte_perm(v[q], 0, 0x3120);  // (two keys of the even dim, two of the odd)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            mma_f16(o[c], from_e4m3x2(v[2 * t]), from_e4m3x2(v[2 * t] >> 16), from_e4m3x2(v[2 * t + 1]),
+                    from_e4m3x2(v[2 * t + 1] >> 16), pb[t][0], pb[t][1]);
+        }
+      }
+      __syncwarp();
+      if (alive && ahead.b < b1) {
+        issue(s);
+        ++issued;
+      }
+      cp_async_commit();
+    }
+
+    // ---- the four warps' pieces joined; warp w joins tiles [w OWN, w OWN + OWN) ----
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, x);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if (g == 0) {
+      ml_s[warp][2 * c4][0] = m0, ml_s[warp][2 * c4][1] = l0;
+      ml_s[warp][2 * c4 + 1][0] = m1, ml_s[warp][2 * c4 + 1][1] = l1;
+    }
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      const int at = c - warp * OWN;
+      if (at >= 0 && at < OWN) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) rec[warp][c < warp * OWN ? c : c - OWN][k][lane] = o[c][k];
+    }
+    __syncthreads();
+    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f, f0[kDecWarps], f1[kDecWarps];
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      M0 = fmaxf(M0, ml_s[w][2 * c4][0]);
+      M1 = fmaxf(M1, ml_s[w][2 * c4 + 1][0]);
+    }
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      const float x0 = ml_s[w][2 * c4][0], x1 = ml_s[w][2 * c4 + 1][0];
+      f0[w] = x0 == -INFINITY ? 0.f : exp2_fast(x0 - M0);
+      f1[w] = x1 == -INFINITY ? 0.f : exp2_fast(x1 - M1);
+      L0 = fmaf(ml_s[w][2 * c4][1], f0[w], L0);
+      L1 = fmaf(ml_s[w][2 * c4 + 1][1], f1[w], L1);
+    }
+    const bool whole_unit = b == u0 && e == u1;
+    const int64_t slot = 2 * (int64_t)blockIdx.x + (first_piece ? 0 : 1);
+    const float inv0 = sq.len == 0 ? 0.f : 1.f / L0, inv1 = sq.len == 0 ? 0.f : 1.f / L1;
+#pragma unroll
+    for (int c = 0; c < NT; ++c) {
+      const int at = c - warp * OWN;
+      if (at < 0 || at >= OWN) continue;
+      float r[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) r[k] = o[c][k] * ((k & 1) ? f1[warp] : f0[warp]);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        if (w == warp) continue;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          r[k] = fmaf(rec[w][c < w * OWN ? c : c - OWN][k][lane], (k & 1) ? f1[w] : f0[w], r[k]);
+      }
+      // dims 16 c + 2 g (r[0], r[1]) and + 1 (r[2], r[3]) of heads 2 c4, 2 c4 + 1
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int head = 2 * c4 + x, dim = 16 * c + 2 * g;
+        if (head >= a.G) continue;
+        if (whole_unit) {
+          const float inv = x ? inv1 : inv0;
+          T* op = static_cast<T*>(a.out) + (int64_t)sq.row * a.ldo + (int64_t)(kh * a.G + head) * D + dim;
+          if (d.vec_o) {
+            *reinterpret_cast<uint32_t*>(op) = Elem<T>::pack(r[x] * inv, r[2 + x] * inv);
+          } else {
+            op[0] = Elem<T>::from(r[x] * inv);
+            op[1] = Elem<T>::from(r[2 + x] * inv);
+          }
+        } else {
+          *reinterpret_cast<float2*>(d.parts + (slot * kDecHeads + head) * D + dim) = make_float2(r[x], r[2 + x]);
+          if (c == 0 && g == 0) d.parts_ml[slot * kDecHeads + head] = make_float2(x ? M1 : M0, x ? L1 : L0);
+        }
+      }
+    }
+    first_piece = false;
+    b = e;
+    __syncthreads();  // (the records are written again)
+  }
+  // no copy is under way when the CTA leaves
+  cp_async_wait<0>();
+  if (lane == 0) {
+    for (int i = consumed; i < issued; ++i)
+      mbar_wait(smem_u32(&bars_s[warp][i % kDecStages]), (uint32_t)((i / kDecStages) & 1), a.err, SITE_KV8_PIPE);
+  }
+}
+
+// Joins the pieces of a unit that several CTAs share, in their order.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ DecArgs d, int grid) {
+  const Kv8Attn& a = d.a;
+  pdl_wait();
+  pdl_launch_dependents();
+  const int kh = blockIdx.y;
+  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+    const int64_t p0 = d.before[i], p1 = d.before[i + 1];
+    if (p1 == p0) continue;
+    const int64_t all = d.before[a.n] * a.kvh, C = dec_ctas(all, grid);
+    const int64_t u0 = p0 * a.kvh + kh * (p1 - p0), u1 = u0 + (p1 - p0);
+    const int64_t c0 = ((u0 + 1) * C - 1) / all, c1 = (u1 * C - 1) / all;  // the CTAs of its first and last block
+    if (c0 == c1) continue;
+    const bool starts = all * c0 / C == u0;
+    const int row = a.off[i];
+    for (int t = threadIdx.x; t < a.G * (D / 4); t += 128) {
+      const int head = t / (D / 4), dim = t % (D / 4) * 4;
+      float M = -INFINITY, L = 0.f;
+      float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int64_t cb = c0; cb <= c1; cb += 4) {
+        float2 ml[4];
+        float4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int64_t c = cb + k;
+          const int64_t at = (2 * c + (c == c0 && !starts ? 1 : 0)) * kDecHeads + head;
+          ml[k] = c <= c1 ? d.parts_ml[at] : make_float2(-INFINITY, 0.f);
+          v[k] = c <= c1 ? *reinterpret_cast<const float4*>(d.parts + at * D + dim) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+        const float f = M == -INFINITY ? 0.f : exp2_fast(M - mn);
+        L *= f;
+        A.x *= f, A.y *= f, A.z *= f, A.w *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float w = ml[k].x == -INFINITY ? 0.f : exp2_fast(ml[k].x - mn);
+          L = fmaf(ml[k].y, w, L);
+          A.x = fmaf(v[k].x, w, A.x);
+          A.y = fmaf(v[k].y, w, A.y);
+          A.z = fmaf(v[k].z, w, A.z);
+          A.w = fmaf(v[k].w, w, A.w);
+        }
+        M = mn;
+      }
+      const float inv = 1.f / L;
+      T* op = static_cast<T*>(a.out) + (int64_t)row * a.ldo + (int64_t)(kh * a.G + head) * D + dim;
+      if (d.vec_o) {
+        reinterpret_cast<uint32_t*>(op)[0] = Elem<T>::pack(A.x * inv, A.y * inv);
+        reinterpret_cast<uint32_t*>(op)[1] = Elem<T>::pack(A.z * inv, A.w * inv);
+      } else {
+        op[0] = Elem<T>::from(A.x * inv), op[1] = Elem<T>::from(A.y * inv);
+        op[2] = Elem<T>::from(A.z * inv), op[3] = Elem<T>::from(A.w * inv);
+      }
+    }
+  }
+}
+
+// Sequences of several rows, one (row, KV head) to a CTA, a key at a time.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv8_rows_kernel(const __grid_constant__ Kv8Attn a) {
+  constexpr int E = D / 32;
+  __shared__ float acc_s[4][kDecHeads][D];
+  __shared__ float ml_s[4][kDecHeads][2];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int row = blockIdx.x, kh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = 0; i < a.n; ++i) {
+    int row0, rows, len;
+    if (!kv8_sequence(a, i, row0, rows, len) || rows < 2 || row < row0 || row >= row0 + rows) continue;
+    const int pos = len - rows + row - row0, lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+    float q[kDecHeads][E], o[kDecHeads][E], m[kDecHeads], l[kDecHeads];
+    for (int h = 0; h < kDecHeads; ++h) {
+      m[h] = -INFINITY, l[h] = 0.f;
+      for (int e = 0; e < E; ++e) {
+        o[h][e] = 0.f;
+        q[h][e] = h < a.G ? Elem<T>::to(static_cast<const T*>(a.q)[row * a.ldq + (int64_t)(kh * a.G + h) * D + lane * E + e]) : 0.f;
+      }
+    }
+    for (int key = lo + warp; key <= pos; key += 4) {
+      const int page = a.bt[i * a.bt_stride + (key >> a.shift)];
+      if (page < 0 || page >= a.num_pages) {
+        report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page);
+        continue;
+      }
+      const int64_t unit = (int64_t)page * a.kvh + kh;
+      const int64_t at = ((unit << a.shift) + (key & ((1 << a.shift) - 1))) * D + lane * E;
+      float k[E], v[E];
+      for (int e = 0; e < E; ++e) {
+        k[e] = e4m3x2_floats(a.k_codes[at + e]).x * a.k_scales[unit];
+        v[e] = e4m3x2_floats(a.v_codes[at + e]).x * a.v_scales[unit];
+      }
+#pragma unroll
+      for (int h = 0; h < kDecHeads; ++h) {
+        if (h >= a.G) break;
+        float s = 0.f;
+        for (int e = 0; e < E; ++e) s = fmaf(q[h][e], k[e], s);
+        s = warp_sum(s) * a.scale;
+        const float mn = fmaxf(m[h], s), f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn), p = exp2f(s - mn);
+        for (int e = 0; e < E; ++e) o[h][e] = fmaf(p, v[e], o[h][e] * f);
+        l[h] = fmaf(l[h], f, p);
+        m[h] = mn;
+      }
+    }
+    for (int h = 0; h < a.G; ++h) {
+      for (int e = 0; e < E; ++e) acc_s[warp][h][lane * E + e] = o[h][e];
+      ml_s[warp][h][0] = m[h], ml_s[warp][h][1] = l[h];
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < a.G * D; t += 128) {
+      const int h = t / D, e = t % D;
+      float M = -INFINITY, L = 0.f, A = 0.f;
+      for (int w = 0; w < 4; ++w) M = fmaxf(M, ml_s[w][h][0]);
+      for (int w = 0; w < 4; ++w) {
+        const float f = ml_s[w][h][0] == -INFINITY ? 0.f : exp2f(ml_s[w][h][0] - M);
+        L = fmaf(ml_s[w][h][1], f, L);
+        A = fmaf(acc_s[w][h][e], f, A);
+      }
+      static_cast<T*>(a.out)[row * a.ldo + (int64_t)(kh * a.G + h) * D + e] = Elem<T>::from(pos < 0 ? 0.f : A / L);
+    }
+    return;
+  }
+}
+
+int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
+
+// The workspace: before, pieces' maxima and sums, pieces.
+struct Space {
+  int64_t before, ml, parts, bytes;
+};
+Space space_of(int n, int head_dim) {
+  const int64_t slots = 2ll * kDecPerSm * num_sms();
+  Space s;
+  s.before = 0;
+  s.ml = up256((n + 1ll) * 8);
+  s.parts = s.ml + up256(slots * kDecHeads * 8);
+  s.bytes = s.parts + slots * kDecHeads * head_dim * 4;
+  return s;
+}
+
+int check_batch(const sar_kv8_batch& b, const sar_kv8* c) {
+  if (!c) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: null cache");
+  SAR_TRY(check_kv8(c, "kv8_attention"));
+  if (b.rows < 0 || b.n < 0 || b.n_q_heads < 1 || b.max_rows < 1 || b.max_len < 0 || b.window < 0)
+    return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: bad sizes");
+  if (b.n_q_heads % c->n_kv_heads || b.n_q_heads / c->n_kv_heads > kDecHeads)
+    return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: query heads are a multiple of the KV heads, at most 8 to each");
+  if (b.rows > 1 << 30 || b.n > 1 << 30 || c->n_kv_heads > 1024)
+    return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: rows, sequences or heads above their limits");
+  return SAR_OK;
+}
+
+template <typename T, int D>
+int launch_kv8(const DecArgs& d, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
+  const int smem = 1024 + kDecWarps * kDecStages * 2 * kDecKeys * D;
+  SAR_TRY(ensure_smem_attr(reinterpret_cast<const void*>(&kv8_decode_kernel<T, D>), smem, "kv8 decode: set smem attribute"));
+  const int grid = kDecPerSm * num_sms();
+  cudaError_t e = launch_pdl(kv8_decode_kernel<T, D>, dim3(grid), dim3(kDecWarps * 32), (size_t)smem, s, tmk, tmv, d);
+  if (e != cudaSuccess) return cuda_error(e, "kv8 decode launch");
+  e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)std::min(d.a.n, 65535), (unsigned)d.a.kvh), dim3(128), 0, s, d, grid);
+  if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
+  count_launches(2);
+  if (d.a.max_rows > 1) {
+    e = launch_pdl(kv8_rows_kernel<T, D>, dim3((unsigned)d.a.rows, (unsigned)d.a.kvh), dim3(128), 0, s, d.a);
+    if (e != cudaSuccess) return cuda_error(e, "kv8 rows launch");
+    count_launches(1);
+  }
+  return SAR_OK;
+}
+
+}  // namespace
+}  // namespace sar
+
+using sar::aligned_to;
+using sar::set_error;
+
+extern "C" {
+
+int sar_kv8_attention_workspace(const sar_kv8_batch* batch, const sar_kv8* cache, int64_t* bytes) try {
+  if (!batch || !bytes) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention_workspace: null pointer");
+  SAR_TRY(sar::check_batch(*batch, cache));
+  *bytes = sar::space_of(batch->n, cache->head_dim).bytes;
+  return SAR_OK;
+} catch (...) {
+  return sar::entry_failed("kv8_attention_workspace");
+}
+
+int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* stream) try {
+  if (!batch) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: null batch");
+  const sar_kv8_batch& b = *batch;
+  SAR_TRY(sar::check_batch(b, cache));
+  if (b.storage != SAR_STORAGE_F16 && b.storage != SAR_STORAGE_BF16)
+    return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: bad storage");
+  if (!(b.scale >= 0.f && b.scale < INFINITY)) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: bad scale");
+  if (b.rows == 0 || b.n == 0) return SAR_OK;
+  if (!b.q || !b.out || !b.row_offsets || !b.lens || !b.block_tables || !b.workspace)
+    return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: null pointer");
+  const int64_t width = (int64_t)b.n_q_heads * cache->head_dim;
+  if (b.ldq < width || b.ldo < width || b.bt_stride < 1)
+    return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: rows shorter than their heads, or no block table");
+  if ((int64_t)b.bt_stride * cache->page_size > INT32_MAX)
+    return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: block tables above 2^31 tokens");
+  if (!aligned_to(b.q, 2) || !aligned_to(b.out, 2) || !aligned_to(b.row_offsets, 4) || !aligned_to(b.lens, 4) ||
+      !aligned_to(b.block_tables, 4) || !aligned_to(b.workspace, 16))
+    return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: array not aligned to its element");
+  const sar::Space sp = sar::space_of(b.n, cache->head_dim);
+  if (b.workspace_bytes < sp.bytes) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: workspace too small");
+  sar::DecArgs d = {};
+  sar::Kv8Attn& a = d.a;
+  a.q = b.q;
+  a.out = b.out;
+  a.ldq = b.ldq;
+  a.ldo = b.ldo;
+  a.off = b.row_offsets;
+  a.lens = b.lens;
+  a.bt = b.block_tables;
+  a.bt_stride = b.bt_stride;
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.k_codes = static_cast<const uint8_t*>(cache->k_codes);
+  a.v_codes = static_cast<const uint8_t*>(cache->v_codes);
+  a.rows = b.rows;
+  a.n = b.n;
+  a.qh = b.n_q_heads;
+  a.kvh = cache->n_kv_heads;
+  a.G = a.qh / a.kvh;
+  a.shift = cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : 6;
+  a.num_pages = cache->num_pages;
+  a.max_rows = b.max_rows;
+  a.window = b.window;
+  a.scale = (b.scale == 0.f ? (float)(1.0 / sqrt((double)cache->head_dim)) : b.scale) * 1.4426950408889634f;
+  SAR_TRY(sar::op_flags(&a.err));
+  uint8_t* ws = static_cast<uint8_t*>(b.workspace);
+  d.before = reinterpret_cast<int64_t*>(ws + sp.before);
+  d.parts_ml = reinterpret_cast<float2*>(ws + sp.ml);
+  d.parts = reinterpret_cast<float*>(ws + sp.parts);
+  d.vec_q = aligned_to(b.q, 16) && b.ldq % 8 == 0;
+  d.vec_o = aligned_to(b.out, 4) && b.ldo % 2 == 0;
+  // the codes as rows of 128 bytes (one key, or two of 64 dims), boxes of up to 32 keys of a page
+  CUtensorMap tmk, tmv;
+  const uint64_t map_rows = (uint64_t)a.num_pages * a.kvh * cache->page_size * cache->head_dim / 128;
+  const uint32_t box = (uint32_t)(std::min(cache->page_size, sar::kDecKeys) * cache->head_dim / 128);
+  SAR_TRY(sar::make_tmap_bytes(&tmk, cache->k_codes, map_rows, 128, box));
+  SAR_TRY(sar::make_tmap_bytes(&tmv, cache->v_codes, map_rows, 128, box));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cache->head_dim == 128)
+    return b.storage == SAR_STORAGE_BF16 ? sar::launch_kv8<__nv_bfloat16, 128>(d, tmk, tmv, s)
+                                         : sar::launch_kv8<__half, 128>(d, tmk, tmv, s);
+  return b.storage == SAR_STORAGE_BF16 ? sar::launch_kv8<__nv_bfloat16, 64>(d, tmk, tmv, s)
+                                       : sar::launch_kv8<__half, 64>(d, tmk, tmv, s);
+} catch (...) {
+  return sar::entry_failed("kv8_attention");
+}
+
+}  // extern "C"

@@ -37,6 +37,13 @@ enum ErrSite {
   SITE_CONTROL_MASK = 74,
   SITE_CONTROL_BIAS = 75,
   SITE_CONTROL_PIPE = 76,
+  SITE_MAP_REQUEST = 80,
+  SITE_MAP_PAGES = 81,
+  SITE_MAP_PAGE = 82,
+  SITE_KV8_SLOT = 83,
+  SITE_KV8_SEQUENCE = 84,
+  SITE_KV8_PAGE = 85,
+  SITE_KV8_PIPE = 86,
 };
 
 // A wait that has not finished after this long gives up (normal waits take

@@ -79,6 +79,11 @@ inline int fp4_tiles(int cols, int format) {
   return (cols + w - 1) / w;
 }
 
+// ---- 8-bit KV cache (qk_rows.cu) --------------------------------------------
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// The cache's pointers and sizes, before anything is launched.
+int check_kv8(const sar_kv8* c, const char* what);
+
 // ---- GEMM (gemm_tc.cu) -----------------------------------------------------
 
 // Encodes a 2D 16-bit (storage type) tensor map over row-major [rows, cols]

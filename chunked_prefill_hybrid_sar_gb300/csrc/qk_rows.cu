@@ -1,0 +1,423 @@
+// Head norms, the rotary embedding and the append to the 8-bit cache, behind a
+// step's QKV projection.
+//
+// A group of head_dim / 8 lanes has a row's head: eight elements a lane, four from
+// each half of the head, so that a rotation pair sits in one lane.  mean(h^2) is a
+// sum over the group.  Angles: position * theta / 2 pi as a fixed-point fraction of
+// a turn, 64 bits that wrap, which reduces any position exactly; then sincospif.
+// They are formed once per row and reused for all of a CTA's heads.
+//
+// Query heads are independent.  For the cache the unit is a run: the rows of a call
+// in one page, which share a scale for each head.  A CTA takes the runs that begin
+// in its window of rows (they may end up to 63 rows behind it), keeps their rows'
+// keys and values in registers, joins the rows' largest magnitudes in shared
+// memory, and writes codes: the input is read once.
+#include <math.h>
+
+#include <algorithm>
+
+#include "kv8.cuh"
+
+namespace sar {
+
+namespace {
+
+constexpr int kQkThreads = 256;
+
+struct QkArgs {
+  sar_qk_rows r;
+  sar_kv8 c;
+  int shift;           // log2 page_size
+  int q_heads_per, q_tasks, k_tasks, kv_tasks;  // query heads per CTA; CTAs per window of rows: queries, k_out, cache
+  int vec_q, vec_k, vec_v, vec_qo, vec_ko;  // rows whose pieces of four are aligned
+  int* err;
+  uint64_t turn[64];   // theta_i / (2 pi) in units of 2^-64 turns
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x) {
+  if constexpr (sizeof(T) == 4)
+    return x;
+  else
+    return Elem<T>::to(x);
+}
+
+// Four adjacent elements.
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, bool vec, float* x) {
+  if (vec) {
+    if constexpr (sizeof(T) == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      x[0] = Elem<T>::lo(v.x), x[1] = Elem<T>::hi(v.x), x[2] = Elem<T>::lo(v.y), x[3] = Elem<T>::hi(v.y);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = to_f<T>(p[e]);
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, bool vec, const float* x) {
+  if (vec) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) p[e] = Elem<T>::from(x[e]);
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// (cos, sin) of a lane's four frequencies at a position.
+__device__ __forceinline__ void angles(const QkArgs& a, int pos, int i0, float* cs, float* sn) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint64_t t = (uint64_t)(int64_t)pos * a.turn[i0 + e];
+    sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn[e], &cs[e]);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void norm_rope(float* x, const float* gain, bool normed, float eps, bool turned, const float* cs,
+                                          const float* sn) {
+  if (normed) {
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    const float inv = rsqrtf(group_sum<D / 8>(ss) * (1.0f / D) + eps);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * gain[e];
+  }
+  if (turned) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float u = x[e], w = x[e + 4];
+      x[e] = u * cs[e] - w * sn[e];
+      x[e + 4] = w * cs[e] + u * sn[e];
+    }
+  }
+}
+
+// TI: the rows' type; TO: the 16-bit type written.
+template <typename TI, typename TO, int D>
+__global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_constant__ QkArgs a) {
+  constexpr int LANES = D / 8, GROUPS = kQkThreads / LANES;  // rows of a pass, and of a window
+  constexpr int PASSES = (GROUPS + 63 + GROUPS - 1) / GROUPS;
+  constexpr int SPAN = PASSES * GROUPS;  // rows that a window's runs can reach
+  const sar_qk_rows& r = a.r;
+  const int grp = threadIdx.x / LANES, l = threadIdx.x % LANES;
+  const int w0 = blockIdx.x * GROUPS, task = blockIdx.y;
+  pdl_wait();
+  pdl_launch_dependents();
+
+  if (task >= a.kv_tasks) {
+    // ---- heads that are written as rows: queries, or keys ----
+    const bool is_q = task < a.kv_tasks + a.q_tasks;
+    const int row = w0 + grp;
+    const int h0 = is_q ? (task - a.kv_tasks) * a.q_heads_per : (task - a.kv_tasks - a.q_tasks) * a.q_heads_per;
+    const int h1 = min(h0 + a.q_heads_per, is_q ? r.n_q_heads : r.n_kv_heads);
+    const bool live = row < r.rows;
+    const float* gp = is_q ? r.q_gain : r.k_gain;
+    float gain[8], cs[4], sn[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gain[e] = gp ? gp[4 * l + e] : 1.f, gain[4 + e] = gp ? gp[D / 2 + 4 * l + e] : 1.f;
+    if (r.positions) angles(a, live ? r.positions[row] : 0, 4 * l, cs, sn);
+    const int64_t ld = is_q ? r.ldq : r.ldk, ldo = is_q ? r.ldq_out : r.ldk_out;
+    const TI* src = static_cast<const TI*>(is_q ? r.q : r.k) + (live ? row : 0) * ld + 4 * l;
+    TO* dst = static_cast<TO*>(is_q ? r.q_out : r.k_out) + row * ldo + 4 * l;
+    const bool vi = is_q ? a.vec_q : a.vec_k, vo = is_q ? a.vec_qo : a.vec_ko;
+    constexpr int AT_ONCE = 4;  // heads whose loads are under way together
+    for (int h = h0; h < h1; h += AT_ONCE) {
+      float x[AT_ONCE][8];
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        const TI* p = src + min(h + u, h1 - 1) * D;
+        load4<TI>(p, vi, x[u]);
+        load4<TI>(p + D / 2, vi, x[u] + 4);
+      }
+#pragma unroll
+      for (int u = 0; u < AT_ONCE; ++u) {
+        norm_rope<D>(x[u], gain, gp != nullptr, r.eps, r.positions != nullptr, cs, sn);
+        if (live && h + u < h1) {
+          store4<TO>(dst + (h + u) * D, vo, x[u]);
+          store4<TO>(dst + (h + u) * D + D / 2, vo, x[u] + 4);
+        }
+      }
+    }
+    return;
+  }
+
+  // ---- one KV head of the runs that begin in this window ----
+  __shared__ int slot_s[SPAN];
+  __shared__ uint32_t flag_s[(SPAN + 31) / 32];  // rows that do not go on from the row before
+  __shared__ float amax_s[2][SPAN];
+  const int kh = task;
+  const int ps = a.c.page_size;
+  const int64_t n_slots = (int64_t)a.c.num_pages * ps;
+  if (threadIdx.x < (SPAN + 31) / 32 * 32) {
+    const int i = threadIdx.x, row = w0 + i;
+    int s = -1;
+    bool flag = true;
+    if (i < SPAN && row < r.rows) {
+      s = r.slots[row];
+      if (s < 0 || s >= n_slots) {
+        if (s != -1 && kh == 0 && i < GROUPS) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SLOT, row);
+        s = -1;
+      } else {
+        flag = row == 0 || (s & (ps - 1)) == 0 || r.slots[row - 1] != s - 1;
+      }
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, flag);
+    if (i < SPAN) slot_s[i] = s;
+    if ((i & 31) == 0) flag_s[i >> 5] = m;
+  }
+  __syncthreads();
+  // row i's run: the last flagged row up to i; -1 where i is in no run of this window
+  auto run_of = [&](int i) -> int {
+    if (slot_s[i] < 0) return -1;
+    int w = i >> 5;
+    uint32_t m = flag_s[w] & (0xffffffffu >> (31 - (i & 31)));
+    while (m == 0 && w > 0) m = flag_s[--w];
+    if (m == 0) return -1;
+    const int s = (w << 5) + 31 - __clz(m);
+    return s < GROUPS ? s : -1;
+  };
+  auto run_end = [&](int i) -> int {  // the first flagged row behind i
+    int j = i + 1;
+    if (j >= SPAN) return SPAN;
+    int w = j >> 5;
+    uint32_t m = flag_s[w] & (0xffffffffu << (j & 31));
+    while (m == 0 && w < (SPAN + 31) / 32 - 1) m = flag_s[++w];
+    return m == 0 ? SPAN : min(SPAN, (w << 5) + __ffs(m) - 1);
+  };
+
+  float gain[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    gain[e] = r.k_gain ? r.k_gain[4 * l + e] : 1.f, gain[4 + e] = r.k_gain ? r.k_gain[D / 2 + 4 * l + e] : 1.f;
+  float x[PASSES][8], y[PASSES][8];
+  float old_k[PASSES], old_v[PASSES];
+  int run[PASSES];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * GROUPS + grp, row = w0 + i;
+    run[p] = run_of(i);
+    old_k[p] = old_v[p] = 0.f;
+    if (run[p] >= 0) {
+      const TI* kp = static_cast<const TI*>(r.k) + row * r.ldk + kh * D + 4 * l;
+      const TI* vp = static_cast<const TI*>(r.v) + row * r.ldv + kh * D + 4 * l;
+      load4<TI>(kp, a.vec_k, x[p]);
+      load4<TI>(kp + D / 2, a.vec_k, x[p] + 4);
+      load4<TI>(vp, a.vec_v, y[p]);
+      load4<TI>(vp + D / 2, a.vec_v, y[p] + 4);
+      const int first = slot_s[run[p]];
+      if (first & (ps - 1)) {  // the page goes on: what it has so far
+        const int64_t at = (int64_t)(first >> a.shift) * a.c.n_kv_heads + kh;
+        old_k[p] = a.c.k_scales[at];
+        old_v[p] = a.c.v_scales[at];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[p][e] = y[p][e] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    const int i = p * GROUPS + grp;
+    // (a pass without a row of this window's runs, as all but the first of single tokens)
+    if (__any_sync(0xffffffffu, run[p] >= 0)) {
+      float cs[4], sn[4];
+      if (r.positions) angles(a, run[p] >= 0 ? r.positions[w0 + i] : 0, 4 * l, cs, sn);
+      norm_rope<D>(x[p], gain, r.k_gain != nullptr, r.eps, r.positions != nullptr, cs, sn);
+    }
+    float mk = 0.f, mv = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = fabsf(x[p][e]), w = fabsf(y[p][e]);
+      mk = fmaxf(mk, u < INFINITY ? u : 0.f);
+      mv = fmaxf(mv, w < INFINITY ? w : 0.f);
+    }
+    mk = group_max<LANES>(mk);
+    mv = group_max<LANES>(mv);
+    if (l == 0) amax_s[0][i] = mk, amax_s[1][i] = mv;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
+    const int i = p * GROUPS + grp;
+    const bool live = run[p] >= 0;
+    float mk = 0.f, mv = 0.f;
+    if (live) {
+      const int end = run_end(i);
+      for (int j = run[p] + l; j < end; j += LANES) mk = fmaxf(mk, amax_s[0][j]), mv = fmaxf(mv, amax_s[1][j]);
+    }
+    mk = group_max<LANES>(mk);
+    mv = group_max<LANES>(mv);
+    if (!live) continue;
+    const float sk = fmaxf(kv8_scale(mk), old_k[p]), sv = fmaxf(kv8_scale(mv), old_v[p]);
+    const int slot = slot_s[i];
+    const int64_t unit = (int64_t)(slot >> a.shift) * a.c.n_kv_heads + kh;
+    uint8_t* kc = static_cast<uint8_t*>(a.c.k_codes) + unit * ps * D;
+    uint8_t* vc = static_cast<uint8_t*>(a.c.v_codes) + unit * ps * D;
+    const int o = (slot & (ps - 1)) * D + 4 * l;
+    const float ik = 1.f / sk, iv = 1.f / sv;  // (exact for powers of two)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const float* u = x[p] + 4 * half;
+      const float* w = y[p] + 4 * half;
+      *reinterpret_cast<uint32_t*>(kc + o + half * (D / 2)) =
+          to_e4m3x2(u[0] * ik, u[1] * ik) | to_e4m3x2(u[2] * ik, u[3] * ik) << 16;
+      *reinterpret_cast<uint32_t*>(vc + o + half * (D / 2)) =
+          to_e4m3x2(w[0] * iv, w[1] * iv) | to_e4m3x2(w[2] * iv, w[3] * iv) << 16;
+    }
+    if (run[p] != i) continue;
+    // the run's first row: the scales, and what the page held under smaller ones
+    if (l == 0) a.c.k_scales[unit] = sk, a.c.v_scales[unit] = sv;
+    const int held = (slot & (ps - 1)) * D;
+    auto anew = [&](uint8_t* codes, float ratio) {
+      for (int j = 4 * l; j < held; j += 4 * LANES) {
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + j);
+        const float2 u = e4m3x2_floats(c), w = e4m3x2_floats(c >> 16);
+        *reinterpret_cast<uint32_t*>(codes + j) =
+            to_e4m3x2(u.x * ratio, u.y * ratio) | to_e4m3x2(w.x * ratio, w.y * ratio) << 16;
+      }
+    };
+    if (held > 0 && old_k[p] > 0.f && sk > old_k[p]) anew(kc, old_k[p] * ik);
+    if (held > 0 && old_v[p] > 0.f && sv > old_v[p]) anew(vc, old_v[p] * iv);
+  }
+}
+
+template <typename TI, typename TO>
+int launch_qk(const QkArgs& a, cudaStream_t s) {
+  const int D = a.r.head_dim;
+  const int window = kQkThreads / (D / 8);
+  const dim3 grid((unsigned)(((int64_t)a.r.rows + window - 1) / window), (unsigned)(a.kv_tasks + a.q_tasks + a.k_tasks));
+  const cudaError_t e = D == 128 ? launch_pdl(qk_rows_kernel<TI, TO, 128>, grid, dim3(kQkThreads), 0, s, a)
+                                 : launch_pdl(qk_rows_kernel<TI, TO, 64>, grid, dim3(kQkThreads), 0, s, a);
+  if (e != cudaSuccess) return cuda_error(e, "qk rows launch");
+  count_launches(1);
+  return SAR_OK;
+}
+
+}  // namespace
+
+int check_kv8(const sar_kv8* c, const char* what) {
+  const std::string w(what);
+  if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return set_error(SAR_ERR_INVALID_ARG, w + ": null cache");
+  if (c->num_pages < 1 || c->n_kv_heads < 1) return set_error(SAR_ERR_INVALID_ARG, w + ": bad cache sizes");
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64)
+    return set_error(SAR_ERR_UNSUPPORTED, w + ": pages of 16, 32 or 64 tokens");
+  if (c->head_dim != 64 && c->head_dim != 128) return set_error(SAR_ERR_UNSUPPORTED, w + ": head_dim 64 or 128");
+  // (a TMA row coordinate is a 32-bit number)
+  if ((int64_t)c->num_pages * c->page_size > INT32_MAX ||
+      (int64_t)c->num_pages * c->page_size * c->n_kv_heads > INT32_MAX)
+    return set_error(SAR_ERR_UNSUPPORTED, w + ": cache rows above 2^31");
+  if (!aligned_to(c->k_codes, 16) || !aligned_to(c->v_codes, 16) || !aligned_to(c->k_scales, 4) || !aligned_to(c->v_scales, 4))
+    return set_error(SAR_ERR_INVALID_ARG, w + ": cache not aligned");
+  return SAR_OK;
+}
+
+}  // namespace sar
+
+using sar::aligned_to;
+using sar::set_error;
+
+extern "C" int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream) try {
+  if (!rows) return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: null rows");
+  const sar_qk_rows& r = *rows;
+  if (r.rows < 0 || r.n_q_heads < 0 || r.n_kv_heads < 0)
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: bad sizes");
+  if (r.type != SAR_TYPE_F16 && r.type != SAR_TYPE_BF16 && r.type != SAR_TYPE_F32)
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: bad element type");
+  if ((r.out_type != SAR_TYPE_F16 && r.out_type != SAR_TYPE_BF16) || (r.type != SAR_TYPE_F32 && r.out_type != r.type))
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: the output type is 16-bit, and the rows' type where that is");
+  if (r.head_dim != 64 && r.head_dim != 128) return set_error(SAR_ERR_UNSUPPORTED, "qk_norm_rope: head_dim 64 or 128");
+  if (r.n_q_heads > 1024 || r.n_kv_heads > 1024) return set_error(SAR_ERR_UNSUPPORTED, "qk_norm_rope: more than 1024 heads");
+  if (r.rows > 1 << 30) return set_error(SAR_ERR_UNSUPPORTED, "qk_norm_rope: more than 2^30 rows");
+  if ((r.q_gain || r.k_gain) && !(r.eps >= 0.f)) return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: negative eps");
+  if (r.positions && !(r.rope_base > 0.f && r.rope_base < INFINITY))
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: rope_base must be positive and finite");
+  if (cache) {
+    SAR_TRY(sar::check_kv8(cache, "qk_norm_rope"));
+    if (cache->n_kv_heads != r.n_kv_heads || cache->head_dim != r.head_dim)
+      return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: the cache has other heads");
+  }
+  if (r.rows == 0) return SAR_OK;
+  const bool q_rows = r.q && r.n_q_heads > 0;
+  if ((r.q != nullptr) != (r.q_out != nullptr)) return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: q and q_out go together");
+  if (r.k_out && !r.k) return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: k_out without k");
+  if (cache && (!r.k || !r.v || !r.slots)) return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: a cache needs k, v and slots");
+  if (cache && r.k_out == r.k)
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: with a cache k_out is not k");
+  const int64_t dq = (int64_t)r.n_q_heads * r.head_dim, dk = (int64_t)r.n_kv_heads * r.head_dim;
+  if ((q_rows && (r.ldq < dq || r.ldq_out < dq)) || (r.k && r.ldk < dk) || (r.k_out && r.ldk_out < dk) ||
+      (cache && r.ldv < dk))
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: rows shorter than their heads");
+  const uintptr_t size = r.type == SAR_TYPE_F32 ? 4 : 2;
+  if (!aligned_to(r.q, size) || !aligned_to(r.k, size) || !aligned_to(r.v, size) || !aligned_to(r.q_out, 2) ||
+      !aligned_to(r.k_out, 2) || !aligned_to(r.q_gain, 4) || !aligned_to(r.k_gain, 4) || !aligned_to(r.positions, 4) ||
+      !aligned_to(r.slots, 4))
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: array not aligned to its element");
+  if ((q_rows && r.q_out == r.q && (r.type == SAR_TYPE_F32 || r.ldq != r.ldq_out)) ||
+      (r.k_out && r.k_out == r.k && (r.type == SAR_TYPE_F32 || r.ldk != r.ldk_out)))
+    return set_error(SAR_ERR_INVALID_ARG, "qk_norm_rope: rows written over have the same 16-bit type and stride");
+
+  sar::QkArgs a = {};
+  a.r = r;
+  if (cache) a.c = *cache;
+  if (!q_rows) a.r.n_q_heads = 0;
+  a.shift = !cache ? 0 : cache->page_size == 16 ? 4 : cache->page_size == 32 ? 5 : 6;
+  auto vec = [](const void* p, int64_t ld, uintptr_t piece, uintptr_t el) {
+    return aligned_to(p, piece) && ld * (int64_t)el % (int64_t)piece == 0;
+  };
+  a.vec_q = vec(r.q, r.ldq, 4 * size, size);
+  a.vec_k = vec(r.k, r.ldk, 4 * size, size);
+  a.vec_v = vec(r.v, r.ldv, 4 * size, size);
+  a.vec_qo = vec(r.q_out, r.ldq_out, 8, 2);
+  a.vec_ko = vec(r.k_out, r.ldk_out, 8, 2);
+  // heads to a CTA: as many as leave every SM a few CTAs
+  const int64_t windows = ((int64_t)r.rows * (r.head_dim / 8) + sar::kQkThreads - 1) / sar::kQkThreads;
+  a.q_heads_per = 1;
+  while (a.q_heads_per < 16 && windows * (a.r.n_q_heads / (2 * a.q_heads_per)) >= 4 * sar::num_sms()) a.q_heads_per *= 2;
+  a.q_tasks = (a.r.n_q_heads + a.q_heads_per - 1) / a.q_heads_per;
+  a.k_tasks = r.k_out ? (r.n_kv_heads + a.q_heads_per - 1) / a.q_heads_per : 0;
+  a.kv_tasks = cache ? r.n_kv_heads : 0;
+  if (a.q_tasks + a.k_tasks + a.kv_tasks == 0) return SAR_OK;
+  if (r.positions) {
+    // (kept for the thread's next call: they depend on these two numbers alone)
+    static thread_local float base = 0.f;
+    static thread_local int dim = 0;
+    static thread_local uint64_t turn[64];
+    if (base != r.rope_base || dim != r.head_dim) {
+      for (int i = 0; i < r.head_dim / 2; ++i) {
+        const double t = pow((double)r.rope_base, -2.0 * i / r.head_dim) / 6.283185307179586476925286766559;
+        turn[i] = (uint64_t)ldexp(t - floor(t), 64);
+      }
+      base = r.rope_base;
+      dim = r.head_dim;
+    }
+    for (int i = 0; i < r.head_dim / 2; ++i) a.turn[i] = turn[i];
+  }
+  SAR_TRY(sar::op_flags(&a.err));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (r.type == SAR_TYPE_F32)
+    return r.out_type == SAR_TYPE_BF16 ? sar::launch_qk<float, __nv_bfloat16>(a, s) : sar::launch_qk<float, __half>(a, s);
+  return r.type == SAR_TYPE_BF16 ? sar::launch_qk<__nv_bfloat16, __nv_bfloat16>(a, s) : sar::launch_qk<__half, __half>(a, s);
+} catch (...) {
+  return sar::entry_failed("qk_norm_rope");
+}

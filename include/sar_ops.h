@@ -167,6 +167,141 @@ int sar_op_gemm_fp4(const void* a, const void* a_scales, const void* w, const vo
                     const void* residual, int32_t M, int32_t N, int32_t K, float alpha, int32_t epilogue, int32_t format,
                     int32_t variant, int32_t storage, void* stream);
 
+/* ---- KV cache in 8 bits ------------------------------------------------- */
+
+/* A paged cache of one layer whose keys and values are held in 8 bits (no
+ * counterpart in the pages, whose cache is 16-bit): e4m3 codes q with one scale s
+ * for each page and head, standing for q * s.  Half the bytes of the 16-bit pages,
+ * and as much less to read for every decode.
+ *   k_codes, v_codes    uint8 [num_pages][n_kv_heads][page_size][head_dim],
+ *                       contiguous, 16-byte aligned
+ *   k_scales, v_scales  fp32 [num_pages][n_kv_heads]
+ * page_size is 16, 32 or 64, head_dim 64 or 128; num_pages * n_kv_heads *
+ * page_size stays below 2^31. */
+typedef struct sar_kv8 {
+  void* k_codes;
+  void* v_codes;
+  float* k_scales;
+  float* v_scales;
+  int32_t num_pages, n_kv_heads, page_size, head_dim;
+} sar_kv8;
+
+/* Block tables and slot maps from request lengths, on the device, so that a
+ * captured step can go from one batch to the next without the host.  Request i
+ * (i < n) has lens[i] tokens in its first ceil(lens[i] / page_size) pages and
+ *   new_lens[i] > 0   gets room for that many more: pages taken from the end of the
+ *                     free list, request by request, into its block table
+ *   new_lens[i] == 0  waits: nothing changes
+ *   new_lens[i] == -1 has ended: its pages go to the end of the free list (request
+ *                     by request, in table order) before any are taken
+ * Results:
+ *   lens_out[i]      lens[i] + new_lens[i]; 0 for a request that has ended
+ *   row_offsets      [n + 1]: request i's rows are row_offsets[i] .. row_offsets[i + 1]
+ *   positions, slots [max_rows]: each row's position in its request, and its place
+ *                    in the cache, page * page_size + offset; rows behind the last
+ *                    request's have slot -1 and position 0
+ *   free_count_out   pages on the list afterwards
+ * Pages go first come, first served: where a request's are not there, neither it nor
+ * a request behind it that needs pages gets any; nor does a request whose rows do
+ * not fit max_rows.  Such a request keeps its length and its rows' slots are -1.
+ * sar_op_sync_status() reports it (SAR_ERR_NO_PAGES, or SAR_ERR_BOUNDS for the rows).
+ * Also SAR_ERR_BOUNDS: a request whose length is negative (it counts as 0) or passes
+ * its block table, with the new tokens too, or whose new_lens is below -1, waits; a
+ * page out of range goes where it would, but rows in it have slot -1.
+ * lens_out may be lens, free_count_out free_count; else no two arrays overlap.
+ * n is at most 8192, n * bt_stride and max_rows at most 2^30.  Async on `stream`;
+ * no workspace. */
+typedef struct sar_page_map_args {
+  const int32_t* lens;     /* [n] */
+  const int32_t* new_lens; /* [n] */
+  int32_t* lens_out;       /* [n] */
+  int32_t* block_tables;   /* [n][bt_stride], read and written */
+  int32_t* free_pages;     /* [num_pages], the first *free_count are free */
+  const int32_t* free_count;
+  int32_t* free_count_out;
+  int32_t* row_offsets; /* [n + 1] */
+  int32_t* positions;   /* [max_rows] */
+  int32_t* slots;       /* [max_rows] */
+  int32_t n, bt_stride, page_size, num_pages, max_rows;
+} sar_page_map_args;
+int sar_page_map(const sar_page_map_args* args, void* stream);
+
+/* A step's query, key and value rows behind their projection.  For every head h of
+ * q and k, in fp32:
+ *   norm      h = h * rsqrt(mean(h^2) + eps) * gain   (q_gain, k_gain fp32
+ *             [head_dim]; NULL: none)
+ *   rotation  the pair (h[i], h[i + head_dim / 2]) turned by position *
+ *             rope_base^(-2 i / head_dim), the angle reduced exactly (positions
+ *             NULL: none)
+ * q_out and k_out (NULL: not written) get them rounded once.  With a cache, k and
+ * v are also written into it at their rows' slots (from sar_page_map; a slot of -1 is
+ * passed over, one out of range passed over and reported): for each page and head
+ * that gets rows, a = the largest finite magnitude among them,
+ *   s = the smallest power of two in [2^-40, 2^60] with a <= 448 s
+ * or the page's present scale where its first new row is not the page's first and
+ * that is larger; codes are h / s rounded to nearest even, at most 448 in magnitude;
+ * infinities and NaN become NaN.  Where a page's scale grows, the rows in front of
+ * its first new one are rounded anew under it.  A page's rows follow one another
+ * in the call, with consecutive slots (otherwise that page's contents are
+ * unspecified), as sar_page_map gives them.
+ * Rows are `type` (SAR_TYPE_*), row r at q + r * ldq elements; q_out and k_out have
+ * the 16-bit type `out_type`, which is `type` where that is 16 bits.  n_kv_heads of k
+ * and v.  q may be NULL (no query heads).  16-bit rows may be written over (q_out is q,
+ * of the same stride; without a cache k_out is k), else outputs overlap nothing.  16-byte aligned rows are faster.  Async on `stream`. */
+typedef struct sar_qk_rows {
+  const void* q;
+  const void* k;
+  const void* v; /* with a cache */
+  void* q_out;
+  void* k_out;
+  int64_t ldq, ldk, ldv, ldq_out, ldk_out;
+  const float* q_gain;
+  const float* k_gain;
+  const int32_t* positions; /* [rows] */
+  const int32_t* slots;     /* [rows], with a cache */
+  int32_t rows, n_q_heads, n_kv_heads, head_dim, type, out_type;
+  float eps, rope_base;
+} sar_qk_rows;
+int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream);
+
+/* Attention over an 8-bit cache.  Sequence i (i < n) has lens[i] tokens in its block
+ * table's pages; its rows row_offsets[i] .. row_offsets[i + 1] of q are its last
+ * tokens, so row j of r stands at position p = lens[i] - r + j and sees the keys at
+ * positions (p - window, p] (window 0: [0, p]).  For each head, in fp32,
+ *   out = sum_k softmax_k(scale * q . K_k) V_k
+ * with query head h reading KV head h / (n_q_heads / n_kv_heads).  A row that sees
+ * nothing (p < 0) is zero; keys that it does not see do not touch it, whatever they
+ * hold.  Single tokens and chunks may stand side by side in a call.  Products of
+ * codes and queries are exact in the tensor cores (codes turn to fp16 without
+ * rounding), probabilities are rounded to fp16.
+ * Rows are 16-bit, row r at q + r * ldq elements, heads of head_dim adjacent; out
+ * likewise.  max_rows bounds a sequence's rows (1: single tokens alone); max_len
+ * (0: unknown) is about the longest length and only guides how work is shared
+ * out.  scale 0 is 1 / sqrt(head_dim).  A cache's scales are positive and lie
+ * within [2^-40, 2^60].  At most 8 query heads per KV head; n, rows and max_len at most 2^30.
+ * The workspace (device, 16-byte aligned, sar_kv8_attention_workspace() bytes; it
+ * holds nothing between calls) belongs to one call at a time.
+ * Sequences whose offsets are out of range or fall, whose rows pass max_rows or
+ * whose length passes its block table are left out, and keys of pages out of range
+ * are passed over; sar_op_sync_status() reports either.  Rows of no sequence stay as they
+ * are.  Async on `stream`; allocates nothing. */
+typedef struct sar_kv8_batch {
+  const void* q;
+  void* out;
+  int64_t ldq, ldo;
+  const int32_t* row_offsets;  /* [n + 1] */
+  const int32_t* lens;         /* [n] */
+  const int32_t* block_tables; /* [n][bt_stride] */
+  void* workspace;
+  int64_t workspace_bytes;
+  int32_t rows, n, n_q_heads, bt_stride, storage, max_rows, max_len, window;
+  float scale;
+} sar_kv8_batch;
+/* Bytes of workspace for such a call (rows, n, n_q_heads, max_rows and max_len of
+ * the batch are read) on the current device. */
+int sar_kv8_attention_workspace(const sar_kv8_batch* batch, const sar_kv8* cache, int64_t* bytes);
+int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* stream);
+
 /* Device address of a step workspace buffer, valid until sar_model_destroy;
  * after a step on a one-layer model it holds that layer's intermediates.
  *   0: normed rows     [max_tokens, hidden] (storage type)
