@@ -590,85 +590,20 @@ __global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ D
   }
 }
 
-// Sequences of several rows, one (row, KV head) to a CTA, a key at a time.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) kv8_rows_kernel(const __grid_constant__ Kv8Attn a) {
-  constexpr int E = D / 32;
-  __shared__ float acc_s[4][kDecHeads][D];
-  __shared__ float ml_s[4][kDecHeads][2];
-  pdl_wait();
-  pdl_launch_dependents();
-  const int row = blockIdx.x, kh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int i = 0; i < a.n; ++i) {
-    int row0, rows, len;
-    if (!kv8_sequence(a, i, row0, rows, len) || rows < 2 || row < row0 || row >= row0 + rows) continue;
-    const int pos = len - rows + row - row0, lo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    float q[kDecHeads][E], o[kDecHeads][E], m[kDecHeads], l[kDecHeads];
-    for (int h = 0; h < kDecHeads; ++h) {
-      m[h] = -INFINITY, l[h] = 0.f;
-      for (int e = 0; e < E; ++e) {
-        o[h][e] = 0.f;
-        q[h][e] = h < a.G ? Elem<T>::to(static_cast<const T*>(a.q)[row * a.ldq + (int64_t)(kh * a.G + h) * D + lane * E + e]) : 0.f;
-      }
-    }
-    for (int key = lo + warp; key <= pos; key += 4) {
-      const int page = a.bt[i * a.bt_stride + (key >> a.shift)];
-      if (page < 0 || page >= a.num_pages) {
-        report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page);
-        continue;
-      }
-      const int64_t unit = (int64_t)page * a.kvh + kh;
-      const int64_t at = ((unit << a.shift) + (key & ((1 << a.shift) - 1))) * D + lane * E;
-      float k[E], v[E];
-      for (int e = 0; e < E; ++e) {
-        k[e] = e4m3x2_floats(a.k_codes[at + e]).x * a.k_scales[unit];
-        v[e] = e4m3x2_floats(a.v_codes[at + e]).x * a.v_scales[unit];
-      }
-#pragma unroll
-      for (int h = 0; h < kDecHeads; ++h) {
-        if (h >= a.G) break;
-        float s = 0.f;
-        for (int e = 0; e < E; ++e) s = fmaf(q[h][e], k[e], s);
-        s = warp_sum(s) * a.scale;
-        const float mn = fmaxf(m[h], s), f = m[h] == -INFINITY ? 0.f : exp2f(m[h] - mn), p = exp2f(s - mn);
-        for (int e = 0; e < E; ++e) o[h][e] = fmaf(p, v[e], o[h][e] * f);
-        l[h] = fmaf(l[h], f, p);
-        m[h] = mn;
-      }
-    }
-    for (int h = 0; h < a.G; ++h) {
-      for (int e = 0; e < E; ++e) acc_s[warp][h][lane * E + e] = o[h][e];
-      ml_s[warp][h][0] = m[h], ml_s[warp][h][1] = l[h];
-    }
-    __syncthreads();
-    for (int t = threadIdx.x; t < a.G * D; t += 128) {
-      const int h = t / D, e = t % D;
-      float M = -INFINITY, L = 0.f, A = 0.f;
-      for (int w = 0; w < 4; ++w) M = fmaxf(M, ml_s[w][h][0]);
-      for (int w = 0; w < 4; ++w) {
-        const float f = ml_s[w][h][0] == -INFINITY ? 0.f : exp2f(ml_s[w][h][0] - M);
-        L = fmaf(ml_s[w][h][1], f, L);
-        A = fmaf(acc_s[w][h][e], f, A);
-      }
-      static_cast<T*>(a.out)[row * a.ldo + (int64_t)(kh * a.G + h) * D + e] = Elem<T>::from(pos < 0 ? 0.f : A / L);
-    }
-    return;
-  }
-}
-
 int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
-// The workspace: before, pieces' maxima and sums, pieces.
+// The workspace: before, pieces' maxima and sums, pieces; then the chunks'.
 struct Space {
-  int64_t before, ml, parts, bytes;
+  int64_t before, ml, parts, chunks, bytes;
 };
-Space space_of(int n, int head_dim) {
+Space space_of(int n, int head_dim, int max_rows) {
   const int64_t slots = 2ll * kDecPerSm * num_sms();
   Space s;
   s.before = 0;
   s.ml = up256((n + 1ll) * 8);
   s.parts = s.ml + up256(slots * kDecHeads * 8);
-  s.bytes = s.parts + slots * kDecHeads * head_dim * 4;
+  s.chunks = s.parts + up256(slots * kDecHeads * head_dim * 4);
+  s.bytes = s.chunks + (max_rows > 1 ? kv8_chunk_space(head_dim) : 0);
   return s;
 }
 
@@ -694,11 +629,6 @@ int launch_kv8(const DecArgs& d, const CUtensorMap& tmk, const CUtensorMap& tmv,
   e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)std::min(d.a.n, 65535), (unsigned)d.a.kvh), dim3(128), 0, s, d, grid);
   if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
   count_launches(2);
-  if (d.a.max_rows > 1) {
-    e = launch_pdl(kv8_rows_kernel<T, D>, dim3((unsigned)d.a.rows, (unsigned)d.a.kvh), dim3(128), 0, s, d.a);
-    if (e != cudaSuccess) return cuda_error(e, "kv8 rows launch");
-    count_launches(1);
-  }
   return SAR_OK;
 }
 
@@ -713,7 +643,7 @@ extern "C" {
 int sar_kv8_attention_workspace(const sar_kv8_batch* batch, const sar_kv8* cache, int64_t* bytes) try {
   if (!batch || !bytes) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention_workspace: null pointer");
   SAR_TRY(sar::check_batch(*batch, cache));
-  *bytes = sar::space_of(batch->n, cache->head_dim).bytes;
+  *bytes = sar::space_of(batch->n, cache->head_dim, batch->max_rows).bytes;
   return SAR_OK;
 } catch (...) {
   return sar::entry_failed("kv8_attention_workspace");
@@ -737,7 +667,7 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   if (!aligned_to(b.q, 2) || !aligned_to(b.out, 2) || !aligned_to(b.row_offsets, 4) || !aligned_to(b.lens, 4) ||
       !aligned_to(b.block_tables, 4) || !aligned_to(b.workspace, 16))
     return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: array not aligned to its element");
-  const sar::Space sp = sar::space_of(b.n, cache->head_dim);
+  const sar::Space sp = sar::space_of(b.n, cache->head_dim, b.max_rows);
   if (b.workspace_bytes < sp.bytes) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: workspace too small");
   sar::DecArgs d = {};
   sar::Kv8Attn& a = d.a;
@@ -777,11 +707,15 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   SAR_TRY(sar::make_tmap_bytes(&tmk, cache->k_codes, map_rows, 128, box));
   SAR_TRY(sar::make_tmap_bytes(&tmv, cache->v_codes, map_rows, 128, box));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = b.storage == SAR_STORAGE_BF16;
+  int rc;
   if (cache->head_dim == 128)
-    return b.storage == SAR_STORAGE_BF16 ? sar::launch_kv8<__nv_bfloat16, 128>(d, tmk, tmv, s)
-                                         : sar::launch_kv8<__half, 128>(d, tmk, tmv, s);
-  return b.storage == SAR_STORAGE_BF16 ? sar::launch_kv8<__nv_bfloat16, 64>(d, tmk, tmv, s)
-                                       : sar::launch_kv8<__half, 64>(d, tmk, tmv, s);
+    rc = bf ? sar::launch_kv8<__nv_bfloat16, 128>(d, tmk, tmv, s) : sar::launch_kv8<__half, 128>(d, tmk, tmv, s);
+  else
+    rc = bf ? sar::launch_kv8<__nv_bfloat16, 64>(d, tmk, tmv, s) : sar::launch_kv8<__half, 64>(d, tmk, tmv, s);
+  if (rc != SAR_OK) return rc;
+  if (b.max_rows == 1 || b.rows == 1) return SAR_OK;
+  return sar::launch_kv8_chunks(a, cache->head_dim, b.storage, ws + sp.chunks, s);
 } catch (...) {
   return sar::entry_failed("kv8_attention");
 }
