@@ -614,7 +614,7 @@ int check_batch(const sar_kv8_batch& b, const sar_kv8* c) {
     return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: bad sizes");
   if (b.n_q_heads % c->n_kv_heads || b.n_q_heads / c->n_kv_heads > kDecHeads)
     return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: query heads are a multiple of the KV heads, at most 8 to each");
-  if (b.rows > 1 << 30 || b.n > 1 << 30 || c->n_kv_heads > 1024)
+  if (b.rows > 1 << 27 || b.n > 1 << 30 || c->n_kv_heads > 1024)
     return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: rows, sequences or heads above their limits");
   return SAR_OK;
 }
