@@ -7,13 +7,16 @@
 //   warps 0..7   softmax, four per tile, a row to a thread: scores S from tensor memory,
 //                running maximum and sum, P (fp16) back over S; O rescaled where a row's
 //                maximum has grown by more than 2^8; at the end O / sum.
-//   warp 13      fetches pages' codes by TMA, 64 keys a step, three steps ahead.
-//   warps 8..11  convert them from e4m3 to fp16 (exactly) into the 128-byte swizzled K and
-//                V tiles of two stages each.
+//   warps 13, 14 fetch pages' codes by TMA: K's as they are multiplied, V's 64 keys a step.
+//   warps 8..11  convert V's from e4m3 to fp16 (exactly) into two stages of 128 keys.
 //   warp 12      one thread issues S_x(j) = Q_x K_j^T and O_x += P_x(j) V_j, the tiles in
 //                turn, so that one tile's products run under the other's softmax.
-// The queries are fp16 too (bf16 rows scaled by a power of two, undone in the scores'
-// factor).  Page scales act as in the single-token kernel: with raw scores S and
+// K is multiplied in e4m3 as it lies in the cache (a conversion took the place of the
+// tensor cores as what bounds this kernel).  A query is then a sum of e4m3 numbers:
+// scaled by a power of two so that its row's largest lies in [128, 256), two parts of
+// four significant bits hold bf16's eight, three fp16's eleven, exactly down to 2^-10;
+// e4m3 products run at twice the rate, so two parts cost what one fp16 product does.
+// Page scales act as in the single-token kernel: with raw scores S and
 // t = S k_scale scale + log2(v_scale), 2^(t - m) weighs V's codes and its sum takes it
 // times 1 / v_scale, 16 keys (which lie in one page) at a time: one multiplication
 // more per 16 keys and row.
@@ -38,9 +41,10 @@ constexpr int kKeys = 128;               // keys of a block
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kChunkThreads = (kSoftWarps + kConvWarps + 4) * 32;  // (whole warpgroups: the last has one warp at work)
 constexpr int kTileRegion = 128 * 128;   // [128 rows][128 bytes]: 64 dims of 128 rows
-constexpr int kScaleRing = 4;
+constexpr int kScaleRing = 4;             // blocks whose scales are kept: three K stages ahead, and the softmax's
 constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log2 and inverse of the value scales, a flag
-constexpr int kRawSteps = 3;              // steps of 64 keys whose codes are under way
+constexpr int kRawSteps = 3;              // steps of 64 keys of V whose codes are under way
+constexpr int kMostK = 3;                 // K stages
 constexpr int kMostTiles = 256;          // of a call whose CTAs take stretches
 constexpr int kLeastBlocks = 4;          // of a stretch
 constexpr float kGrowth = 8.f;           // log2 of a maximum's growth that O tolerates
@@ -48,12 +52,13 @@ constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its first 64 
 constexpr uint32_t kColsO = 256;         // O_x at 256 + x * 128
 
 struct ChunkBars {
-  uint64_t k_full[2], v_full[2], k_free[2], v_free[2];
+  uint64_t k_full[kMostK], k_free[kMostK], v_full[2], v_free[2];
   uint64_t raw_full[kRawSteps], raw_free[kRawSteps];
   uint64_t s_full[2], p_full[2];
   uint64_t q_ready, mma_done;
   uint32_t tmem;
-  int nan;  // a NaN code of V came by
+  int nan;                    // a NaN code of V came by
+  uint32_t read[kScaleRing];  // runs of a block whose V was read
 };
 
 // The plan, in the workspace, for the joining kernel.
@@ -73,21 +78,47 @@ struct ChunkArgs8 {
   int sms, vec_q, vec_o;
 };
 
-template <int D>
+template <typename T, int D>
 struct ChunkSmem {
-  static constexpr int kOperand = (D / 64) * kTileRegion;  // Q_x, K or V of a block
-  static constexpr int kK = 2 * kOperand, kV = kK + 2 * kOperand;
-  static constexpr int kRawStep = 64 * D;                           // codes of a step
-  static constexpr int kRaw = kV + 2 * kOperand, kBars = kRaw + kRawSteps * kRawStep;
-  static constexpr int kScales = kBars + 256;                       
+  static constexpr int kParts = Elem<T>::kMmaFormat == 1 ? 2 : 3;  // e4m3 numbers to a query's element
+  static constexpr int kPart = 128 * D;                            // of 128 rows
+  static constexpr int kStagesK = kParts == 2 ? 3 : 2;
+  static constexpr int kStageV = (D / 64) * kTileRegion;           // fp16
+  static constexpr int kRawStep = 64 * D;
+  static constexpr int kK = 2 * kParts * kPart, kV = kK + kStagesK * kPart, kRaw = kV + 2 * kStageV;
+  static constexpr int kBars = kRaw + kRawSteps * kRawStep;
+  static constexpr int kScales = kBars + 256;
   static constexpr int kTable = kScales + kScaleRing * kScaleFloats * 4;  // before [tiles + 1], seq, u
   static constexpr int kBytes = 1024 + kTable + (3 * kMostTiles + 1) * 4;
 };
 static_assert(sizeof(ChunkBars) <= 256, "barrier area");
-static_assert(ChunkSmem<128>::kBytes <= 226 * 1024, "shared memory per CTA");
+static_assert(ChunkSmem<__half, 128>::kBytes <= 226 * 1024, "shared memory per CTA");
 
-__device__ __forceinline__ uint32_t idesc_f16(int n, uint32_t b_mn) {
+// Instruction descriptor: fp32 sums, M = 128; both operands of format 0 (fp16 of
+// kind::f16, e4m3 of kind::f8f6f4), A K-major, B K-major or MN-major.
+__device__ __forceinline__ uint32_t idesc_of(int n, uint32_t b_mn) {
   return (1u << 4) | (b_mn << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// D (+)= A B^T over K = 32 of e4m3.
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Descriptor of a K-major operand whose rows are D bytes, with a swizzle as wide.
+template <int D>
+__device__ __forceinline__ uint64_t rows_desc(uint32_t saddr) {
+  if constexpr (D == 128) return sw128_desc(saddr);
+  uint64_t d = 0;
+  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)1 << 16;
+  d |= (uint64_t)(512 >> 4) << 32;  // eight rows
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)4 << 61;  // 64-byte swizzle
+  return d;
 }
 
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* err) {
@@ -161,16 +192,16 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     kv8_chunk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ ChunkArgs8 args) {
-  using M = ChunkSmem<D>;
+  using M = ChunkSmem<T, D>;
   constexpr int PASS = kConvWarps * 32 * 16 / D;  // keys of a pass of the converting warps, 16 bytes to a thread
   constexpr int STEP_PASSES = 64 / PASS;
   const Kv8Attn& a = args.a;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  auto q_reg = [&](int x) { return sbase + (uint32_t)(x * M::kOperand); };
-  auto k_reg = [&](int s) { return sbase + (uint32_t)(M::kK + s * M::kOperand); };
-  auto v_reg = [&](int s) { return sbase + (uint32_t)(M::kV + s * M::kOperand); };
+  auto q_reg = [&](int x) { return sbase + (uint32_t)(x * M::kParts * M::kPart); };
+  auto k_reg = [&](int s) { return sbase + (uint32_t)(M::kK + s * M::kPart); };
+  auto v_reg = [&](int s) { return sbase + (uint32_t)(M::kV + s * M::kStageV); };
   ChunkBars* bars = reinterpret_cast<ChunkBars*>(smem + M::kBars);
   float* scales = reinterpret_cast<float*>(smem + M::kScales);
   int32_t* before = reinterpret_cast<int32_t*>(smem + M::kTable);
@@ -181,10 +212,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(smem_u32(&bars->k_full[s]), kConvWarps);
-      mbar_init(smem_u32(&bars->v_full[s]), kConvWarps);
+    for (int s = 0; s < kMostK; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 1);
       mbar_init(smem_u32(&bars->k_free[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&bars->v_full[s]), kConvWarps);
       mbar_init(smem_u32(&bars->v_free[s]), 1);
       mbar_init(smem_u32(&bars->s_full[s]), 1);
       mbar_init(smem_u32(&bars->p_full[s]), kSoftWarps / 2);
@@ -341,10 +374,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // ---------------- products ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == kSoftWarps + kConvWarps && elect_one()) {
-      const uint32_t id_s = idesc_f16(kKeys, 0), id_pv = idesc_f16(D, 1);
-      const uint64_t dqa = sw128_desc(q_reg(0)), dqb = sw128_desc(q_reg(1));
-      const uint64_t dk0 = sw128_desc(k_reg(0)), dk1 = sw128_desc(k_reg(1));
-      const uint64_t dv0 = sw128_desc_mn(v_reg(0), kTileRegion, 1024), dv1 = sw128_desc_mn(v_reg(1), kTileRegion, 1024);
+      const uint32_t id_s = idesc_of(kKeys, 0), id_pv = idesc_of(D, 1);
+      const uint64_t dqa = rows_desc<D>(q_reg(0)), dk = rows_desc<D>(k_reg(0));
+      const uint64_t dv0 = sw128_desc_mn(v_reg(0), kTileRegion, 1024);
       bool ok = true;
       uint32_t base = 0, done_a = 0, done_b = 0, pieces = 0;  // blocks so far: of the stages, of each tile
       for (int b = b0; b < b1; ++pieces) {
@@ -355,17 +387,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
         // S_x(j); the last tile to read the block frees its K stage
         auto issue_s = [&](int x, int j) -> bool {
-          const uint32_t jt = base + j, s = jt & 1;
+          const uint32_t jt = base + j, s = jt % M::kStagesK;
           const bool first = x == 0 || j >= p.na, last = x == 1 || !has_b;
-          if (first && !mbar_wait(smem_u32(&bars->k_full[s]), (jt >> 1) & 1, a.err, SITE_KV8_PIPE)) return false;
+          if (first && !mbar_wait(smem_u32(&bars->k_full[s]), (jt / M::kStagesK) & 1, a.err, SITE_KV8_PIPE)) return false;
           tc_fence_after();
           const uint32_t d = tmem + kColsS * (uint32_t)x;
-          const uint64_t db = s ? dk1 : dk0, dq = x ? dqb : dqa;
+          const uint64_t db = dk + s * (M::kPart / 16), dq = dqa + (uint32_t)x * (M::kParts * M::kPart / 16);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint64_t o = (uint64_t)(((kk >> 2) * kTileRegion + (kk & 3) * 32) >> 4);
-            mma_f16<false>(d, dq + o, db + o, id_s, kk != 0);
-          }
+          for (int kk = 0; kk < M::kParts * (D / 32); ++kk)
+            mma_f8(d, dq + (uint64_t)(kk / (D / 32) * (M::kPart / 16) + kk % (D / 32) * 2), db + (uint64_t)(kk % (D / 32) * 2), id_s,
+                   kk != 0);
           mma_commit(smem_u32(&bars->s_full[x]));
           if (last) mma_commit(smem_u32(&bars->k_free[s]));
           return true;
@@ -377,7 +408,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (first && !mbar_wait(smem_u32(&bars->v_full[s]), (jt >> 1) & 1, a.err, SITE_KV8_PIPE)) return false;
           tc_fence_after();
           const uint32_t pcol = tmem + kColsS * (uint32_t)x, dO = tmem + kColsO + kColsS * (uint32_t)x;
-          const uint64_t dv = s ? dv1 : dv0;
+          const uint64_t dv = dv0 + s * (M::kStageV / 16);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
             mma_f16_ts(dO, pcol + kk * 8, dv + (uint64_t)(kk * (16 * 128 / 16)), id_pv, (j > 0 || kk > 0) ? 1u : 0u);
@@ -400,37 +431,35 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         mbar_wait(smem_u32(&bars->mma_done), pieces & 1, a.err, SITE_KV8_PIPE);
       }
     }
-    if (warp == kSoftWarps + kConvWarps + 1) {
-      // ---------------- codes to shared memory ----------------
-      // Lanes 0..7 know the pages and scales of a block's eight runs of 16 keys, looked up
-      // a block ahead; boxes are whole pages, or 64 keys.
+    if (warp == kSoftWarps + kConvWarps + 1 || warp == kSoftWarps + kConvWarps + 2) {
+      // ---------------- codes to shared memory: K's, V's ----------------
+      // Lanes 0..7 know the pages (and the K warp's the scales) of a block's eight runs of 16
+      // keys, looked up ahead; boxes are whole pages.
+      const bool is_k = warp == kSoftWarps + kConvWarps + 1;
+      const CUtensorMap* map = is_k ? &tmk : &tmv;
       const int ps = 1 << a.shift, run = lane & 7;
-      const uint32_t first_runs = ps == 16 ? 15u : ps == 32 ? 5u : 1u;
+      const uint32_t firsts = ps == 16 ? 0xffu : ps == 32 ? 0x55u : 0x11u;  // the runs that boxes begin with
       bool ok = true;
-      uint32_t st = 0, jt = 0;
-      if (lane == 0) {
-        tma_prefetch_desc(&tmk);
-        tma_prefetch_desc(&tmv);
-      }
+      uint32_t jt = 0;
+      if (lane == 0) tma_prefetch_desc(map);
       for (int b = b0; b < b1 && ok;) {
         const Piece p = piece_at(b);
         const int nb = p.jb - p.ja;
         b = p.next;
-        // -1: the call reads nothing of the run's page
-        auto look_up = [&](int j) -> int {
-          const int key = (p.ja + j) * kKeys + run * 16, first = key & ~(ps - 1);
-          return j < nb && first < p.len && first + ps > p.t.lo ? a.bt[(int64_t)p.seq * a.bt_stride + (key >> a.shift)] : -1;
-        };
+        // whether the call reads of the run's page, and the page
         auto wanted = [&](int j) -> bool {
           const int first = ((p.ja + j) * kKeys + run * 16) & ~(ps - 1);
-          return first < p.len && first + ps > p.t.lo;
+          return j < nb && first < p.len && first + ps > p.t.lo;
+        };
+        auto look_up = [&](int j) -> int {
+          return wanted(j) ? a.bt[(int64_t)p.seq * a.bt_stride + (((p.ja + j) * kKeys + run * 16) >> a.shift)] : -1;
         };
         // scales of the block behind the present one, pages of two: no load is waited for
         int next = look_up(0), next2 = look_up(1);
         float ks_next, vs_next;
         auto scales_of = [&](int g) {
-          ks_next = 1.f, vs_next = 0.f;
-          if (g >= 0 && g < a.num_pages) {
+          ks_next = vs_next = 1.f;
+          if (is_k && g >= 0 && g < a.num_pages) {
             ks_next = a.k_scales[(int64_t)g * a.kvh + p.kh];
             vs_next = a.v_scales[(int64_t)g * a.kvh + p.kh];
           }
@@ -439,144 +468,139 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         for (int j = 0; j < nb && ok; ++j, ++jt) {
           int page = next;
           const float ks = ks_next, vs = vs_next;
-          const bool want = wanted(j);
-          if (want && (page < 0 || page >= a.num_pages)) {
-            if (lane < 8) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page);
+          const bool lost = wanted(j) && (page < 0 || page >= a.num_pages);
+          if (lost) {
+            if (is_k && lane < 8) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page);
             page = -1;
           }
           next = next2;
           next2 = look_up(j + 2);
           scales_of(next);
-          const bool lost = __any_sync(0xffffffffu, want && page < 0);
-          // (rows of the maps are 128 bytes: one key, or two of 64 dims)
-          const int row = (int)((((int64_t)page * a.kvh + p.kh) << a.shift) * D / 128);
-          const uint32_t have = __ballot_sync(0xffffffffu, page >= 0);
-          for (int step = 0; step < 4; ++step, ++st) {
-            const uint32_t slot = st % kRawSteps;
-            int w = 1;
-            if (lane == 0) w = mbar_wait(smem_u32(&bars->raw_free[slot]), ((st / kRawSteps) & 1) ^ 1, a.err, SITE_KV8_PIPE);
-            ok = __shfl_sync(0xffffffffu, w, 0) != 0;
+          const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0) & 0xffu, boxes = pages & firsts;
+          const uint32_t any_lost = __ballot_sync(0xffffffffu, lost);
+          // (rows of the maps are as long as a key's)
+          const int row = (int)(((int64_t)page * a.kvh + p.kh) << a.shift);
+          int y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, row, i);
+          if (is_k) {
+            const uint32_t s = jt % M::kStagesK, bar = smem_u32(&bars->k_full[s]);
+            ok = warp_wait(&bars->k_free[s], ((jt / M::kStagesK) & 1) ^ 1, a.err);
             if (!ok) break;
-            if (step == 0) {
-              if (lane < 8) {
-                float* sc = scales + (jt % kScaleRing) * kScaleFloats + lane;
-                if (lane == 0) sc[24] = lost ? 1.f : 0.f;  // a run's keys are passed over
-                sc[0] = want && page < 0 ? -1.f : ks;
-                sc[8] = page >= 0 ? log2f(vs) : 0.f;
-                sc[16] = page >= 0 ? 1.f / vs : 0.f;  // zero: codes that were not read
-              }
-              __syncwarp();
+            if (lane < 8) {
+              float* sc = scales + (jt % kScaleRing) * kScaleFloats + lane;
+              if (lane == 0) sc[24] = any_lost ? 1.f : 0.f;
+              sc[0] = lost ? -1.f : ks;  // negative: keys that are passed over
+              sc[8] = log2f(vs);
+              sc[16] = 1.f / vs;
             }
-            const uint32_t bar = smem_u32(&bars->raw_full[slot]);
-            const uint32_t dst = sbase + (uint32_t)(M::kRaw + slot * M::kRawStep);
-            // boxes begin at every per_box-th run of the step
-            const int run0 = (step & 1) * 4;
-            const uint32_t boxes = have >> run0 & first_runs;
-            const int y0 = __shfl_sync(0xffffffffu, row, run0), y1 = __shfl_sync(0xffffffffu, row, run0 + 1);
-            const int y2 = __shfl_sync(0xffffffffu, row, run0 + 2), y3 = __shfl_sync(0xffffffffu, row, run0 + 3);
-            const CUtensorMap* map = step & 2 ? &tmv : &tmk;
+            __syncwarp();
             if (elect_one()) {
               if (boxes)
                 mbar_expect_tx(bar, (uint32_t)__popc(boxes) * (uint32_t)(ps * D));
               else
                 mbar_arrive(bar);
-              if (boxes & 1) tma_load_2d(dst, map, 0, y0, bar);
-              if (boxes & 2) tma_load_2d(dst + 16 * D, map, 0, y1, bar);
-              if (boxes & 4) tma_load_2d(dst + 32 * D, map, 0, y2, bar);
-              if (boxes & 8) tma_load_2d(dst + 48 * D, map, 0, y3, bar);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (boxes >> i & 1) tma_load_2d(k_reg(0) + s * M::kPart + i * (16 * D), map, 0, y[i], bar);
             }
             __syncwarp();
+          } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t st = 2 * jt + h, slot = st % kRawSteps, bar = smem_u32(&bars->raw_full[slot]);
+              if (ok) ok = warp_wait(&bars->raw_free[slot], ((st / kRawSteps) & 1) ^ 1, a.err);
+              if (!ok) break;
+              if (elect_one()) {
+                if (h == 0) bars->read[jt % kScaleRing] = pages;
+                const uint32_t half = boxes >> (4 * h) & 15;
+                if (half)
+                  mbar_expect_tx(bar, (uint32_t)__popc(half) * (uint32_t)(ps * D));
+                else
+                  mbar_arrive(bar);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (half >> i & 1)
+                    tma_load_2d(sbase + (uint32_t)M::kRaw + slot * M::kRawStep + i * (16 * D), map, 0, y[4 * h + i], bar);
+              }
+              __syncwarp();
+            }
           }
         }
       }
       // no copy is under way when the CTA leaves
       if (lane == 0) {
-        for (uint32_t i = st > kRawSteps ? st - kRawSteps : 0; i < st; ++i)
-          mbar_wait(smem_u32(&bars->raw_full[i % kRawSteps]), (i / kRawSteps) & 1, a.err, SITE_KV8_PIPE);
+        const uint32_t stages = is_k ? M::kStagesK : kRawSteps, n = is_k ? jt : 2 * jt;
+        for (uint32_t i = n > stages ? n - stages : 0; i < n; ++i)
+          mbar_wait(smem_u32(is_k ? &bars->k_full[i % stages] : &bars->raw_full[i % stages]), (i / stages) & 1, a.err, SITE_KV8_PIPE);
       }
     }
     __syncwarp();
   } else if (warp >= kSoftWarps) {
     // ---------------- codes to fp16 ----------------
-    // Steps of 64 keys of K or of V (K, K, V, V of a block), 16 bytes of a key to a thread.
-    // Eight lanes read rows q and q ^ 5 of a step's bytes (one row of two keys where
-    // head_dim is 64): both the 128-byte swizzled reads and the writes then touch
-    // every bank once.
+    // Steps of 64 keys of V, 16 bytes of a key to a thread, consecutive bytes to
+    // consecutive threads.  head_dim 128: lanes of the second half of a key write their
+    // two chunks the other way round, so that eight lanes touch every bank once.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     const int t = threadIdx.x - kSoftWarps * 32;
-    const int c4 = t & 3, hb = (t >> 2) & 1, q3 = (t >> 3) & 3, w4 = t >> 5;
-    const int half = D == 128 ? w4 & 1 : 0;
-    const int rin = D == 128 ? (w4 >> 1) * 8 + (hb ? q3 ^ 5 : q3) : w4 * 8 + q3 * 2 + hb;
+    const int c4 = t & 3, half = D == 128 ? (t >> 2) & 1 : 0, rin = D == 128 ? t >> 3 : t >> 2;
     bool ok = true;
-    uint32_t jt = 0, st = 0;
+    uint32_t jt = 0;
     for (int b = b0; b < b1 && ok;) {
       const Piece p = piece_at(b);
-      const int steps = (p.jb - p.ja) * 4;
       b = p.next;
-      for (int step = 0; step < steps; ++step, ++st) {
-        const uint32_t s = jt & 1, slot = st % kRawSteps;
-        const bool is_v = step & 2;
-        if (!(step & 1)) ok = warp_wait(is_v ? &bars->v_free[s] : &bars->k_free[s], ((jt >> 1) & 1) ^ 1, a.err);
+#pragma unroll 1
+      for (int k = 2 * p.ja; k < 2 * p.jb; ++k) {  // steps of the sequence
+        const uint32_t s = jt & 1, st = 2 * jt + (k & 1), slot = st % kRawSteps;
+        if (!(k & 1)) ok = warp_wait(&bars->v_free[s], ((jt >> 1) & 1) ^ 1, a.err);
         if (ok) ok = warp_wait(&bars->raw_full[slot], (st / kRawSteps) & 1, a.err);
         if (!ok) break;
         uint4 w[STEP_PASSES];
 #pragma unroll
-        for (int i = 0; i < STEP_PASSES; ++i) {
-          const int key = i * PASS + rin;
-          const int row = D == 128 ? key : key >> 1, chunk = D == 128 ? half * 4 + c4 : (key & 1) * 4 + c4;
-          w[i] = *reinterpret_cast<const uint4*>(smem + M::kRaw + slot * M::kRawStep + row * 128 + ((chunk ^ (row & 7)) << 4));
-        }
-        if (is_v) {
-          // codes of keys behind the end, and of pages that were not read, count as zero
-          const int key0 = (p.ja + (step >> 2)) * kKeys + (step & 1) * 64;
-          const float4 iv = *reinterpret_cast<const float4*>(scales + (jt % kScaleRing) * kScaleFloats + 16 + (step & 1) * 4);
-          if (key0 + 64 > p.len || fminf(fminf(iv.x, iv.y), fminf(iv.z, iv.w)) == 0.f) {
+        for (int i = 0; i < STEP_PASSES; ++i)
+          w[i] = *reinterpret_cast<const uint4*>(smem + M::kRaw + slot * M::kRawStep + i * (kConvWarps * 512) + t * 16);
+        // codes of keys behind the end, and of pages that were not read, count as zero
+        const uint32_t read = bars->read[jt % kScaleRing] >> (4 * (k & 1)) & 15;
+        if (k * 64 + 64 > p.len || read != 15) {
 #pragma unroll
-            for (int i = 0; i < STEP_PASSES; ++i) {
-              const int key = i * PASS + rin, run = key >> 4;
-              const float f = run == 0 ? iv.x : run == 1 ? iv.y : run == 2 ? iv.z : iv.w;
-              if (key0 + key >= p.len || f == 0.f) w[i] = make_uint4(0, 0, 0, 0);
-            }
+          for (int i = 0; i < STEP_PASSES; ++i) {
+            const int key = i * PASS + rin;
+            if (k * 64 + key >= p.len || !(read >> (key >> 4) & 1)) w[i] = make_uint4(0, 0, 0, 0);
           }
         }
-        const uint32_t dst = (is_v ? v_reg(s) : k_reg(s)) + (uint32_t)(half * kTileRegion);
+        const uint32_t dst = v_reg(s) + (uint32_t)(half * kTileRegion);
         __half2 nan = __floats2half2_rn(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < STEP_PASSES; ++i) {
-          const int row = (step & 1) * 64 + i * PASS + rin;
+          const int row = (k & 1) * 64 + i * PASS + rin;
           const uint32_t h[8] = {from_e4m3x2(w[i].x), from_e4m3x2(w[i].x >> 16), from_e4m3x2(w[i].y), from_e4m3x2(w[i].y >> 16),
                                  from_e4m3x2(w[i].z), from_e4m3x2(w[i].z >> 16), from_e4m3x2(w[i].w), from_e4m3x2(w[i].w >> 16)};
-          if (is_v) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) nan = __hfma2(*reinterpret_cast<const __half2*>(&h[k]), __floats2half2_rn(0.f, 0.f), nan);
-          }
-          const uint32_t at = dst + (uint32_t)(row * 128);
-          sts_u4(at + (uint32_t)(((2 * c4) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-          sts_u4(at + (uint32_t)(((2 * c4 + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+          for (int e = 0; e < 8; ++e) nan = __hfma2(*reinterpret_cast<const __half2*>(&h[e]), __floats2half2_rn(0.f, 0.f), nan);
+          const uint32_t at = dst + (uint32_t)(row * 128), c0 = (uint32_t)(((2 * c4) ^ (row & 7)) << 4), c1 = c0 ^ 16;
+          sts_u4(at + (half ? c1 : c0), half ? h[4] : h[0], half ? h[5] : h[1], half ? h[6] : h[2], half ? h[7] : h[3]);
+          sts_u4(at + (half ? c0 : c1), half ? h[0] : h[4], half ? h[1] : h[5], half ? h[2] : h[6], half ? h[3] : h[7]);
         }
-        if (is_v && !(__low2float(nan) == 0.f && __high2float(nan) == 0.f)) {
-          // V's NaN codes: zero, and known to have been there
+        if (!(__low2float(nan) == 0.f && __high2float(nan) == 0.f)) {
+          // NaN codes: zero, and known to have been there
           bars->nan = 1;
 #pragma unroll 1
-          for (int i = 0; i < STEP_PASSES; ++i) {
-            const int row = (step & 1) * 64 + i * PASS + rin;
-#pragma unroll 1
-            for (int k = 0; k < 8; ++k) {
-              const uint32_t at = dst + (uint32_t)(row * 128 + (((2 * c4 + (k >> 2)) ^ (row & 7)) << 4) + (k & 3) * 4);
-              uint32_t x;
-              asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at));
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pack_f16(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f)) : "memory");
-            }
+          for (int i = 0; i < STEP_PASSES * 8; ++i) {
+            const int row = (k & 1) * 64 + (i >> 3) * PASS + rin;
+            const uint32_t at = dst + (uint32_t)(row * 128 + (((2 * c4 + (i >> 2 & 1)) ^ (row & 7)) << 4) + (i & 3) * 4);
+            uint32_t x;
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x) : "r"(at));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x));
+            asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(pack_f16(f.x == f.x ? f.x : 0.f, f.y == f.y ? f.y : 0.f)) : "memory");
           }
         }
-        if (step & 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor core
+        if (k & 1) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // visible to the tensor core
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(smem_u32(&bars->raw_free[slot]));
-          if (step & 1) mbar_arrive(smem_u32(is_v ? &bars->v_full[s] : &bars->k_full[s]));
+          if (k & 1) mbar_arrive(smem_u32(&bars->v_full[s]));
         }
-        if ((step & 3) == 3) ++jt;
+        jt += k & 1;
       }
     }
     __syncwarp();
@@ -599,38 +623,54 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int lo = a.window > 0 ? pos - a.window + 1 : 0;
       float fac = a.scale;
       {
-        // the query -> fp16, swizzled as the product reads it
+        // the query as sums of e4m3 numbers, swizzled as the product reads them
         const T* qp = static_cast<const T*>(a.q) + (int64_t)(p.row0 + token) * a.ldq + (int64_t)head * D;
-        auto eight = [&](int k) -> uint4 {  // dims [8 k, 8 k + 8)
-          if (!valid) return make_uint4(0, 0, 0, 0);
-          if (args.vec_q) return *reinterpret_cast<const uint4*>(qp + 8 * k);
-          const unsigned short* h = reinterpret_cast<const unsigned short*>(qp + 8 * k);
-          return make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
-                            h[6] | (uint32_t)h[7] << 16);
-        };
-        float inv = 1.f;
-        if constexpr (Elem<T>::kMmaFormat == 1) {
-          // by a power of two into [1, 2): bf16's range into fp16's
-          float m = 0.f;
-#pragma unroll 4
-          for (int k = 0; k < D / 8; ++k) {
-            const uint4 v = eight(k);
-            m = fmaxf(fmaxf(m, fmaxf(fabsf(Elem<T>::lo(v.x)), fabsf(Elem<T>::hi(v.x)))),
-                      fmaxf(fabsf(Elem<T>::lo(v.y)), fabsf(Elem<T>::hi(v.y))));
-            m = fmaxf(fmaxf(m, fmaxf(fabsf(Elem<T>::lo(v.z)), fabsf(Elem<T>::hi(v.z)))),
-                      fmaxf(fabsf(Elem<T>::lo(v.w)), fabsf(Elem<T>::hi(v.w))));
+        auto eight = [&](int k, float* f) {  // dims [8 k, 8 k + 8)
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (valid) {
+            if (args.vec_q) {
+              v = *reinterpret_cast<const uint4*>(qp + 8 * k);
+            } else {
+              const unsigned short* h = reinterpret_cast<const unsigned short*>(qp + 8 * k);
+              v = make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
+                             h[6] | (uint32_t)h[7] << 16);
+            }
           }
-          const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 253u);
-          fac *= __uint_as_float(ex << 23);
-          inv = __uint_as_float((254u - ex) << 23);
-        }
-#pragma unroll 4
+          f[0] = Elem<T>::lo(v.x), f[1] = Elem<T>::hi(v.x), f[2] = Elem<T>::lo(v.y), f[3] = Elem<T>::hi(v.y);
+          f[4] = Elem<T>::lo(v.z), f[5] = Elem<T>::hi(v.z), f[6] = Elem<T>::lo(v.w), f[7] = Elem<T>::hi(v.w);
+        };
+        float m = 0.f;
+#pragma unroll 2
         for (int k = 0; k < D / 8; ++k) {
-          uint4 v = eight(k);
-          if constexpr (Elem<T>::kMmaFormat == 1)
-            v = make_uint4(pack_f16(Elem<T>::lo(v.x) * inv, Elem<T>::hi(v.x) * inv), pack_f16(Elem<T>::lo(v.y) * inv, Elem<T>::hi(v.y) * inv),
-                           pack_f16(Elem<T>::lo(v.z) * inv, Elem<T>::hi(v.z) * inv), pack_f16(Elem<T>::lo(v.w) * inv, Elem<T>::hi(v.w) * inv));
-          sts_u4(q_reg(x) + (uint32_t)((k >> 3) * kTileRegion + r * 128 + (((k & 7) ^ (r & 7)) << 4)), v.x, v.y, v.z, v.w);
+          float f[8];
+          eight(k, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+        }
+        // (powers whose inverse is a normal number too)
+        const uint32_t ex = min(max(__float_as_uint(m) >> 23, 10u), 253u);
+        fac *= __uint_as_float((ex - 7) << 23);
+        const float inv = __uint_as_float((261u - ex) << 23);
+#pragma unroll 1
+        for (int k = 0; k < D / 8; ++k) {
+          float f[8];
+          eight(k, f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] *= inv;
+          const int c = k >> 1;  // 16-byte chunk of the row
+          const uint32_t at = q_reg(x) + (uint32_t)(r * D + ((D == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4) + (k & 1) * 8);
+#pragma unroll
+          for (int i = 0; i < M::kParts; ++i) {
+            uint32_t u[2];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t code = to_e4m3x2(f[2 * e], f[2 * e + 1]);
+              const float2 g = e4m3x2_floats(code);
+              f[2 * e] -= g.x, f[2 * e + 1] -= g.y;
+              u[e >> 1] = e & 1 ? u[e >> 1] | code << 16 : code;
+            }
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + (uint32_t)(i * M::kPart)), "r"(u[0]), "r"(u[1]) : "memory");
+          }
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();  // (the piece before's O has been read)
@@ -852,7 +892,7 @@ __global__ void __launch_bounds__(256) kv8_chunk_join_kernel(const __grid_consta
 
 template <typename T, int D>
 int launch_chunk8(const ChunkArgs8& c, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
-  const int smem = ChunkSmem<D>::kBytes;
+  const int smem = ChunkSmem<T, D>::kBytes;
   SAR_TRY(ensure_smem_attr(reinterpret_cast<const void*>(&kv8_chunk_kernel<T, D>), smem, "kv8 chunk: set smem attribute"));
   // as many CTAs as units can come to, one per SM at least
   const int64_t pairs = (int64_t)c.a.rows * c.a.G;
@@ -887,12 +927,11 @@ int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, 
   c.parts = reinterpret_cast<float*>(w + up256(2ll * c.sms * 256 * 8));
   c.vec_q = aligned_to(a.q, 16) && a.ldq % 8 == 0;
   c.vec_o = aligned_to(a.out, 16) && a.ldo % 8 == 0;
-  // the codes as rows of 128 bytes, a page to a box
+  // the codes as rows of head_dim bytes, a page to a box: K swizzled as the product reads it
   CUtensorMap k, v;
-  const uint64_t map_rows = ((uint64_t)a.num_pages * a.kvh << a.shift) * head_dim / 128;
-  const uint32_t box = (uint32_t)((head_dim << a.shift) / 128);
-  SAR_TRY(make_tmap_bytes(&k, a.k_codes, map_rows, 128, box));
-  SAR_TRY(make_tmap_bytes(&v, a.v_codes, map_rows, 128, box));
+  const uint64_t map_rows = (uint64_t)a.num_pages * a.kvh << a.shift;
+  SAR_TRY(make_tmap_rows8(&k, a.k_codes, map_rows, head_dim, 1u << a.shift, true));
+  SAR_TRY(make_tmap_rows8(&v, a.v_codes, map_rows, head_dim, 1u << a.shift, false));
   const bool bf = storage == SAR_STORAGE_BF16;
   if (head_dim == 128) return bf ? launch_chunk8<__nv_bfloat16, 128>(c, k, v, s) : launch_chunk8<__half, 128>(c, k, v, s);
   return bf ? launch_chunk8<__nv_bfloat16, 64>(c, k, v, s) : launch_chunk8<__half, 64>(c, k, v, s);

@@ -1084,6 +1084,22 @@ int make_tmap_bytes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t r
   return SAR_OK;
 }
 
+int make_tmap_rows8(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t row_bytes, uint32_t box_rows, bool swizzle) {
+  auto fn = encode_fn();
+  if (!fn) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");
+  if ((reinterpret_cast<uintptr_t>(ptr) & 15) || (row_bytes != 64 && row_bytes != 128) || rows == 0 || box_rows == 0 || box_rows > 256)
+    return set_error(SAR_ERR_INVALID_ARG, "tensor map (8-bit rows): pointer not 16-byte aligned or bad box");
+  cuuint64_t dims[2] = {row_bytes, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {row_bytes, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUtensorMapSwizzle sw = !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+  return SAR_OK;
+}
+
 int make_tmap_words(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows) {
   auto fn = encode_fn();
   if (!fn) return set_error(SAR_ERR_CUDA, "cuTensorMapEncodeTiled unavailable");

@@ -95,6 +95,10 @@ int make_tmap_16(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols
 // 128-byte x box_rows box and 128-byte swizzle; bytes behind a row read zero.
 int make_tmap_bytes(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes, uint32_t box_rows);
 
+// A 2D map over rows of row_bytes (64 or 128) bytes, boxes of box_rows whole rows,
+// with a swizzle as wide as a row or none.
+int make_tmap_rows8(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t row_bytes, uint32_t box_rows, bool swizzle);
+
 // A 2D map of 32-bit words over row-major [rows, cols], boxes of box_rows whole
 // rows (cols <= 256), no swizzle; rows behind the last read zero.
 int make_tmap_words(CUtensorMap* map, const void* ptr, uint64_t rows, uint32_t cols, uint32_t box_rows);
