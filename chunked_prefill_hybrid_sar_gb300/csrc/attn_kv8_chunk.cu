@@ -558,7 +558,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         uint4 w[STEP_PASSES];
 #pragma unroll
         for (int i = 0; i < STEP_PASSES; ++i)
-          w[i] = *reinterpret_cast<const uint4*>(smem + M::kRaw + slot * M::kRawStep + i * (kConvWarps * 512) + t * 16);
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[i].x), "=r"(w[i].y), "=r"(w[i].z), "=r"(w[i].w)
+                       : "r"(sbase + (uint32_t)(M::kRaw + slot * M::kRawStep + i * (kConvWarps * 512) + t * 16)));
         // codes of keys behind the end, and of pages that were not read, count as zero
         const uint32_t read = bars->read[jt % kScaleRing] >> (4 * (k & 1)) & 15;
         if (k * 64 + 64 > p.len || read != 15) {
@@ -682,41 +683,62 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int j = 0; j < nb && alive; ++j) {
         if (!(alive = warp_wait(&bars->s_full[x], (mine_done + j) & 1, a.err))) break;
         tc_fence_after();
-        float sv[128];
-#pragma unroll
-        for (int c = 0; c < 128; c += 32) tmem_ld32(scol + c, reinterpret_cast<uint32_t*>(sv) + c);
+        // 64 keys at a time, in loops that are not unrolled: six roles' code contends for the
+        // instruction cache, and a row's 128 scores at once took half of the clocks that
+        // reading them again does.
         const int key0 = (p.ja + j) * kKeys;
-        const float* sc = scales + ((base + j) % kScaleRing) * kScaleFloats;
-        const bool edge = key0 + kKeys - 1 > pos || key0 < lo || sc[24] != 0.f;
-        tmem_wait_ld();
-        // keys that this row does not see, and pages out of range: raw score times factor is -inf
-        if (edge) {
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const int k0 = key0 + 32 * w;  // bit c: key k0 + c is seen
+        const uint32_t sc = sbase + (uint32_t)(M::kScales + ((base + j) % kScaleRing) * (kScaleFloats * 4));
+        const bool lost = lds_f4(sc + 96).x != 0.f;
+        if (__any_sync(0xffffffffu, key0 + kKeys - 1 > pos || key0 < lo || lost)) {
+          // keys that this row does not see, and pages out of range: -inf, in tensor memory
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            const int k0 = key0 + 32 * c;  // bit e: key k0 + e is seen
             uint32_t seen = pos < k0 ? 0u : pos - k0 >= 31 ? 0xffffffffu : (2u << (pos - k0)) - 1;
             seen &= lo <= k0 ? 0xffffffffu : lo - k0 > 31 ? 0u : 0xffffffffu << (lo - k0);
-            if (sc[2 * w] < 0.f) seen &= 0xffff0000u;
-            if (sc[2 * w + 1] < 0.f) seen &= 0xffffu;
+            if (lost) {
+              const float4 k4 = lds_f4(sc + (c >> 1) * 16);
+              if ((c & 1 ? k4.z : k4.x) < 0.f) seen &= 0xffff0000u;
+              if ((c & 1 ? k4.w : k4.y) < 0.f) seen &= 0xffffu;
+            }
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!(seen >> c & 1)) sv[32 * w + c] = -INFINITY;
+            for (int h = 0; h < 2; ++h) {
+              uint32_t u[16];
+              tmem_ld16(scol + c * 32 + h * 16, u);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e)
+                if (!(seen >> (16 * h + e) & 1)) u[e] = 0xff800000u;
+              tmem_st16(scol + c * 32 + h * 16, u);
+            }
           }
+          tmem_wait_st();
         }
         // (a factor is above zero, where -inf times it would be NaN)
-        float f[8], pm = -INFINITY;
+        auto factor = [&](float k) { return fmaxf(fabsf(k) * fac, 1.2e-38f); };
+        float pm = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float sv[64];
+          tmem_ld32(scol + c * 64, reinterpret_cast<uint32_t*>(sv));
+          tmem_ld32(scol + c * 64 + 32, reinterpret_cast<uint32_t*>(sv) + 32);
+          const float4 k4 = lds_f4(sc + c * 16), lv4 = lds_f4(sc + 32 + c * 16);
+          tmem_wait_ld();
 #pragma unroll
-        for (int g = 0; g < 8; ++g) {
-          f[g] = fmaxf(fabsf(sc[g]) * fac, 1.2e-38f);
-          // (three to an instruction, in two chains)
-          float x0 = sv[g * 16], x1 = sv[g * 16 + 1];
+          for (int g = 0; g < 4; ++g) {
+            // (three to an instruction, in two chains)
+            float x0 = sv[g * 16], x1 = sv[g * 16 + 1];
 #pragma unroll
-          for (int c = 2; c < 14; c += 4) {
-            x0 = fmaxf(fmaxf(x0, sv[g * 16 + c]), sv[g * 16 + c + 1]);
-            x1 = fmaxf(fmaxf(x1, sv[g * 16 + c + 2]), sv[g * 16 + c + 3]);
+            for (int e = 2; e < 14; e += 4) {
+              x0 = fmaxf(fmaxf(x0, sv[g * 16 + e]), sv[g * 16 + e + 1]);
+              x1 = fmaxf(fmaxf(x1, sv[g * 16 + e + 2]), sv[g * 16 + e + 3]);
+            }
+            x0 = fmaxf(fmaxf(x0, sv[g * 16 + 14]), sv[g * 16 + 15]);
+            const float k = g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w;
+            const float lv = g == 0 ? lv4.x : g == 1 ? lv4.y : g == 2 ? lv4.z : lv4.w;
+            pm = fmaxf(pm, fmaf(fmaxf(x0, x1), factor(k), lv));
           }
-          x0 = fmaxf(fmaxf(x0, sv[g * 16 + 14]), sv[g * 16 + 15]);
-          pm = fmaxf(pm, fmaf(fmaxf(x0, x1), f[g], sc[8 + g]));
         }
         const float m_new = fmaxf(m_used, pm);
         const bool need = m_new > m_used + kGrowth;
@@ -739,26 +761,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (need) m_used = m_new;
         }
         const float ref = m_used == -INFINITY ? 0.f : m_used;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t u[16];
+        // P's columns [32 c, 32 c + 32) lie over scores that have been read
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          float sv[64];
+          tmem_ld32(scol + c * 64, reinterpret_cast<uint32_t*>(sv));
+          tmem_ld32(scol + c * 64 + 32, reinterpret_cast<uint32_t*>(sv) + 32);
+          const float4 k4 = lds_f4(sc + c * 16), lv4 = lds_f4(sc + 32 + c * 16), iv4 = lds_f4(sc + 64 + c * 16);
+          tmem_wait_ld();
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int g = 2 * c + h;
-            const float off = sc[8 + g] - ref;
-            const uint64_t f2 = pair_of(f[g], f[g]), off2 = pair_of(off, off);
-            uint64_t ls[2] = {0, 0};
+            uint32_t u[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 t = of_pair(fma_pair(pair_of(sv[g * 16 + 2 * e], sv[g * 16 + 2 * e + 1]), f2, off2));
-              const float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
-              ls[e & 1] = add_pair(ls[e & 1], pair_of(p0, p1));
-              u[h * 8 + e] = pack_f16(p0, p1);
+            for (int gg = 0; gg < 2; ++gg) {
+              const int g = 2 * h + gg;
+              const float f = factor(g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w);
+              const float off = (g == 0 ? lv4.x : g == 1 ? lv4.y : g == 2 ? lv4.z : lv4.w) - ref;
+              const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
+              uint64_t ls[2] = {0, 0};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float2 t = of_pair(fma_pair(pair_of(sv[g * 16 + 2 * e], sv[g * 16 + 2 * e + 1]), f2, off2));
+                const float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
+                ls[e & 1] = add_pair(ls[e & 1], pair_of(p0, p1));
+                u[gg * 8 + e] = pack_f16(p0, p1);
+              }
+              const float2 sum = of_pair(add_pair(ls[0], ls[1]));
+              l = fmaf(sum.x + sum.y, g == 0 ? iv4.x : g == 1 ? iv4.y : g == 2 ? iv4.z : iv4.w, l);
             }
-            const float2 sum = of_pair(add_pair(ls[0], ls[1]));
-            l = fmaf(sum.x + sum.y, sc[16 + g], l);
+            tmem_st16(scol + c * 32 + h * 16, u);
           }
-          tmem_st16(scol + c * 16, u);
         }
         tmem_wait_st();
         tc_fence_before();
