@@ -48,7 +48,7 @@ constexpr int kMostK = 3;                 // K stages
 constexpr int kMostTiles = 256;          // of a call whose CTAs take stretches
 constexpr int kLeastBlocks = 4;          // of a stretch
 constexpr float kGrowth = 8.f;           // log2 of a maximum's growth that O tolerates
-constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its first 64 columns
+constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its last 64 columns
 constexpr uint32_t kColsO = 256;         // O_x at 256 + x * 128
 
 struct ChunkBars {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (!mbar_wait(smem_u32(&bars->p_full[x]), jx & 1, a.err, SITE_KV8_PIPE)) return false;
           if (first && !mbar_wait(smem_u32(&bars->v_full[s]), (jt >> 1) & 1, a.err, SITE_KV8_PIPE)) return false;
           tc_fence_after();
-          const uint32_t pcol = tmem + kColsS * (uint32_t)x, dO = tmem + kColsO + kColsS * (uint32_t)x;
+          const uint32_t pcol = tmem + kColsS * (uint32_t)x + 64, dO = tmem + kColsO + kColsS * (uint32_t)x;
           const uint64_t dv = dv0 + s * (M::kStageV / 16);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
@@ -683,9 +683,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (int j = 0; j < nb && alive; ++j) {
         if (!(alive = warp_wait(&bars->s_full[x], (mine_done + j) & 1, a.err))) break;
         tc_fence_after();
-        // 64 keys at a time, in loops that are not unrolled: six roles' code contends for the
-        // instruction cache, and a row's 128 scores at once took half of the clocks that
-        // reading them again does.
+        // (loops that are not unrolled: six roles' code contends for the instruction cache)
         const int key0 = (p.ja + j) * kKeys;
         const uint32_t sc = sbase + (uint32_t)(M::kScales + ((base + j) % kScaleRing) * (kScaleFloats * 4));
         const bool lost = lds_f4(sc + 96).x != 0.f;
@@ -717,29 +715,34 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         // (a factor is above zero, where -inf times it would be NaN)
         auto factor = [&](float k) { return fmaxf(fabsf(k) * fac, 1.2e-38f); };
+        float sv[64], first[64];  // keys 64 .. 127, and those before
+        tmem_ld32(scol, reinterpret_cast<uint32_t*>(first));
+        tmem_ld32(scol + 32, reinterpret_cast<uint32_t*>(first) + 32);
+        tmem_ld32(scol + 64, reinterpret_cast<uint32_t*>(sv));
+        tmem_ld32(scol + 96, reinterpret_cast<uint32_t*>(sv) + 32);
+        float4 k4 = lds_f4(sc + 16), lv4 = lds_f4(sc + 48);
         float pm = -INFINITY;
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          float sv[64];
-          tmem_ld32(scol + c * 64, reinterpret_cast<uint32_t*>(sv));
-          tmem_ld32(scol + c * 64 + 32, reinterpret_cast<uint32_t*>(sv) + 32);
-          const float4 k4 = lds_f4(sc + c * 16), lv4 = lds_f4(sc + 32 + c * 16);
-          tmem_wait_ld();
+        auto largest = [&](const float* x, const float4& k, const float4& lv) {
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             // (three to an instruction, in two chains)
-            float x0 = sv[g * 16], x1 = sv[g * 16 + 1];
+            float x0 = x[g * 16], x1 = x[g * 16 + 1];
 #pragma unroll
             for (int e = 2; e < 14; e += 4) {
-              x0 = fmaxf(fmaxf(x0, sv[g * 16 + e]), sv[g * 16 + e + 1]);
-              x1 = fmaxf(fmaxf(x1, sv[g * 16 + e + 2]), sv[g * 16 + e + 3]);
+              x0 = fmaxf(fmaxf(x0, x[g * 16 + e]), x[g * 16 + e + 1]);
+              x1 = fmaxf(fmaxf(x1, x[g * 16 + e + 2]), x[g * 16 + e + 3]);
             }
-            x0 = fmaxf(fmaxf(x0, sv[g * 16 + 14]), sv[g * 16 + 15]);
-            const float k = g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w;
-            const float lv = g == 0 ? lv4.x : g == 1 ? lv4.y : g == 2 ? lv4.z : lv4.w;
-            pm = fmaxf(pm, fmaf(fmaxf(x0, x1), factor(k), lv));
+            x0 = fmaxf(fmaxf(x0, x[g * 16 + 14]), x[g * 16 + 15]);
+            pm = fmaxf(pm, fmaf(fmaxf(x0, x1), factor(g == 0 ? k.x : g == 1 ? k.y : g == 2 ? k.z : k.w),
+                                g == 0 ? lv.x : g == 1 ? lv.y : g == 2 ? lv.z : lv.w));
           }
+        };
+        {
+          const float4 k0 = lds_f4(sc), lv0 = lds_f4(sc + 32);
+          tmem_wait_ld();
+          largest(first, k0, lv0);
         }
+        largest(sv, k4, lv4);
         const float m_new = fmaxf(m_used, pm);
         const bool need = m_new > m_used + kGrowth;
         // P_x(j - 1) V has landed before S_x(j), which was issued behind it
@@ -761,37 +764,36 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           if (need) m_used = m_new;
         }
         const float ref = m_used == -INFINITY ? 0.f : m_used;
-        // P's columns [32 c, 32 c + 32) lie over scores that have been read
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          float sv[64];
-          tmem_ld32(scol + c * 64, reinterpret_cast<uint32_t*>(sv));
-          tmem_ld32(scol + c * 64 + 32, reinterpret_cast<uint32_t*>(sv) + 32);
-          const float4 k4 = lds_f4(sc + c * 16), lv4 = lds_f4(sc + 32 + c * 16), iv4 = lds_f4(sc + 64 + c * 16);
-          tmem_wait_ld();
+        // P lies over the scores' upper half
+        auto weigh = [&](const float* x, int c, const float4& k, const float4& lv) {
+          const float4 iv = lds_f4(sc + 64 + c * 16);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t u[16];
 #pragma unroll
             for (int gg = 0; gg < 2; ++gg) {
               const int g = 2 * h + gg;
-              const float f = factor(g == 0 ? k4.x : g == 1 ? k4.y : g == 2 ? k4.z : k4.w);
-              const float off = (g == 0 ? lv4.x : g == 1 ? lv4.y : g == 2 ? lv4.z : lv4.w) - ref;
+              const float f = factor(g == 0 ? k.x : g == 1 ? k.y : g == 2 ? k.z : k.w);
+              const float off = (g == 0 ? lv.x : g == 1 ? lv.y : g == 2 ? lv.z : lv.w) - ref;
               const uint64_t f2 = pair_of(f, f), off2 = pair_of(off, off);
               uint64_t ls[2] = {0, 0};
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const float2 t = of_pair(fma_pair(pair_of(sv[g * 16 + 2 * e], sv[g * 16 + 2 * e + 1]), f2, off2));
+                const float2 t = of_pair(fma_pair(pair_of(x[g * 16 + 2 * e], x[g * 16 + 2 * e + 1]), f2, off2));
                 const float p0 = exp2_fast(t.x), p1 = exp2_fast(t.y);
                 ls[e & 1] = add_pair(ls[e & 1], pair_of(p0, p1));
                 u[gg * 8 + e] = pack_f16(p0, p1);
               }
               const float2 sum = of_pair(add_pair(ls[0], ls[1]));
-              l = fmaf(sum.x + sum.y, g == 0 ? iv4.x : g == 1 ? iv4.y : g == 2 ? iv4.z : iv4.w, l);
+              l = fmaf(sum.x + sum.y, g == 0 ? iv.x : g == 1 ? iv.y : g == 2 ? iv.z : iv.w, l);
             }
-            tmem_st16(scol + c * 32 + h * 16, u);
+            tmem_st16(scol + 64 + c * 32 + h * 16, u);
           }
-        }
+        };
+        weigh(sv, 1, k4, lv4);
+        k4 = lds_f4(sc);
+        lv4 = lds_f4(sc + 32);
+        weigh(first, 0, k4, lv4);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
