@@ -9,14 +9,15 @@
 // fill the machine.  The plan is three prefix sums' worth of arithmetic on the
 // lengths, formed by every CTA itself.
 //
-// Inside a CTA four warps take the stretch's blocks in turn, each with a ring of
+// Inside a CTA six warps take the stretch's blocks in turn, each with a ring of
 // blocks of its own, filled by TMA with the 128-byte swizzle across unit ends, so
 // the stream does not stop where a unit does.  Keys are the rows of the products:
 // S^T = K Q^T has 16 keys x 8 heads a tile and O^T = V^T P^T 16 dims x 8 heads, so a
 // group of up to eight heads wastes half as much as it would as the rows.  Codes
-// turn to fp16 in registers, exactly, on their way into the products; the order of
-// the dims inside a K = 16 step is free, and taken so that a lane's 16 bytes of a key
-// are its operands.  V's bytes are turned by ldmatrix over pairs of dims.
+// turn to fp16 in registers, exactly, on their way into the products (an e4m3 mma.sync
+// does the same, and with the queries too, at every use: 139 us against 127 for four
+// contexts of up to 131072); the order of the dims inside a step is free, and taken so that a lane's 16
+// bytes of a key are its operands.  V's bytes are transposed by ldmatrix over pairs of dims.
 //
 // Scales cost nothing: with t = S k_scale scale + log2(v_scale) in base 2 and m the
 // running maximum of t, 2^(t - m) weighs V's codes, and the sum takes it times
@@ -30,9 +31,9 @@ namespace sar {
 
 namespace {
 
-constexpr int kDecWarps = 4;
+constexpr int kDecWarps = 6;
 constexpr int kDecKeys = 32;    // keys of a block
-constexpr int kDecStages = 3;   // blocks of a warp's ring
+constexpr int kDecStages = 2;   // blocks of a warp's ring
 constexpr int kDecHeads = 8;    // query heads of a KV head: the products' columns
 constexpr int kDecPerSm = 2;
 constexpr int kDecLeast = 8;    // blocks of a CTA's stretch at least, where there are so few
@@ -68,6 +69,16 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 // 2^x by the SFU (relative error 2^-22; 2^-inf = 0): a weight that is rounded to
 // fp16 next.
@@ -107,13 +118,13 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
   constexpr int BLK = kDecKeys * D;          // bytes of a block's keys
   constexpr int STAGE = 2 * BLK;
   constexpr int NT = D / 16;                 // tiles of 16 dims
-  constexpr int OWN = NT / kDecWarps;        // of which a warp joins so many
+  constexpr int JOINERS = NT / 2;            // warps that join pieces: a tile each in each of two rounds
   constexpr int HALVES = D / 64;
   constexpr int kThreads = kDecWarps * 32;
   const Kv8Attn& a = d.a;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  __shared__ float rec[kDecWarps][NT - OWN][4][32];  // tiles for the other warps to join
+  __shared__ float rec[kDecWarps][JOINERS][4][32];  // half a piece's tiles, for the joining warps
   __shared__ float ml_s[kDecWarps][kDecHeads][2];
   __shared__ float scale_s[kDecWarps][kDecStages][2][2];  // a block's two pages: key, value scale; key < 0: no page
   __shared__ uint64_t bars_s[kDecWarps][kDecStages];
@@ -183,35 +194,42 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
   }
   __syncthreads();
 
-  // A place on the line: block b of sequence seq, whose blocks begin at `start`.
+  // A place on the line: block j of KV head kh of sequence seq.
   struct Place {
-    int64_t b, start;
-    int seq;
+    int seq, kh, j;
     DecSeq s;
   };
-  auto settle = [&](Place& p) {  // to the sequence that holds p.b (p.b < b1)
-    while (p.b >= p.start + (int64_t)p.s.blocks * a.kvh) {
-      p.start += (int64_t)p.s.blocks * a.kvh;
-      p.s = dec_sequence(a, ++p.seq);
+  // n blocks on; the caller knows that the line is that long
+  auto advance = [&](Place& p, int n) {
+    p.j += n;
+    while (p.j >= p.s.blocks) {
+      p.j -= p.s.blocks;
+      if (++p.kh < a.kvh) continue;
+      p.kh = 0;
+      do p.s = dec_sequence(a, ++p.seq);
+      while (p.s.blocks == 0);
     }
   };
+  const int64_t count = b1 - b0;  // this CTA's blocks, counted from 0 below
   Place here;
-  here.b = b0;
-  here.start = first_s[1];
   here.seq = (int)first_s[0];
   here.s = dec_sequence(a, here.seq);
+  {
+    const int64_t o = b0 - first_s[1];
+    here.kh = (int)(o / here.s.blocks);
+    here.j = (int)(o - (int64_t)here.kh * here.s.blocks);
+  }
 
-  // ---- loads: a warp's blocks are b0 + warp, + 4, ... ----
+  // ---- loads: a warp's blocks are warp, warp + 4, ... ----
   Place ahead = here;
-  ahead.b += warp;
+  int64_t at = warp;  // the next block to fetch
+  if (at < count) advance(ahead, warp);
   int kh_a = 0, key_a = 0, page_a = -1;
   // the page of the next block's 16 keys (lane 0: the first, lane 1: the second)
   auto look_up = [&]() {
-    if (ahead.b >= b1) return;
-    settle(ahead);
-    const int64_t j = ahead.b - ahead.start;
-    kh_a = (int)(j / ahead.s.blocks);
-    key_a = (ahead.s.lo / kDecKeys + (int)(j - (int64_t)kh_a * ahead.s.blocks)) * kDecKeys;
+    if (at >= count) return;
+    kh_a = ahead.kh;
+    key_a = (ahead.s.lo / kDecKeys + ahead.j) * kDecKeys;
     page_a = -1;
     const int key = key_a + 16 * lane;
     if (lane < 2 && key < ahead.s.len && key + (a.shift > 4 ? kDecKeys : 16) > ahead.s.lo) {  // (pages behind a window may be gone)
@@ -254,14 +272,15 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
         scale_s[warp][s][lane][0] = -1.f;
       }
     }
-    ahead.b += kDecWarps;
+    at += kDecWarps;
+    if (at < count) advance(ahead, kDecWarps);
     look_up();
   };
   look_up();
   int issued = 0, consumed = 0;
 #pragma unroll
   for (int s = 0; s < kDecStages; ++s) {
-    if (ahead.b < b1) {
+    if (at < count) {
       issue(s);
       ++issued;
     }
@@ -270,54 +289,51 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
 
   bool alive = true;  // false once a wait gave up: the CTA's barriers stay matched
   bool first_piece = true;
-  int64_t next = b0 + warp;  // this warp's next block
-  for (int64_t b = b0; b < b1;) {
-    // ---- one unit's piece: blocks [b, e) ----
-    here.b = b;
-    settle(here);
-    const DecSeq& sq = here.s;
-    const int kh = (int)((b - here.start) / sq.blocks);
-    const int64_t u0 = here.start + (int64_t)kh * sq.blocks, u1 = u0 + sq.blocks;
-    const int64_t e = min(b1, u1);
+  int64_t next = warp;  // this warp's next block
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int64_t b = 0; b < count;) {
+    // ---- one unit's piece: blocks [b, e), of which b is the unit's block here.j ----
+    const DecSeq sq = here.s;
+    const int kh = here.kh, j0 = here.j, blocks = sq.blocks;
+    const int len = (int)min(count - b, (int64_t)(blocks - j0));
+    const int64_t e = b + len;
 
     // queries: head g, its dims in the order of the products' steps, scaled by a power of
     // two so that the largest lies in [1, 2): bf16's range goes into fp16's
-    uint32_t qf[HALVES * 4][2];
+    uint32_t qf[HALVES * 8];
     float fac;
     {
-      uint32_t w[HALVES * 8];
       const bool live = g < a.G;
       const T* qp = static_cast<const T*>(a.q) + (int64_t)sq.row * a.ldq + (int64_t)(kh * a.G + (live ? g : 0)) * D;
 #pragma unroll
-      for (int h = 0; h < HALVES; ++h) {
-        const T* p = qp + 16 * (HALVES * c4 + h);
+      for (int h = 0; h < HALVES * 2; ++h) {
+        const T* p = qp + 16 * HALVES * c4 + 8 * h;
         if (d.vec_q) {
-          const uint4 x = *reinterpret_cast<const uint4*>(p), y = *reinterpret_cast<const uint4*>(p + 8);
-          w[8 * h] = x.x, w[8 * h + 1] = x.y, w[8 * h + 2] = x.z, w[8 * h + 3] = x.w;
-          w[8 * h + 4] = y.x, w[8 * h + 5] = y.y, w[8 * h + 6] = y.z, w[8 * h + 7] = y.w;
+          const uint4 v = *reinterpret_cast<const uint4*>(p);
+          qf[4 * h] = v.x, qf[4 * h + 1] = v.y, qf[4 * h + 2] = v.z, qf[4 * h + 3] = v.w;
         } else {
           const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) w[8 * h + k] = u[2 * k] | (uint32_t)u[2 * k + 1] << 16;
+          for (int k = 0; k < 4; ++k) qf[4 * h + k] = u[2 * k] | (uint32_t)u[2 * k + 1] << 16;
         }
       }
-      float pow2 = 1.f;
+      fac = a.scale;
       if constexpr (Elem<T>::kMmaFormat == 1) {
         float m = 0.f;
 #pragma unroll
-        for (int k = 0; k < HALVES * 8; ++k) m = fmaxf(m, fmaxf(fabsf(Elem<T>::lo(w[k])), fabsf(Elem<T>::hi(w[k]))));
+        for (int k = 0; k < HALVES * 8; ++k) m = fmaxf(m, fmaxf(fabsf(Elem<T>::lo(qf[k])), fabsf(Elem<T>::hi(qf[k]))));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         // (an exponent whose inverse is a normal number too; infinities stay what they are)
         const uint32_t ex = min(max(__float_as_uint(m) >> 23, 1u), 253u);
-        pow2 = __uint_as_float(ex << 23);
+        fac *= __uint_as_float(ex << 23);
         const float inv = __uint_as_float((254u - ex) << 23);
 #pragma unroll
-        for (int k = 0; k < HALVES * 8; ++k) w[k] = pack_f16(Elem<T>::lo(w[k]) * inv, Elem<T>::hi(w[k]) * inv);
+        for (int k = 0; k < HALVES * 8; ++k) qf[k] = pack_f16(Elem<T>::lo(qf[k]) * inv, Elem<T>::hi(qf[k]) * inv);
       }
 #pragma unroll
-      for (int k = 0; k < HALVES * 4; ++k) qf[k][0] = live ? w[2 * k] : 0u, qf[k][1] = live ? w[2 * k + 1] : 0u;
-      fac = pow2 * a.scale;
+      for (int k = 0; k < HALVES * 8; ++k) qf[k] = live ? qf[k] : 0u;
     }
     // of the columns' heads, 2 c4 and 2 c4 + 1
     const float fac0 = __shfl_sync(0xffffffffu, fac, 8 * c4), fac1 = __shfl_sync(0xffffffffu, fac, 8 * c4 + 4);
@@ -328,18 +344,19 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
     for (; next < e; next += kDecWarps) {
-      const int s = consumed % kDecStages;
+      const int s = stage;
       cp_async_wait<kDecStages - 1>();
       if (alive) {
         int got = 0;
         if (lane == 0)
-          got = mbar_wait(smem_u32(&bars_s[warp][s]), (uint32_t)((consumed / kDecStages) & 1), a.err, SITE_KV8_PIPE) ? 1 : 0;
+          got = mbar_wait(smem_u32(&bars_s[warp][s]), phase, a.err, SITE_KV8_PIPE) ? 1 : 0;
         alive = __shfl_sync(0xffffffffu, got, 0) != 0;
       }
       __syncwarp();
       ++consumed;
+      if (++stage == kDecStages) stage = 0, phase ^= 1u;
       if (alive && sq.len > 0) {
-        const int key0 = (sq.lo / kDecKeys + (int)(next - u0)) * kDecKeys;
+        const int key0 = (sq.lo / kDecKeys + j0 + (int)(next - b)) * kDecKeys;
         const uint32_t kb = ring + s * STAGE, vb = kb + BLK;
         float ks[2], lv[2], iv[2];
         bool page[2];
@@ -348,8 +365,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
           ks[t] = scale_s[warp][s][t][0];
           const float v = scale_s[warp][s][t][1];
           page[t] = ks[t] >= 0.f;
-          lv[t] = page[t] ? log2f(v) : 0.f;
-          iv[t] = page[t] ? 1.f / v : 0.f;
+          lv[t] = page[t] ? log2_fast(v) : 0.f;
+          iv[t] = page[t] ? rcp_fast(v) : 0.f;
         }
         const bool edge = key0 < sq.lo || key0 + kDecKeys > sq.len || !page[0] || !page[1];
         // ---- S^T = K Q^T ----
@@ -371,7 +388,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
 #pragma unroll
             for (int w = 0; w < 4; ++w)
               mma_f16(sc[t], from_e4m3x2(lo[w]), from_e4m3x2(hi[w]), from_e4m3x2(lo[w] >> 16), from_e4m3x2(hi[w] >> 16),
-                      qf[4 * h + w][0], qf[4 * h + w][1]);
+                      qf[8 * h + 2 * w], qf[8 * h + 2 * w + 1]);
           }
         }
         // ---- softmax over keys t * 16 + 8 u + g, of heads 2 c4 (even) and 2 c4 + 1 ----
@@ -444,14 +461,14 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
         }
       }
       __syncwarp();
-      if (alive && ahead.b < b1) {
+      if (alive && at < count) {
         issue(s);
         ++issued;
       }
       cp_async_commit();
     }
 
-    // ---- the four warps' pieces joined; warp w joins tiles [w OWN, w OWN + OWN) ----
+    // ---- the warps' pieces joined; in round r warp w joins tile r JOINERS + w ----
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, x);
@@ -461,68 +478,63 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       ml_s[warp][2 * c4][0] = m0, ml_s[warp][2 * c4][1] = l0;
       ml_s[warp][2 * c4 + 1][0] = m1, ml_s[warp][2 * c4 + 1][1] = l1;
     }
-#pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int at = c - warp * OWN;
-      if (at >= 0 && at < OWN) continue;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) rec[warp][c < warp * OWN ? c : c - OWN][k][lane] = o[c][k];
-    }
-    __syncthreads();
-    float M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f, f0[kDecWarps], f1[kDecWarps];
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      M0 = fmaxf(M0, ml_s[w][2 * c4][0]);
-      M1 = fmaxf(M1, ml_s[w][2 * c4 + 1][0]);
-    }
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      const float x0 = ml_s[w][2 * c4][0], x1 = ml_s[w][2 * c4 + 1][0];
-      f0[w] = x0 == -INFINITY ? 0.f : exp2_fast(x0 - M0);
-      f1[w] = x1 == -INFINITY ? 0.f : exp2_fast(x1 - M1);
-      L0 = fmaf(ml_s[w][2 * c4][1], f0[w], L0);
-      L1 = fmaf(ml_s[w][2 * c4 + 1][1], f1[w], L1);
-    }
-    const bool whole_unit = b == u0 && e == u1;
+    const bool whole_unit = len == blocks;
     const int64_t slot = 2 * (int64_t)blockIdx.x + (first_piece ? 0 : 1);
-    const float inv0 = sq.len == 0 ? 0.f : 1.f / L0, inv1 = sq.len == 0 ? 0.f : 1.f / L1;
+    float f0[kDecWarps], f1[kDecWarps], M0 = -INFINITY, M1 = -INFINITY, L0 = 0.f, L1 = 0.f;
 #pragma unroll
-    for (int c = 0; c < NT; ++c) {
-      const int at = c - warp * OWN;
-      if (at < 0 || at >= OWN) continue;
-      float r[4];
+    for (int round = 0; round < 2; ++round) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) r[k] = o[c][k] * ((k & 1) ? f1[warp] : f0[warp]);
+      for (int c = 0; c < JOINERS; ++c)
 #pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        if (w == warp) continue;
+        for (int k = 0; k < 4; ++k) rec[warp][c][k][lane] = o[round * JOINERS + c][k];
+      __syncthreads();
+      if (warp < JOINERS) {
+        if (round == 0) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          r[k] = fmaf(rec[w][c < w * OWN ? c : c - OWN][k][lane], (k & 1) ? f1[w] : f0[w], r[k]);
-      }
-      // dims 16 c + 2 g (r[0], r[1]) and + 1 (r[2], r[3]) of heads 2 c4, 2 c4 + 1
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int head = 2 * c4 + x, dim = 16 * c + 2 * g;
-        if (head >= a.G) continue;
-        if (whole_unit) {
-          const float inv = x ? inv1 : inv0;
-          T* op = static_cast<T*>(a.out) + (int64_t)sq.row * a.ldo + (int64_t)(kh * a.G + head) * D + dim;
-          if (d.vec_o) {
-            *reinterpret_cast<uint32_t*>(op) = Elem<T>::pack(r[x] * inv, r[2 + x] * inv);
-          } else {
-            op[0] = Elem<T>::from(r[x] * inv);
-            op[1] = Elem<T>::from(r[2 + x] * inv);
+          for (int w = 0; w < kDecWarps; ++w) {
+            f0[w] = ml_s[w][2 * c4][0], f1[w] = ml_s[w][2 * c4 + 1][0];
+            M0 = fmaxf(M0, f0[w]);
+            M1 = fmaxf(M1, f1[w]);
           }
-        } else {
-          *reinterpret_cast<float2*>(d.parts + (slot * kDecHeads + head) * D + dim) = make_float2(r[x], r[2 + x]);
-          if (c == 0 && g == 0) d.parts_ml[slot * kDecHeads + head] = make_float2(x ? M1 : M0, x ? L1 : L0);
+#pragma unroll
+          for (int w = 0; w < kDecWarps; ++w) {
+            f0[w] = f0[w] == -INFINITY ? 0.f : exp2_fast(f0[w] - M0);
+            f1[w] = f1[w] == -INFINITY ? 0.f : exp2_fast(f1[w] - M1);
+            L0 = fmaf(ml_s[w][2 * c4][1], f0[w], L0);
+            L1 = fmaf(ml_s[w][2 * c4 + 1][1], f1[w], L1);
+          }
+        }
+        float r[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) r[k] = fmaf(rec[w][warp][k][lane], (k & 1) ? f1[w] : f0[w], r[k]);
+        // dims 16 c + 2 g (r[0], r[1]) and + 1 (r[2], r[3]) of heads 2 c4, 2 c4 + 1
+        const int c = round * JOINERS + warp;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int head = 2 * c4 + x, dim = 16 * c + 2 * g;
+          if (head >= a.G) continue;
+          if (whole_unit) {
+            const float inv = sq.len == 0 ? 0.f : 1.f / (x ? L1 : L0);
+            T* op = static_cast<T*>(a.out) + (int64_t)sq.row * a.ldo + (int64_t)(kh * a.G + head) * D + dim;
+            if (d.vec_o) {
+              *reinterpret_cast<uint32_t*>(op) = Elem<T>::pack(r[x] * inv, r[2 + x] * inv);
+            } else {
+              op[0] = Elem<T>::from(r[x] * inv);
+              op[1] = Elem<T>::from(r[2 + x] * inv);
+            }
+          } else {
+            *reinterpret_cast<float2*>(d.parts + (slot * kDecHeads + head) * D + dim) = make_float2(r[x], r[2 + x]);
+            if (c == 0 && g == 0) d.parts_ml[slot * kDecHeads + head] = make_float2(x ? M1 : M0, x ? L1 : L0);
+          }
         }
       }
+      __syncthreads();  // (the records are written again)
     }
     first_piece = false;
     b = e;
-    __syncthreads();  // (the records are written again)
+    if (b < count) advance(here, len);
   }
   // no copy is under way when the CTA leaves
   cp_async_wait<0>();
