@@ -38,9 +38,20 @@ constexpr int kDecHeads = 8;    // query heads of a KV head: the products' colum
 constexpr int kDecPerSm = 2;
 constexpr int kDecLeast = 8;    // blocks of a CTA's stretch at least, where there are so few
 
+// Where a CTA's stretch begins inside a unit: that unit (seq < 0: it does not).
+struct DecStart {
+  int64_t u0;      // the unit's first block on the line
+  int32_t blocks;  // of the unit
+  int32_t seq, kh, row;
+};
+struct DecLine {
+  int64_t all, ctas;
+};
+
 struct DecArgs {
   Kv8Attn a;
-  int64_t* before;   // [n + 1] blocks of a KV head before each sequence
+  DecLine* line;
+  DecStart* starts;  // [CTAs]
   float* parts;      // [2 * CTAs][8][D]: a CTA's first and last piece
   float2* parts_ml;  // [2 * CTAs][8] maximum and sum
   int vec_q, vec_o;
@@ -168,16 +179,9 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     total += sums_s[w];
   }
   const int64_t excl = incl - mine;
-  if (blockIdx.x == 0) {
-    int64_t at = excl;
-    for (int i = i0; i < i1; ++i) {
-      d.before[i] = at;
-      at += dec_sequence(a, i).blocks;
-    }
-    if (threadIdx.x == 0) d.before[a.n] = total;
-  }
   const int64_t all = total * a.kvh;
   const int64_t C = dec_ctas(all, gridDim.x);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *d.line = {all, C};
   if (all == 0 || blockIdx.x >= C) return;
   const int64_t b0 = all * blockIdx.x / C, b1 = all * (blockIdx.x + 1) / C;
   if (b0 >= excl * a.kvh && b0 < incl * a.kvh) {
@@ -218,6 +222,8 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     const int64_t o = b0 - first_s[1];
     here.kh = (int)(o / here.s.blocks);
     here.j = (int)(o - (int64_t)here.kh * here.s.blocks);
+    if (threadIdx.x == 0)
+      d.starts[blockIdx.x] = {b0 - here.j, here.s.blocks, here.j > 0 ? here.seq : -1, here.kh, here.s.row};
   }
 
   // ---- loads: a warp's blocks are warp, warp + 4, ... ----
@@ -289,6 +295,24 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
 
   bool alive = true;  // false once a wait gave up: the CTA's barriers stay matched
   bool first_piece = true;
+  // queries: head g's dims in the order of the products' steps, as they are
+  uint32_t qf[HALVES * 8];
+  auto load_q = [&]() {
+    const T* qp = static_cast<const T*>(a.q) + (int64_t)here.s.row * a.ldq + (int64_t)(here.kh * a.G + (g < a.G ? g : 0)) * D;
+#pragma unroll
+    for (int h = 0; h < HALVES * 2; ++h) {
+      const T* p = qp + 16 * HALVES * c4 + 8 * h;
+      if (d.vec_q) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        qf[4 * h] = v.x, qf[4 * h + 1] = v.y, qf[4 * h + 2] = v.z, qf[4 * h + 3] = v.w;
+      } else {
+        const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qf[4 * h + k] = u[2 * k] | (uint32_t)u[2 * k + 1] << 16;
+      }
+    }
+  };
+  load_q();
   int64_t next = warp;  // this warp's next block
   int stage = 0;
   uint32_t phase = 0;
@@ -299,25 +323,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     const int len = (int)min(count - b, (int64_t)(blocks - j0));
     const int64_t e = b + len;
 
-    // queries: head g, its dims in the order of the products' steps, scaled by a power of
-    // two so that the largest lies in [1, 2): bf16's range goes into fp16's
-    uint32_t qf[HALVES * 8];
+    // the queries scaled by a power of two so that the largest lies in [1, 2): bf16's
+    // range goes into fp16's
     float fac;
     {
       const bool live = g < a.G;
-      const T* qp = static_cast<const T*>(a.q) + (int64_t)sq.row * a.ldq + (int64_t)(kh * a.G + (live ? g : 0)) * D;
-#pragma unroll
-      for (int h = 0; h < HALVES * 2; ++h) {
-        const T* p = qp + 16 * HALVES * c4 + 8 * h;
-        if (d.vec_q) {
-          const uint4 v = *reinterpret_cast<const uint4*>(p);
-          qf[4 * h] = v.x, qf[4 * h + 1] = v.y, qf[4 * h + 2] = v.z, qf[4 * h + 3] = v.w;
-        } else {
-          const unsigned short* u = reinterpret_cast<const unsigned short*>(p);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) qf[4 * h + k] = u[2 * k] | (uint32_t)u[2 * k + 1] << 16;
-        }
-      }
       fac = a.scale;
       if constexpr (Elem<T>::kMmaFormat == 1) {
         float m = 0.f;
@@ -468,6 +478,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       cp_async_commit();
     }
 
+    b = e;
+    if (b < count) {  // the next unit's queries come while this one's pieces are joined
+      advance(here, len);
+      load_q();
+    }
     // ---- the warps' pieces joined; in round r warp w joins tile r JOINERS + w ----
 #pragma unroll
     for (int x = 4; x < 32; x <<= 1) {
@@ -533,8 +548,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       __syncthreads();  // (the records are written again)
     }
     first_piece = false;
-    b = e;
-    if (b < count) advance(here, len);
   }
   // no copy is under way when the CTA leaves
   cp_async_wait<0>();
@@ -544,75 +557,85 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
   }
 }
 
-// Joins the pieces of a unit that several CTAs share, in their order.
+// Joins a unit that several CTAs share: block (c, h) head h of the unit that CTA c + 1
+// begins inside of, if no CTA before does.  A warp takes every eighth piece, the
+// loads of four under way together; then the warps' sums are joined in their order.
+constexpr int kJoinWarps = 8;
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv8_join_kernel(const __grid_constant__ DecArgs d, int grid) {
+__global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ DecArgs d) {
+  constexpr int E = D / 32;  // dims of a lane
   const Kv8Attn& a = d.a;
+  __shared__ float acc_s[kJoinWarps][D];
+  __shared__ float2 ml_s[kJoinWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const int kh = blockIdx.y;
-  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
-    const int64_t p0 = d.before[i], p1 = d.before[i + 1];
-    if (p1 == p0) continue;
-    const int64_t all = d.before[a.n] * a.kvh, C = dec_ctas(all, grid);
-    const int64_t u0 = p0 * a.kvh + kh * (p1 - p0), u1 = u0 + (p1 - p0);
-    const int64_t c0 = ((u0 + 1) * C - 1) / all, c1 = (u1 * C - 1) / all;  // the CTAs of its first and last block
-    if (c0 == c1) continue;
-    const bool starts = all * c0 / C == u0;
-    const int row = a.off[i];
-    for (int t = threadIdx.x; t < a.G * (D / 4); t += 128) {
-      const int head = t / (D / 4), dim = t % (D / 4) * 4;
-      float M = -INFINITY, L = 0.f;
-      float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int64_t cb = c0; cb <= c1; cb += 4) {
-        float2 ml[4];
-        float4 v[4];
+  const int64_t all = d.line->all, C = d.line->ctas;
+  const int64_t first = blockIdx.x, second = first + 1;
+  if (all == 0 || second >= C) return;
+  const DecStart u = d.starts[second];
+  const int64_t begins = all * first / C;  // the CTA before's first block
+  if (u.seq < 0 || begins > u.u0) return;
+  const int64_t last = ((u.u0 + u.blocks) * C - 1) / all;
+  const int head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the first CTA's piece is its last one, unless the unit begins with it
+  auto slot = [&](int64_t c) { return (2 * c + (c == first && begins != u.u0 ? 1 : 0)) * kDecHeads + head; };
+  float M = -INFINITY, L = 0.f, A[E];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int64_t c = cb + k;
-          const int64_t at = (2 * c + (c == c0 && !starts ? 1 : 0)) * kDecHeads + head;
-          ml[k] = c <= c1 ? d.parts_ml[at] : make_float2(-INFINITY, 0.f);
-          v[k] = c <= c1 ? *reinterpret_cast<const float4*>(d.parts + at * D + dim) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        const float mn = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
-        const float f = M == -INFINITY ? 0.f : exp2_fast(M - mn);
-        L *= f;
-        A.x *= f, A.y *= f, A.z *= f, A.w *= f;
+  for (int e = 0; e < E; ++e) A[e] = 0.f;
+  for (int64_t c0 = first + warp; c0 <= last; c0 += 4 * kJoinWarps) {
+    float2 ml[4];
+    float v[4][E];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float w = ml[k].x == -INFINITY ? 0.f : exp2_fast(ml[k].x - mn);
-          L = fmaf(ml[k].y, w, L);
-          A.x = fmaf(v[k].x, w, A.x);
-          A.y = fmaf(v[k].y, w, A.y);
-          A.z = fmaf(v[k].z, w, A.z);
-          A.w = fmaf(v[k].w, w, A.w);
-        }
-        M = mn;
-      }
-      const float inv = 1.f / L;
-      T* op = static_cast<T*>(a.out) + (int64_t)row * a.ldo + (int64_t)(kh * a.G + head) * D + dim;
-      if (d.vec_o) {
-        reinterpret_cast<uint32_t*>(op)[0] = Elem<T>::pack(A.x * inv, A.y * inv);
-        reinterpret_cast<uint32_t*>(op)[1] = Elem<T>::pack(A.z * inv, A.w * inv);
-      } else {
-        op[0] = Elem<T>::from(A.x * inv), op[1] = Elem<T>::from(A.y * inv);
-        op[2] = Elem<T>::from(A.z * inv), op[3] = Elem<T>::from(A.w * inv);
-      }
+    for (int k = 0; k < 4; ++k) {
+      const int64_t c = c0 + k * kJoinWarps, s = slot(min(c, last));
+      ml[k] = c <= last ? d.parts_ml[s] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] = d.parts[s * D + e * 32 + lane];
     }
+    const float mn = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+    const float f = M == -INFINITY ? 0.f : exp2_fast(M - mn);
+    L *= f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) A[e] *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool some = ml[k].x != -INFINITY;
+      const float w = some ? exp2_fast(ml[k].x - mn) : 0.f;
+      L = fmaf(ml[k].y, w, L);
+#pragma unroll
+      for (int e = 0; e < E; ++e) A[e] = fmaf(some ? v[k][e] : 0.f, w, A[e]);
+    }
+    M = mn;
+  }
+  if (lane == 0) ml_s[warp] = make_float2(M, L);
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc_s[warp][e * 32 + lane] = A[e];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float Mx = -INFINITY, Lx = 0.f, Ax = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) Mx = fmaxf(Mx, ml_s[w].x);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float f = ml_s[w].x == -INFINITY ? 0.f : exp2_fast(ml_s[w].x - Mx);
+      Lx = fmaf(ml_s[w].y, f, Lx);
+      Ax = fmaf(acc_s[w][threadIdx.x], f, Ax);
+    }
+    static_cast<T*>(a.out)[(int64_t)u.row * a.ldo + (int64_t)(u.kh * a.G + head) * D + threadIdx.x] = Elem<T>::from(Ax / Lx);
   }
 }
 
 int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
 
-// The workspace: before, pieces' maxima and sums, pieces; then the chunks'.
+// The workspace: the line, where stretches begin, pieces' maxima and sums, pieces; then the chunks'.
 struct Space {
-  int64_t before, ml, parts, chunks, bytes;
+  int64_t starts, ml, parts, chunks, bytes;
 };
-Space space_of(int n, int head_dim, int max_rows) {
+Space space_of(int head_dim, int max_rows) {
   const int64_t slots = 2ll * kDecPerSm * num_sms();
   Space s;
-  s.before = 0;
-  s.ml = up256((n + 1ll) * 8);
+  s.starts = 256;
+  s.ml = s.starts + up256(slots / 2 * sizeof(DecStart));
   s.parts = s.ml + up256(slots * kDecHeads * 8);
   s.chunks = s.parts + up256(slots * kDecHeads * head_dim * 4);
   s.bytes = s.chunks + (max_rows > 1 ? kv8_chunk_space(head_dim) : 0);
@@ -638,7 +661,7 @@ int launch_kv8(const DecArgs& d, const CUtensorMap& tmk, const CUtensorMap& tmv,
   const int grid = kDecPerSm * num_sms();
   cudaError_t e = launch_pdl(kv8_decode_kernel<T, D>, dim3(grid), dim3(kDecWarps * 32), (size_t)smem, s, tmk, tmv, d);
   if (e != cudaSuccess) return cuda_error(e, "kv8 decode launch");
-  e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)std::min(d.a.n, 65535), (unsigned)d.a.kvh), dim3(128), 0, s, d, grid);
+  e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)d.a.G), dim3(kJoinWarps * 32), 0, s, d);
   if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
   count_launches(2);
   return SAR_OK;
@@ -655,7 +678,7 @@ extern "C" {
 int sar_kv8_attention_workspace(const sar_kv8_batch* batch, const sar_kv8* cache, int64_t* bytes) try {
   if (!batch || !bytes) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention_workspace: null pointer");
   SAR_TRY(sar::check_batch(*batch, cache));
-  *bytes = sar::space_of(batch->n, cache->head_dim, batch->max_rows).bytes;
+  *bytes = sar::space_of(cache->head_dim, batch->max_rows).bytes;
   return SAR_OK;
 } catch (...) {
   return sar::entry_failed("kv8_attention_workspace");
@@ -679,7 +702,7 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   if (!aligned_to(b.q, 2) || !aligned_to(b.out, 2) || !aligned_to(b.row_offsets, 4) || !aligned_to(b.lens, 4) ||
       !aligned_to(b.block_tables, 4) || !aligned_to(b.workspace, 16))
     return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: array not aligned to its element");
-  const sar::Space sp = sar::space_of(b.n, cache->head_dim, b.max_rows);
+  const sar::Space sp = sar::space_of(cache->head_dim, b.max_rows);
   if (b.workspace_bytes < sp.bytes) return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: workspace too small");
   sar::DecArgs d = {};
   sar::Kv8Attn& a = d.a;
@@ -707,7 +730,8 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   a.scale = (b.scale == 0.f ? (float)(1.0 / sqrt((double)cache->head_dim)) : b.scale) * 1.4426950408889634f;
   SAR_TRY(sar::op_flags(&a.err));
   uint8_t* ws = static_cast<uint8_t*>(b.workspace);
-  d.before = reinterpret_cast<int64_t*>(ws + sp.before);
+  d.line = reinterpret_cast<sar::DecLine*>(ws);
+  d.starts = reinterpret_cast<sar::DecStart*>(ws + sp.starts);
   d.parts_ml = reinterpret_cast<float2*>(ws + sp.ml);
   d.parts = reinterpret_cast<float*>(ws + sp.parts);
   d.vec_q = aligned_to(b.q, 16) && b.ldq % 8 == 0;
