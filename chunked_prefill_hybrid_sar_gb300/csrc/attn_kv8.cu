@@ -3,7 +3,7 @@
 // Bound by the cache's bytes: 2 D of them per key and KV head, for 4 D G flops.
 //
 // All (sequence, KV head) units' keys, in blocks of 32, form one line, of which every
-// CTA takes an equal stretch, whatever the lengths.  Where a stretch begins or ends
+// CTA takes a stretch, whatever the lengths.  Where a stretch begins or ends
 // inside a unit, the CTA writes that piece unnormalised, and a second kernel joins a
 // unit's pieces; so a call of a few long sequences and one of many short ones both
 // fill the machine.  The plan is three prefix sums' worth of arithmetic on the
@@ -31,12 +31,15 @@ namespace sar {
 
 namespace {
 
-constexpr int kDecWarps = 6;
+constexpr int kDecWarps = 4;
 constexpr int kDecKeys = 32;    // keys of a block
 constexpr int kDecStages = 2;   // blocks of a warp's ring
 constexpr int kDecHeads = 8;    // query heads of a KV head: the products' columns
-constexpr int kDecPerSm = 2;
+constexpr int kDecPerSm = 3;
 constexpr int kDecLeast = 8;    // blocks of a CTA's stretch at least, where there are so few
+constexpr int kDecWaves = 2;    // CTAs to a place on an SM, where there are
+constexpr int kDecMany = 256;   // so many blocks to a place
+constexpr int kDecUnit = 32;    // blocks of the longest sequence up to which a CTA takes a unit
 
 // Where a CTA's stretch begins inside a unit: that unit (seq < 0: it does not).
 struct DecStart {
@@ -44,9 +47,7 @@ struct DecStart {
   int32_t blocks;  // of the unit
   int32_t seq, kh, row;
 };
-struct DecLine {
-  int64_t all, ctas;
-};
+struct DecLine;
 
 struct DecArgs {
   Kv8Attn a;
@@ -54,6 +55,8 @@ struct DecArgs {
   DecStart* starts;  // [CTAs]
   float* parts;      // [2 * CTAs][8][D]: a CTA's first and last piece
   float2* parts_ml;  // [2 * CTAs][8] maximum and sum
+  int resident;  // CTAs that stay on the SMs at once
+  int units;     // a unit to a CTA, and nothing to join
   int vec_q, vec_o;
 };
 
@@ -117,10 +120,34 @@ __device__ __forceinline__ DecSeq dec_sequence(const Kv8Attn& a, int i) {
   return s;
 }
 
-// The stretches: CTA c of C has blocks [T c / C, T (c + 1) / C).
-__device__ __forceinline__ int64_t dec_ctas(int64_t T, int64_t grid) {
-  return max((int64_t)1, min(grid, T / kDecLeast));
-}
+// How the line is cut.  SMs are not equally near to the memory that their keys lie in:
+// of 304 CTAs with equal stretches the last ended 25% after the median.  So the
+// resident CTAs take equal shares of the line's first 7/8, and twice as many more
+// share the rest, each started as a place on an SM gets free.
+struct DecLine {
+  int64_t all, head;  // blocks; those of the first CTAs
+  int32_t first, ctas;
+  __device__ __forceinline__ static int64_t quotient(int64_t x, int64_t y) {
+    // (64-bit divisions are long; these are made before anything is loaded)
+    return x >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+  }
+  __device__ __forceinline__ static DecLine of(int64_t all, int resident, int grid) {
+    DecLine l;
+    l.all = all;
+    const bool many = all >= (int64_t)resident * kDecMany && grid >= kDecWaves * resident;
+    l.first = many ? resident : (int)max((int64_t)1, min((int64_t)min(resident, grid), all / kDecLeast));
+    l.ctas = many ? kDecWaves * resident : l.first;
+    l.head = many ? all - all / 8 : all;
+    return l;
+  }
+  // CTA c's first block, and the CTA that has block b
+  __device__ __forceinline__ int64_t at(int c) const {
+    return c <= first ? quotient(head * c, first) : head + quotient((all - head) * (c - first), ctas - first);
+  }
+  __device__ __forceinline__ int cta(int64_t b) const {
+    return (int)(b < head ? quotient((b + 1) * first - 1, head) : first + quotient((b - head + 1) * (ctas - first) - 1, all - head));
+  }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
@@ -139,7 +166,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
   __shared__ float ml_s[kDecWarps][kDecHeads][2];
   __shared__ float scale_s[kDecWarps][kDecStages][2][2];  // a block's two pages: key, value scale; key < 0: no page
   __shared__ uint64_t bars_s[kDecWarps][kDecStages];
-  __shared__ int64_t sums_s[kThreads];
+  __shared__ int64_t sums_s[kDecWarps];
   __shared__ int64_t first_s[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c4 = lane & 3;
@@ -151,58 +178,83 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     tma_prefetch_desc(&tmv);
   }
   pdl_wait();
-  pdl_launch_dependents();
 
+  auto check = [&](int i) {  // (once for the call)
+    int r0, rows, len;
+    if (!kv8_sequence(a, i, r0, rows, len)) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SEQUENCE, i);
+  };
   // ---- this CTA's stretch ----
-  const int per = (a.n + kThreads - 1) / kThreads;
-  const int i0 = min(a.n, (int)threadIdx.x * per), i1 = min(a.n, i0 + per);
-  int64_t mine = 0;
-  for (int i = i0; i < i1; ++i) {
-    mine += dec_sequence(a, i).blocks;
-    if (blockIdx.x == 0) {  // (once for the call)
-      int r0, rows, len;
-      if (!kv8_sequence(a, i, r0, rows, len)) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SEQUENCE, i);
-    }
-  }
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += x;
-  }
-  if (lane == 31) sums_s[warp] = incl;
-  __syncthreads();
-  int64_t total = 0;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) incl += sums_s[w];
-    total += sums_s[w];
-  }
-  const int64_t excl = incl - mine;
-  const int64_t all = total * a.kvh;
-  const int64_t C = dec_ctas(all, gridDim.x);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *d.line = {all, C};
-  if (all == 0 || blockIdx.x >= C) return;
-  const int64_t b0 = all * blockIdx.x / C, b1 = all * (blockIdx.x + 1) / C;
-  if (b0 >= excl * a.kvh && b0 < incl * a.kvh) {
-    int64_t at = excl;
-    int i = i0;
-    while (true) {
-      const int nb = dec_sequence(a, i).blocks;
-      if (b0 < (at + nb) * a.kvh) break;
-      at += nb;
-      ++i;
-    }
-    first_s[0] = i;
-    first_s[1] = at * a.kvh;
-  }
-  __syncthreads();
-
-  // A place on the line: block j of KV head kh of sequence seq.
-  struct Place {
+  struct Place {  // block j of KV head kh of sequence seq
     int seq, kh, j;
     DecSeq s;
   };
+  Place here;
+  int count;  // this CTA's blocks, counted from 0 below
+  if (d.units) {
+    here.seq = (int)(blockIdx.x / (unsigned)a.kvh);
+    here.kh = (int)(blockIdx.x - (unsigned)here.seq * a.kvh);
+    here.j = 0;
+    here.s = dec_sequence(a, here.seq);
+    count = here.s.blocks;
+    if (here.kh == 0 && threadIdx.x == 0) check(here.seq);
+    if (count == 0) return;
+  } else {
+    const int per = (a.n + kThreads - 1) / kThreads;
+    const int i0 = min(a.n, (int)threadIdx.x * per), i1 = min(a.n, i0 + per);
+    int64_t mine = 0;
+    for (int i = i0; i < i1; ++i) {
+      mine += dec_sequence(a, i).blocks;
+      if (blockIdx.x == 0) check(i);
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sums_s[warp] = incl;
+    __syncthreads();
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) incl += sums_s[w];
+      total += sums_s[w];
+    }
+    const int64_t excl = incl - mine;
+    const int64_t all = total * a.kvh;
+    const DecLine line = DecLine::of(all, d.resident, gridDim.x);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *d.line = line;
+    if (all == 0 || blockIdx.x >= line.ctas) return;
+    // (with more CTAs than places the joining kernel's would take the ones that get free)
+    if (line.ctas == line.first) pdl_launch_dependents();
+    const int64_t b0 = line.at(blockIdx.x), b1 = line.at(blockIdx.x + 1);
+    if (b0 >= excl * a.kvh && b0 < incl * a.kvh) {
+      int64_t at = excl;
+      int i = i0;
+      while (true) {
+        const int nb = dec_sequence(a, i).blocks;
+        if (b0 < (at + nb) * a.kvh) break;
+        at += nb;
+        ++i;
+      }
+      first_s[0] = i;
+      first_s[1] = at * a.kvh;
+    }
+    __syncthreads();
+    if (b1 - b0 > 0x7fffff00) {  // (2^36 keys to a CTA)
+      if (threadIdx.x == 0) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SEQUENCE, -1);
+      return;
+    }
+    count = (int)(b1 - b0);
+    here.seq = (int)first_s[0];
+    here.s = dec_sequence(a, here.seq);
+    const int64_t o = b0 - first_s[1];
+    here.kh = (int)DecLine::quotient(o, here.s.blocks);
+    here.j = (int)(o - (int64_t)here.kh * here.s.blocks);
+    if (threadIdx.x == 0)
+      d.starts[blockIdx.x] = {b0 - here.j, here.s.blocks, here.j > 0 ? here.seq : -1, here.kh, here.s.row};
+  }
+
   // n blocks on; the caller knows that the line is that long
   auto advance = [&](Place& p, int n) {
     p.j += n;
@@ -214,39 +266,29 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       while (p.s.blocks == 0);
     }
   };
-  const int64_t count = b1 - b0;  // this CTA's blocks, counted from 0 below
-  Place here;
-  here.seq = (int)first_s[0];
-  here.s = dec_sequence(a, here.seq);
-  {
-    const int64_t o = b0 - first_s[1];
-    here.kh = (int)(o / here.s.blocks);
-    here.j = (int)(o - (int64_t)here.kh * here.s.blocks);
-    if (threadIdx.x == 0)
-      d.starts[blockIdx.x] = {b0 - here.j, here.s.blocks, here.j > 0 ? here.seq : -1, here.kh, here.s.row};
-  }
 
   // ---- loads: a warp's blocks are warp, warp + 4, ... ----
   Place ahead = here;
-  int64_t at = warp;  // the next block to fetch
+  int at = warp;  // the next block to fetch
   if (at < count) advance(ahead, warp);
   int kh_a = 0, key_a = 0, page_a = -1;
-  // the page of the next block's 16 keys (lane 0: the first, lane 1: the second)
+  bool want_a = false;
+  // the page of the next block's 16 keys (lane 0: the first, lane 1: the second); looked at
+  // when the block is fetched, a block later: a test here would wait for the load
   auto look_up = [&]() {
     if (at >= count) return;
     kh_a = ahead.kh;
     key_a = (ahead.s.lo / kDecKeys + ahead.j) * kDecKeys;
-    page_a = -1;
     const int key = key_a + 16 * lane;
-    if (lane < 2 && key < ahead.s.len && key + (a.shift > 4 ? kDecKeys : 16) > ahead.s.lo) {  // (pages behind a window may be gone)
-      page_a = a.bt[(int64_t)ahead.seq * a.bt_stride + (key >> a.shift)];
-      if (page_a < 0 || page_a >= a.num_pages) {
-        report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page_a);
-        page_a = -1;
-      }
-    }
+    want_a = lane < 2 && key < ahead.s.len && key + (a.shift > 4 ? kDecKeys : 16) > ahead.s.lo;  // (pages behind a window may be gone)
+    if (want_a) page_a = a.bt[(int64_t)ahead.seq * a.bt_stride + (key >> a.shift)];
   };
   auto issue = [&](int s) {  // that block into stage s, and the look-up of the one after
+    if (want_a && (page_a < 0 || page_a >= a.num_pages)) {
+      report(a.err, SAR_ERR_BOUNDS, SITE_KV8_PAGE, page_a);
+      page_a = -1;
+    }
+    if (!want_a) page_a = -1;
     const uint32_t bar = smem_u32(&bars_s[warp][s]), dst = ring + s * STAGE;
     // pages of 32 keys and up: one box holds the block
     const bool whole = a.shift > 4;
@@ -313,15 +355,27 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     }
   };
   load_q();
-  int64_t next = warp;  // this warp's next block
+  // a lane's places in a block: its 16-byte chunks of K (keys g, + 8, + 16, + 24 lie 8
+  // keys' bytes apart) and its row of V
+  uint32_t k_at[HALVES], v_at[NT];
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h) {
+    const int row = D == 128 ? g : g >> 1, chunk = D == 128 ? 2 * c4 + h : (g & 1) * 4 + c4;
+    k_at[h] = (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+  }
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const int row = D == 128 ? lane : lane >> 1, chunk = D == 128 ? c : (lane & 1) * 4 + c;
+    v_at[c] = (uint32_t)(BLK + row * 128 + ((chunk ^ (row & 7)) << 4));
+  }
+  int next = warp;  // this warp's next block
   int stage = 0;
   uint32_t phase = 0;
-  for (int64_t b = 0; b < count;) {
+  for (int b = 0; b < count;) {
     // ---- one unit's piece: blocks [b, e), of which b is the unit's block here.j ----
     const DecSeq sq = here.s;
     const int kh = here.kh, j0 = here.j, blocks = sq.blocks;
-    const int len = (int)min(count - b, (int64_t)(blocks - j0));
-    const int64_t e = b + len;
+    const int len = min(count - b, blocks - j0), e = b + len;
 
     // the queries scaled by a power of two so that the largest lies in [1, 2): bf16's
     // range goes into fp16's
@@ -366,19 +420,17 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       ++consumed;
       if (++stage == kDecStages) stage = 0, phase ^= 1u;
       if (alive && sq.len > 0) {
-        const int key0 = (sq.lo / kDecKeys + j0 + (int)(next - b)) * kDecKeys;
-        const uint32_t kb = ring + s * STAGE, vb = kb + BLK;
+        const int key0 = (sq.lo / kDecKeys + j0 + next - b) * kDecKeys;
+        const uint32_t kb = ring + s * STAGE;
         float ks[2], lv[2], iv[2];
-        bool page[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           ks[t] = scale_s[warp][s][t][0];
           const float v = scale_s[warp][s][t][1];
-          page[t] = ks[t] >= 0.f;
-          lv[t] = page[t] ? log2_fast(v) : 0.f;
-          iv[t] = page[t] ? rcp_fast(v) : 0.f;
+          lv[t] = log2_fast(v);
+          iv[t] = rcp_fast(v);
         }
-        const bool edge = key0 < sq.lo || key0 + kDecKeys > sq.len || !page[0] || !page[1];
+        const bool edge = key0 < sq.lo || key0 + kDecKeys > sq.len || fminf(ks[0], ks[1]) < 0.f;
         // ---- S^T = K Q^T ----
         float sc[2][4];
 #pragma unroll
@@ -386,15 +438,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
           sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
-            uint4 x[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              // key k's 16-byte chunk c: rows of 128 bytes hold one key, or two
-              const int k = t * 16 + u * 8 + g;
-              const int row = D == 128 ? k : k >> 1, chunk = D == 128 ? 2 * c4 + h : (k & 1) * 4 + c4;
-              x[u] = lds_u4(kb + row * 128 + ((chunk ^ (row & 7)) << 4));
-            }
-            const uint32_t lo[4] = {x[0].x, x[0].y, x[0].z, x[0].w}, hi[4] = {x[1].x, x[1].y, x[1].z, x[1].w};
+            // keys t * 16 + g, and + 8: 8 D bytes on, at the same place of the swizzle
+            // where a row holds one key; where it holds two, rows 4 on have bit 2 turned
+            const uint32_t p = kb + t * (16 * D);
+            const uint4 x = lds_u4(p + k_at[h]), y = lds_u4(p + (D == 128 ? k_at[h] + 8 * D : (k_at[h] + 8 * D) ^ 64));
+            const uint32_t lo[4] = {x.x, x.y, x.z, x.w}, hi[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w)
               mma_f16(sc[t], from_e4m3x2(lo[w]), from_e4m3x2(hi[w]), from_e4m3x2(lo[w] >> 16), from_e4m3x2(hi[w] >> 16),
@@ -402,7 +450,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
           }
         }
         // ---- softmax over keys t * 16 + 8 u + g, of heads 2 c4 (even) and 2 c4 + 1 ----
-        float mx0 = m0, mx1 = m1;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const float f0 = fac0 * ks[t], f1 = fac1 * ks[t];
@@ -410,27 +457,45 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
           for (int u = 0; u < 2; ++u) {
             sc[t][2 * u] = fmaf(sc[t][2 * u], f0, lv[t]);
             sc[t][2 * u + 1] = fmaf(sc[t][2 * u + 1], f1, lv[t]);
-            if (edge) {
-              const int key = key0 + t * 16 + u * 8 + g;
-              if (key < sq.lo || key >= sq.len || !page[t]) sc[t][2 * u] = sc[t][2 * u + 1] = -INFINITY;
-            }
-            mx0 = fmaxf(mx0, sc[t][2 * u]);
-            mx1 = fmaxf(mx1, sc[t][2 * u + 1]);
           }
         }
+        if (edge) {
+          // keys that are not seen: no score, and codes of V that count as zero
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const bool page = ks[t] >= 0.f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int key = key0 + t * 16 + u * 8 + g;
+              if (key < sq.lo || key >= sq.len || !page) sc[t][2 * u] = sc[t][2 * u + 1] = -INFINITY;
+            }
+            if (!page) iv[t] = 0.f;
+          }
+          if (key0 + lane < sq.lo || key0 + lane >= sq.len || (lane < 16 ? ks[0] : ks[1]) < 0.f) {
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(kb + v_at[c]), "r"(0u) : "memory");
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // (the stage is filled by TMA again)
+          __syncwarp();
+        }
+        float mx0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+        float mx1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
           mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, x));
           mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, x));
         }
-        if (__any_sync(0xffffffffu, mx0 > m0 || mx1 > m1)) {
-          const float r0 = m0 == -INFINITY ? 0.f : exp2_fast(m0 - mx0), r1 = m1 == -INFINITY ? 0.f : exp2_fast(m1 - mx1);
+        // O is scaled anew where a maximum has grown by more than 2^8 (weights stay below it)
+        const bool need0 = mx0 > m0 + 8.f, need1 = mx1 > m1 + 8.f;
+        if (__any_sync(0xffffffffu, need0 || need1)) {
+          const float r0 = need0 ? exp2_fast(m0 - mx0) : 1.f, r1 = need1 ? exp2_fast(m1 - mx1) : 1.f;  // (0 from -inf)
 #pragma unroll
           for (int c = 0; c < NT; ++c) o[c][0] *= r0, o[c][1] *= r1, o[c][2] *= r0, o[c][3] *= r1;
           l0 *= r0;
           l1 *= r1;
-          m0 = mx0;
-          m1 = mx1;
+          m0 = need0 ? mx0 : m0;
+          m1 = need1 ? mx1 : m1;
         }
         const float ref0 = m0 == -INFINITY ? 0.f : m0, ref1 = m1 == -INFINITY ? 0.f : m1;
         uint32_t pb[2][2];
@@ -443,25 +508,11 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
           pb[t][0] = transposed(pack_f16(p0, p1));
           pb[t][1] = transposed(pack_f16(p2, p3));
         }
-        // ---- O^T += V^T P^T; codes of keys that are not seen count as zero ----
-        uint32_t keep[4];
-        if (edge) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int key = key0 + 8 * q + 2 * c4;
-            keep[q] = (key >= sq.lo && key < sq.len && page[q >> 1] ? 0xffffu : 0u) |
-                      (key + 1 >= sq.lo && key + 1 < sq.len && page[q >> 1] ? 0xffff0000u : 0u);
-          }
-        }
+        // ---- O^T += V^T P^T ----
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
           uint32_t v[4];
-          const int row = D == 128 ? lane : lane >> 1, chunk = D == 128 ? c : (lane & 1) * 4 + c;
-          ldsm_x4_t(vb + row * 128 + ((chunk ^ (row & 7)) << 4), v);
-          if (edge) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) v[q] &= keep[q];
-          }
+          ldsm_x4_t(kb + v_at[c], v);
 #pragma unroll
           for (int q = 0; q < 4; ++q) v[q] = __byte_perm(v[q], 0, 0x3120);  // (two keys of the even dim, two of the odd)
 #pragma unroll
@@ -569,25 +620,27 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_
   __shared__ float2 ml_s[kJoinWarps];
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t all = d.line->all, C = d.line->ctas;
-  const int64_t first = blockIdx.x, second = first + 1;
-  if (all == 0 || second >= C) return;
+  const DecLine line = *d.line;
+  const int first = blockIdx.x, second = first + 1;
+  if (line.all == 0 || second >= line.ctas) return;
   const DecStart u = d.starts[second];
-  const int64_t begins = all * first / C;  // the CTA before's first block
-  if (u.seq < 0 || begins > u.u0) return;
-  const int64_t last = ((u.u0 + u.blocks) * C - 1) / all;
+  if (u.seq < 0) return;
+  const int64_t begins = line.at(first);  // the CTA before's first block
+  if (begins > u.u0) return;
+  const int last = line.cta(u.u0 + u.blocks - 1);
   const int head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the first CTA's piece is its last one, unless the unit begins with it
-  auto slot = [&](int64_t c) { return (2 * c + (c == first && begins != u.u0 ? 1 : 0)) * kDecHeads + head; };
+  auto slot = [&](int c) { return (int64_t)(2 * c + (c == first && begins != u.u0 ? 1 : 0)) * kDecHeads + head; };
   float M = -INFINITY, L = 0.f, A[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) A[e] = 0.f;
-  for (int64_t c0 = first + warp; c0 <= last; c0 += 4 * kJoinWarps) {
+  for (int c0 = first + warp; c0 <= last; c0 += 4 * kJoinWarps) {
     float2 ml[4];
     float v[4][E];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int64_t c = c0 + k * kJoinWarps, s = slot(min(c, last));
+      const int c = c0 + k * kJoinWarps;
+      const int64_t s = slot(min(c, last));
       ml[k] = c <= last ? d.parts_ml[s] : make_float2(-INFINITY, 0.f);
 #pragma unroll
       for (int e = 0; e < E; ++e) v[k][e] = d.parts[s * D + e * 32 + lane];
@@ -632,7 +685,7 @@ struct Space {
   int64_t starts, ml, parts, chunks, bytes;
 };
 Space space_of(int head_dim, int max_rows) {
-  const int64_t slots = 2ll * kDecPerSm * num_sms();
+  const int64_t slots = 2ll * kDecWaves * kDecPerSm * num_sms();
   Space s;
   s.starts = 256;
   s.ml = s.starts + up256(slots / 2 * sizeof(DecStart));
@@ -654,16 +707,19 @@ int check_batch(const sar_kv8_batch& b, const sar_kv8* c) {
   return SAR_OK;
 }
 
+// blocks: of the line at most, where the longest sequence is as long as the caller says.
 template <typename T, int D>
-int launch_kv8(const DecArgs& d, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
+int launch_kv8(const DecArgs& d, int64_t blocks, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
   const int smem = 1024 + kDecWarps * kDecStages * 2 * kDecKeys * D;
   SAR_TRY(ensure_smem_attr(reinterpret_cast<const void*>(&kv8_decode_kernel<T, D>), smem, "kv8 decode: set smem attribute"));
-  const int grid = kDecPerSm * num_sms();
+  const int grid = d.units ? d.a.n * d.a.kvh : blocks >= (int64_t)d.resident * kDecMany ? kDecWaves * d.resident : d.resident;
   cudaError_t e = launch_pdl(kv8_decode_kernel<T, D>, dim3(grid), dim3(kDecWarps * 32), (size_t)smem, s, tmk, tmv, d);
   if (e != cudaSuccess) return cuda_error(e, "kv8 decode launch");
+  count_launches(1);
+  if (d.units) return SAR_OK;
   e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)d.a.G), dim3(kJoinWarps * 32), 0, s, d);
   if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
-  count_launches(2);
+  count_launches(1);
   return SAR_OK;
 }
 
@@ -734,6 +790,12 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   d.starts = reinterpret_cast<sar::DecStart*>(ws + sp.starts);
   d.parts_ml = reinterpret_cast<float2*>(ws + sp.ml);
   d.parts = reinterpret_cast<float*>(ws + sp.parts);
+  // (max_len and the tables' width only guide how work is shared out)
+  const int64_t longest = b.max_len > 0 ? b.max_len : (int64_t)b.bt_stride * cache->page_size;
+  const int64_t most = (b.window > 0 ? std::min<int64_t>(longest, b.window) : longest) / sar::kDecKeys + 2;
+  const int64_t blocks = most * b.n * cache->n_kv_heads;
+  d.resident = sar::kDecPerSm * sar::num_sms();
+  d.units = most <= sar::kDecUnit + 2 && (int64_t)b.n * cache->n_kv_heads <= 1 << 20;
   d.vec_q = aligned_to(b.q, 16) && b.ldq % 8 == 0;
   d.vec_o = aligned_to(b.out, 4) && b.ldo % 2 == 0;
   // the codes as rows of 128 bytes (one key, or two of 64 dims), boxes of up to 32 keys of a page
@@ -746,9 +808,9 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   const bool bf = b.storage == SAR_STORAGE_BF16;
   int rc;
   if (cache->head_dim == 128)
-    rc = bf ? sar::launch_kv8<__nv_bfloat16, 128>(d, tmk, tmv, s) : sar::launch_kv8<__half, 128>(d, tmk, tmv, s);
+    rc = bf ? sar::launch_kv8<__nv_bfloat16, 128>(d, blocks, tmk, tmv, s) : sar::launch_kv8<__half, 128>(d, blocks, tmk, tmv, s);
   else
-    rc = bf ? sar::launch_kv8<__nv_bfloat16, 64>(d, tmk, tmv, s) : sar::launch_kv8<__half, 64>(d, tmk, tmv, s);
+    rc = bf ? sar::launch_kv8<__nv_bfloat16, 64>(d, blocks, tmk, tmv, s) : sar::launch_kv8<__half, 64>(d, blocks, tmk, tmv, s);
   if (rc != SAR_OK) return rc;
   if (b.max_rows == 1 || b.rows == 1) return SAR_OK;
   return sar::launch_kv8_chunks(a, cache->head_dim, b.storage, ws + sp.chunks, s);
