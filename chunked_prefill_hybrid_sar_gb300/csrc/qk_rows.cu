@@ -10,7 +10,7 @@
 // Query heads are independent.  For the cache the unit is a run: the rows of a call
 // in one page, which share a scale for each head.  A CTA takes the runs that begin
 // in its window of rows (they may end up to 63 rows behind it), keeps their rows'
-// keys and values in registers, joins the rows' largest magnitudes in shared
+// keys or values in registers, joins the rows' largest magnitudes in shared
 // memory, and writes codes: the input is read once.
 #include <math.h>
 
@@ -87,7 +87,13 @@ __device__ __forceinline__ void angles(const QkArgs& a, int pos, int i0, float* 
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint64_t t = (uint64_t)(int64_t)pos * a.turn[i0 + e];
-    sincospif((float)(int32_t)(t >> 32) * 0x1p-31f, &sn[e], &cs[e]);
+    const int32_t h = (int32_t)(t >> 32);  // half turns in units of 2^-31
+    const float f = (float)h, rest = (float)(int32_t)((int64_t)h - (int64_t)f) * (0x1p-31f * 3.14159265f);
+    float c, s;
+    sincospif(f * 0x1p-31f, &s, &c);
+    // what h lost in 24 bits: up to 2^-25 of a half turn
+    cs[e] = fmaf(-s, rest, c);
+    sn[e] = fmaf(c, rest, s);
   }
 }
 
@@ -114,7 +120,7 @@ __device__ __forceinline__ void norm_rope(float* x, const float* gain, bool norm
 
 // TI: the rows' type; TO: the 16-bit type written.
 template <typename TI, typename TO, int D>
-__global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, 3) qk_rows_kernel(const __grid_constant__ QkArgs a) {
   constexpr int LANES = D / 8, GROUPS = kQkThreads / LANES;  // rows of a pass, and of a window
   constexpr int PASSES = (GROUPS + 63 + GROUPS - 1) / GROUPS;
   constexpr int SPAN = PASSES * GROUPS;  // rows that a window's runs can reach
@@ -161,11 +167,12 @@ __global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_consta
     return;
   }
 
-  // ---- one KV head of the runs that begin in this window ----
+  // ---- keys or values of one KV head, of the runs that begin in this window ----
   __shared__ int slot_s[SPAN];
   __shared__ uint32_t flag_s[(SPAN + 31) / 32];  // rows that do not go on from the row before
-  __shared__ float amax_s[2][SPAN];
-  const int kh = task;
+  __shared__ float amax_s[SPAN];
+  const bool is_k = task < r.n_kv_heads;
+  const int kh = is_k ? task : task - r.n_kv_heads;
   const int ps = a.c.page_size;
   const int64_t n_slots = (int64_t)a.c.num_pages * ps;
   if (threadIdx.x < (SPAN + 31) / 32 * 32) {
@@ -174,11 +181,12 @@ __global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_consta
     bool flag = true;
     if (i < SPAN && row < r.rows) {
       s = r.slots[row];
+      const int before = row > 0 ? r.slots[row - 1] : -1;
       if (s < 0 || s >= n_slots) {
-        if (s != -1 && kh == 0 && i < GROUPS) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SLOT, row);
+        if (s != -1 && task == 0 && i < GROUPS) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SLOT, row);
         s = -1;
       } else {
-        flag = row == 0 || (s & (ps - 1)) == 0 || r.slots[row - 1] != s - 1;
+        flag = row == 0 || (s & (ps - 1)) == 0 || before != s - 1;
       }
     }
     const uint32_t m = __ballot_sync(0xffffffffu, flag);
@@ -205,55 +213,53 @@ __global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_consta
     return m == 0 ? SPAN : min(SPAN, (w << 5) + __ffs(m) - 1);
   };
 
-  float gain[8];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    gain[e] = r.k_gain ? r.k_gain[4 * l + e] : 1.f, gain[4 + e] = r.k_gain ? r.k_gain[D / 2 + 4 * l + e] : 1.f;
-  float x[PASSES][8], y[PASSES][8];
-  float old_k[PASSES], old_v[PASSES];
+  const int64_t ld = is_k ? r.ldk : r.ldv;
+  const TI* src = static_cast<const TI*>(is_k ? r.k : r.v) + w0 * ld + kh * D + 4 * l;
+  const bool vec = is_k ? a.vec_k : a.vec_v;
+  float* scales = is_k ? a.c.k_scales : a.c.v_scales;
+  uint8_t* codes = static_cast<uint8_t*>(is_k ? a.c.k_codes : a.c.v_codes);
+  float x[PASSES][8], old[PASSES];
   int run[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int i = p * GROUPS + grp, row = w0 + i;
+    const int i = p * GROUPS + grp;
     run[p] = run_of(i);
-    old_k[p] = old_v[p] = 0.f;
+    old[p] = 0.f;
     if (run[p] >= 0) {
-      const TI* kp = static_cast<const TI*>(r.k) + row * r.ldk + kh * D + 4 * l;
-      const TI* vp = static_cast<const TI*>(r.v) + row * r.ldv + kh * D + 4 * l;
-      load4<TI>(kp, a.vec_k, x[p]);
-      load4<TI>(kp + D / 2, a.vec_k, x[p] + 4);
-      load4<TI>(vp, a.vec_v, y[p]);
-      load4<TI>(vp + D / 2, a.vec_v, y[p] + 4);
+      load4<TI>(src + i * ld, vec, x[p]);
+      load4<TI>(src + i * ld + D / 2, vec, x[p] + 4);
       const int first = slot_s[run[p]];
-      if (first & (ps - 1)) {  // the page goes on: what it has so far
-        const int64_t at = (int64_t)(first >> a.shift) * a.c.n_kv_heads + kh;
-        old_k[p] = a.c.k_scales[at];
-        old_v[p] = a.c.v_scales[at];
-      }
+      // (the page goes on: what it has so far)
+      if (first & (ps - 1)) old[p] = scales[(int64_t)(first >> a.shift) * a.c.n_kv_heads + kh];
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[p][e] = y[p][e] = 0.f;
+      for (int e = 0; e < 8; ++e) x[p][e] = 0.f;
+    }
+  }
+  if (is_k && (r.k_gain || r.positions)) {
+    float gain[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      gain[e] = r.k_gain ? r.k_gain[4 * l + e] : 1.f, gain[4 + e] = r.k_gain ? r.k_gain[D / 2 + 4 * l + e] : 1.f;
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      // (passes without a row of this window's runs, as all but the first of single tokens)
+      if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
+      float cs[4], sn[4];
+      if (r.positions) angles(a, run[p] >= 0 ? r.positions[w0 + p * GROUPS + grp] : 0, 4 * l, cs, sn);
+      norm_rope<D>(x[p], gain, r.k_gain != nullptr, r.eps, r.positions != nullptr, cs, sn);
     }
   }
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int i = p * GROUPS + grp;
-    // (a pass without a row of this window's runs, as all but the first of single tokens)
-    if (__any_sync(0xffffffffu, run[p] >= 0)) {
-      float cs[4], sn[4];
-      if (r.positions) angles(a, run[p] >= 0 ? r.positions[w0 + i] : 0, 4 * l, cs, sn);
-      norm_rope<D>(x[p], gain, r.k_gain != nullptr, r.eps, r.positions != nullptr, cs, sn);
-    }
-    float mk = 0.f, mv = 0.f;
+    float m = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float u = fabsf(x[p][e]), w = fabsf(y[p][e]);
-      mk = fmaxf(mk, u < INFINITY ? u : 0.f);
-      mv = fmaxf(mv, w < INFINITY ? w : 0.f);
+      const float u = fabsf(x[p][e]);
+      m = fmaxf(m, u < INFINITY ? u : 0.f);
     }
-    mk = group_max<LANES>(mk);
-    mv = group_max<LANES>(mv);
-    if (l == 0) amax_s[0][i] = mk, amax_s[1][i] = mv;
+    m = group_max<LANES>(m);
+    if (l == 0) amax_s[p * GROUPS + grp] = m;
   }
   __syncthreads();
 #pragma unroll
@@ -261,44 +267,37 @@ __global__ void __launch_bounds__(kQkThreads) qk_rows_kernel(const __grid_consta
     if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
     const int i = p * GROUPS + grp;
     const bool live = run[p] >= 0;
-    float mk = 0.f, mv = 0.f;
+    float m = 0.f;
     if (live) {
       const int end = run_end(i);
-      for (int j = run[p] + l; j < end; j += LANES) mk = fmaxf(mk, amax_s[0][j]), mv = fmaxf(mv, amax_s[1][j]);
+      for (int j = run[p] + l; j < end; j += LANES) m = fmaxf(m, amax_s[j]);
     }
-    mk = group_max<LANES>(mk);
-    mv = group_max<LANES>(mv);
+    m = group_max<LANES>(m);
     if (!live) continue;
-    const float sk = fmaxf(kv8_scale(mk), old_k[p]), sv = fmaxf(kv8_scale(mv), old_v[p]);
+    const float scale = fmaxf(kv8_scale(m), old[p]);
     const int slot = slot_s[i];
     const int64_t unit = (int64_t)(slot >> a.shift) * a.c.n_kv_heads + kh;
-    uint8_t* kc = static_cast<uint8_t*>(a.c.k_codes) + unit * ps * D;
-    uint8_t* vc = static_cast<uint8_t*>(a.c.v_codes) + unit * ps * D;
+    uint8_t* page = codes + unit * ps * D;
     const int o = (slot & (ps - 1)) * D + 4 * l;
-    const float ik = 1.f / sk, iv = 1.f / sv;  // (exact for powers of two)
+    const float inv = 1.f / scale;  // (exact for powers of two)
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const float* u = x[p] + 4 * half;
-      const float* w = y[p] + 4 * half;
-      *reinterpret_cast<uint32_t*>(kc + o + half * (D / 2)) =
-          to_e4m3x2(u[0] * ik, u[1] * ik) | to_e4m3x2(u[2] * ik, u[3] * ik) << 16;
-      *reinterpret_cast<uint32_t*>(vc + o + half * (D / 2)) =
-          to_e4m3x2(w[0] * iv, w[1] * iv) | to_e4m3x2(w[2] * iv, w[3] * iv) << 16;
+      *reinterpret_cast<uint32_t*>(page + o + half * (D / 2)) =
+          to_e4m3x2(u[0] * inv, u[1] * inv) | to_e4m3x2(u[2] * inv, u[3] * inv) << 16;
     }
     if (run[p] != i) continue;
-    // the run's first row: the scales, and what the page held under smaller ones
-    if (l == 0) a.c.k_scales[unit] = sk, a.c.v_scales[unit] = sv;
-    const int held = (slot & (ps - 1)) * D;
-    auto anew = [&](uint8_t* codes, float ratio) {
-      for (int j = 4 * l; j < held; j += 4 * LANES) {
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(codes + j);
+    // the run's first row: the scale, and what the page held under a smaller one
+    if (l == 0) scales[unit] = scale;
+    if (old[p] > 0.f && scale > old[p]) {
+      const float ratio = old[p] * inv;
+#pragma unroll 1
+      for (int j = 4 * l; j < (slot & (ps - 1)) * D; j += 4 * LANES) {
+        const uint32_t c = *reinterpret_cast<const uint32_t*>(page + j);
         const float2 u = e4m3x2_floats(c), w = e4m3x2_floats(c >> 16);
-        *reinterpret_cast<uint32_t*>(codes + j) =
-            to_e4m3x2(u.x * ratio, u.y * ratio) | to_e4m3x2(w.x * ratio, w.y * ratio) << 16;
+        *reinterpret_cast<uint32_t*>(page + j) = to_e4m3x2(u.x * ratio, u.y * ratio) | to_e4m3x2(w.x * ratio, w.y * ratio) << 16;
       }
-    };
-    if (held > 0 && old_k[p] > 0.f && sk > old_k[p]) anew(kc, old_k[p] * ik);
-    if (held > 0 && old_v[p] > 0.f && sv > old_v[p]) anew(vc, old_v[p] * iv);
+    }
   }
 }
 
@@ -396,7 +395,7 @@ extern "C" int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, v
   while (a.q_heads_per < 16 && windows * (a.r.n_q_heads / (2 * a.q_heads_per)) >= 4 * sar::num_sms()) a.q_heads_per *= 2;
   a.q_tasks = (a.r.n_q_heads + a.q_heads_per - 1) / a.q_heads_per;
   a.k_tasks = r.k_out ? (r.n_kv_heads + a.q_heads_per - 1) / a.q_heads_per : 0;
-  a.kv_tasks = cache ? r.n_kv_heads : 0;
+  a.kv_tasks = cache ? 2 * r.n_kv_heads : 0;
   if (a.q_tasks + a.k_tasks + a.kv_tasks == 0) return SAR_OK;
   if (r.positions) {
     // (kept for the thread's next call: they depend on these two numbers alone)
