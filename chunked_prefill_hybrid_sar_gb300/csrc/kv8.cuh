@@ -22,13 +22,15 @@ __device__ __forceinline__ float kv8_scale(float a) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-// Two values to e4m3, nearest even, at most 448 in magnitude; infinities become NaN.
-__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+// Two values to e4m3, nearest even, at most 448 in magnitude; NaN stays NaN.
+__device__ __forceinline__ uint32_t finite_e4m3x2(float lo, float hi) {
   uint16_t r;
-  lo = fabsf(lo) == INFINITY ? NAN : lo;
-  hi = fabsf(hi) == INFINITY ? NAN : hi;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
+}
+// The same; infinities become NaN.
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
+  return finite_e4m3x2(fabsf(lo) == INFINITY ? NAN : lo, fabsf(hi) == INFINITY ? NAN : hi);
 }
 
 // Two e4m3 codes (the low 16 bits) as fp16, exactly.

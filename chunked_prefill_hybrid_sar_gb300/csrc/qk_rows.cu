@@ -22,13 +22,14 @@ namespace sar {
 
 namespace {
 
-constexpr int kQkThreads = 256;
+constexpr int kQkThreads = 512;
 
 struct QkArgs {
   sar_qk_rows r;
   sar_kv8 c;
   int shift;           // log2 page_size
-  int q_heads_per, q_tasks, k_tasks, kv_tasks;  // query heads per CTA; CTAs per window of rows: queries, k_out, cache
+  int q_heads_per, kv_heads_per;     // heads of a CTA
+  int q_tasks, k_tasks, kv_tasks;    // CTAs of a window of rows: queries, k_out, cache (keys, then values)
   int vec_q, vec_k, vec_v, vec_qo, vec_ko;  // rows whose pieces of four are aligned
   int* err;
   uint64_t turn[64];   // theta_i / (2 pi) in units of 2^-64 turns
@@ -68,6 +69,9 @@ __device__ __forceinline__ void store4(T* p, bool vec, const float* x) {
     for (int e = 0; e < 4; ++e) p[e] = Elem<T>::from(x[e]);
   }
 }
+
+// Asks for a line to come to L2.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
@@ -120,7 +124,7 @@ __device__ __forceinline__ void norm_rope(float* x, const float* gain, bool norm
 
 // TI: the rows' type; TO: the 16-bit type written.
 template <typename TI, typename TO, int D>
-__global__ void __launch_bounds__(kQkThreads, 3) qk_rows_kernel(const __grid_constant__ QkArgs a) {
+__global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_constant__ QkArgs a) {
   constexpr int LANES = D / 8, GROUPS = kQkThreads / LANES;  // rows of a pass, and of a window
   constexpr int PASSES = (GROUPS + 63 + GROUPS - 1) / GROUPS;
   constexpr int SPAN = PASSES * GROUPS;  // rows that a window's runs can reach
@@ -147,7 +151,12 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_rows_kernel(const __grid_con
     TO* dst = static_cast<TO*>(is_q ? r.q_out : r.k_out) + row * ldo + 4 * l;
     const bool vi = is_q ? a.vec_q : a.vec_k, vo = is_q ? a.vec_qo : a.vec_ko;
     constexpr int AT_ONCE = 4;  // heads whose loads are under way together
+    constexpr int LINES = D * (int)sizeof(TI) / 128;  // of a head
     for (int h = h0; h < h1; h += AT_ONCE) {
+      // the next heads come to L2 while these are worked on
+      for (int k = l; k < AT_ONCE * LINES; k += LANES)
+        if (live && h + AT_ONCE + k / LINES < h1)
+          prefetch_l2(reinterpret_cast<const char*>(src - 4 * l + (h + AT_ONCE) * D) + k * 128);
       float x[AT_ONCE][8];
 #pragma unroll
       for (int u = 0; u < AT_ONCE; ++u) {
@@ -167,14 +176,16 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_rows_kernel(const __grid_con
     return;
   }
 
-  // ---- keys or values of one KV head, of the runs that begin in this window ----
+  // ---- keys or values of some KV heads, of the runs that begin in this window ----
   __shared__ int slot_s[SPAN];
   __shared__ uint32_t flag_s[(SPAN + 31) / 32];  // rows that do not go on from the row before
   __shared__ float amax_s[SPAN];
-  const bool is_k = task < r.n_kv_heads;
-  const int kh = is_k ? task : task - r.n_kv_heads;
+  extern __shared__ __align__(16) float angle_s[];  // [SPAN][LANES][8], where a CTA has several heads
+  const bool is_k = task < a.kv_tasks / 2;
+  const int kh0 = (is_k ? task : task - a.kv_tasks / 2) * a.kv_heads_per, kh1 = min(kh0 + a.kv_heads_per, r.n_kv_heads);
   const int ps = a.c.page_size;
   const int64_t n_slots = (int64_t)a.c.num_pages * ps;
+  int begins = 0;
   if (threadIdx.x < (SPAN + 31) / 32 * 32) {
     const int i = threadIdx.x, row = w0 + i;
     int s = -1;
@@ -192,8 +203,9 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_rows_kernel(const __grid_con
     const uint32_t m = __ballot_sync(0xffffffffu, flag);
     if (i < SPAN) slot_s[i] = s;
     if ((i & 31) == 0) flag_s[i >> 5] = m;
+    begins = s >= 0 && flag && i < GROUPS;
   }
-  __syncthreads();
+  if (!__syncthreads_or(begins)) return;  // (three windows of four, in chunks over pages of 64)
   // row i's run: the last flagged row up to i; -1 where i is in no run of this window
   auto run_of = [&](int i) -> int {
     if (slot_s[i] < 0) return -1;
@@ -214,90 +226,120 @@ __global__ void __launch_bounds__(kQkThreads, 3) qk_rows_kernel(const __grid_con
   };
 
   const int64_t ld = is_k ? r.ldk : r.ldv;
-  const TI* src = static_cast<const TI*>(is_k ? r.k : r.v) + w0 * ld + kh * D + 4 * l;
+  const TI* src = static_cast<const TI*>(is_k ? r.k : r.v) + w0 * ld + 4 * l;
   const bool vec = is_k ? a.vec_k : a.vec_v;
   float* scales = is_k ? a.c.k_scales : a.c.v_scales;
   uint8_t* codes = static_cast<uint8_t*>(is_k ? a.c.k_codes : a.c.v_codes);
-  float x[PASSES][8], old[PASSES];
-  int run[PASSES];
+  int run[PASSES], end[PASSES];
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
-    const int i = p * GROUPS + grp;
-    run[p] = run_of(i);
-    old[p] = 0.f;
-    if (run[p] >= 0) {
-      load4<TI>(src + i * ld, vec, x[p]);
-      load4<TI>(src + i * ld + D / 2, vec, x[p] + 4);
-      const int first = slot_s[run[p]];
-      // (the page goes on: what it has so far)
-      if (first & (ps - 1)) old[p] = scales[(int64_t)(first >> a.shift) * a.c.n_kv_heads + kh];
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[p][e] = 0.f;
-    }
+    run[p] = run_of(p * GROUPS + grp);
+    end[p] = run[p] >= 0 ? run_end(p * GROUPS + grp) : 0;
+    // all of this CTA's heads of the row come to L2
+    constexpr int LINES = D * (int)sizeof(TI) / 128;
+    for (int k = l; run[p] >= 0 && k < (kh1 - kh0) * LINES; k += LANES)
+      prefetch_l2(reinterpret_cast<const char*>(src - 4 * l + (p * GROUPS + grp) * ld + kh0 * D) + k * 128);
   }
-  if (is_k && (r.k_gain || r.positions)) {
-    float gain[8];
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      gain[e] = r.k_gain ? r.k_gain[4 * l + e] : 1.f, gain[4 + e] = r.k_gain ? r.k_gain[D / 2 + 4 * l + e] : 1.f;
+#pragma unroll 1
+  for (int kh = kh0; kh < kh1; ++kh) {
+    float x[PASSES][8], old[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
-      // (passes without a row of this window's runs, as all but the first of single tokens)
-      if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
-      float cs[4], sn[4];
-      if (r.positions) angles(a, run[p] >= 0 ? r.positions[w0 + p * GROUPS + grp] : 0, 4 * l, cs, sn);
-      norm_rope<D>(x[p], gain, r.k_gain != nullptr, r.eps, r.positions != nullptr, cs, sn);
-    }
-  }
+      const int i = p * GROUPS + grp;
+      old[p] = 0.f;
+      if (run[p] >= 0) {
+        load4<TI>(src + i * ld + kh * D, vec, x[p]);
+        load4<TI>(src + i * ld + kh * D + D / 2, vec, x[p] + 4);
+        const int first = slot_s[run[p]];
+        // (the page goes on: what it has so far)
+        if (first & (ps - 1)) old[p] = scales[(int64_t)(first >> a.shift) * a.c.n_kv_heads + kh];
+      } else {
 #pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    float m = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float u = fabsf(x[p][e]);
-      m = fmaxf(m, u < INFINITY ? u : 0.f);
-    }
-    m = group_max<LANES>(m);
-    if (l == 0) amax_s[p * GROUPS + grp] = m;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int p = 0; p < PASSES; ++p) {
-    if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
-    const int i = p * GROUPS + grp;
-    const bool live = run[p] >= 0;
-    float m = 0.f;
-    if (live) {
-      const int end = run_end(i);
-      for (int j = run[p] + l; j < end; j += LANES) m = fmaxf(m, amax_s[j]);
-    }
-    m = group_max<LANES>(m);
-    if (!live) continue;
-    const float scale = fmaxf(kv8_scale(m), old[p]);
-    const int slot = slot_s[i];
-    const int64_t unit = (int64_t)(slot >> a.shift) * a.c.n_kv_heads + kh;
-    uint8_t* page = codes + unit * ps * D;
-    const int o = (slot & (ps - 1)) * D + 4 * l;
-    const float inv = 1.f / scale;  // (exact for powers of two)
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const float* u = x[p] + 4 * half;
-      *reinterpret_cast<uint32_t*>(page + o + half * (D / 2)) =
-          to_e4m3x2(u[0] * inv, u[1] * inv) | to_e4m3x2(u[2] * inv, u[3] * inv) << 16;
-    }
-    if (run[p] != i) continue;
-    // the run's first row: the scale, and what the page held under a smaller one
-    if (l == 0) scales[unit] = scale;
-    if (old[p] > 0.f && scale > old[p]) {
-      const float ratio = old[p] * inv;
-#pragma unroll 1
-      for (int j = 4 * l; j < (slot & (ps - 1)) * D; j += 4 * LANES) {
-        const uint32_t c = *reinterpret_cast<const uint32_t*>(page + j);
-        const float2 u = e4m3x2_floats(c), w = e4m3x2_floats(c >> 16);
-        *reinterpret_cast<uint32_t*>(page + j) = to_e4m3x2(u.x * ratio, u.y * ratio) | to_e4m3x2(w.x * ratio, w.y * ratio) << 16;
+        for (int e = 0; e < 8; ++e) x[p][e] = 0.f;
       }
     }
+    if (is_k && (r.k_gain || r.positions)) {
+      float gain[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        gain[e] = r.k_gain ? r.k_gain[4 * l + e] : 1.f, gain[4 + e] = r.k_gain ? r.k_gain[D / 2 + 4 * l + e] : 1.f;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) {
+        // (passes without a row of this window's runs, as all but the first of single tokens)
+        if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
+        float cs[4], sn[4];
+        if (r.positions) {
+          // formed once, kept for the CTA's other heads
+          float4* kept = reinterpret_cast<float4*>(angle_s) + ((p * GROUPS + grp) * LANES + l) * 2;
+          if (kh == kh0) {
+            angles(a, run[p] >= 0 ? r.positions[w0 + p * GROUPS + grp] : 0, 4 * l, cs, sn);
+            if (kh1 - kh0 > 1) kept[0] = make_float4(cs[0], cs[1], cs[2], cs[3]), kept[1] = make_float4(sn[0], sn[1], sn[2], sn[3]);
+          } else {
+            const float4 c = kept[0], t = kept[1];
+            cs[0] = c.x, cs[1] = c.y, cs[2] = c.z, cs[3] = c.w;
+            sn[0] = t.x, sn[1] = t.y, sn[2] = t.z, sn[3] = t.w;
+          }
+        }
+        norm_rope<D>(x[p], gain, r.k_gain != nullptr, r.eps, r.positions != nullptr, cs, sn);
+      }
+    }
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[p][e]));  // (passes over NaN)
+      m = group_max<LANES>(m);
+      if (__any_sync(0xffffffffu, m == INFINITY)) {  // infinities become NaN, and count for nothing
+        m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[p][e] = fabsf(x[p][e]) < INFINITY ? x[p][e] : NAN;
+          m = fmaxf(m, fabsf(x[p][e]));
+        }
+        m = group_max<LANES>(m);
+      }
+      if (l == 0) amax_s[p * GROUPS + grp] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
+      const int i = p * GROUPS + grp;
+      const bool live = run[p] >= 0;
+      float m = 0.f;
+      if (live)
+        for (int j = run[p] + l; j < end[p]; j += LANES) m = fmaxf(m, amax_s[j]);
+      m = group_max<LANES>(m);
+      if (!live) continue;
+      const float scale = fmaxf(kv8_scale(m), old[p]);
+      const int slot = slot_s[i];
+      const int64_t unit = (int64_t)(slot >> a.shift) * a.c.n_kv_heads + kh;
+      uint8_t* page = codes + unit * ps * D;
+      const int o = (slot & (ps - 1)) * D + 4 * l;
+      // (a power of two's inverse, exactly, without the division)
+      const uint32_t bits = __float_as_uint(scale);
+      const float inv = (bits & 0x7fffffu) == 0 ? __uint_as_float(0x7f000000u - bits) : 1.f / scale;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float* u = x[p] + 4 * half;
+        *reinterpret_cast<uint32_t*>(page + o + half * (D / 2)) =
+            finite_e4m3x2(u[0] * inv, u[1] * inv) | finite_e4m3x2(u[2] * inv, u[3] * inv) << 16;
+      }
+      if (run[p] != i) continue;
+      // the run's first row: the scale, and what the page held under a smaller one
+      if (l == 0) scales[unit] = scale;
+      if (old[p] > 0.f && scale > old[p]) {
+        const float ratio = old[p] * inv;
+#pragma unroll 1
+        for (int j = 4 * l; j < (slot & (ps - 1)) * D; j += 4 * LANES) {
+          const uint32_t c = *reinterpret_cast<const uint32_t*>(page + j);
+          const float2 u = e4m3x2_floats(c), w = e4m3x2_floats(c >> 16);
+          *reinterpret_cast<uint32_t*>(page + j) = finite_e4m3x2(u.x * ratio, u.y * ratio) | finite_e4m3x2(w.x * ratio, w.y * ratio) << 16;
+        }
+      }
+    }
+    __syncthreads();  // (the largest magnitudes are written again)
   }
 }
 
@@ -306,8 +348,14 @@ int launch_qk(const QkArgs& a, cudaStream_t s) {
   const int D = a.r.head_dim;
   const int window = kQkThreads / (D / 8);
   const dim3 grid((unsigned)(((int64_t)a.r.rows + window - 1) / window), (unsigned)(a.kv_tasks + a.q_tasks + a.k_tasks));
-  const cudaError_t e = D == 128 ? launch_pdl(qk_rows_kernel<TI, TO, 128>, grid, dim3(kQkThreads), 0, s, a)
-                                 : launch_pdl(qk_rows_kernel<TI, TO, 64>, grid, dim3(kQkThreads), 0, s, a);
+  const int passes = (window + 63 + window - 1) / window;
+  const size_t smem = a.kv_heads_per > 1 && a.r.positions ? (size_t)passes * kQkThreads * 32 : 0;
+  if (smem > 0)
+    SAR_TRY(ensure_smem_attr(D == 128 ? reinterpret_cast<const void*>(&qk_rows_kernel<TI, TO, 128>)
+                                      : reinterpret_cast<const void*>(&qk_rows_kernel<TI, TO, 64>),
+                             (int)smem, "qk rows: set smem attribute"));
+  const cudaError_t e = D == 128 ? launch_pdl(qk_rows_kernel<TI, TO, 128>, grid, dim3(kQkThreads), smem, s, a)
+                                 : launch_pdl(qk_rows_kernel<TI, TO, 64>, grid, dim3(kQkThreads), smem, s, a);
   if (e != cudaSuccess) return cuda_error(e, "qk rows launch");
   count_launches(1);
   return SAR_OK;
@@ -389,13 +437,23 @@ extern "C" int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, v
   a.vec_v = vec(r.v, r.ldv, 4 * size, size);
   a.vec_qo = vec(r.q_out, r.ldq_out, 8, 2);
   a.vec_ko = vec(r.k_out, r.ldk_out, 8, 2);
-  // heads to a CTA: as many as leave every SM a few CTAs
+  // heads to a CTA: as few as let all CTAs be resident at once (two to an SM), and no
+  // more than amortise a row's angles and slots
   const int64_t windows = ((int64_t)r.rows * (r.head_dim / 8) + sar::kQkThreads - 1) / sar::kQkThreads;
-  a.q_heads_per = 1;
-  while (a.q_heads_per < 16 && windows * (a.r.n_q_heads / (2 * a.q_heads_per)) >= 4 * sar::num_sms()) a.q_heads_per *= 2;
-  a.q_tasks = (a.r.n_q_heads + a.q_heads_per - 1) / a.q_heads_per;
-  a.k_tasks = r.k_out ? (r.n_kv_heads + a.q_heads_per - 1) / a.q_heads_per : 0;
-  a.kv_tasks = cache ? 2 * r.n_kv_heads : 0;
+  auto up = [](int n, int per) { return (n + per - 1) / per; };
+  a.q_heads_per = a.kv_heads_per = 1;
+  while (true) {
+    a.q_tasks = up(a.r.n_q_heads, a.q_heads_per);
+    a.k_tasks = r.k_out ? up(r.n_kv_heads, a.q_heads_per) : 0;
+    a.kv_tasks = cache ? 2 * up(r.n_kv_heads, a.kv_heads_per) : 0;
+    if (windows * (a.q_tasks + a.k_tasks + a.kv_tasks) <= 2 * sar::num_sms()) break;
+    if (a.q_heads_per < 16 && (a.kv_heads_per >= 4 || a.q_tasks + a.k_tasks >= a.kv_tasks))
+      a.q_heads_per *= 2;
+    else if (a.kv_heads_per < 4)
+      a.kv_heads_per *= 2;
+    else
+      break;
+  }
   if (a.q_tasks + a.k_tasks + a.kv_tasks == 0) return SAR_OK;
   if (r.positions) {
     // (kept for the thread's next call: they depend on these two numbers alone)
