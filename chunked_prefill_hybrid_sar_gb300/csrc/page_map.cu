@@ -24,13 +24,15 @@ namespace sar {
 
 namespace {
 
-constexpr int kMapThreads = 512;
+constexpr int kMapThreads = 1024;
 constexpr int kMapCtas = 8;     // CTAs of a large call's cluster
+constexpr int kMapAlone = 1024; // rows up to which one CTA takes the call
 constexpr int kMapMost = 8192;  // requests: four shared-memory words each
 
 struct MapArgs {
   sar_page_map_args m;
   int shift;  // log2 page_size
+  int vec;    // positions and slots are 16-byte aligned
   int* err;
 };
 
@@ -178,21 +180,44 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) 
     report(a.err, SAR_ERR_BOUNDS, SITE_MAP_PAGE, page);
     return false;
   };
-  for (int r = (int)gt; r < m.max_rows; r += (int)gn) {
-    int pos = 0, slot = -1;
-    if (n > 0 && r < row_at[n]) {
-      const int i = owner(row_at, n, r);
+  // Rows of chunks, four to a thread, are mostly one request's, in one page, and then take
+  // one search and one look-up (64 chunks of up to 2048 rows: 12.4 us; 18.4 with a row at a
+  // time).  Where there is a thread for every row, a row each: single tokens'
+  // look-ups do not wait for one another (256 mixed requests: 10 us; 18 with four).
+  const int live = n > 0 ? row_at[n] : 0;
+  const int each = m.max_rows > 2 * (int)gn ? 4 : 1;
+  for (int r0 = each * (int)gt; r0 < m.max_rows; r0 += each * (int)gn) {
+    int pos[4], slot[4], i = -1, page = -1, of = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int r = r0 + k;
+      pos[k] = 0;
+      slot[k] = -1;
+      if (r >= live || k >= each) continue;
+      if (i < 0 || r >= row_at[i + 1]) {
+        i = owner(row_at, n, r);
+        of = -1;
+      }
       const bool ok = len_s[i] >= 0;
       const int len = ok ? len_s[i] : ~len_s[i];
-      pos = len + (r - row_at[i]);
-      if (ok) {
-        const int held = (int)(((int64_t)len + ps - 1) >> shift), b = pos >> shift;
-        const int page = b < held ? m.block_tables[(int64_t)i * m.bt_stride + b] : listed(have - 1 - (take_at[i] + b - held));
-        if (in_pool(page)) slot = (page << shift) + (pos & (ps - 1));
+      pos[k] = len + (r - row_at[i]);
+      if (!ok) continue;
+      const int held = (int)(((int64_t)len + ps - 1) >> shift), b = pos[k] >> shift;
+      if (b != of) {
+        of = b;
+        page = b < held ? m.block_tables[(int64_t)i * m.bt_stride + b] : listed(have - 1 - (take_at[i] + b - held));
+        if (!in_pool(page)) page = -1;
       }
+      if (page >= 0) slot[k] = (page << shift) + (pos[k] & (ps - 1));
     }
-    m.positions[r] = pos;
-    m.slots[r] = slot;
+    if (a.vec && each == 4 && r0 + 4 <= m.max_rows) {
+      *reinterpret_cast<int4*>(m.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+      *reinterpret_cast<int4*>(m.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < each && r0 + k < m.max_rows) m.positions[r0 + k] = pos[k], m.slots[r0 + k] = slot[k];
+    }
   }
   for (int i = (int)gt; i <= n; i += (int)gn) {
     m.row_offsets[i] = row_at[i];
@@ -243,11 +268,12 @@ extern "C" int sar_page_map(const sar_page_map_args* args, void* stream) try {
                        m.row_offsets, m.positions, m.slots};
   for (const void* p : all)
     if (!sar::on4(p)) return set_error(SAR_ERR_INVALID_ARG, "page_map: array not aligned to its element");
-  sar::MapArgs a = {m, m.page_size == 16 ? 4 : m.page_size == 32 ? 5 : 6, nullptr};
+  sar::MapArgs a = {m, m.page_size == 16 ? 4 : m.page_size == 32 ? 5 : 6, 0, nullptr};
+  a.vec = ((reinterpret_cast<uintptr_t>(m.positions) | reinterpret_cast<uintptr_t>(m.slots)) & 15) == 0;
   SAR_TRY(sar::op_flags(&a.err));
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
-  const unsigned ctas = m.n + m.max_rows > 2 * sar::kMapThreads ? sar::kMapCtas : 1;
+  const unsigned ctas = m.max_rows > sar::kMapAlone ? sar::kMapCtas : 1;
   lc.gridDim = dim3(ctas);
   lc.blockDim = dim3(sar::kMapThreads);
   lc.dynamicSmemBytes = (size_t)(4 * m.n + 3) * 4;
