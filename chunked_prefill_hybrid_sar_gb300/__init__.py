@@ -403,6 +403,7 @@ def rmsnorm(x, gain, y, eps: float, stream=None) -> None:
 # microseconds: they read each attribute once and make no call into the library.
 
 _ROW_TYPES: dict = {}  # torch dtype -> SAR_TYPE_*, filled at the first call
+_INT32_TYPE = [None]   # torch.int32, likewise
 
 
 def _row_types() -> dict:
@@ -410,6 +411,7 @@ def _row_types() -> dict:
         import torch
         _ROW_TYPES.update({torch.float16: _lib.SAR_TYPE_F16, torch.bfloat16: _lib.SAR_TYPE_BF16,
                            torch.float32: _lib.SAR_TYPE_F32})
+        _INT32_TYPE[0] = torch.int32
     return _ROW_TYPES
 
 
@@ -649,6 +651,7 @@ class KV8Cache:
         self.device = k_codes.get_device()
         self.c = _lib.sar_kv8(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
                               *k_codes.shape)
+        self.ref = ctypes.byref(self.c)
 
     @classmethod
     def empty(cls, num_pages: int, n_kv_heads: int, page_size: int, head_dim: int, device="cuda") -> "KV8Cache":
@@ -660,8 +663,7 @@ class KV8Cache:
 
 
 def _int32(what: str, t, least: int, name: str) -> int:
-    import torch
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < least:
+    if t.dtype is not _INT32_TYPE[0] or not t.is_contiguous() or t.numel() < least:
         raise ValueError(f"{what}: {name} must be contiguous int32, {least} long at least")
     return t.data_ptr()
 
@@ -683,6 +685,7 @@ def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, 
     [rows] of the step's rows.  ``lens_out`` and ``free_count_out`` default to ``lens``
     and ``free_count``, in place; see ``sar_page_map``."""
     what, n = "page_map", lens.numel()
+    _row_types()
     lens_out = lens if lens_out is None else lens_out
     free_count_out = free_count if free_count_out is None else free_count_out
     stride = _tables(what, block_tables, n)
@@ -700,83 +703,90 @@ def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, 
     check(lib().sar_page_map(ctypes.byref(a), st))
 
 
+def _gain(t, head_dim: int) -> int:
+    import torch
+    if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != head_dim:
+        raise ValueError("qk_norm_rope: gains must be contiguous float32, one per dim of a head")
+    return t.data_ptr()
+
+
 def qk_norm_rope(q, k, q_out, head_dim: int, positions=None, v=None, k_out=None, cache: "KV8Cache | None" = None,
                  slots=None, q_gain=None, k_gain=None, eps: float = 1e-5, rope_base: float = 10000.0, stream=None) -> None:
     """q_out (and k_out) = the heads of the rows q [rows, heads * head_dim] (and k),
     normalised where there is a gain (fp32 [head_dim]) and rotated to ``positions``
     (int32 [rows]); with a ``cache``, k and v also go into it at ``slots`` (int32
     [rows], -1: not).  ``q`` and ``q_out`` may be None; see ``sar_qk_norm_rope``."""
-    import torch
     what = "qk_norm_rope"
     if q is None and k is None:
         raise ValueError("qk_norm_rope: neither queries nor keys")
-    a = _lib.sar_qk_rows()
-    a.head_dim = head_dim
-    rows, cols, ld, kind = _rows(what, k if q is None else q)
-    a.rows, a.type = rows, kind
-    for name, t, out in (("q", q, q_out), ("k", k, k_out), ("v", v, None)):
-        if t is None:
-            if out is not None:
-                raise ValueError(f"qk_norm_rope: {name}_out without {name}")
-            continue
-        n, cols, ld, t_kind = _rows(what, t)
-        if n != rows or t_kind != kind or cols % head_dim:
+    if (q_out is not None and q is None) or (k_out is not None and k is None):
+        raise ValueError("qk_norm_rope: output rows without theirs")
+    rows, width, ld, kind = _rows(what, k if q is None else q)
+    q_at = k_at = v_at = qo_at = ko_at = None
+    ldq = ldk = ldv = ldqo = ldko = heads = kv_heads = 0
+    if q is not None:
+        q_at, ldq, heads = q.data_ptr(), ld, width // head_dim
+        if width % head_dim:
+            raise ValueError("qk_norm_rope: rows must hold whole heads")
+    if k is not None:
+        n, cols, ldk, k_kind = (rows, width, ld, kind) if q is None else _rows(what, k)
+        if n != rows or k_kind != kind or cols % head_dim:
             raise ValueError("qk_norm_rope: q, k and v must have the same rows and type, and whole heads")
-        setattr(a, name, t.data_ptr())
-        setattr(a, "ld" + name, ld)
-        if name == "q":
-            a.n_q_heads = cols // head_dim
-        elif name == "k":
-            a.n_kv_heads = cols // head_dim
-        elif k is None or cols != k.shape[1]:
-            raise ValueError("qk_norm_rope: v must have k's heads")
-    a.out_type = kind if kind != _lib.SAR_TYPE_F32 else _lib.SAR_TYPE_BF16
-    for name, t, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        if t is None:
-            continue
-        n, cols, ld, a.out_type = _rows(what, t)
-        if (n, cols) != tuple(like.shape):
-            raise ValueError(f"qk_norm_rope: {name} must have its rows' shape")
-        setattr(a, name, t.data_ptr())
-        setattr(a, "ld" + name, ld)
-    if q_out is not None and k_out is not None and q_out.dtype != k_out.dtype:
-        raise ValueError("qk_norm_rope: q_out and k_out must have one type")
-    for name, t in (("q_gain", q_gain), ("k_gain", k_gain)):
-        if t is not None:
-            if t.dtype is not torch.float32 or not t.is_contiguous() or t.numel() != head_dim:
-                raise ValueError("qk_norm_rope: gains must be contiguous float32, one per dim of a head")
-            setattr(a, name, t.data_ptr())
+        k_at, kv_heads = k.data_ptr(), cols // head_dim
+    if v is not None:
+        n, v_cols, ldv, v_kind = _rows(what, v)
+        if k is None or n != rows or v_kind != kind or v_cols != cols:
+            raise ValueError("qk_norm_rope: v must have k's rows, type and heads")
+        v_at = v.data_ptr()
+    out_kind = kind if kind != _lib.SAR_TYPE_F32 else None
+    if q_out is not None:
+        n, o_cols, ldqo, out_kind = _rows(what, q_out)
+        if n != rows or o_cols != width:
+            raise ValueError("qk_norm_rope: q_out must have q's shape")
+        qo_at = q_out.data_ptr()
+    if k_out is not None:
+        n, o_cols, ldko, o_kind = _rows(what, k_out)
+        if n != rows or o_cols != cols or (q_out is not None and o_kind != out_kind):
+            raise ValueError("qk_norm_rope: k_out must have k's shape, and q_out's type")
+        ko_at, out_kind = k_out.data_ptr(), o_kind
+    if out_kind is None:
+        out_kind = _lib.SAR_TYPE_BF16  # (nothing is written in it)
+    gq = gk = pos_at = slots_at = None
+    if q_gain is not None:
+        gq = _gain(q_gain, head_dim)
+    if k_gain is not None:
+        gk = gq if k_gain is q_gain else _gain(k_gain, head_dim)
     if positions is not None:
-        a.positions = _int32(what, positions, rows, "positions")
+        pos_at = _int32(what, positions, rows, "positions")
+    handle = None
     if cache is not None:
         if slots is None or v is None or k is None:
             raise ValueError("qk_norm_rope: a cache needs k, v and slots")
-        a.slots = _int32(what, slots, rows, "slots")
-    a.eps, a.rope_base = eps, rope_base
+        if cache.device != k.get_device():
+            raise ValueError("qk_norm_rope: the cache is on another device")
+        slots_at, handle = _int32(what, slots, rows, "slots"), cache.ref
     st = _launch_stream(what, stream, q, k, v, q_out, k_out, q_gain, k_gain, positions, slots)
-    if cache is not None and cache.device != (k if q is None else q).get_device():
-        raise ValueError("qk_norm_rope: the cache is on another device")
-    check(lib().sar_qk_norm_rope(ctypes.byref(a), ctypes.byref(cache.c) if cache is not None else None, st))
+    a = _lib.sar_qk_rows(q_at, k_at, v_at, qo_at, ko_at, ldq, ldk, ldv, ldqo, ldko, gq, gk, pos_at, slots_at, rows, heads,
+                         kv_heads, head_dim, kind, out_kind, eps, rope_base)
+    rc = lib().sar_qk_norm_rope(ctypes.byref(a), handle, st)
+    if rc:
+        check(rc)
 
 
-def _kv8_batch(cache: KV8Cache, q, n: int, max_rows, max_len):
-    what = "kv8_attention"
-    rows, cols, ld, kind = _rows(what, q)
+def _kv8_rows(cache: KV8Cache, q):
+    rows, cols, ld, kind = _rows("kv8_attention", q)
     if kind == _lib.SAR_TYPE_F32 or cols % cache.head_dim:
         raise ValueError("kv8_attention: q must be float16 or bfloat16, with whole heads of the cache's head_dim")
-    b = _lib.sar_kv8_batch()
-    b.q, b.ldq, b.rows, b.n, b.n_q_heads = q.data_ptr(), ld, rows, n, cols // cache.head_dim
-    b.storage = kind
-    b.max_rows = max(1, rows) if max_rows is None else max_rows
-    b.max_len = 0 if max_len is None else max_len
-    return b
+    return rows, cols, ld, kind
 
 
 def kv8_attention_workspace(cache: KV8Cache, q, n: int, max_rows: int | None = None, max_len: int | None = None) -> int:
     """Bytes of workspace of ``kv8_attention`` for rows like ``q`` of ``n`` sequences."""
+    rows, cols, ld, kind = _kv8_rows(cache, q)
     out = ctypes.c_int64()
-    check(lib().sar_kv8_attention_workspace(ctypes.byref(_kv8_batch(cache, q, n, max_rows, max_len)),
-                                            ctypes.byref(cache.c), ctypes.byref(out)))
+    b = _lib.sar_kv8_batch(None, None, ld, ld, None, None, None, None, 0, rows, n, cols // cache.head_dim, 1, kind,
+                           max(1, rows) if max_rows is None else max_rows, max_len or 0, 0, 0.0)
+    check(lib().sar_kv8_attention_workspace(ctypes.byref(b), cache.ref, ctypes.byref(out)))
     return out.value
 
 
@@ -791,22 +801,20 @@ def kv8_attention(q, cache: KV8Cache, row_offsets, lens, block_tables, out, max_
     import torch
     what = "kv8_attention"
     n = lens.numel()
-    b = _kv8_batch(cache, q, n, max_rows, max_len)
-    rows, cols, b.ldo, kind = _rows(what, out)
-    if (rows, cols, kind) != (b.rows, q.shape[1], b.storage):
+    rows, cols, ld, kind = _kv8_rows(cache, q)
+    if out.shape != q.shape or out.dtype is not q.dtype:
         raise ValueError("kv8_attention: out must have q's shape and type")
-    b.out = out.data_ptr()
-    b.row_offsets = _int32(what, row_offsets, n + 1, "row_offsets")
-    b.lens = _int32(what, lens, n, "lens")
-    b.bt_stride = _tables(what, block_tables, n)
-    b.block_tables = block_tables.data_ptr()
-    b.window, b.scale = window, scale
-    st = _launch_stream(what, stream, q, out, row_offsets, lens, block_tables, workspace)
+    ldo = _rows(what, out)[2]
     if cache.device != q.get_device():
         raise ValueError("kv8_attention: the cache is on another device")
-    if workspace is None and b.rows and n:
+    b = _lib.sar_kv8_batch(q.data_ptr(), out.data_ptr(), ld, ldo, _int32(what, row_offsets, n + 1, "row_offsets"),
+                           _int32(what, lens, n, "lens"), block_tables.data_ptr(), None, 0, rows, n, cols // cache.head_dim,
+                           _tables(what, block_tables, n), kind, max(1, rows) if max_rows is None else max_rows, max_len or 0,
+                           window, scale)
+    st = _launch_stream(what, stream, q, out, row_offsets, lens, block_tables, workspace)
+    if workspace is None and rows and n:
         need = ctypes.c_int64()
-        check(lib().sar_kv8_attention_workspace(ctypes.byref(b), ctypes.byref(cache.c), ctypes.byref(need)))
+        check(lib().sar_kv8_attention_workspace(ctypes.byref(b), cache.ref, ctypes.byref(need)))
         # (allocated under the stream that it is used on, which the caching allocator ties it to)
         with contextlib.nullcontext() if stream is None else torch.cuda.stream(
                 torch.cuda.ExternalStream(st) if st else torch.cuda.default_stream()):
@@ -815,4 +823,6 @@ def kv8_attention(q, cache: KV8Cache, row_offsets, lens, block_tables, out, max_
         if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
             raise ValueError("kv8_attention: workspace must be contiguous uint8")
         b.workspace, b.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    check(lib().sar_kv8_attention(ctypes.byref(b), ctypes.byref(cache.c), st))
+    rc = lib().sar_kv8_attention(ctypes.byref(b), cache.ref, st)
+    if rc:
+        check(rc)

@@ -681,7 +681,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < nb && alive; ++j) {
-        if (!(alive = warp_wait(&bars->s_full[x], (mine_done + j) & 1, a.err))) break;
+        // (every lane polls: a broadcast costs the chain of a block's steps its latency)
+        alive = __all_sync(0xffffffffu, mbar_wait(smem_u32(&bars->s_full[x]), (mine_done + j) & 1, a.err, SITE_KV8_PIPE));
+        if (!alive) break;
         tc_fence_after();
         // (loops that are not unrolled: six roles' code contends for the instruction cache)
         const int key0 = (p.ja + j) * kKeys;
