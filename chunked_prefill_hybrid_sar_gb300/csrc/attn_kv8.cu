@@ -197,6 +197,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     here.s = dec_sequence(a, here.seq);
     count = here.s.blocks;
     if (here.kh == 0 && threadIdx.x == 0) check(here.seq);
+    pdl_launch_dependents();
     if (count == 0) return;
   } else {
     const int per = (a.n + kThreads - 1) / kThreads;
@@ -707,19 +708,25 @@ int check_batch(const sar_kv8_batch& b, const sar_kv8* c) {
   return SAR_OK;
 }
 
-// blocks: of the line at most, where the longest sequence is as long as the caller says.
+// blocks: of the line at most, where the longest sequence is as long as the caller says;
+// chunks: workspace of the sequences of several rows, null where there are none.
 template <typename T, int D>
-int launch_kv8(const DecArgs& d, int64_t blocks, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
+int launch_kv8(const DecArgs& d, int64_t blocks, void* chunks, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
+  const int storage = Elem<T>::kMmaFormat == 1 ? SAR_STORAGE_BF16 : SAR_STORAGE_F16;
   const int smem = 1024 + kDecWarps * kDecStages * 2 * kDecKeys * D;
   SAR_TRY(ensure_smem_attr(reinterpret_cast<const void*>(&kv8_decode_kernel<T, D>), smem, "kv8 decode: set smem attribute"));
   const int grid = d.units ? d.a.n * d.a.kvh : blocks >= (int64_t)d.resident * kDecMany ? kDecWaves * d.resident : d.resident;
   cudaError_t e = launch_pdl(kv8_decode_kernel<T, D>, dim3(grid), dim3(kDecWarps * 32), (size_t)smem, s, tmk, tmv, d);
   if (e != cudaSuccess) return cuda_error(e, "kv8 decode launch");
   count_launches(1);
-  if (d.units) return SAR_OK;
-  e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)d.a.G), dim3(kJoinWarps * 32), 0, s, d);
-  if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
-  count_launches(1);
+  // (the chunks' kernel comes before the joins, so that it can start beside this one)
+  if (chunks) SAR_TRY(launch_kv8_chunks(d.a, D, storage, chunks, s));
+  if (!d.units) {
+    e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)d.a.G), dim3(kJoinWarps * 32), 0, s, d);
+    if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
+    count_launches(1);
+  }
+  if (chunks) SAR_TRY(launch_kv8_chunk_join(d.a, D, storage, chunks, s));
   return SAR_OK;
 }
 
@@ -806,14 +813,13 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   SAR_TRY(sar::make_tmap_bytes(&tmv, cache->v_codes, map_rows, 128, box));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = b.storage == SAR_STORAGE_BF16;
+  void* chunks = b.max_rows == 1 || b.rows == 1 ? nullptr : ws + sp.chunks;
   int rc;
   if (cache->head_dim == 128)
-    rc = bf ? sar::launch_kv8<__nv_bfloat16, 128>(d, blocks, tmk, tmv, s) : sar::launch_kv8<__half, 128>(d, blocks, tmk, tmv, s);
+    rc = bf ? sar::launch_kv8<__nv_bfloat16, 128>(d, blocks, chunks, tmk, tmv, s) : sar::launch_kv8<__half, 128>(d, blocks, chunks, tmk, tmv, s);
   else
-    rc = bf ? sar::launch_kv8<__nv_bfloat16, 64>(d, blocks, tmk, tmv, s) : sar::launch_kv8<__half, 64>(d, blocks, tmk, tmv, s);
-  if (rc != SAR_OK) return rc;
-  if (b.max_rows == 1 || b.rows == 1) return SAR_OK;
-  return sar::launch_kv8_chunks(a, cache->head_dim, b.storage, ws + sp.chunks, s);
+    rc = bf ? sar::launch_kv8<__nv_bfloat16, 64>(d, blocks, chunks, tmk, tmv, s) : sar::launch_kv8<__half, 64>(d, blocks, chunks, tmk, tmv, s);
+  return rc;
 } catch (...) {
   return sar::entry_failed("kv8_attention");
 }

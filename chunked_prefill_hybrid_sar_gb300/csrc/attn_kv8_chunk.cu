@@ -75,7 +75,7 @@ struct ChunkArgs8 {
   ChunkPlan* plan;
   float* parts;      // [2 * SMs][256][D]
   float2* parts_ml;  // [2 * SMs][256]
-  int sms, vec_q, vec_o;
+  int sms, behind, vec_q, vec_o;
 };
 
 template <typename T, int D>
@@ -231,8 +231,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     bars->nan = 0;
     fence_mbar_init();
   }
-  pdl_wait();
+  // Launched right behind the single tokens' kernel, which has waited for what came
+  // before it when it lets this one start, and whose results this one does not read:
+  // only the last CTA waits for it, so that the kernels behind see both complete.
+  if (!args.behind) pdl_wait();
   pdl_launch_dependents();
+  const bool waits = args.behind && blockIdx.x == gridDim.x - 1;
 
   // ---- the plan: tiles of every sequence, then this CTA's stretch or unit ----
   auto block_sum = [&](int64_t v, int64_t& total) -> int64_t {  // exclusive
@@ -310,12 +314,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       }
     }
     __syncthreads();
-    if (all == 0 || blockIdx.x >= (unsigned)C) return;
+    if (all == 0 || blockIdx.x >= (unsigned)C) {
+      if (waits) pdl_wait();
+      return;
+    }
     b0 = line_at(all, blockIdx.x, C);
     b1 = line_at(all, blockIdx.x + 1, C);
   } else {
     if (blockIdx.x == 0 && threadIdx.x == 0) args.plan->all = 0;
-    if (blockIdx.x >= nt * a.kvh) return;
+    if (blockIdx.x >= nt * a.kvh) {
+      if (waits) pdl_wait();
+      return;
+    }
   }
 
   // A piece: blocks [ja, jb) of one unit.
@@ -866,6 +876,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     tc_fence_after();
     tmem_dealloc<false>(tmem, 512);
   }
+  if (waits) pdl_wait();
 }
 
 // Joins the pieces of units that several CTAs share, in their order: a CTA per 16
@@ -937,9 +948,14 @@ int launch_chunk8(const ChunkArgs8& c, const CUtensorMap& tmk, const CUtensorMap
   if (grid > INT32_MAX) return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: more than 2^31 units");
   cudaError_t e = launch_pdl(kv8_chunk_kernel<T, D>, dim3((unsigned)grid), dim3(kChunkThreads), (size_t)smem, s, tmk, tmv, c);
   if (e != cudaSuccess) return cuda_error(e, "kv8 chunk launch");
-  e = launch_pdl(kv8_chunk_join_kernel<T, D>, dim3((unsigned)std::min(grid * 16, (int64_t)8 * c.sms)), dim3(256), 0, s, c);
+  count_launches(1);
+  return SAR_OK;
+}
+template <typename T, int D>
+int launch_chunk_join(const ChunkArgs8& c, cudaStream_t s) {
+  const cudaError_t e = launch_pdl(kv8_chunk_join_kernel<T, D>, dim3((unsigned)(8 * c.sms)), dim3(256), 0, s, c);
   if (e != cudaSuccess) return cuda_error(e, "kv8 chunk join launch");
-  count_launches(2);
+  count_launches(1);
   return SAR_OK;
 }
 
@@ -952,7 +968,7 @@ int64_t kv8_chunk_space(int head_dim) {
   return up256(sizeof(ChunkPlan)) + up256(slots * 8) + slots * head_dim * 4;
 }
 
-int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s) {
+static ChunkArgs8 chunk_args(const Kv8Attn& a, void* space) {
   ChunkArgs8 c = {};
   c.a = a;
   c.sms = num_sms();
@@ -961,8 +977,14 @@ int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, 
   w += up256(sizeof(ChunkPlan));
   c.parts_ml = reinterpret_cast<float2*>(w);
   c.parts = reinterpret_cast<float*>(w + up256(2ll * c.sms * 256 * 8));
+  c.behind = 1;
   c.vec_q = aligned_to(a.q, 16) && a.ldq % 8 == 0;
   c.vec_o = aligned_to(a.out, 16) && a.ldo % 8 == 0;
+  return c;
+}
+
+int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s) {
+  const ChunkArgs8 c = chunk_args(a, space);
   // the codes as rows of head_dim bytes, a page to a box: K swizzled as the product reads it
   CUtensorMap k, v;
   const uint64_t map_rows = (uint64_t)a.num_pages * a.kvh << a.shift;
@@ -971,6 +993,13 @@ int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, 
   const bool bf = storage == SAR_STORAGE_BF16;
   if (head_dim == 128) return bf ? launch_chunk8<__nv_bfloat16, 128>(c, k, v, s) : launch_chunk8<__half, 128>(c, k, v, s);
   return bf ? launch_chunk8<__nv_bfloat16, 64>(c, k, v, s) : launch_chunk8<__half, 64>(c, k, v, s);
+}
+
+int launch_kv8_chunk_join(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s) {
+  const ChunkArgs8 c = chunk_args(a, space);
+  const bool bf = storage == SAR_STORAGE_BF16;
+  if (head_dim == 128) return bf ? launch_chunk_join<__nv_bfloat16, 128>(c, s) : launch_chunk_join<__half, 128>(c, s);
+  return bf ? launch_chunk_join<__nv_bfloat16, 64>(c, s) : launch_chunk_join<__half, 64>(c, s);
 }
 
 }  // namespace sar

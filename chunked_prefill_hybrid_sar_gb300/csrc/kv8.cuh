@@ -72,8 +72,10 @@ __device__ __forceinline__ bool kv8_sequence(const Kv8Attn& a, int i, int& row0,
          len <= (a.bt_stride << a.shift);
 }
 
-// Sequences of several rows (attn_kv8_chunk.cu), and the workspace that they take.
+// Sequences of several rows (attn_kv8_chunk.cu): the workspace that they take, their
+// kernel, launched right behind the single tokens', and the one that joins its pieces.
 int64_t kv8_chunk_space(int head_dim);
 int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s);
+int launch_kv8_chunk_join(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s);
 
 }  // namespace sar
