@@ -73,7 +73,7 @@ __device__ __forceinline__ int line_at(int all, int c, int C) { return (int)((in
 struct ChunkArgs8 {
   Kv8Attn a;
   ChunkPlan* plan;
-  float* parts;      // [2 * SMs][256][D]
+  float* parts;      // [2 * SMs][D / 4][256][4]
   float2* parts_ml;  // [2 * SMs][256]
   int sms, behind, vec_q, vec_o;
 };
@@ -159,6 +159,11 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ void sts_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
@@ -193,6 +198,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     kv8_chunk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ ChunkArgs8 args) {
   using M = ChunkSmem<T, D>;
+  constexpr int CHUNKS = D / 8, STEP_ROWS = 32 / CHUNKS;  // 16-byte chunks of a 16-bit row; rows of a warp's step over them
   constexpr int PASS = kConvWarps * 32 * 16 / D;  // keys of a pass of the converting warps, 16 bytes to a thread
   constexpr int STEP_PASSES = 64 / PASS;
   const Kv8Attn& a = args.a;
@@ -632,6 +638,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int token = (int)(pair / (unsigned)a.G), head = p.kh * a.G + (int)(pair % (unsigned)a.G);
       const int pos = valid ? p.len - p.rows + token : -1;  // keys (pos - window, pos] are seen
       const int lo = a.window > 0 ? pos - a.window + 1 : 0;
+      // 16-byte chunk c of a row of the queries' parts, a part's chunks after another's
+      auto q_at = [&](int row, int c) -> uint32_t {
+        const int k = c % (D / 16);
+        return q_reg(x) + (uint32_t)(c / (D / 16) * M::kPart + row * D + ((D == 128 ? k ^ (row & 7) : k ^ (row >> 1 & 3)) << 4));
+      };
       float fac = a.scale;
       {
         // the query as sums of e4m3 numbers, swizzled as the product reads them
@@ -833,35 +844,55 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         __syncwarp();
         const int64_t slot = 2 * (int64_t)blockIdx.x + (pieces == 0 ? 0 : 1);
         // (a row that sees keys and has no sum is NaN)
-        const float inv = p.whole ? (pos < 0 ? 0.f : 1.f / l) : 1.f;
+        const float inv = pos < 0 ? 0.f : 1.f / l;
         if (!p.whole) args.parts_ml[slot * 256 + x * 128 + r] = make_float2(m_used, l);
+        // (A row's 16-bit results leave through the place of its own queries' first two parts,
+        // so that rows are written whole; other warps may be at the next piece already. Partial
+        // results lie dims first, rows next to one another.)
+        const int64_t to = (int64_t)(p.row0 + token) * a.ldo + (int64_t)head * D;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
           float o[16];
           tmem_ld16(ocol + c, *reinterpret_cast<uint32_t(*)[16]>(o));
           tmem_wait_ld();
           const uint32_t bits = (c < 32 ? nan[0] : c < 64 ? nan[1] : c < 96 ? nan[D / 32 - 2] : nan[D / 32 - 1]) >> (c & 31);
+          if (bits & 0xffff) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = bits >> e & 1 ? NAN : o[e] * inv;
-          if (p.whole) {
-            if (valid) {
-              T* op = static_cast<T*>(a.out) + (int64_t)(p.row0 + token) * a.ldo + (int64_t)head * D + c;
-              if (args.vec_o) {
-#pragma unroll
-                for (int e = 0; e < 16; e += 8)
-                  *reinterpret_cast<uint4*>(op + e) =
-                      make_uint4(Elem<T>::pack(o[e], o[e + 1]), Elem<T>::pack(o[e + 2], o[e + 3]),
-                                 Elem<T>::pack(o[e + 4], o[e + 5]), Elem<T>::pack(o[e + 6], o[e + 7]));
-              } else {
-#pragma unroll
-                for (int e = 0; e < 16; ++e) op[e] = Elem<T>::from(o[e]);
-              }
-            }
-          } else if (nb > 0) {
-            float4* pp = reinterpret_cast<float4*>(args.parts + (slot * 256 + x * 128 + r) * D + c);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pp[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 16; ++e)
+              if (bits >> e & 1) o[e] = NAN;
           }
+          if (!p.whole) {
+            if (nb > 0) {
+              float4* pp = reinterpret_cast<float4*>(args.parts) + (slot * (D / 4) + c / 4) * 256 + x * 128 + r;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) pp[e * 256] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            }
+            continue;
+          }
+          uint32_t h[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) h[e] = Elem<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+          sts_u4(q_at(r, c >> 3), h[0], h[1], h[2], h[3]);
+          sts_u4(q_at(r, c >> 3 | 1), h[4], h[5], h[6], h[7]);
+        }
+        if (p.whole) {
+          __syncwarp();
+#pragma unroll 1
+          for (int i = 0; i < CHUNKS; ++i) {
+            const int row = i * STEP_ROWS + lane / CHUNKS, ch = lane % CHUNKS;
+            const int64_t of = __shfl_sync(0xffffffffu, to, row);
+            const uint4 v = lds_u4(q_at(qq * 32 + row, ch));
+            if (x * 128 + qq * 32 + row >= p.t.pairs) continue;
+            T* op = static_cast<T*>(a.out) + of + 8 * ch;
+            if (args.vec_o) {
+              *reinterpret_cast<uint4*>(op) = v;
+            } else {
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+              for (int e = 0; e < 8; ++e) reinterpret_cast<unsigned short*>(op)[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+            }
+          }
+          __syncwarp();
         }
       }
       base += p.jb - p.ja;
@@ -902,7 +933,7 @@ __global__ void __launch_bounds__(256) kv8_chunk_join_kernel(const __grid_consta
     kv8_sequence(a, plan.seq[t], row0, rows, len);
     const Tile tl = tile_of(a, rows, len, plan.u[t]);
     for (int k = threadIdx.x; k < 16 * (D / 4); k += 256) {
-      const int r = sub * 16 + k / (D / 4), dim = k % (D / 4) * 4;
+      const int r = sub * 16 + k % 16, dim = k / 16 * 4;
       if (r >= tl.pairs) continue;
       const unsigned pair = (unsigned)(tl.pair0 + r);
       const int token = (int)(pair / (unsigned)a.G), head = kh * a.G + (int)(pair % (unsigned)a.G);
@@ -915,7 +946,7 @@ __global__ void __launch_bounds__(256) kv8_chunk_join_kernel(const __grid_consta
           L += ml.y;  // (zero, or NaN)
           continue;
         }
-        const float4 v = *reinterpret_cast<const float4*>(args.parts + (slot * 256 + r) * D + dim);
+        const float4 v = reinterpret_cast<const float4*>(args.parts)[(slot * (D / 4) + dim / 4) * 256 + r];
         const float mn = fmaxf(Mx, ml.x);
         const float f = Mx == -INFINITY ? 0.f : exp2_fast(Mx - mn), g = exp2_fast(ml.x - mn);
         L = fmaf(ml.y, g, L * f);
