@@ -9,7 +9,7 @@
 // fill the machine.  The plan is three prefix sums' worth of arithmetic on the
 // lengths, formed by every CTA itself.
 //
-// Inside a CTA six warps take the stretch's blocks in turn, each with a ring of
+// Inside a CTA four warps take the stretch's blocks in turn, each with a ring of
 // blocks of its own, filled by TMA with the 128-byte swizzle across unit ends, so
 // the stream does not stop where a unit does.  Keys are the rows of the products:
 // S^T = K Q^T has 16 keys x 8 heads a tile and O^T = V^T P^T 16 dims x 8 heads, so a
@@ -224,8 +224,16 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
     const int64_t excl = incl - mine;
     const int64_t all = total * a.kvh;
     const DecLine line = DecLine::of(all, d.resident, gridDim.x);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *d.line = line;
-    if (all == 0 || blockIdx.x >= line.ctas) return;
+    // (a CTA counts its blocks in 32 bits: 2^36 keys)
+    const bool fits = all <= (int64_t)line.first * 0x7fffff00;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      *d.line = line;
+      if (!fits) {
+        d.line->all = 0;  // nothing to join
+        report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SEQUENCE, -1);
+      }
+    }
+    if (all == 0 || !fits || blockIdx.x >= line.ctas) return;
     // (with more CTAs than places the joining kernel's would take the ones that get free)
     if (line.ctas == line.first) pdl_launch_dependents();
     const int64_t b0 = line.at(blockIdx.x), b1 = line.at(blockIdx.x + 1);
@@ -242,10 +250,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       first_s[1] = at * a.kvh;
     }
     __syncthreads();
-    if (b1 - b0 > 0x7fffff00) {  // (2^36 keys to a CTA)
-      if (threadIdx.x == 0) report(a.err, SAR_ERR_BOUNDS, SITE_KV8_SEQUENCE, -1);
-      return;
-    }
     count = (int)(b1 - b0);
     here.seq = (int)first_s[0];
     here.s = dec_sequence(a, here.seq);
@@ -760,7 +764,8 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   const int64_t width = (int64_t)b.n_q_heads * cache->head_dim;
   if (b.ldq < width || b.ldo < width || b.bt_stride < 1)
     return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: rows shorter than their heads, or no block table");
-  if ((int64_t)b.bt_stride * cache->page_size > INT32_MAX)
+  // (256: the blocks looked up ahead of a sequence's end)
+  if ((int64_t)b.bt_stride * cache->page_size > INT32_MAX - 256)
     return set_error(SAR_ERR_UNSUPPORTED, "kv8_attention: block tables above 2^31 tokens");
   if (!aligned_to(b.q, 2) || !aligned_to(b.out, 2) || !aligned_to(b.row_offsets, 4) || !aligned_to(b.lens, 4) ||
       !aligned_to(b.block_tables, 4) || !aligned_to(b.workspace, 16))

@@ -14,7 +14,7 @@
 // K is multiplied in e4m3 as it lies in the cache (a conversion took the place of the
 // tensor cores as what bounds this kernel).  A query is then a sum of e4m3 numbers:
 // scaled by a power of two so that its row's largest lies in [128, 256), two parts of
-// four significant bits hold bf16's eight, three fp16's eleven, exactly down to 2^-10;
+// four significant bits hold bf16's eight, three fp16's eleven, off by 2^-10 at most;
 // e4m3 products run at twice the rate, so two parts cost what one fp16 product does.
 // Page scales act as in the single-token kernel: with raw scores S and
 // t = S k_scale scale + log2(v_scale), 2^(t - m) weighs V's codes and its sum takes it
@@ -75,7 +75,7 @@ struct ChunkArgs8 {
   ChunkPlan* plan;
   float* parts;      // [2 * SMs][D / 4][256][4]
   float2* parts_ml;  // [2 * SMs][256]
-  int sms, behind, vec_q, vec_o;
+  int sms, vec_q, vec_o;
 };
 
 template <typename T, int D>
@@ -240,9 +240,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // Launched right behind the single tokens' kernel, which has waited for what came
   // before it when it lets this one start, and whose results this one does not read:
   // only the last CTA waits for it, so that the kernels behind see both complete.
-  if (!args.behind) pdl_wait();
   pdl_launch_dependents();
-  const bool waits = args.behind && blockIdx.x == gridDim.x - 1;
+  const bool waits = blockIdx.x == gridDim.x - 1;
 
   // ---- the plan: tiles of every sequence, then this CTA's stretch or unit ----
   auto block_sum = [&](int64_t v, int64_t& total) -> int64_t {  // exclusive
@@ -1008,7 +1007,6 @@ static ChunkArgs8 chunk_args(const Kv8Attn& a, void* space) {
   w += up256(sizeof(ChunkPlan));
   c.parts_ml = reinterpret_cast<float2*>(w);
   c.parts = reinterpret_cast<float*>(w + up256(2ll * c.sms * 256 * 8));
-  c.behind = 1;
   c.vec_q = aligned_to(a.q, 16) && a.ldq % 8 == 0;
   c.vec_o = aligned_to(a.out, 16) && a.ldo % 8 == 0;
   return c;

@@ -247,7 +247,8 @@ int sar_page_map(const sar_page_map_args* args, void* stream);
  * Rows are `type` (SAR_TYPE_*), row r at q + r * ldq elements; q_out and k_out have
  * the 16-bit type `out_type`, which is `type` where that is 16 bits.  n_kv_heads of k
  * and v.  q may be NULL (no query heads).  16-bit rows may be written over (q_out is q,
- * of the same stride; without a cache k_out is k), else outputs overlap nothing.  16-byte aligned rows are faster.  Async on `stream`. */
+ * of the same stride; without a cache k_out is k), else outputs overlap nothing.  16-byte
+ * aligned rows are faster.  Async on `stream`. */
 typedef struct sar_qk_rows {
   const void* q;
   const void* k;
@@ -271,14 +272,15 @@ int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream
  *   out = sum_k softmax_k(scale * q . K_k) V_k
  * with query head h reading KV head h / (n_q_heads / n_kv_heads).  A row that sees
  * nothing (p < 0) is zero; keys that it does not see do not touch it, whatever they
- * hold.  Single tokens and chunks may stand side by side in a call.  Products of
- * codes and queries are exact in the tensor cores (codes turn to fp16 without
- * rounding), probabilities are rounded to fp16.
+ * hold.  Single tokens and chunks may stand side by side in a call.  Codes are
+ * multiplied as they are, sums are fp32; a query's elements are off by 2^-17 of the
+ * largest of their row and head at most, probabilities are rounded to fp16.
  * Rows are 16-bit, row r at q + r * ldq elements, heads of head_dim adjacent; out
  * likewise.  max_rows bounds a sequence's rows (1: single tokens alone); max_len
  * (0: unknown) is about the longest length and only guides how work is shared
  * out.  scale 0 is 1 / sqrt(head_dim).  A cache's scales are positive and lie
- * within [2^-40, 2^60].  At most 8 query heads per KV head; at most 2^27 rows and 2^30 sequences.
+ * within [2^-40, 2^60].  At most 8 query heads per KV head, 2^27 rows, 2^30 sequences and block
+ * tables of 2^31 - 257 tokens.  q and out do not overlap.
  * The workspace (device, 16-byte aligned, sar_kv8_attention_workspace() bytes; it
  * holds nothing between calls) belongs to one call at a time.
  * Sequences whose offsets are out of range or fall, whose rows pass max_rows or

@@ -3,7 +3,8 @@
 Tolerance: the output's rounding (half a step), and of the weighted mean of |V|:
 weights rounded to fp16 (2^-11); scores of D <= 128 products added up in fp32 (D
 2^-23 of their magnitudes' sum, about sqrt(D) here: under 2^-12.5, in numerator and
-sum alike); exponentials and factors (2^-20).  Together below 2^-10.  A weight
+sum alike); a query's elements off by 2^-17 of its largest (D of them of either sign
+add up to about sqrt(D), times a scale of 1 / sqrt(D): under 2^-14); exponentials and factors (2^-20).  Together below 2^-10.  A weight
 under fp16's smallest normal number is off by 2^-25 of the largest: times the keys,
 2^-25 n of the largest |V| of the row's keys.
 """
@@ -310,3 +311,94 @@ def test_python_refusals():
         sar.kv8_attention(**good, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
     empty = good["q"][:0]
     sar.kv8_attention(empty, good["cache"], good["row_offsets"][:1], good["lens"][:0], good["block_tables"], empty)
+
+
+@pytest.mark.parametrize("seqs,heads,kv_heads,d", [
+    ([(2 + i % 4, 20 + i) for i in range(270)], 4, 2, 64),                   # more sequences than a call shares out
+    ([(400, 500)] + [(2 + i % 5, 100 + i) for i in range(74)], 32, 8, 64),   # four units and more to an SM
+    ([(3, 60 + i % 50) if i % 3 else (1, 200) for i in range(150)], 56, 8, 128),
+])
+def test_many_chunks(seqs, heads, kv_heads, d):
+    Batch(seqs, heads, kv_heads, d, 16, "bf16", seed=len(seqs)).check(extra=1)
+    sar.op_sync_status()
+
+
+def on_device(heads, kv_heads, d, page, pages, seqs, seed, room=0):
+    """Sequences over the last pages of a pool that is filled there, and on the device their float64 attention."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    need = [-(-m // page) for _, m in seqs]
+    first = room
+    order = first + torch.randperm(pages, generator=g, device="cuda")
+    codes = [torch.empty(first + pages, kv_heads, page, d, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scales = [torch.full((first + pages, kv_heads), 2.0 ** -6, device="cuda") for _ in range(2)]
+    for c in codes:
+        for at in range(first, first + pages, 512):  # (a piece at a time)
+            part = c[at:at + 512]
+            x = torch.randn(part.shape, generator=g, device="cuda") * 60
+            part.copy_(x.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8))
+    tables = torch.full((len(seqs), max(need)), -1, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, n in enumerate(need):
+        tables[i, :n] = order[at:at + n].int()
+        at += n
+    rows = [r for r, _ in seqs]
+    off = torch.tensor([0] + list(np.cumsum(rows)), dtype=torch.int32, device="cuda")
+    lens = torch.tensor([m for _, m in seqs], dtype=torch.int32, device="cuda")
+    # (large queries: a few keys decide, wherever they lie)
+    q = (3.0 * torch.randn(sum(rows), heads * d, generator=g, device="cuda")).half()
+    table = torch.tensor(kv8.E4M3, device="cuda")
+
+    def want(i):
+        a, b, m = int(off[i]), int(off[i + 1]), seqs[i][1]
+        p = tables[i, :need[i]].long()
+        k, v = (table[c[p].long()].mul_(2.0 ** -6).transpose(1, 2).reshape(-1, kv_heads, d)[:m] for c in codes)
+        x = q[a:b].double().view(b - a, kv_heads, heads // kv_heads, d)
+        s = torch.einsum("rhgd,khd->rhgk", x, k) * d ** -0.5
+        pos = torch.arange(m - (b - a), m, device="cuda")
+        s.masked_fill_(torch.arange(m, device="cuda")[None, None, None] > pos[:, None, None, None], float("-inf"))
+        w = torch.softmax(s, -1)
+        far = v.abs().max() * m * 2.0 ** -25
+        out, mean = (torch.einsum("rhgk,khd->rhgd", w, u).reshape(b - a, -1) for u in (v, v.abs()))
+        return slice(a, b), out, 2.0 ** -11 * out.abs() + 2.0 ** -10 * mean + far
+
+    return q, sar.KV8Cache(*codes, *scales), off, lens, tables, want
+
+
+def test_more_keys_than_one_wave_of_stretches():
+    """Single tokens over so many keys that the line's end is shared out a second time."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    seqs = [(1, sms * 1100 - 1111 * i) for i in range(12)]  # over 3 * 256 * 32 keys to an SM, in two heads
+    assert sum(m for _, m in seqs) * 2 // 32 > 3 * sms * 256
+    q, cache, off, lens, tables, want = on_device(4, 2, 64, 64, sum(-(-m // 64) for _, m in seqs), seqs, 1)
+    out = torch.empty_like(q)
+    sar.kv8_attention(q, cache, off, lens, tables, out, max_rows=1)
+    for i in range(len(seqs)):
+        rows, w, tol = want(i)
+        assert bool(((out[rows].double() - w).abs() <= tol).all()), i
+    # and cut by hints, into fewer stretches, and with a window
+    for kw in (dict(max_len=1000), dict(max_len=10 ** 8)):
+        again = torch.empty_like(q)
+        sar.kv8_attention(q, cache, off, lens, tables, again, max_rows=1, **kw)
+        assert bool(((again[rows].double() - w).abs() <= tol).all())
+    sar.op_sync_status()
+
+
+def test_codes_beyond_four_gigabytes():
+    """Pages whose codes lie more than 2^32 bytes into the cache: appended to, and read by both kernels."""
+    heads, kv_heads, d, page = 8, 4, 128, 64
+    room = 2 ** 32 // (kv_heads * d * page) + 5
+    seqs = [(1, 1000), (70, 333), (1, 64), (2, 129)]
+    q, cache, off, lens, tables, want = on_device(heads, kv_heads, d, page, 30, seqs, 2, room=room)
+    out = torch.empty_like(q)
+    sar.kv8_attention(q, cache, off, lens, tables, out)
+    for i in range(len(seqs)):
+        rows, w, tol = want(i)
+        assert bool(((out[rows].double() - w).abs() <= tol).all()), i
+    # a key of 2^-6 * 64 in the last page's last place: code 2^6, of a scale that stays
+    k = torch.ones(1, kv_heads * d, dtype=torch.float16, device="cuda")
+    slot = (room + 30) * page - 1
+    sar.qk_norm_rope(None, k, None, head_dim=d, v=k, cache=cache, slots=torch.tensor([slot], dtype=torch.int32, device="cuda"))
+    one = torch.tensor([64.0]).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    for codes, scales in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
+        assert bool((codes[-1, :, -1] == one).all()) and bool((scales[-1] == 2.0 ** -6).all())
+    sar.op_sync_status()
