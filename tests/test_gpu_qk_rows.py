@@ -244,3 +244,43 @@ def test_python_refusals():
             sar.qk_norm_rope(None, k, None, head_dim=128, **(dict(v=v, cache=cache, slots=slots) | kw))
     with pytest.raises(sar.SarError):
         sar.qk_norm_rope(q, None, torch.empty_like(q).bfloat16(), head_dim=128)
+
+
+@pytest.mark.parametrize("kind,d,page", [("bf16", 128, 64), ("f32", 64, 16), ("f16", 128, 16), ("f32", 128, 32)])
+def test_many_rows_are_as_few_at_a_time(kind, d, page):
+    """So many rows that a CTA takes several heads: equal to the same rows in calls of a page each."""
+    heads, kv_heads, pages = 24, 8, 7000 // page
+    g = torch.Generator().manual_seed(page + d)
+    order = torch.randperm(pages, generator=g).tolist()
+    parts, at = [], 0  # runs of slots: whole pages, their ends, single tokens, rows that are not cached
+    for p in order:
+        first = 0 if at % 3 else int(torch.randint(0, page, (1,), generator=g))
+        last = page if at % 4 else first + 1
+        parts.append([p * page + o for o in range(first, last)])
+        if at % 50 == 7:
+            parts.append([-1] * 3)
+        at += 1
+    slots = torch.tensor(sum(parts, []), dtype=torch.int32, device="cuda")
+    rows = slots.numel()
+    x = torch.randn(rows, (heads + 2 * kv_heads) * d, generator=g).to(TYPES[kind]).cuda()
+    pos = torch.randint(0, 200000, (rows,), generator=g, dtype=torch.int32).cuda()
+    gain = (torch.rand(d, generator=g) + 0.5).cuda()
+    out_type = torch.bfloat16 if kind == "f32" else TYPES[kind]
+
+    def run(cuts):
+        cache = sar.KV8Cache.empty(pages, kv_heads, page, d)
+        for s in (cache.k_scales, cache.v_scales):
+            s.fill_(2.0 ** -8)
+        q_out = torch.zeros(rows, heads * d, dtype=out_type, device="cuda")
+        k_out = torch.zeros(rows, kv_heads * d, dtype=out_type, device="cuda")
+        for a, b in zip(cuts, cuts[1:]):
+            q, k, v = x[a:b].split([heads * d, kv_heads * d, kv_heads * d], 1)
+            sar.qk_norm_rope(q, k, q_out[a:b], d, positions=pos[a:b], v=v, k_out=k_out[a:b], cache=cache, slots=slots[a:b],
+                             q_gain=gain, k_gain=gain)
+        return q_out, k_out, cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales
+
+    whole = run([0, rows])
+    for got, want in zip(whole, run(np.cumsum([0] + [len(p) for p in parts]).tolist())):
+        assert torch.equal(got, want)
+    assert bool((whole[2] != 0).any()) and bool((whole[0] != 0).any(-1).all())
+    sar.op_sync_status()
