@@ -34,20 +34,8 @@ namespace {
 constexpr int kDecWarps = 4;
 constexpr int kDecKeys = 32;    // keys of a block
 constexpr int kDecStages = 2;   // blocks of a warp's ring
-constexpr int kDecHeads = 8;    // query heads of a KV head: the products' columns
 constexpr int kDecPerSm = 3;
-constexpr int kDecLeast = 8;    // blocks of a CTA's stretch at least, where there are so few
-constexpr int kDecWaves = 2;    // CTAs to a place on an SM, where there are
-constexpr int kDecMany = 256;   // so many blocks to a place
 constexpr int kDecUnit = 32;    // blocks of the longest sequence up to which a CTA takes a unit
-
-// Where a CTA's stretch begins inside a unit: that unit (seq < 0: it does not).
-struct DecStart {
-  int64_t u0;      // the unit's first block on the line
-  int32_t blocks;  // of the unit
-  int32_t seq, kh, row;
-};
-struct DecLine;
 
 struct DecArgs {
   Kv8Attn a;
@@ -64,11 +52,6 @@ __device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr));
-}
-__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
 }
 // The transpose of an 8 x 8 matrix of 16-bit elements, a row's pair to a lane.
 __device__ __forceinline__ uint32_t transposed(uint32_t x) {
@@ -94,18 +77,6 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// 2^x by the SFU (relative error 2^-22; 2^-inf = 0): a weight that is rounded to
-// fp16 next.
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // A sequence of one row, as the decode kernel sees it.
 struct DecSeq {
   int row, len, lo;  // its row, its length, the oldest key it sees
@@ -119,35 +90,6 @@ __device__ __forceinline__ DecSeq dec_sequence(const Kv8Attn& a, int i) {
   s.blocks = ok && rows == 1 ? max(1, (s.len + kDecKeys - 1) / kDecKeys - s.lo / kDecKeys) : 0;
   return s;
 }
-
-// How the line is cut.  SMs are not equally near to the memory that their keys lie in:
-// of 304 CTAs with equal stretches the last ended 25% after the median.  So the
-// resident CTAs take equal shares of the line's first 7/8, and twice as many more
-// share the rest, each started as a place on an SM gets free.
-struct DecLine {
-  int64_t all, head;  // blocks; those of the first CTAs
-  int32_t first, ctas;
-  __device__ __forceinline__ static int64_t quotient(int64_t x, int64_t y) {
-    // (64-bit divisions are long; these are made before anything is loaded)
-    return x >> 32 == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
-  }
-  __device__ __forceinline__ static DecLine of(int64_t all, int resident, int grid) {
-    DecLine l;
-    l.all = all;
-    const bool many = all >= (int64_t)resident * kDecMany && grid >= kDecWaves * resident;
-    l.first = many ? resident : (int)max((int64_t)1, min((int64_t)min(resident, grid), all / kDecLeast));
-    l.ctas = many ? kDecWaves * resident : l.first;
-    l.head = many ? all - all / 8 : all;
-    return l;
-  }
-  // CTA c's first block, and the CTA that has block b
-  __device__ __forceinline__ int64_t at(int c) const {
-    return c <= first ? quotient(head * c, first) : head + quotient((all - head) * (c - first), ctas - first);
-  }
-  __device__ __forceinline__ int cta(int64_t b) const {
-    return (int)(b < head ? quotient((b + 1) * first - 1, head) : first + quotient((b - head + 1) * (ctas - first) - 1, all - head));
-  }
-};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
@@ -613,78 +555,6 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
   }
 }
 
-// Joins a unit that several CTAs share: block (c, h) head h of the unit that CTA c + 1
-// begins inside of, if no CTA before does.  A warp takes every eighth piece, the
-// loads of four under way together; then the warps' sums are joined in their order.
-constexpr int kJoinWarps = 8;
-template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ DecArgs d) {
-  constexpr int E = D / 32;  // dims of a lane
-  const Kv8Attn& a = d.a;
-  __shared__ float acc_s[kJoinWarps][D];
-  __shared__ float2 ml_s[kJoinWarps];
-  pdl_wait();
-  pdl_launch_dependents();
-  const DecLine line = *d.line;
-  const int first = blockIdx.x, second = first + 1;
-  if (line.all == 0 || second >= line.ctas) return;
-  const DecStart u = d.starts[second];
-  if (u.seq < 0) return;
-  const int64_t begins = line.at(first);  // the CTA before's first block
-  if (begins > u.u0) return;
-  const int last = line.cta(u.u0 + u.blocks - 1);
-  const int head = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the first CTA's piece is its last one, unless the unit begins with it
-  auto slot = [&](int c) { return (int64_t)(2 * c + (c == first && begins != u.u0 ? 1 : 0)) * kDecHeads + head; };
-  float M = -INFINITY, L = 0.f, A[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) A[e] = 0.f;
-  for (int c0 = first + warp; c0 <= last; c0 += 4 * kJoinWarps) {
-    float2 ml[4];
-    float v[4][E];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k * kJoinWarps;
-      const int64_t s = slot(min(c, last));
-      ml[k] = c <= last ? d.parts_ml[s] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = d.parts[s * D + e * 32 + lane];
-    }
-    const float mn = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
-    const float f = M == -INFINITY ? 0.f : exp2_fast(M - mn);
-    L *= f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) A[e] *= f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const bool some = ml[k].x != -INFINITY;
-      const float w = some ? exp2_fast(ml[k].x - mn) : 0.f;
-      L = fmaf(ml[k].y, w, L);
-#pragma unroll
-      for (int e = 0; e < E; ++e) A[e] = fmaf(some ? v[k][e] : 0.f, w, A[e]);
-    }
-    M = mn;
-  }
-  if (lane == 0) ml_s[warp] = make_float2(M, L);
-#pragma unroll
-  for (int e = 0; e < E; ++e) acc_s[warp][e * 32 + lane] = A[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float Mx = -INFINITY, Lx = 0.f, Ax = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) Mx = fmaxf(Mx, ml_s[w].x);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = ml_s[w].x == -INFINITY ? 0.f : exp2_fast(ml_s[w].x - Mx);
-      Lx = fmaf(ml_s[w].y, f, Lx);
-      Ax = fmaf(acc_s[w][threadIdx.x], f, Ax);
-    }
-    static_cast<T*>(a.out)[(int64_t)u.row * a.ldo + (int64_t)(u.kh * a.G + head) * D + threadIdx.x] = Elem<T>::from(Ax / Lx);
-  }
-}
-
-int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
-
 // The workspace: the line, where stretches begin, pieces' maxima and sums, pieces; then the chunks'.
 struct Space {
   int64_t starts, ml, parts, chunks, bytes;
@@ -724,13 +594,11 @@ int launch_kv8(const DecArgs& d, int64_t blocks, void* chunks, const CUtensorMap
   if (e != cudaSuccess) return cuda_error(e, "kv8 decode launch");
   count_launches(1);
   // (the chunks' kernel comes before the joins, so that it can start beside this one)
-  if (chunks) SAR_TRY(launch_kv8_chunks(d.a, D, storage, chunks, s));
-  if (!d.units) {
-    e = launch_pdl(kv8_join_kernel<T, D>, dim3((unsigned)(grid - 1), (unsigned)d.a.G), dim3(kJoinWarps * 32), 0, s, d);
-    if (e != cudaSuccess) return cuda_error(e, "kv8 join launch");
-    count_launches(1);
-  }
-  if (chunks) SAR_TRY(launch_kv8_chunk_join(d.a, D, storage, chunks, s));
+  // one kernel joins what either leaves in pieces
+  Kv8Pieces p = {};
+  if (!d.units) p.line = d.line, p.starts = d.starts, p.parts = d.parts, p.parts_ml = d.parts_ml;
+  if (chunks) SAR_TRY(launch_kv8_chunks(d.a, D, storage, chunks, &p, s));
+  if (!d.units || chunks) SAR_TRY(launch_kv8_join(d.a, D, storage, p, grid, s));
   return SAR_OK;
 }
 

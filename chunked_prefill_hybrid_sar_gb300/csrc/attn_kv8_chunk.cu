@@ -45,7 +45,6 @@ constexpr int kScaleRing = 4;             // blocks whose scales are kept: three
 constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log2 and inverse of the value scales, a flag
 constexpr int kRawSteps = 3;              // steps of 64 keys of V whose codes are under way
 constexpr int kMostK = 3;                 // K stages
-constexpr int kMostTiles = 256;          // of a call whose CTAs take stretches
 constexpr int kLeastBlocks = 4;          // of a stretch
 constexpr float kGrowth = 8.f;           // log2 of a maximum's growth that O tolerates
 constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its last 64 columns
@@ -60,15 +59,6 @@ struct ChunkBars {
   int nan;                    // a NaN code of V came by
   uint32_t read[kScaleRing];  // runs of a block whose V was read
 };
-
-// The plan, in the workspace, for the joining kernel.
-struct ChunkPlan {
-  int32_t all;    // blocks on the line; 0: nothing to join
-  int32_t ctas, tiles;
-  int32_t seq[kMostTiles], u[kMostTiles], before[kMostTiles + 1];
-};
-// CTA c of C has blocks [line(c), line(c + 1)) of the line.
-__device__ __forceinline__ int line_at(int all, int c, int C) { return (int)((int64_t)all * c / C); }
 
 struct ChunkArgs8 {
   Kv8Attn a;
@@ -129,15 +119,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* e
   return ok != 0;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
   uint64_t r;
@@ -158,11 +139,6 @@ __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-__device__ __forceinline__ uint4 lds_u4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
 }
 __device__ __forceinline__ void sts_u4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -293,10 +269,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   int b0 = 0, b1 = 1;
   if (stretches) {
     int blocks = 0;
+    int row0 = 0, rows = 0, len = 0;
+    Tile tl = {};
     if (threadIdx.x < nt) {
-      int r0, rows, len;
-      kv8_sequence(a, t_seq[threadIdx.x], r0, rows, len);
-      const Tile tl = tile_of(a, rows, len, t_u[threadIdx.x]);
+      kv8_sequence(a, t_seq[threadIdx.x], row0, rows, len);
+      tl = tile_of(a, rows, len, t_u[threadIdx.x]);
       blocks = tl.j1 - tl.j0;
     }
     const int64_t at = block_sum(blocks, all64);
@@ -304,15 +281,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (threadIdx.x < nt) {
       before[threadIdx.x] = (int)at;
       if (blockIdx.x == 0) {
-        args.plan->seq[threadIdx.x] = t_seq[threadIdx.x];
-        args.plan->u[threadIdx.x] = t_u[threadIdx.x];
-        args.plan->before[threadIdx.x] = (int)at;
+        args.plan->tile[threadIdx.x] = {(int)at, row0, len - rows, tl.pair0, tl.pairs};
       }
     }
     if (threadIdx.x == 0) {
       before[nt] = (int)all64;
       if (blockIdx.x == 0) {
-        args.plan->before[nt] = (int)all64;
+        args.plan->tile[nt].before = (int)all64;
         args.plan->all = all;
         args.plan->ctas = C;
         args.plan->tiles = (int)nt;
@@ -909,64 +884,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   if (waits) pdl_wait();
 }
 
-// Joins the pieces of units that several CTAs share, in their order: a CTA per 16
-// pairs of a unit.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) kv8_chunk_join_kernel(const __grid_constant__ ChunkArgs8 args) {
-  const Kv8Attn& a = args.a;
-  pdl_wait();
-  pdl_launch_dependents();
-  const ChunkPlan& plan = *args.plan;
-  const int all = plan.all, C = plan.ctas;
-  if (all == 0) return;
-  const int work = plan.tiles * a.kvh * 16;
-  for (int w = blockIdx.x; w < work; w += gridDim.x) {
-    const int sub = w & 15, unit = w >> 4, t = (int)((unsigned)unit / (unsigned)a.kvh), kh = unit - t * a.kvh;
-    const int nb = plan.before[t + 1] - plan.before[t];
-    const int u0 = plan.before[t] * a.kvh + kh * nb, u1 = u0 + nb;
-    // the CTAs of its first and last block
-    const int c0 = (int)(((int64_t)(u0 + 1) * C - 1) / all), c1 = (int)(((int64_t)u1 * C - 1) / all);
-    if (c0 == c1) continue;
-    const bool starts = line_at(all, c0, C) == u0;
-    int row0, rows, len;
-    kv8_sequence(a, plan.seq[t], row0, rows, len);
-    const Tile tl = tile_of(a, rows, len, plan.u[t]);
-    for (int k = threadIdx.x; k < 16 * (D / 4); k += 256) {
-      const int r = sub * 16 + k % 16, dim = k / 16 * 4;
-      if (r >= tl.pairs) continue;
-      const unsigned pair = (unsigned)(tl.pair0 + r);
-      const int token = (int)(pair / (unsigned)a.G), head = kh * a.G + (int)(pair % (unsigned)a.G);
-      float Mx = -INFINITY, L = 0.f;
-      float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int c = c0; c <= c1; ++c) {
-        const int64_t slot = 2 * c + (c == c0 && !starts ? 1 : 0);
-        const float2 ml = args.parts_ml[slot * 256 + r];
-        if (ml.x == -INFINITY) {
-          L += ml.y;  // (zero, or NaN)
-          continue;
-        }
-        const float4 v = reinterpret_cast<const float4*>(args.parts)[(slot * (D / 4) + dim / 4) * 256 + r];
-        const float mn = fmaxf(Mx, ml.x);
-        const float f = Mx == -INFINITY ? 0.f : exp2_fast(Mx - mn), g = exp2_fast(ml.x - mn);
-        L = fmaf(ml.y, g, L * f);
-        A.x = fmaf(v.x, g, A.x * f);
-        A.y = fmaf(v.y, g, A.y * f);
-        A.z = fmaf(v.z, g, A.z * f);
-        A.w = fmaf(v.w, g, A.w * f);
-        Mx = mn;
-      }
-      const float inv = len - rows + token < 0 ? 0.f : 1.f / L;
-      T* op = static_cast<T*>(a.out) + (int64_t)(row0 + token) * a.ldo + (int64_t)head * D + dim;
-      if (args.vec_o) {
-        *reinterpret_cast<uint2*>(op) = make_uint2(Elem<T>::pack(A.x * inv, A.y * inv), Elem<T>::pack(A.z * inv, A.w * inv));
-      } else {
-        op[0] = Elem<T>::from(A.x * inv), op[1] = Elem<T>::from(A.y * inv);
-        op[2] = Elem<T>::from(A.z * inv), op[3] = Elem<T>::from(A.w * inv);
-      }
-    }
-  }
-}
-
 template <typename T, int D>
 int launch_chunk8(const ChunkArgs8& c, const CUtensorMap& tmk, const CUtensorMap& tmv, cudaStream_t s) {
   const int smem = ChunkSmem<T, D>::kBytes;
@@ -981,16 +898,6 @@ int launch_chunk8(const ChunkArgs8& c, const CUtensorMap& tmk, const CUtensorMap
   count_launches(1);
   return SAR_OK;
 }
-template <typename T, int D>
-int launch_chunk_join(const ChunkArgs8& c, cudaStream_t s) {
-  const cudaError_t e = launch_pdl(kv8_chunk_join_kernel<T, D>, dim3((unsigned)(8 * c.sms)), dim3(256), 0, s, c);
-  if (e != cudaSuccess) return cuda_error(e, "kv8 chunk join launch");
-  count_launches(1);
-  return SAR_OK;
-}
-
-int64_t up256(int64_t x) { return (x + 255) & ~int64_t(255); }
-
 }  // namespace
 
 int64_t kv8_chunk_space(int head_dim) {
@@ -1012,8 +919,11 @@ static ChunkArgs8 chunk_args(const Kv8Attn& a, void* space) {
   return c;
 }
 
-int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s) {
+int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, Kv8Pieces* p, cudaStream_t s) {
   const ChunkArgs8 c = chunk_args(a, space);
+  p->plan = c.plan;
+  p->chunk_parts = c.parts;
+  p->chunk_parts_ml = c.parts_ml;
   // the codes as rows of head_dim bytes, a page to a box: K swizzled as the product reads it
   CUtensorMap k, v;
   const uint64_t map_rows = (uint64_t)a.num_pages * a.kvh << a.shift;
@@ -1022,13 +932,6 @@ int launch_kv8_chunks(const Kv8Attn& a, int head_dim, int storage, void* space, 
   const bool bf = storage == SAR_STORAGE_BF16;
   if (head_dim == 128) return bf ? launch_chunk8<__nv_bfloat16, 128>(c, k, v, s) : launch_chunk8<__half, 128>(c, k, v, s);
   return bf ? launch_chunk8<__nv_bfloat16, 64>(c, k, v, s) : launch_chunk8<__half, 64>(c, k, v, s);
-}
-
-int launch_kv8_chunk_join(const Kv8Attn& a, int head_dim, int storage, void* space, cudaStream_t s) {
-  const ChunkArgs8 c = chunk_args(a, space);
-  const bool bf = storage == SAR_STORAGE_BF16;
-  if (head_dim == 128) return bf ? launch_chunk_join<__nv_bfloat16, 128>(c, s) : launch_chunk_join<__half, 128>(c, s);
-  return bf ? launch_chunk_join<__nv_bfloat16, 64>(c, s) : launch_chunk_join<__half, 64>(c, s);
 }
 
 }  // namespace sar
