@@ -10,8 +10,15 @@
 // Query heads are independent.  For the cache the unit is a run: the rows of a call
 // in one page, which share a scale for each head.  A CTA takes the runs that begin
 // in its window of rows (they may end up to 63 rows behind it), keeps their rows'
-// keys or values in registers, joins the rows' largest magnitudes in shared
-// memory, and writes codes: the input is read once.
+// keys or values in registers, joins the rows' largest magnitudes by a shared-memory
+// maximum per run (whose order does not matter), and writes codes: the input is read once.
+//
+// Rows of queries are bound by memory (12288 x 56 heads of 128, bf16: 61 us, where a copy of
+// them takes 53), the cache's part by its instructions, about 200 to 32 lanes' rows (8 + 8
+// heads: 39 us; 45 where every row of a run searched the maxima of the others).
+// Both in one launch: 93 us on consecutive inputs, 98 on inputs that are not in L2, against
+// 63 for the bytes.  Their CTAs in turn instead of the cache's first: 98 too; a window's
+// tasks side by side: 105, as the longest then come last as well.
 #include <math.h>
 
 #include <algorithm>
@@ -179,12 +186,13 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_con
   // ---- keys or values of some KV heads, of the runs that begin in this window ----
   __shared__ int slot_s[SPAN];
   __shared__ uint32_t flag_s[(SPAN + 31) / 32];  // rows that do not go on from the row before
-  __shared__ float amax_s[SPAN];
+  __shared__ uint32_t amax_s[3][GROUPS];  // a run's largest magnitude (its bits, which order as it does), three heads in turn
   extern __shared__ __align__(16) float angle_s[];  // [SPAN][LANES][8], where a CTA has several heads
   const bool is_k = task < a.kv_tasks / 2;
   const int kh0 = (is_k ? task : task - a.kv_tasks / 2) * a.kv_heads_per, kh1 = min(kh0 + a.kv_heads_per, r.n_kv_heads);
   const int ps = a.c.page_size;
   const int64_t n_slots = (int64_t)a.c.num_pages * ps;
+  for (int i = threadIdx.x; i < 3 * GROUPS; i += kQkThreads) amax_s[0][i] = 0;
   int begins = 0;
   if (threadIdx.x < (SPAN + 31) / 32 * 32) {
     const int i = threadIdx.x, row = w0 + i;
@@ -216,32 +224,26 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_con
     const int s = (w << 5) + 31 - __clz(m);
     return s < GROUPS ? s : -1;
   };
-  auto run_end = [&](int i) -> int {  // the first flagged row behind i
-    int j = i + 1;
-    if (j >= SPAN) return SPAN;
-    int w = j >> 5;
-    uint32_t m = flag_s[w] & (0xffffffffu << (j & 31));
-    while (m == 0 && w < (SPAN + 31) / 32 - 1) m = flag_s[++w];
-    return m == 0 ? SPAN : min(SPAN, (w << 5) + __ffs(m) - 1);
-  };
-
   const int64_t ld = is_k ? r.ldk : r.ldv;
   const TI* src = static_cast<const TI*>(is_k ? r.k : r.v) + w0 * ld + 4 * l;
   const bool vec = is_k ? a.vec_k : a.vec_v;
   float* scales = is_k ? a.c.k_scales : a.c.v_scales;
   uint8_t* codes = static_cast<uint8_t*>(is_k ? a.c.k_codes : a.c.v_codes);
-  int run[PASSES], end[PASSES];
+  int run[PASSES];
+  bool one[PASSES];  // all rows of this warp are of one run
 #pragma unroll
   for (int p = 0; p < PASSES; ++p) {
     run[p] = run_of(p * GROUPS + grp);
-    end[p] = run[p] >= 0 ? run_end(p * GROUPS + grp) : 0;
+    one[p] = __all_sync(0xffffffffu, run[p] == __shfl_sync(0xffffffffu, run[p], 0));
     // all of this CTA's heads of the row come to L2
     constexpr int LINES = D * (int)sizeof(TI) / 128;
     for (int k = l; run[p] >= 0 && k < (kh1 - kh0) * LINES; k += LANES)
       prefetch_l2(reinterpret_cast<const char*>(src - 4 * l + (p * GROUPS + grp) * ld + kh0 * D) + k * 128);
   }
+  int turn = 0;
 #pragma unroll 1
   for (int kh = kh0; kh < kh1; ++kh) {
+    uint32_t* now = amax_s[turn];
     float x[PASSES][8], old[PASSES];
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
@@ -286,20 +288,20 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_con
 #pragma unroll
     for (int p = 0; p < PASSES; ++p) {
       if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
-      float m = 0.f;
+      auto largest = [&]() -> uint32_t {
+        float m = fabsf(x[p][0]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[p][e]));  // (passes over NaN)
-      m = group_max<LANES>(m);
-      if (__any_sync(0xffffffffu, m == INFINITY)) {  // infinities become NaN, and count for nothing
-        m = 0.f;
+        for (int e = 1; e < 7; e += 2) m = fmaxf(fmaxf(m, fabsf(x[p][e])), fabsf(x[p][e + 1]));  // (passes over NaN)
+        m = fmaxf(fmaxf(m, fabsf(x[p][7])), 0.f);
+        return one[p] ? __reduce_max_sync(0xffffffffu, __float_as_uint(m)) : __float_as_uint(group_max<LANES>(m));
+      };
+      uint32_t m = largest();
+      if (__any_sync(0xffffffffu, m == 0x7f800000u)) {  // infinities become NaN, and count for nothing
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[p][e] = fabsf(x[p][e]) < INFINITY ? x[p][e] : NAN;
-          m = fmaxf(m, fabsf(x[p][e]));
-        }
-        m = group_max<LANES>(m);
+        for (int e = 0; e < 8; ++e) x[p][e] = fabsf(x[p][e]) < INFINITY ? x[p][e] : NAN;
+        m = largest();
       }
-      if (l == 0) amax_s[p * GROUPS + grp] = m;
+      if (one[p] ? (threadIdx.x & 31) == 0 : l == 0 && run[p] >= 0) atomicMax(&now[run[p]], m);
     }
     __syncthreads();
 #pragma unroll
@@ -307,12 +309,8 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_con
       if (!__any_sync(0xffffffffu, run[p] >= 0)) continue;
       const int i = p * GROUPS + grp;
       const bool live = run[p] >= 0;
-      float m = 0.f;
-      if (live)
-        for (int j = run[p] + l; j < end[p]; j += LANES) m = fmaxf(m, amax_s[j]);
-      m = group_max<LANES>(m);
       if (!live) continue;
-      const float scale = fmaxf(kv8_scale(m), old[p]);
+      const float scale = fmaxf(kv8_scale(__uint_as_float(now[run[p]])), old[p]);
       const int slot = slot_s[i];
       const int64_t unit = (int64_t)(slot >> a.shift) * a.c.n_kv_heads + kh;
       uint8_t* page = codes + unit * ps * D;
@@ -339,7 +337,9 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_con
         }
       }
     }
-    __syncthreads();  // (the largest magnitudes are written again)
+    // (a barrier lies between this and the head that writes there, as between the last reads and this)
+    if (threadIdx.x < GROUPS) amax_s[turn == 0 ? 2 : turn - 1][threadIdx.x] = 0;
+    turn = turn == 2 ? 0 : turn + 1;
   }
 }
 
