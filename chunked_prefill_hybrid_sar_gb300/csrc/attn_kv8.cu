@@ -177,8 +177,7 @@ __global__ void __launch_bounds__(kDecWarps * 32, kDecPerSm)
       }
     }
     if (all == 0 || !fits || blockIdx.x >= line.ctas) return;
-    // (with more CTAs than places the joining kernel's would take the ones that get free)
-    if (line.ctas == line.first) pdl_launch_dependents();
+    pdl_launch_dependents();
     const int64_t b0 = line.at(blockIdx.x), b1 = line.at(blockIdx.x + 1);
     if (b0 >= excl * a.kvh && b0 < incl * a.kvh) {
       int64_t at = excl;

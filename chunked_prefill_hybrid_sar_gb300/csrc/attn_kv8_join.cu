@@ -13,46 +13,48 @@ namespace {
 constexpr int kJoinWarps = 8;
 constexpr int kJoinRows = 16;  // (row, head) pairs of a chunk's unit that a CTA joins
 
-// Head `head` of the single tokens' unit that CTA first + 1 begins inside of, if no CTA
-// before does.  A warp takes every eighth piece, the loads of four under way
-// together; then the warps' sums are joined in their order.
+// The single tokens' unit that CTA first + 1 begins inside of, if no CTA before does: a
+// warp to a head, the loads of eight pieces under way together.
 template <typename T, int D>
-__device__ __forceinline__ void join_tokens(const Kv8Attn& a, const Kv8Pieces& p, int first, int head) {
-  constexpr int E = D / 32;  // dims of a lane
-  __shared__ float acc_s[kJoinWarps][D];
-  __shared__ float2 ml_s[kJoinWarps];
+__device__ __forceinline__ void join_tokens(const Kv8Attn& a, const Kv8Pieces& p, int first) {
+  constexpr int E = D / 32, AT_ONCE = 8;  // dims of a lane
+  const int head = threadIdx.x >> 5, lane = threadIdx.x & 31, second = first + 1;
   const DecLine line = *p.line;
-  const int second = first + 1;
-  if (line.all == 0 || second >= line.ctas) return;
   const DecStart u = p.starts[second];
-  if (u.seq < 0) return;
+  if (head >= a.G || line.all == 0 || second >= line.ctas || u.seq < 0) return;
   const int64_t begins = line.at(first);  // the CTA before's first block
   if (begins > u.u0) return;
   const int last = line.cta(u.u0 + u.blocks - 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the first CTA's piece is its last one, unless the unit begins with it
   auto slot = [&](int c) { return (int64_t)(2 * c + (c == first && begins != u.u0 ? 1 : 0)) * kDecHeads + head; };
   float M = -INFINITY, L = 0.f, A[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) A[e] = 0.f;
-  for (int c0 = first + warp; c0 <= last; c0 += 4 * kJoinWarps) {
-    float2 ml[4];
-    float v[4][E];
+  for (int c0 = first; c0 <= last; c0 += AT_ONCE) {
+    float2 ml[AT_ONCE];
+    float v[AT_ONCE][E];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int c = c0 + k * kJoinWarps;
-      const int64_t s = slot(min(c, last));
-      ml[k] = c <= last ? p.parts_ml[s] : make_float2(-INFINITY, 0.f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] = p.parts[s * D + e * 32 + lane];
+    for (int k = 0; k < AT_ONCE; ++k) {
+      const int64_t s = slot(min(c0 + k, last));
+      ml[k] = c0 + k <= last ? p.parts_ml[s] : make_float2(-INFINITY, 0.f);
+      const float* row = p.parts + s * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(row);
+        v[k][0] = x.x, v[k][1] = x.y, v[k][2] = x.z, v[k][3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(row);
+        v[k][0] = x.x, v[k][1] = x.y;
+      }
     }
-    const float mn = fmaxf(fmaxf(fmaxf(M, ml[0].x), fmaxf(ml[1].x, ml[2].x)), ml[3].x);
+    float mn = M;
+#pragma unroll
+    for (int k = 0; k < AT_ONCE; ++k) mn = fmaxf(mn, ml[k].x);
     const float f = M == -INFINITY ? 0.f : exp2_fast(M - mn);
     L *= f;
 #pragma unroll
     for (int e = 0; e < E; ++e) A[e] *= f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < AT_ONCE; ++k) {
       const bool some = ml[k].x != -INFINITY;
       const float w = some ? exp2_fast(ml[k].x - mn) : 0.f;
       L = fmaf(ml[k].y, w, L);
@@ -61,21 +63,15 @@ __device__ __forceinline__ void join_tokens(const Kv8Attn& a, const Kv8Pieces& p
     }
     M = mn;
   }
-  if (lane == 0) ml_s[warp] = make_float2(M, L);
+  const float inv = 1.f / L;
+  T* op = static_cast<T*>(a.out) + (int64_t)u.row * a.ldo + (int64_t)(u.kh * a.G + head) * D + lane * E;
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc_s[warp][e * 32 + lane] = A[e];
-  __syncthreads();
-  if (threadIdx.x < D) {
-    float Mx = -INFINITY, Lx = 0.f, Ax = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) Mx = fmaxf(Mx, ml_s[w].x);
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      const float f = ml_s[w].x == -INFINITY ? 0.f : exp2_fast(ml_s[w].x - Mx);
-      Lx = fmaf(ml_s[w].y, f, Lx);
-      Ax = fmaf(acc_s[w][threadIdx.x], f, Ax);
+  for (int e = 0; e < E; e += 2) {
+    if (p.vec_o) {
+      *reinterpret_cast<uint32_t*>(op + e) = Elem<T>::pack(A[e] * inv, A[e + 1] * inv);
+    } else {
+      op[e] = Elem<T>::from(A[e] * inv), op[e + 1] = Elem<T>::from(A[e + 1] * inv);
     }
-    static_cast<T*>(a.out)[(int64_t)u.row * a.ldo + (int64_t)(u.kh * a.G + head) * D + threadIdx.x] = Elem<T>::from(Ax / Lx);
   }
 }
 
@@ -152,15 +148,14 @@ __device__ __forceinline__ void join_chunk(const Kv8Attn& a, const Kv8Pieces& p,
   }
 }
 
-// The first dec_blocks CTAs: a CTA's unit and a head each; the others share the chunks' units.
+// The first dec_blocks CTAs: a single token's unit each; the others share the chunks' units.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_constant__ Kv8Attn a,
                                                                    const __grid_constant__ Kv8Pieces p) {
   pdl_wait();
   pdl_launch_dependents();
   if ((int)blockIdx.x < p.dec_blocks) {
-    const int first = (int)blockIdx.x / a.G;
-    join_tokens<T, D>(a, p, first, (int)blockIdx.x - first * a.G);
+    join_tokens<T, D>(a, p, blockIdx.x);
     return;
   }
   const int all = p.plan->all, C = p.plan->ctas;
@@ -182,7 +177,7 @@ int launch_join(const Kv8Attn& a, const Kv8Pieces& p, cudaStream_t s) {
 
 int launch_kv8_join(const Kv8Attn& a, int head_dim, int storage, const Kv8Pieces& pieces, int dec_ctas, cudaStream_t s) {
   Kv8Pieces p = pieces;
-  p.dec_blocks = p.line ? (dec_ctas - 1) * a.G : 0;
+  p.dec_blocks = p.line ? dec_ctas - 1 : 0;
   p.vec_o = aligned_to(a.out, 8) && a.ldo % 4 == 0;
   const bool bf = storage == SAR_STORAGE_BF16;
   if (head_dim == 128) return bf ? launch_join<__nv_bfloat16, 128>(a, p, s) : launch_join<__half, 128>(a, p, s);
