@@ -46,6 +46,7 @@ constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log
 constexpr int kRawSteps = 3;              // steps of 64 keys of V whose codes are under way
 constexpr int kMostK = 3;                 // K stages
 constexpr int kLeastBlocks = 4;          // of a stretch
+constexpr int kPieceBlocks = 12;         // a CTA's second piece takes as long as so many blocks more
 constexpr float kGrowth = 8.f;           // log2 of a maximum's growth that O tolerates
 constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its last 64 columns
 constexpr uint32_t kColsO = 256;         // O_x at 256 + x * 128
@@ -190,7 +191,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   int32_t* t_seq = before + kMostTiles + 1;
   int32_t* t_u = t_seq + kMostTiles;
   __shared__ int64_t sums[kChunkThreads / 32];
-  __shared__ int first_s[2];
+  __shared__ int first_s[2], most_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(smem_u32(&bars->q_ready), kSoftWarps);
     mbar_init(smem_u32(&bars->mma_done), 1);
     bars->nan = 0;
+    most_s = 0;
     fence_mbar_init();
   }
   // Launched right behind the single tokens' kernel, which has waited for what came
@@ -275,9 +277,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       kv8_sequence(a, t_seq[threadIdx.x], row0, rows, len);
       tl = tile_of(a, rows, len, t_u[threadIdx.x]);
       blocks = tl.j1 - tl.j0;
+      atomicMax(&most_s, blocks);
     }
     const int64_t at = block_sum(blocks, all64);
-    const int all = (int)(all64 * a.kvh), C = max(1, min(min(args.sms, (int)gridDim.x), all / kLeastBlocks));
+    const int all = (int)(all64 * a.kvh), units = (int)nt * a.kvh, most = most_s;
+    int C = max(1, min(args.sms, all / kLeastBlocks));
+    // A CTA with an equal stretch has two pieces mostly.  Where units are alike (within a
+    // quarter), the same number of CTAs to each, and so one piece to a CTA, ends sooner
+    // although some SMs stay idle: 512 rows 2048 deep 73 -> 58 us, 256 rows 16384 deep
+    // 115 -> 104; three chunks of 33 to 100 rows 3000 to 1000 deep would take 54 for 49.
+    int each = 0;
+    if (units > 0 && units <= args.sms && (int64_t)most * units <= all + all / 4) {
+      each = min(args.sms / units, max(1, most / kLeastBlocks));
+      if (most / each > all / C + kPieceBlocks) each = 0;
+    }
+    if (each > 0) C = each * units;
     if (threadIdx.x < nt) {
       before[threadIdx.x] = (int)at;
       if (blockIdx.x == 0) {
@@ -289,6 +303,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (blockIdx.x == 0) {
         args.plan->tile[nt].before = (int)all64;
         args.plan->all = all;
+        args.plan->each = each;
         args.plan->ctas = C;
         args.plan->tiles = (int)nt;
       }
@@ -298,8 +313,20 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (waits) pdl_wait();
       return;
     }
-    b0 = line_at(all, blockIdx.x, C);
-    b1 = line_at(all, blockIdx.x + 1, C);
+    if (each > 0) {
+      const int unit = (int)(blockIdx.x / (unsigned)each), part = (int)blockIdx.x - unit * each;
+      const int t = (int)((unsigned)unit / (unsigned)a.kvh), kh = unit - t * a.kvh;
+      const int nb = before[t + 1] - before[t], u0 = before[t] * a.kvh + kh * nb, parts = min(each, nb);
+      if (part >= parts) {
+        if (waits) pdl_wait();
+        return;
+      }
+      b0 = u0 + line_at(nb, part, parts);
+      b1 = u0 + line_at(nb, part + 1, parts);
+    } else {
+      b0 = line_at(all, blockIdx.x, C);
+      b1 = line_at(all, blockIdx.x + 1, C);
+    }
   } else {
     if (blockIdx.x == 0 && threadIdx.x == 0) args.plan->all = 0;
     if (blockIdx.x >= nt * a.kvh) {

@@ -77,7 +77,7 @@ __device__ __forceinline__ void join_tokens(const Kv8Attn& a, const Kv8Pieces& p
 
 // 16 pairs of a unit of a chunk; a thread has four dims of a pair, or two times four.
 template <typename T, int D>
-__device__ __forceinline__ void join_chunk(const Kv8Attn& a, const Kv8Pieces& p, int64_t all, int C, int item) {
+__device__ __forceinline__ void join_chunk(const Kv8Attn& a, const Kv8Pieces& p, int64_t all, int each, int C, int item) {
   constexpr int E = kJoinRows * D / 4 / (kJoinWarps * 32), AT_ONCE = 4 / E;
   static_assert(E == 1 || E == 2, "elements of a thread");
   const int sub = item % (256 / kJoinRows), unit = item / (256 / kJoinRows);
@@ -86,10 +86,11 @@ __device__ __forceinline__ void join_chunk(const Kv8Attn& a, const Kv8Pieces& p,
   const int nb = p.plan->tile[t + 1].before - tile.before;
   const int64_t u0 = (int64_t)tile.before * a.kvh + (int64_t)kh * nb, u1 = u0 + nb;
   // the CTAs of its first and last block
-  const int c0 = (int)DecLine::quotient((u0 + 1) * C - 1, all), c1 = (int)DecLine::quotient(u1 * C - 1, all);
+  const int c0 = each ? unit * each : (int)DecLine::quotient((u0 + 1) * C - 1, all);
+  const int c1 = each ? c0 + min(each, nb) - 1 : (int)DecLine::quotient(u1 * C - 1, all);
   const int r = sub * kJoinRows + threadIdx.x % kJoinRows;
   if (c0 == c1 || r >= tile.pairs) return;
-  const bool starts = line_at((int)all, c0, C) == u0;
+  const bool starts = each || line_at((int)all, c0, C) == u0;
   const float4* parts = reinterpret_cast<const float4*>(p.chunk_parts) + (int64_t)(threadIdx.x / kJoinRows) * 256 + r;
   float Mx = -INFINITY, L = 0.f;
   float4 A[E];
@@ -158,10 +159,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) kv8_join_kernel(const __grid_
     join_tokens<T, D>(a, p, blockIdx.x);
     return;
   }
-  const int all = p.plan->all, C = p.plan->ctas;
+  const int all = p.plan->all, each = p.plan->each, C = p.plan->ctas;
   if (all == 0) return;
   const int items = p.plan->tiles * a.kvh * (256 / kJoinRows);
-  for (int w = blockIdx.x - p.dec_blocks; w < items; w += gridDim.x - p.dec_blocks) join_chunk<T, D>(a, p, all, C, w);
+  for (int w = blockIdx.x - p.dec_blocks; w < items; w += gridDim.x - p.dec_blocks) join_chunk<T, D>(a, p, all, each, C, w);
 }
 
 template <typename T, int D>

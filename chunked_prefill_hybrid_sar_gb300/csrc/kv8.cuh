@@ -136,14 +136,15 @@ constexpr int kMostTiles = 256;  // of a call whose CTAs take stretches
 
 // The plan, in the workspace, for the joining kernel: tiles of 256 (row, head) pairs.
 struct ChunkPlan {
-  int32_t all;  // blocks on the line; 0: nothing to join
+  int32_t all;   // blocks on the line; 0: nothing to join
+  int32_t each;  // CTAs to a unit; 0: equal stretches of the line, of ctas CTAs
   int32_t ctas, tiles;
   struct {
     int32_t before;  // blocks of the tiles before, of a KV head
     int32_t row0, past, pair0, pairs;  // the sequence's first row, its tokens before that; the tile's pairs
   } tile[kMostTiles + 1];
 };
-// CTA c of C has blocks [line(c), line(c + 1)) of the line.
+// CTA c of C has blocks [line(c), line(c + 1)) of the line, or of the unit of each = C.
 __device__ __forceinline__ int line_at(int all, int c, int C) { return (int)((int64_t)all * c / C); }
 
 // What the joining kernel takes (attn_kv8_join.cu): single tokens' pieces, where line is

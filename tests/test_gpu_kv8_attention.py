@@ -402,3 +402,14 @@ def test_codes_beyond_four_gigabytes():
     for codes, scales in ((cache.k_codes, cache.k_scales), (cache.v_codes, cache.v_scales)):
         assert bool((codes[-1, :, -1] == one).all()) and bool((scales[-1] == 2.0 ** -6).all())
     sar.op_sync_status()
+
+
+@pytest.mark.parametrize("seqs,window", [
+    ([(64, 2000)], 0), ([(50, 1500)] * 3 + [(1, 300)], 0), ([(3, 700)] * 20, 256), ([(130, 130)], 0), ([(2, 5000)], 0),
+    ([(40, 1200), (40, 400), (40, 30)], 0), ([(9, 640)] * 90, 0),
+])
+@pytest.mark.parametrize("kind", list(TYPES))
+def test_units_alike_and_not(seqs, window, kind):
+    """Chunks whose units get the same number of CTAs each, and some of very different lengths."""
+    Batch(seqs, 8, 2, 128, 32, kind, seed=len(seqs)).check(window=window)
+    sar.op_sync_status()
