@@ -1,6 +1,8 @@
 // Attention of single tokens over the 8-bit paged cache.
 //
-// Bound by the cache's bytes: 2 D of them per key and KV head, for 4 D G flops.
+// Bound by the cache's bytes: 2 D of them per key and KV head, for 4 D G flops.  128
+// sequences of up to 8192 keys (1.09 GB): 173 us with the join, 6.3 TB/s (170 without it);
+// four of up to 131072: 116.6 us, 5.8 TB/s; one of 500 keys: 10.3 us, latencies.
 //
 // All (sequence, KV head) units' keys, in blocks of 32, form one line, of which every
 // CTA takes a stretch, whatever the lengths.  Where a stretch begins or ends
@@ -15,9 +17,9 @@
 // S^T = K Q^T has 16 keys x 8 heads a tile and O^T = V^T P^T 16 dims x 8 heads, so a
 // group of up to eight heads wastes half as much as it would as the rows.  Codes
 // turn to fp16 in registers, exactly, on their way into the products (an e4m3 mma.sync
-// does the same, and with the queries too, at every use: 139 us against 127 for four
-// contexts of up to 131072); the order of the dims inside a step is free, and taken so that a lane's 16
-// bytes of a key are its operands.  V's bytes are transposed by ldmatrix over pairs of dims.
+// does the same, and with the queries too, at every use: 139 us against 127 when it was
+// tried); the order of the dims inside a step is free, and taken so that a lane's 16 bytes
+// of a key are its operands.  V's bytes are transposed by ldmatrix over pairs of dims.
 //
 // Scales cost nothing: with t = S k_scale scale + log2(v_scale) in base 2 and m the
 // running maximum of t, 2^(t - m) weighs V's codes, and the sum takes it times
@@ -35,8 +37,12 @@ constexpr int kDecWarps = 4;
 constexpr int kDecKeys = 32;    // keys of a block
 constexpr int kDecStages = 2;   // blocks of a warp's ring
 constexpr int kDecPerSm = 3;
-constexpr int kDecUnit = 32;    // blocks of the longest sequence up to which a CTA takes a unit,
-constexpr int kDecUnitBeside = 8;  // and where chunks, whose CTAs take whole SMs, wait for the last (42.4 -> 39.3 us)
+// A CTA takes a unit where the longest sequence has few blocks (six requests of up to 300
+// keys 8.9 us; 13 cut), or some more and there are many units (16 requests of up to 1000
+// keys, 128 units: 15.9 us, 18.5 cut; 32: 18 and 26; but eight 15.5 and 12.3, one 16.5 and
+// 10.9); else the line is cut, for a second kernel to join; so it is where chunks,
+// whose CTAs take whole SMs, wait for the last (42.4 and 39.3 us).
+constexpr int kDecFew = 16, kDecUnit = 32, kDecUnits = 96;
 
 struct DecArgs {
   Kv8Attn a;
@@ -676,7 +682,9 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   const int64_t blocks = most * b.n * cache->n_kv_heads;
   d.resident = sar::kDecPerSm * sar::num_sms();
   void* chunks = b.max_rows == 1 || b.rows == 1 ? nullptr : ws + sp.chunks;
-  d.units = most <= (chunks ? sar::kDecUnitBeside : sar::kDecUnit) + 2 && (int64_t)b.n * cache->n_kv_heads <= 1 << 20;
+  const int64_t units = (int64_t)b.n * cache->n_kv_heads;
+  d.units = most <= sar::kDecFew + 2 || (!chunks && most <= sar::kDecUnit + 2 && units >= sar::kDecUnits);
+  d.units = d.units && units <= 1 << 20;
   d.vec_q = aligned_to(b.q, 16) && b.ldq % 8 == 0;
   d.vec_o = aligned_to(b.out, 4) && b.ldo % 2 == 0;
   // the codes as rows of 128 bytes (one key, or two of 64 dims), boxes of up to 32 keys of a page

@@ -92,7 +92,7 @@ __device__ __forceinline__ bool kv8_sequence(const Kv8Attn& a, int i, int& row0,
 
 // ---- how single tokens' work is cut (attn_kv8.cu), for the kernel that joins it ----
 constexpr int kDecHeads = 8;    // query heads of a KV head: the products' columns
-constexpr int kDecLeast = 8;    // blocks of a CTA's stretch at least, where there are so few
+constexpr int kDecLeast = 4;    // blocks of a CTA's stretch at least, where there are so few
 constexpr int kDecWaves = 2;    // CTAs to a place on an SM, where there are
 constexpr int kDecMany = 256;   // so many blocks to a place
 
