@@ -24,20 +24,23 @@
 // NaN codes of V count as zero in the product, where they would reach rows that do not
 // see their key; if any came by, the rows look through their own keys at the end.
 //
-// Units' blocks of 128 keys form one line.  Where there are few units, every CTA (one
-// per SM) takes an equal stretch of it, or every unit gets as many CTAs, and pieces of a
-// unit are joined by the kernel behind (attn_kv8_join.cu); where there are four or more
-// units to an SM, a CTA takes a whole one, the longest of a sequence first: a stretch's
-// two pieces cost 256 KB of partial results more.
+// Units' blocks of 128 keys form one line.  Every CTA (one per SM) takes an equal stretch of
+// it, or every unit gets as many CTAs, or a CTA a whole unit, whichever should end first;
+// pieces of a unit are joined by the kernel behind (attn_kv8_join.cu).  With four or more
+// units to an SM a CTA always takes a whole one, the longest of a sequence first.
 //
 // Bound by a tile's chain (its Q K^T, its softmax, its P V, and the handing over, about
-// 2.1 us for a block's two tiles), which the two tiles hide from one another in part: the
-// tensor pipe is at work 42% of the time, instructions issue in 46% of the cycles.  8192
-// rows of 32 heads, bf16: 548 us, 1.0 PFLOP/s; 512 rows 16384 deep, f16, beside five single
-// tokens: 171 us, 0.79 PFLOP/s.  Steps of 64 keys with two buffers of scores, so that a
-// tile's next product does not wait for its softmax, took longer (666 us and 195): products
-// 64 columns wide run at half the rate.  So did both tiles on the same 128 pairs, where
-// there are no more, with the blocks in turn (171 -> 180 us for 1.2 of 43.7 elsewhere).
+// 2 us for a block's two tiles), which the two tiles hide from one another in part, and by
+// a piece's queries and results, as long as some blocks.  8192 rows of 32 heads, bf16:
+// 510 us, 1.08 PFLOP/s; 512 rows 16384 deep, f16, beside five single tokens: 160 us, 0.84
+// PFLOP/s; 25 chunks of up to 6 rows in a window of 1024 keys, beside seven: 34 us.
+// Taken at an earlier state: steps of 64 keys with two buffers of scores, so that a tile's
+// next product does not wait for its softmax (666 for 554 us and 195 for 172: products 64
+// columns wide run at half the rate); both tiles on the same 128 pairs, where there are no
+// more, with the blocks in turn (180 for 171 us; 42.5 for 43.7 with 25 short chunks).
+// The loop over blocks is sensitive to what else is in the function: with a piece's
+// results and the search for NaN out of line the first took 510 us, with all in line 554,
+// with the queries out of line too 669.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -180,12 +183,160 @@ __device__ __forceinline__ Tile tile_of(const Kv8Attn& a, int rows, int len, int
   return t;
 }
 
+// 16-byte chunk c of a row of a warp's queries, or of its 16-bit results: a part's chunks
+// after another's, swizzled as the product reads the queries.
+template <typename T, int D>
+__device__ __forceinline__ uint32_t chunk_at(uint32_t base, int row, int c) {
+  const int k = c % (D / 16);
+  return base + (uint32_t)(c / (D / 16) * ChunkSmem<T, D>::kPart + row * D + ((D == 128 ? k ^ (row & 7) : k ^ (row >> 1 & 3)) << 4));
+}
+// A warp's 32 rows of queries, pairs pair0 on of which `live` are the unit's, as sums of
+// e4m3 numbers.  The rows come into the place of their own first two parts, all under way
+// together, and are turned there, a row's eight dims to a lane (with a row to a thread
+// and two loads at a time a unit's queries took 10 us: 2048 rows of a prompt 286 us for 217
+// when its units were cut evenly).
+// Returns what the row of this lane's scores is to be multiplied by.
+template <typename T, int D>
+__device__ __forceinline__ float chunk_queries(const ChunkArgs8& args, uint32_t base, int row0, int kh, int pair0, int live) {
+  using M = ChunkSmem<T, D>;
+  constexpr int CHUNKS = D / 8, STEP_ROWS = 32 / CHUNKS;
+  const Kv8Attn& a = args.a;
+  const int lane = threadIdx.x & 31, ch = lane % CHUNKS, of_step = lane / CHUNKS;
+#pragma unroll 1
+  for (int i = 0; i < CHUNKS; ++i) {
+    const int row = i * STEP_ROWS + of_step;
+    const uint32_t to = chunk_at<T, D>(base, row, ch);
+    if (row >= live) {
+      sts_u4(to, 0, 0, 0, 0);
+      continue;
+    }
+    const unsigned of = (unsigned)(pair0 + row), tok = of / (unsigned)a.G;
+    const T* qp = static_cast<const T*>(a.q) + (int64_t)(row0 + (int)tok) * a.ldq + (int64_t)(kh * a.G + (int)(of - tok * a.G)) * D + 8 * ch;
+    if (args.vec_q) {
+      cp_async16(to, qp, 16);
+    } else {
+      const unsigned short* h = reinterpret_cast<const unsigned short*>(qp);
+      sts_u4(to, h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16, h[6] | (uint32_t)h[7] << 16);
+    }
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  __syncwarp();
+  float fac = a.scale;
+#pragma unroll 1
+  for (int i = 0; i < CHUNKS; ++i) {
+    const uint4 v = lds_u4(chunk_at<T, D>(base, i * STEP_ROWS + of_step, ch));
+    float f[8] = {Elem<T>::lo(v.x), Elem<T>::hi(v.x), Elem<T>::lo(v.y), Elem<T>::hi(v.y),
+                  Elem<T>::lo(v.z), Elem<T>::hi(v.z), Elem<T>::lo(v.w), Elem<T>::hi(v.w)};
+    float m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+#pragma unroll
+    for (int o = CHUNKS / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // (powers whose inverse is a normal number too)
+    const uint32_t ex = min(max(__float_as_uint(m) >> 23, 10u), 253u);
+    const float of_lane = __shfl_sync(0xffffffffu, __uint_as_float((ex - 7) << 23), lane % STEP_ROWS * CHUNKS);
+    if (lane / STEP_ROWS == i) fac = a.scale * of_lane;
+    const float inv = __uint_as_float((261u - ex) << 23);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] *= inv;
+    const uint32_t at = chunk_at<T, D>(base, i * STEP_ROWS + of_step, ch >> 1) + (ch & 1) * 8;
+    __syncwarp();  // (the rows have been read)
+#pragma unroll
+    for (int k = 0; k < M::kParts; ++k) {
+      uint32_t u[2];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t code = k == 0 ? to_e4m3x2(f[2 * e], f[2 * e + 1]) : finite_e4m3x2(f[2 * e], f[2 * e + 1]);
+        const float2 g = e4m3x2_floats(code);
+        f[2 * e] -= g.x, f[2 * e + 1] -= g.y;
+        u[e >> 1] = e & 1 ? u[e >> 1] | code << 16 : code;
+      }
+      asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + (uint32_t)(k * M::kPart)), "r"(u[0]), "r"(u[1]) : "memory");
+    }
+  }
+  return fac;
+}
+// The dims, a bit to each, in which a value of keys [k0, k1] is NaN.
+template <int D>
+__device__ __noinline__ uint4 nan_dims(const Kv8Attn& a, int seq, int kh, int k0, int k1) {
+  uint32_t nan[4] = {};
+  for (int key = k0; key <= k1; ++key) {
+    const int g = a.bt[(int64_t)seq * a.bt_stride + (key >> a.shift)];
+    if (g < 0 || g >= a.num_pages) continue;
+    const uint8_t* c = a.v_codes + ((((int64_t)g * a.kvh + kh) << a.shift) + (key & ((1 << a.shift) - 1))) * D;
+#pragma unroll
+    for (int k = 0; k < D / 4; ++k) {  // (unrolled: nan[] stays in registers)
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(c + 4 * k);
+      const uint32_t m = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+      nan[k >> 3] |= ((m & 1) | (m >> 7 & 2) | (m >> 14 & 4) | (m >> 21 & 8)) << ((k & 7) * 4);
+    }
+  }
+  return make_uint4(nan[0], nan[1], nan[2], nan[3]);
+}
+// NaN into the dims (of 32) whose bit is set
+__device__ __forceinline__ void poison(float (&o)[32], uint32_t bits) {
+  if (bits == 0) return;
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (bits >> e & 1) o[e] = NAN;
+}
+// A row of O times inv, in 16 bits, row by row through the place of the warp's own
+// queries' first two parts (other warps may be at the next piece already).
+template <typename T, int D>
+__device__ __noinline__ void chunk_rows_out(const ChunkArgs8& args, uint32_t ocol, uint32_t base, float inv, uint4 nan,
+                                               int64_t to, int live) {
+  constexpr int CHUNKS = D / 8, STEP_ROWS = 32 / CHUNKS;
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_ld32(ocol + c, *reinterpret_cast<uint32_t(*)[32]>(o));
+    tmem_wait_ld();
+    poison(o, c == 0 ? nan.x : c == 32 ? nan.y : c == 64 ? nan.z : nan.w);
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+      sts_u4(chunk_at<T, D>(base, lane, (c + e) >> 3), Elem<T>::pack(o[e] * inv, o[e + 1] * inv), Elem<T>::pack(o[e + 2] * inv, o[e + 3] * inv),
+             Elem<T>::pack(o[e + 4] * inv, o[e + 5] * inv), Elem<T>::pack(o[e + 6] * inv, o[e + 7] * inv));
+  }
+  __syncwarp();
+#pragma unroll 4
+  for (int i = 0; i < CHUNKS; ++i) {
+    const int row = i * STEP_ROWS + lane / CHUNKS, ch = lane % CHUNKS;
+    const int64_t of = __shfl_sync(0xffffffffu, to, row);
+    const uint4 v = lds_u4(chunk_at<T, D>(base, row, ch));
+    if (row >= live) continue;
+    T* op = static_cast<T*>(args.a.out) + of + 8 * ch;
+    if (args.vec_o) {
+      *reinterpret_cast<uint4*>(op) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) reinterpret_cast<unsigned short*>(op)[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+  __syncwarp();
+}
+// A row of O as it is, four dims of all of a unit's rows next to one another.
+template <int D>
+__device__ __noinline__ void chunk_piece_out(const ChunkArgs8& args, uint32_t ocol, uint4 nan, int64_t slot, int row) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    float o[32];
+    tmem_ld32(ocol + c, *reinterpret_cast<uint32_t(*)[32]>(o));
+    tmem_wait_ld();
+    poison(o, c == 0 ? nan.x : c == 32 ? nan.y : c == 64 ? nan.z : nan.w);
+    float4* pp = reinterpret_cast<float4*>(args.parts) + (slot * (D / 4) + c / 4) * 256 + row;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pp[e * 256] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     kv8_chunk_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const __grid_constant__ ChunkArgs8 args) {
   using M = ChunkSmem<T, D>;
-  constexpr int CHUNKS = D / 8, STEP_ROWS = 32 / CHUNKS;  // 16-byte chunks of a 16-bit row; rows of a warp's step over them
   constexpr int PASS = kConvWarps * 32 * 16 / D;  // keys of a pass of the converting warps, 16 bytes to a thread
   constexpr int STEP_PASSES = 64 / PASS;
   const Kv8Attn& a = args.a;
@@ -201,7 +352,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   int32_t* t_seq = before + kMostTiles + 1;
   int32_t* t_u = t_seq + kMostTiles;
   __shared__ int64_t sums[kChunkThreads / 32];
-  __shared__ int first_s[2], most_s;
+  __shared__ int first_s[2], most_s, least_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -223,6 +374,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(smem_u32(&bars->mma_done), 1);
     bars->nan = 0;
     most_s = 0;
+    least_s = 1 << 30;
     fence_mbar_init();
   }
   // Launched right behind the single tokens' kernel, which has waited for what came
@@ -288,18 +440,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       tl = tile_of(a, rows, len, t_u[threadIdx.x]);
       blocks = tl.j1 - tl.j0;
       atomicMax(&most_s, blocks);
+      atomicMin(&least_s, blocks);
     }
     const int64_t at = block_sum(blocks, all64);
     const int all = (int)(all64 * a.kvh), units = (int)nt * a.kvh, most = most_s;
     int C = max(1, min(args.sms, all / kLeastBlocks));
-    // A CTA with an equal stretch has two pieces mostly.  Where units are alike (within a
-    // quarter), the same number of CTAs to each, and so one piece to a CTA, ends sooner
-    // although some SMs stay idle: 512 rows 2048 deep 73 -> 58 us, 256 rows 16384 deep
-    // 115 -> 104; three chunks of 33 to 100 rows 3000 to 1000 deep would take 54 for 49.
-    int each = 0;
+    // Times in blocks: an equal stretch, with the pieces of as short units as there are ...
+    const int even = all / C, P = kPieceBlocks;
+    int best = even + P * (even / max(1, least_s) + 1), each = 0;
+    // ... the same number of CTAs to each unit, where these are alike (within a quarter), so
+    // that a CTA has one piece although some SMs stay idle (512 rows 2048 deep 58 us, 73 cut
+    // evenly; 256 rows 16384 deep 104 and 115; three unlike ones of 33 to 100 rows 3000 to
+    // 1000 deep 54 and 49) ...
     if (units > 0 && units <= args.sms && (int64_t)most * units <= all + all / 4) {
-      each = min(args.sms / units, max(1, most / kLeastBlocks));
-      if (most / each > all / C + kPieceBlocks) each = 0;
+      const int k = min(args.sms / units, max(1, most / kLeastBlocks));
+      if (most / k <= even + P) each = k, best = min(best, most / k + P);
+    }
+    // ... and a unit to a CTA, the last ones, which are a sequence's longest, first (2048
+    // rows of a prompt 75 us, 286 cut evenly; 16384 deep 480 and 463)
+    if (units > 0) {
+      const int rounds = (units + args.sms - 1) / args.sms;
+      if (min(rounds * most, even + (most + 1) / 2) + P * rounds < best && (units > args.sms || most + P < best)) each = 1;
     }
     if (each > 0) C = each * units;
     if (threadIdx.x < nt) {
@@ -324,7 +485,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       return;
     }
     if (each > 0) {
-      const int unit = (int)(blockIdx.x / (unsigned)each), part = (int)blockIdx.x - unit * each;
+      const int from = (int)(blockIdx.x / (unsigned)each), part = (int)blockIdx.x - from * each;
+      const int unit = each == 1 ? units - 1 - from : from;
       const int t = (int)((unsigned)unit / (unsigned)a.kvh), kh = unit - t * a.kvh;
       const int nb = before[t + 1] - before[t], u0 = before[t] * a.kvh + kh * nb, parts = min(each, nb);
       if (part >= parts) {
@@ -649,62 +811,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int token = (int)(pair / (unsigned)a.G), head = p.kh * a.G + (int)(pair % (unsigned)a.G);
       const int pos = valid ? p.len - p.rows + token : -1;  // keys (pos - window, pos] are seen
       const int lo = a.window > 0 ? pos - a.window + 1 : 0;
-      // 16-byte chunk c of a row of the queries' parts, a part's chunks after another's
-      auto q_at = [&](int row, int c) -> uint32_t {
-        const int k = c % (D / 16);
-        return q_reg(x) + (uint32_t)(c / (D / 16) * M::kPart + row * D + ((D == 128 ? k ^ (row & 7) : k ^ (row >> 1 & 3)) << 4));
-      };
-      float fac = a.scale;
+      const float fac = chunk_queries<T, D>(args, q_reg(x) + (uint32_t)(qq * 32 * D), p.row0, p.kh, p.t.pair0 + x * 128 + qq * 32,
+                                            p.t.pairs - x * 128 - qq * 32);
       {
-        // the query as sums of e4m3 numbers, swizzled as the product reads them
-        const T* qp = static_cast<const T*>(a.q) + (int64_t)(p.row0 + token) * a.ldq + (int64_t)head * D;
-        auto eight = [&](int k, float* f) {  // dims [8 k, 8 k + 8)
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (valid) {
-            if (args.vec_q) {
-              v = *reinterpret_cast<const uint4*>(qp + 8 * k);
-            } else {
-              const unsigned short* h = reinterpret_cast<const unsigned short*>(qp + 8 * k);
-              v = make_uint4(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16, h[4] | (uint32_t)h[5] << 16,
-                             h[6] | (uint32_t)h[7] << 16);
-            }
-          }
-          f[0] = Elem<T>::lo(v.x), f[1] = Elem<T>::hi(v.x), f[2] = Elem<T>::lo(v.y), f[3] = Elem<T>::hi(v.y);
-          f[4] = Elem<T>::lo(v.z), f[5] = Elem<T>::hi(v.z), f[6] = Elem<T>::lo(v.w), f[7] = Elem<T>::hi(v.w);
-        };
-        float m = 0.f;
-#pragma unroll 2
-        for (int k = 0; k < D / 8; ++k) {
-          float f[8];
-          eight(k, f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
-        }
-        // (powers whose inverse is a normal number too)
-        const uint32_t ex = min(max(__float_as_uint(m) >> 23, 10u), 253u);
-        fac *= __uint_as_float((ex - 7) << 23);
-        const float inv = __uint_as_float((261u - ex) << 23);
-#pragma unroll 1
-        for (int k = 0; k < D / 8; ++k) {
-          float f[8];
-          eight(k, f);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) f[e] *= inv;
-          const int c = k >> 1;  // 16-byte chunk of the row
-          const uint32_t at = q_reg(x) + (uint32_t)(r * D + ((D == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4) + (k & 1) * 8);
-#pragma unroll
-          for (int i = 0; i < M::kParts; ++i) {
-            uint32_t u[2];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t code = to_e4m3x2(f[2 * e], f[2 * e + 1]);
-              const float2 g = e4m3x2_floats(code);
-              f[2 * e] -= g.x, f[2 * e + 1] -= g.y;
-              u[e >> 1] = e & 1 ? u[e >> 1] | code << 16 : code;
-            }
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + (uint32_t)(i * M::kPart)), "r"(u[0]), "r"(u[1]) : "memory");
-          }
-        }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tc_fence_before();  // (the piece before's O has been read)
         __syncwarp();
@@ -837,74 +946,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (alive) alive = warp_wait(&bars->mma_done, pieces & 1, a.err);
       if (alive && x * 128 < p.t.pairs) {
         tc_fence_after();
-        uint32_t nan[D / 32] = {};  // dims whose value is NaN under a key that this row sees
-        if (*reinterpret_cast<volatile int*>(&bars->nan)) {
-          const int k0 = max(max(lo, 0), p.ja * kKeys), k1 = min(pos, p.jb * kKeys - 1);
-          for (int key = k0; key <= k1; ++key) {
-            const int g = a.bt[(int64_t)p.seq * a.bt_stride + (key >> a.shift)];
-            if (g < 0 || g >= a.num_pages) continue;
-            const uint8_t* c = a.v_codes + ((((int64_t)g * a.kvh + p.kh) << a.shift) + (key & ((1 << a.shift) - 1))) * D;
-#pragma unroll
-            for (int k = 0; k < D / 4; ++k) {  // (unrolled: nan[] stays in registers)
-              const uint32_t w = *reinterpret_cast<const uint32_t*>(c + 4 * k);
-              const uint32_t m = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-              nan[k >> 3] |= ((m & 1) | (m >> 7 & 2) | (m >> 14 & 4) | (m >> 21 & 8)) << ((k & 7) * 4);
-            }
-          }
-        }
+        uint4 nan = make_uint4(0, 0, 0, 0);  // dims whose value is NaN under a key that this row sees
+        if (*reinterpret_cast<volatile int*>(&bars->nan))
+          nan = nan_dims<D>(a, p.seq, p.kh, max(max(lo, 0), p.ja * kKeys), min(pos, p.jb * kKeys - 1));
         __syncwarp();
         const int64_t slot = 2 * (int64_t)blockIdx.x + (pieces == 0 ? 0 : 1);
         // (a row that sees keys and has no sum is NaN)
         const float inv = pos < 0 ? 0.f : 1.f / l;
         if (!p.whole) args.parts_ml[slot * 256 + x * 128 + r] = make_float2(m_used, l);
-        // (A row's 16-bit results leave through the place of its own queries' first two parts,
-        // so that rows are written whole; other warps may be at the next piece already. Partial
-        // results lie dims first, rows next to one another.)
         const int64_t to = (int64_t)(p.row0 + token) * a.ldo + (int64_t)head * D;
-#pragma unroll 1
-        for (int c = 0; c < D; c += 16) {
-          float o[16];
-          tmem_ld16(ocol + c, *reinterpret_cast<uint32_t(*)[16]>(o));
-          tmem_wait_ld();
-          const uint32_t bits = (c < 32 ? nan[0] : c < 64 ? nan[1] : c < 96 ? nan[D / 32 - 2] : nan[D / 32 - 1]) >> (c & 31);
-          if (bits & 0xffff) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (bits >> e & 1) o[e] = NAN;
-          }
-          if (!p.whole) {
-            if (nb > 0) {
-              float4* pp = reinterpret_cast<float4*>(args.parts) + (slot * (D / 4) + c / 4) * 256 + x * 128 + r;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) pp[e * 256] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-            }
-            continue;
-          }
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = Elem<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
-          sts_u4(q_at(r, c >> 3), h[0], h[1], h[2], h[3]);
-          sts_u4(q_at(r, c >> 3 | 1), h[4], h[5], h[6], h[7]);
-        }
-        if (p.whole) {
-          __syncwarp();
-#pragma unroll 1
-          for (int i = 0; i < CHUNKS; ++i) {
-            const int row = i * STEP_ROWS + lane / CHUNKS, ch = lane % CHUNKS;
-            const int64_t of = __shfl_sync(0xffffffffu, to, row);
-            const uint4 v = lds_u4(q_at(qq * 32 + row, ch));
-            if (x * 128 + qq * 32 + row >= p.t.pairs) continue;
-            T* op = static_cast<T*>(a.out) + of + 8 * ch;
-            if (args.vec_o) {
-              *reinterpret_cast<uint4*>(op) = v;
-            } else {
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int e = 0; e < 8; ++e) reinterpret_cast<unsigned short*>(op)[e] = (unsigned short)(w[e >> 1] >> (16 * (e & 1)));
-            }
-          }
-          __syncwarp();
-        }
+        if (p.whole)
+          chunk_rows_out<T, D>(args, ocol, q_reg(x) + (uint32_t)(qq * 32 * D), inv, nan, to, p.t.pairs - x * 128 - qq * 32);
+        else if (nb > 0)
+          chunk_piece_out<D>(args, ocol, nan, slot, x * 128 + r);
       }
       base += p.jb - p.ja;
       mine_done += nb;

@@ -316,6 +316,7 @@ def test_python_refusals():
 @pytest.mark.parametrize("seqs,heads,kv_heads,d", [
     ([(2 + i % 4, 20 + i) for i in range(270)], 4, 2, 64),                   # more sequences than a call shares out
     ([(400, 500)] + [(2 + i % 5, 100 + i) for i in range(74)], 32, 8, 64),   # four units and more to an SM
+    ([(1300, 1300)], 32, 8, 64),                                             # one and more
     ([(3, 60 + i % 50) if i % 3 else (1, 200) for i in range(150)], 56, 8, 128),
 ])
 def test_many_chunks(seqs, heads, kv_heads, d):
