@@ -4,7 +4,7 @@
 // A group of head_dim / 8 lanes has a row's head: eight elements a lane, four from
 // each half of the head, so that a rotation pair sits in one lane.  mean(h^2) is a
 // sum over the group.  Angles: position * theta / 2 pi as a fixed-point fraction of
-// a turn, 64 bits that wrap, which reduces any position exactly; then sincospif.
+// a turn, 64 bits that wrap, which reduces any position exactly; then two short series.
 // They are formed once per row and reused for all of a CTA's heads.
 //
 // Query heads are independent.  For the cache the unit is a run: the rows of a call
@@ -16,9 +16,9 @@
 // Rows of queries are bound by memory (12288 x 56 heads of 128, bf16: 61 us, where a copy of
 // them takes 53), the cache's part by its instructions, about 200 to 32 lanes' rows (8 + 8
 // heads: 39 us; 45 where every row of a run searched the maxima of the others).
-// Both in one launch: 93 us on consecutive inputs, 98 on inputs that are not in L2, against
-// 63 for the bytes.  Their CTAs in turn instead of the cache's first: 98 too; a window's
-// tasks side by side: 105, as the longest then come last as well.
+// Both in one launch 100 us on inputs that are not in L2, against 63 for the bytes.  At an
+// earlier state (98): their CTAs in turn instead of the cache's first, 98 too; a window's
+// tasks side by side, 105, as the longest then come last as well.
 #include <math.h>
 
 #include <algorithm>
@@ -93,18 +93,30 @@ __device__ __forceinline__ float group_max(float v) {
   return v;
 }
 
-// (cos, sin) of a lane's four frequencies at a position.
+// (cos, sin) of a lane's four frequencies at a position, off by little more than the
+// rounding to fp32 (a key that lies near a border of two codes falls on the side that the
+// formula's does): the angle less its nearest multiple of a quarter turn, x = hi + lo, and
+// Taylor's series on |x| <= pi / 4, whose first terms are added last, with what they lose.
 __device__ __forceinline__ void angles(const QkArgs& a, int pos, int i0, float* cs, float* sn) {
+  constexpr float kTo = (float)(3.14159265358979323846 / 2147483648.0);  // from units of 2^-31 half turns
+  constexpr float kToLow = (float)(3.14159265358979323846 / 2147483648.0 - (double)kTo);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint64_t t = (uint64_t)(int64_t)pos * a.turn[i0 + e];
-    const int32_t h = (int32_t)(t >> 32);  // half turns in units of 2^-31
-    const float f = (float)h, rest = (float)(int32_t)((int64_t)h - (int64_t)f) * (0x1p-31f * 3.14159265f);
-    float c, s;
-    sincospif(f * 0x1p-31f, &s, &c);
-    // what h lost in 24 bits: up to 2^-25 of a half turn
-    cs[e] = fmaf(-s, rest, c);
-    sn[e] = fmaf(c, rest, s);
+    const uint32_t h = (uint32_t)(t >> 32);  // half turns in units of 2^-31, around the circle
+    const uint32_t quarter = (h + (1u << 29)) >> 30;
+    const int32_t r = (int32_t)(h - (quarter << 30));
+    const float rf = (float)r, hi = rf * kTo;
+    const float lo = fmaf(rf, kTo, -hi) + fmaf(rf, kToLow, (float)(r - (int32_t)rf) * kTo);
+    const float x2 = hi * hi;
+    const float s = hi + fmaf(hi * x2, fmaf(x2, fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f),
+                                                     1.f / 120.f), -1.f / 6.f), lo);
+    const float low2 = fmaf(hi, hi, -x2), w = fmaf(-0.5f, x2, 1.f);
+    const float c = w + (fmaf(-0.5f, x2, 1.f - w) - fmaf(hi, lo, 0.5f * low2) +
+                         x2 * x2 * fmaf(x2, fmaf(x2, fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f));
+    const float u = quarter & 1 ? s : c, v = quarter & 1 ? c : s;
+    cs[e] = (quarter + 1) & 2 ? -u : u;
+    sn[e] = quarter & 2 ? -v : v;
   }
 }
 
@@ -123,8 +135,10 @@ __device__ __forceinline__ void norm_rope(float* x, const float* gain, bool norm
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float u = x[e], w = x[e + 4];
-      x[e] = u * cs[e] - w * sn[e];
-      x[e + 4] = w * cs[e] + u * sn[e];
+      // (products rounded before they are added, as fp32 programs of this formula have them: of
+      // keys on a border of two codes, both then take the same)
+      x[e] = __fsub_rn(__fmul_rn(u, cs[e]), __fmul_rn(w, sn[e]));
+      x[e + 4] = __fadd_rn(__fmul_rn(w, cs[e]), __fmul_rn(u, sn[e]));
     }
   }
 }
