@@ -280,7 +280,7 @@ int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream
  * (0: unknown) is about the longest length and only guides how work is shared
  * out.  scale 0 is 1 / sqrt(head_dim).  A cache's scales are positive and lie
  * within [2^-40, 2^60].  At most 8 query heads per KV head, 2^27 rows, 2^30 sequences and block
- * tables of 2^31 - 257 tokens.  q and out do not overlap.
+ * tables of 2^31 - 257 tokens.  q and out do not overlap; no row is two sequences'.
  * The workspace (device, 16-byte aligned, sar_kv8_attention_workspace() bytes; it
  * holds nothing between calls) belongs to one call at a time.
  * Sequences whose offsets are out of range or fall, whose rows pass max_rows or
