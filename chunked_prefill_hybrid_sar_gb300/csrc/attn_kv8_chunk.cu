@@ -59,7 +59,8 @@ constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log
 constexpr int kRawSteps = 3;              // steps of 64 keys of V whose codes are under way
 constexpr int kMostK = 3;                 // K stages
 constexpr int kLeastBlocks = 4;          // of a stretch
-constexpr int kPieceBlocks = 12;         // a CTA's second piece takes as long as so many blocks more
+constexpr int kPieceBlocks = 12;         // a CTA's second piece takes as long as so many blocks more (four chunks of up to
+                                         // 512 rows 90 us; 106 where 8 or 5 are reckoned; others alike)
 constexpr float kGrowth = 8.f;           // log2 of a maximum's growth that O tolerates
 constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its last 64 columns
 constexpr uint32_t kColsO = 256;         // O_x at 256 + x * 128

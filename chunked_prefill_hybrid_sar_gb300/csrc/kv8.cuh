@@ -104,7 +104,7 @@ struct DecStart {
 };
 // How the line is cut.  SMs are not equally near to the memory that their keys lie in:
 // of CTAs with equal stretches the last ended 25% after the median.  So the
-// resident CTAs take equal shares of the line's first 7/8, and twice as many more
+// resident CTAs take equal shares of the line's first 7/8, and as many more
 // share the rest, each started as a place on an SM gets free (128 sequences of up to 8192
 // keys 174 us, 181 in equal stretches).
 struct DecLine {
