@@ -668,12 +668,14 @@ def _int32(what: str, t, least: int, name: str) -> int:
     return t.data_ptr()
 
 
-def _tables(what: str, t, n: int) -> int:
-    """The row stride of block tables."""
+def _tables(what: str, t, n: int):
+    """(row stride, columns) of block tables, which may be columns of wider ones."""
     import torch
     if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] < n or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: block_tables must be two-dimensional int32 with adjacent columns, a row per request")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if n > 0 and t.shape[1] == 0:
+        raise ValueError(f"{what}: block_tables have no columns")
+    return (t.stride(0) if t.shape[0] > 1 else t.shape[1]), t.shape[1]
 
 
 def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, positions, slots, page_size: int,
@@ -688,8 +690,8 @@ def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, 
     _row_types()
     lens_out = lens if lens_out is None else lens_out
     free_count_out = free_count if free_count_out is None else free_count_out
-    stride = _tables(what, block_tables, n)
-    if block_tables.shape[0] > 1 and stride < block_tables.shape[1]:
+    stride, cols = _tables(what, block_tables, n)
+    if stride < cols:
         raise ValueError("page_map: rows of block_tables overlap")
     rows = positions.numel()
     a = _lib.sar_page_map_args(
@@ -697,7 +699,7 @@ def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, 
         block_tables.data_ptr(), _int32(what, free_pages, 1, "free_pages"), _int32(what, free_count, 1, "free_count"),
         _int32(what, free_count_out, 1, "free_count_out"), _int32(what, row_offsets, n + 1, "row_offsets"),
         _int32(what, positions, rows, "positions"), _int32(what, slots, rows, "slots"), n, stride, page_size,
-        free_pages.numel(), rows)
+        free_pages.numel(), rows, cols)
     st = _launch_stream(what, stream, lens, new_lens, lens_out, block_tables, free_pages, free_count, free_count_out,
                         row_offsets, positions, slots)
     check(lib().sar_page_map(ctypes.byref(a), st))
@@ -807,10 +809,11 @@ def kv8_attention(q, cache: KV8Cache, row_offsets, lens, block_tables, out, max_
     ldo = _rows(what, out)[2]
     if cache.device != q.get_device():
         raise ValueError("kv8_attention: the cache is on another device")
+    stride, table_cols = _tables(what, block_tables, n)
     b = _lib.sar_kv8_batch(q.data_ptr(), out.data_ptr(), ld, ldo, _int32(what, row_offsets, n + 1, "row_offsets"),
                            _int32(what, lens, n, "lens"), block_tables.data_ptr(), None, 0, rows, n, cols // cache.head_dim,
-                           _tables(what, block_tables, n), kind, max(1, rows) if max_rows is None else max_rows, max_len or 0,
-                           window, scale)
+                           stride, kind, max(1, rows) if max_rows is None else max_rows, max_len or 0, window, scale,
+                           min(stride, table_cols))
     st = _launch_stream(what, stream, q, out, row_offsets, lens, block_tables, workspace)
     if workspace is None and rows and n:
         need = ctypes.c_int64()

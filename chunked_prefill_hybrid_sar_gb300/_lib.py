@@ -94,7 +94,7 @@ class sar_kv8(ctypes.Structure):
 class sar_page_map_args(ctypes.Structure):
     _fields_ = [(n, vp) for n in ("lens", "new_lens", "lens_out", "block_tables", "free_pages", "free_count",
                                   "free_count_out", "row_offsets", "positions", "slots")] + [
-        (n, i32) for n in ("n", "bt_stride", "page_size", "num_pages", "max_rows")]
+        (n, i32) for n in ("n", "bt_stride", "page_size", "num_pages", "max_rows", "bt_cols")]
 
 
 class sar_qk_rows(ctypes.Structure):
@@ -109,7 +109,7 @@ class sar_kv8_batch(ctypes.Structure):
     _fields_ = [(n, vp) for n in ("q", "out")] + [("ldq", i64), ("ldo", i64)] + [
         (n, vp) for n in ("row_offsets", "lens", "block_tables", "workspace")] + [("workspace_bytes", i64)] + [
         (n, i32) for n in ("rows", "n", "n_q_heads", "bt_stride", "storage", "max_rows", "max_len", "window")] + [
-        ("scale", f32)]
+        ("scale", f32), ("bt_cols", i32)]
 
 
 # name -> (restype, argtypes)

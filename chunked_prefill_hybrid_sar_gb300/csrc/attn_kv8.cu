@@ -636,7 +636,7 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   if (!b.q || !b.out || !b.row_offsets || !b.lens || !b.block_tables || !b.workspace)
     return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: null pointer");
   const int64_t width = (int64_t)b.n_q_heads * cache->head_dim;
-  if (b.ldq < width || b.ldo < width || b.bt_stride < 1)
+  if (b.ldq < width || b.ldo < width || b.bt_stride < 1 || b.bt_cols < 0 || b.bt_cols > b.bt_stride)
     return set_error(SAR_ERR_INVALID_ARG, "kv8_attention: rows shorter than their heads, or no block table");
   // (256: the blocks looked up ahead of a sequence's end)
   if ((int64_t)b.bt_stride * cache->page_size > INT32_MAX - 256)
@@ -656,6 +656,7 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   a.lens = b.lens;
   a.bt = b.block_tables;
   a.bt_stride = b.bt_stride;
+  a.bt_cols = b.bt_cols > 0 ? b.bt_cols : b.bt_stride;
   a.k_scales = cache->k_scales;
   a.v_scales = cache->v_scales;
   a.k_codes = static_cast<const uint8_t*>(cache->k_codes);
@@ -677,7 +678,7 @@ int sar_kv8_attention(const sar_kv8_batch* batch, const sar_kv8* cache, void* st
   d.parts_ml = reinterpret_cast<float2*>(ws + sp.ml);
   d.parts = reinterpret_cast<float*>(ws + sp.parts);
   // (max_len and the tables' width only guide how work is shared out)
-  const int64_t longest = b.max_len > 0 ? b.max_len : (int64_t)b.bt_stride * cache->page_size;
+  const int64_t longest = b.max_len > 0 ? b.max_len : a.bt_cols * cache->page_size;
   const int64_t most = (b.window > 0 ? std::min<int64_t>(longest, b.window) : longest) / sar::kDecKeys + 2;
   const int64_t blocks = most * b.n * cache->n_kv_heads;
   d.resident = sar::kDecPerSm * sar::num_sms();

@@ -427,7 +427,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       at0 = block_sum(t, nt);
       // (a line's blocks, as many as the block tables allow, stay within 32 bits)
       stretches = nt <= kMostTiles && nt * a.kvh < 4 * args.sms &&
-                  nt * a.kvh * (((a.bt_stride << a.shift) / kKeys) + 1) < (1 << 30);
+                  nt * a.kvh * (((a.bt_cols << a.shift) / kKeys) + 1) < (1 << 30);
     }
   }
   __syncthreads();

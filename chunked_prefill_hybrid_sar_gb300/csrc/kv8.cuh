@@ -70,7 +70,7 @@ struct Kv8Attn {
   const int32_t* off;
   const int32_t* lens;
   const int32_t* bt;
-  int64_t bt_stride;
+  int64_t bt_stride, bt_cols;  // a table's place, and the pages that it holds
   const float* k_scales;
   const float* v_scales;
   const uint8_t* k_codes;
@@ -87,7 +87,7 @@ __device__ __forceinline__ bool kv8_sequence(const Kv8Attn& a, int i, int& row0,
   len = a.lens[i];
   rows = row1 - row0;
   return row0 >= 0 && row1 >= row0 && row1 <= a.rows && rows <= a.max_rows && len >= 0 &&
-         len <= (a.bt_stride << a.shift);
+         len <= (a.bt_cols << a.shift);
 }
 
 // ---- how single tokens' work is cut (attn_kv8.cu), for the kernel that joins it ----

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kMapThreads) page_map_kernel(const MapArgs a) 
   pdl_launch_dependents();
   const int f_raw = *m.free_count;
   const int f = min(max(f_raw, 0), m.num_pages);
-  const int64_t most = (int64_t)m.bt_stride << shift;
+  const int64_t most = (int64_t)m.bt_cols << shift;  // (not the stride: behind the columns lies what is not ours)
   const bool first_cta = rank == 0;
   if (first_cta && threadIdx.x == 0 && f != f_raw) report(a.err, SAR_ERR_BOUNDS, SITE_MAP_REQUEST, -1);
 
@@ -251,7 +251,7 @@ using sar::set_error;
 extern "C" int sar_page_map(const sar_page_map_args* args, void* stream) try {
   if (!args) return set_error(SAR_ERR_INVALID_ARG, "page_map: null arguments");
   const sar_page_map_args& m = *args;
-  if (m.n < 0 || m.bt_stride < 1 || m.num_pages < 1 || m.max_rows < 0)
+  if (m.n < 0 || m.bt_stride < 1 || m.num_pages < 1 || m.max_rows < 0 || m.bt_cols < 0 || m.bt_cols > m.bt_stride)
     return set_error(SAR_ERR_INVALID_ARG, "page_map: bad sizes");
   if (m.page_size != 16 && m.page_size != 32 && m.page_size != 64)
     return set_error(SAR_ERR_UNSUPPORTED, "page_map: pages of 16, 32 or 64 tokens");
@@ -270,6 +270,7 @@ extern "C" int sar_page_map(const sar_page_map_args* args, void* stream) try {
   for (const void* p : all)
     if (!sar::on4(p)) return set_error(SAR_ERR_INVALID_ARG, "page_map: array not aligned to its element");
   sar::MapArgs a = {m, m.page_size == 16 ? 4 : m.page_size == 32 ? 5 : 6, 0, nullptr};
+  if (a.m.bt_cols == 0) a.m.bt_cols = m.bt_stride;
   a.vec = ((reinterpret_cast<uintptr_t>(m.positions) | reinterpret_cast<uintptr_t>(m.slots)) & 15) == 0;
   SAR_TRY(sar::op_flags(&a.err));
   cudaLaunchConfig_t lc = {};

@@ -208,14 +208,15 @@ typedef struct sar_kv8 {
  * Also SAR_ERR_BOUNDS: a request whose length is negative (it counts as 0) or passes
  * its block table, with the new tokens too, or whose new_lens is below -1, waits; a
  * page out of range goes where it would, but rows in it have slot -1.
- * lens_out may be lens, free_count_out free_count; else no two arrays overlap.
+ * lens_out may be lens, free_count_out free_count; else no two arrays overlap.  bt_cols
+ * is at most bt_stride, so that block_tables may be columns of a wider table.
  * n is at most 8192, n * bt_stride and max_rows at most 2^30.  Async on `stream`;
  * no workspace. */
 typedef struct sar_page_map_args {
   const int32_t* lens;     /* [n] */
   const int32_t* new_lens; /* [n] */
   int32_t* lens_out;       /* [n] */
-  int32_t* block_tables;   /* [n][bt_stride], read and written */
+  int32_t* block_tables;   /* [n][bt_stride], of which bt_cols are read and written */
   int32_t* free_pages;     /* [num_pages], the first *free_count are free */
   const int32_t* free_count;
   int32_t* free_count_out;
@@ -223,6 +224,7 @@ typedef struct sar_page_map_args {
   int32_t* positions;   /* [max_rows] */
   int32_t* slots;       /* [max_rows] */
   int32_t n, bt_stride, page_size, num_pages, max_rows;
+  int32_t bt_cols; /* pages that a request's row of block_tables has room for; 0: bt_stride */
 } sar_page_map_args;
 int sar_page_map(const sar_page_map_args* args, void* stream);
 
@@ -284,7 +286,7 @@ int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream
  * The workspace (device, 16-byte aligned, sar_kv8_attention_workspace() bytes; it
  * holds nothing between calls) belongs to one call at a time.
  * Sequences whose offsets are out of range or fall, whose rows pass max_rows or
- * whose length passes its block table are left out, and keys of pages out of range
+ * whose length passes its block table's bt_cols pages are left out, and keys of pages out of range
  * are passed over; sar_op_sync_status() reports either.  Rows of no sequence stay as they
  * are.  Async on `stream`; allocates nothing. */
 typedef struct sar_kv8_batch {
@@ -293,11 +295,12 @@ typedef struct sar_kv8_batch {
   int64_t ldq, ldo;
   const int32_t* row_offsets;  /* [n + 1] */
   const int32_t* lens;         /* [n] */
-  const int32_t* block_tables; /* [n][bt_stride] */
+  const int32_t* block_tables; /* [n][bt_stride], of which bt_cols are read */
   void* workspace;
   int64_t workspace_bytes;
   int32_t rows, n, n_q_heads, bt_stride, storage, max_rows, max_len, window;
   float scale;
+  int32_t bt_cols; /* columns of a block table, at most bt_stride; 0: bt_stride */
 } sar_kv8_batch;
 /* Bytes of workspace for such a call (rows, n, n_q_heads, max_rows and max_len of
  * the batch are read) on the current device. */
