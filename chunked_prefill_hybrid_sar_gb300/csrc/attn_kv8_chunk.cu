@@ -162,6 +162,12 @@ __device__ __forceinline__ void sts_u4(uint32_t addr, uint32_t a, uint32_t b, ui
 // (rows * G stays below 2^30)
 __device__ __forceinline__ int tiles_of(int rows, int G) { return rows < 2 ? 0 : (rows * G + 255) >> 8; }
 
+// The oldest key that a row at position p sees (p may be in front of the sequence, where
+// p - window passes 32 bits).
+__device__ __forceinline__ int oldest_seen(const Kv8Attn& a, int p) {
+  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
+}
+
 // Tile u of a sequence: its pairs, and the blocks of 128 keys that they see.
 struct Tile {
   int pair0;           // its first pair
@@ -177,7 +183,7 @@ __device__ __forceinline__ Tile tile_of(const Kv8Attn& a, int rows, int len, int
   const int first = len - rows + (int)((unsigned)t.pair0 / G);
   const int last = len - rows + (int)((unsigned)(t.pair0 + t.pairs - 1) / G);
   const int last_a = len - rows + (int)((unsigned)(t.pair0 + min(t.pairs, 128) - 1) / G);
-  t.lo = a.window > 0 ? max(0, first - a.window + 1) : 0;
+  t.lo = oldest_seen(a, first);
   t.j0 = t.lo / kKeys;
   t.j1 = max(last, 0) / kKeys + 1;
   t.j1a = max(last_a, 0) / kKeys + 1;
@@ -811,7 +817,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const unsigned pair = valid ? p.t.pair0 + x * 128 + r : 0u;
       const int token = (int)(pair / (unsigned)a.G), head = p.kh * a.G + (int)(pair % (unsigned)a.G);
       const int pos = valid ? p.len - p.rows + token : -1;  // keys (pos - window, pos] are seen
-      const int lo = a.window > 0 ? pos - a.window + 1 : 0;
+      const int lo = oldest_seen(a, pos);
       const float fac = chunk_queries<T, D>(args, q_reg(x) + (uint32_t)(qq * 32 * D), p.row0, p.kh, p.t.pair0 + x * 128 + qq * 32,
                                             p.t.pairs - x * 128 - qq * 32);
       {
@@ -949,7 +955,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc_fence_after();
         uint4 nan = make_uint4(0, 0, 0, 0);  // dims whose value is NaN under a key that this row sees
         if (*reinterpret_cast<volatile int*>(&bars->nan))
-          nan = nan_dims<D>(a, p.seq, p.kh, max(max(lo, 0), p.ja * kKeys), min(pos, p.jb * kKeys - 1));
+          nan = nan_dims<D>(a, p.seq, p.kh, max(lo, p.ja * kKeys), min(pos, p.jb * kKeys - 1));
         __syncwarp();
         const int64_t slot = 2 * (int64_t)blockIdx.x + (pieces == 0 ? 0 : 1);
         // (a row that sees keys and has no sum is NaN)
