@@ -645,6 +645,7 @@ class KV8Cache:
             raise ValueError("KV8Cache: codes must be [pages, kv heads, page size, head_dim], keys as values")
         if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
             raise ValueError("KV8Cache: scales must be [pages, kv heads]")
+        _fit32("KV8Cache", *k_codes.shape)
         _launch_stream("KV8Cache", 0, k_codes, v_codes, k_scales, v_scales)
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
         self.num_pages, self.n_kv_heads, self.page_size, self.head_dim = k_codes.shape
@@ -666,6 +667,12 @@ def _int32(what: str, t, least: int, name: str) -> int:
     if t.dtype is not _INT32_TYPE[0] or not t.is_contiguous() or t.numel() < least:
         raise ValueError(f"{what}: {name} must be contiguous int32, {least} long at least")
     return t.data_ptr()
+
+
+def _fit32(what: str, *numbers) -> None:
+    """Refuses numbers that 32-bit fields do not hold (ctypes cuts them silently)."""
+    if max(numbers) > 0x7FFFFFFF or min(numbers) < -0x80000000:
+        raise ValueError(f"{what}: sizes and limits must fit 32 bits, these do not all: {numbers}")
 
 
 def _tables(what: str, t, n: int):
@@ -694,6 +701,7 @@ def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, 
     if stride < cols:
         raise ValueError("page_map: rows of block_tables overlap")
     rows = positions.numel()
+    _fit32(what, n, stride, page_size, free_pages.numel(), rows)
     a = _lib.sar_page_map_args(
         _int32(what, lens, n, "lens"), _int32(what, new_lens, n, "new_lens"), _int32(what, lens_out, n, "lens_out"),
         block_tables.data_ptr(), _int32(what, free_pages, 1, "free_pages"), _int32(what, free_count, 1, "free_count"),
@@ -724,6 +732,9 @@ def qk_norm_rope(q, k, q_out, head_dim: int, positions=None, v=None, k_out=None,
     if (q_out is not None and q is None) or (k_out is not None and k is None):
         raise ValueError("qk_norm_rope: output rows without theirs")
     rows, width, ld, kind = _rows(what, k if q is None else q)
+    if head_dim < 1:
+        raise ValueError("qk_norm_rope: head_dim must be positive")
+    _fit32(what, rows, width, head_dim)
     q_at = k_at = v_at = qo_at = ko_at = None
     ldq = ldk = ldv = ldqo = ldko = heads = kv_heads = 0
     if q is not None:
@@ -785,6 +796,7 @@ def _kv8_rows(cache: KV8Cache, q):
 def kv8_attention_workspace(cache: KV8Cache, q, n: int, max_rows: int | None = None, max_len: int | None = None) -> int:
     """Bytes of workspace of ``kv8_attention`` for rows like ``q`` of ``n`` sequences."""
     rows, cols, ld, kind = _kv8_rows(cache, q)
+    _fit32("kv8_attention_workspace", rows, n, max_rows or 0, max_len or 0)
     out = ctypes.c_int64()
     b = _lib.sar_kv8_batch(None, None, ld, ld, None, None, None, None, 0, rows, n, cols // cache.head_dim, 1, kind,
                            max(1, rows) if max_rows is None else max_rows, max_len or 0, 0, 0.0)
@@ -810,6 +822,7 @@ def kv8_attention(q, cache: KV8Cache, row_offsets, lens, block_tables, out, max_
     if cache.device != q.get_device():
         raise ValueError("kv8_attention: the cache is on another device")
     stride, table_cols = _tables(what, block_tables, n)
+    _fit32(what, rows, n, stride, max_rows or 0, max_len or 0, window)
     b = _lib.sar_kv8_batch(q.data_ptr(), out.data_ptr(), ld, ldo, _int32(what, row_offsets, n + 1, "row_offsets"),
                            _int32(what, lens, n, "lens"), block_tables.data_ptr(), None, 0, rows, n, cols // cache.head_dim,
                            stride, kind, max(1, rows) if max_rows is None else max_rows, max_len or 0, window, scale,
