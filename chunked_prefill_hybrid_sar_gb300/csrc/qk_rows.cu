@@ -329,9 +329,16 @@ __global__ void __launch_bounds__(kQkThreads, 2) qk_rows_kernel(const __grid_con
       const int64_t unit = (int64_t)(slot >> a.shift) * a.c.n_kv_heads + kh;
       uint8_t* page = codes + unit * ps * D;
       const int o = (slot & (ps - 1)) * D + 4 * l;
-      // (a power of two's inverse, exactly, without the division)
+      // a power of two's inverse, exactly, without the division; a page that another program
+      // filled may go on under a scale that is none, and then h / s itself is rounded (by the
+      // inverse it was off a little, and ties fell to the wrong code)
       const uint32_t bits = __float_as_uint(scale);
-      const float inv = (bits & 0x7fffffu) == 0 ? __uint_as_float(0x7f000000u - bits) : 1.f / scale;
+      float inv = __uint_as_float(0x7f000000u - bits);
+      if (bits & 0x7fffffu) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[p][e] = __fdiv_rn(x[p][e], scale);
+        inv = 1.f;  // (such a scale is the old one: nothing is rounded anew)
+      }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const float* u = x[p] + 4 * half;
