@@ -22,9 +22,9 @@
 // more per 16 keys and row.
 //
 // NaN codes of V count as zero in the product, where they would reach rows that do not
-// see their key; a block that has any is marked, and once its product has landed the rows
-// look through those of its keys that they see (a NaN under 64 rows 200000 deep: 134 us;
-// 2650 when the rows looked through all of their keys at the end, 114 without a NaN).
+// see their key; the blocks that have any are marked, and at a piece's end its rows look through
+// those of their keys that they see (a NaN under 64 rows 200000 deep: 131 us; 2650 when
+// they looked through all of the piece's, 114 without a NaN).
 //
 // Units' blocks of 128 keys form one line.  Every CTA (one per SM) takes an equal stretch of
 // it, or every unit gets as many CTAs, or a CTA a whole unit, whichever should end first;
@@ -57,8 +57,9 @@ constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kChunkThreads = (kSoftWarps + kConvWarps + 4) * 32;  // (whole warpgroups: the last has one warp at work)
 constexpr int kTileRegion = 128 * 128;   // [128 rows][128 bytes]: 64 dims of 128 rows
 constexpr int kScaleRing = 4;             // blocks whose scales are kept: three K stages ahead, and the softmax's
-constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log2 and inverse of the value scales; a flag of
-                                         // pages that are not there; the block's number, where the one before has a NaN
+constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log2 and inverse of the value scales, a flag
+constexpr int kPieceRing = 4;            // pieces that are known at once: V's codes are turned two blocks ahead
+constexpr int kMarks = 512;              // of a piece's blocks, for one or some of which each stands
 constexpr int kRawSteps = 3;              // steps of 64 keys of V whose codes are under way
 constexpr int kMostK = 3;                 // K stages
 constexpr int kLeastBlocks = 4;          // of a stretch
@@ -75,6 +76,7 @@ struct ChunkBars {
   uint64_t q_ready, mma_done;
   uint32_t tmem;
   uint32_t read[kScaleRing];  // runs of a block whose V was read
+  uint32_t nan[kPieceRing];   // a piece's number + 1, where V has NaN codes
 };
 
 struct ChunkArgs8 {
@@ -96,7 +98,8 @@ struct ChunkSmem {
   static constexpr int kBars = kRaw + kRawSteps * kRawStep;
   static constexpr int kScales = kBars + 256;
   static constexpr int kTable = kScales + kScaleRing * kScaleFloats * 4;  // before [tiles + 1], seq, u
-  static constexpr int kBytes = 1024 + kTable + (3 * kMostTiles + 1) * 4;
+  static constexpr int kNan = kTable + (3 * kMostTiles + 1) * 4;  // [pieces][marks] bytes
+  static constexpr int kBytes = 1024 + kNan + kPieceRing * kMarks;
 };
 static_assert(sizeof(ChunkBars) <= 256, "barrier area");
 static_assert(ChunkSmem<__half, 128>::kBytes <= 226 * 1024, "shared memory per CTA");
@@ -164,12 +167,6 @@ __device__ __forceinline__ void sts_u4(uint32_t addr, uint32_t a, uint32_t b, ui
 // (rows * G stays below 2^30)
 __device__ __forceinline__ int tiles_of(int rows, int G) { return rows < 2 ? 0 : (rows * G + 255) >> 8; }
 
-// The oldest key that a row at position p sees (p may be in front of the sequence, where
-// p - window passes 32 bits).
-__device__ __forceinline__ int oldest_seen(const Kv8Attn& a, int p) {
-  return a.window > 0 && p >= a.window ? p - a.window + 1 : 0;
-}
-
 // Tile u of a sequence: its pairs, and the blocks of 128 keys that they see.
 struct Tile {
   int pair0;           // its first pair
@@ -185,7 +182,8 @@ __device__ __forceinline__ Tile tile_of(const Kv8Attn& a, int rows, int len, int
   const int first = len - rows + (int)((unsigned)t.pair0 / G);
   const int last = len - rows + (int)((unsigned)(t.pair0 + t.pairs - 1) / G);
   const int last_a = len - rows + (int)((unsigned)(t.pair0 + min(t.pairs, 128) - 1) / G);
-  t.lo = oldest_seen(a, first);
+  // (rows in front of the sequence see nothing; their positions less a window may pass 32 bits)
+  t.lo = a.window > 0 ? max(0, max(first, -1) - a.window + 1) : 0;
   t.j0 = t.lo / kKeys;
   t.j1 = max(last, 0) / kKeys + 1;
   t.j1a = max(last_a, 0) / kKeys + 1;
@@ -266,33 +264,46 @@ __device__ __forceinline__ float chunk_queries(const ChunkArgs8& args, uint32_t 
   }
   return fac;
 }
-// NaN into O in the dims in which a value of block `block` is NaN under a key of [lo, pos]:
-// it stays there, whatever is added or multiplied.  The lanes look through four keys each
-// and tell one another of those that have any.
+// Block j's mark among those of a piece of nb blocks; what marks it: stamps of a place's pieces
+// differ for so long that an old one costs time alone.
+__device__ __forceinline__ int mark_of(int j, int nb) { return nb <= kMarks ? j : (int)((int64_t)j * kMarks / nb); }
+__device__ __forceinline__ uint8_t stamp_of(uint32_t piece) { return (uint8_t)(piece / kPieceRing % 255 + 1); }
+// NaN into O in the dims in which a value is NaN under a key of [lo, pos], of the piece's marked
+// blocks.  The lanes look through four keys of a block each and tell one another of those that have any.
 template <int D>
-__device__ __noinline__ void nan_into(const Kv8Attn& a, uint32_t ocol, int seq, int len, int kh, int block, int lo, int pos) {
+__device__ __noinline__ void nan_into(const Kv8Attn& a, uint32_t ocol, const uint8_t* marks, uint32_t stamp, int seq, int len, int kh,
+                                      int ja, int nb, int lo, int pos) {
+  const int lane = threadIdx.x & 31, n = min(nb, kMarks);
   uint32_t nan[D / 32] = {};
 #pragma unroll 1
-  for (int k0 = block * kKeys; k0 < block * kKeys + kKeys; k0 += 32) {
-    const int key = k0 + (threadIdx.x & 31);
-    const int g = key < len ? a.bt[(int64_t)seq * a.bt_stride + (key >> a.shift)] : -1;
-    uint32_t mine[D / 32] = {}, any = 0;
-    if (g >= 0 && g < a.num_pages) {
-      const uint8_t* c = a.v_codes + ((((int64_t)g * a.kvh + kh) << a.shift) + (key & ((1 << a.shift) - 1))) * D;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+#pragma unroll 1
+    for (uint32_t set = __ballot_sync(0xffffffffu, i0 + lane < n && marks[i0 + lane] == stamp); set; set &= set - 1) {
+      const int64_t i = i0 + __ffs(set) - 1;  // it stands for blocks [i nb / n, (i + 1) nb / n), rounded up
+      const int k1 = (ja + (int)(((i + 1) * nb + n - 1) / n)) * kKeys;
+#pragma unroll 1
+      for (int k0 = (ja + (int)((i * nb + n - 1) / n)) * kKeys; k0 < k1; k0 += 32) {
+        const int key = k0 + lane;
+        const int g = key < len ? a.bt[(int64_t)seq * a.bt_stride + (key >> a.shift)] : -1;
+        uint32_t mine[D / 32] = {}, any = 0;
+        if (g >= 0 && g < a.num_pages) {
+          const uint8_t* c = a.v_codes + ((((int64_t)g * a.kvh + kh) << a.shift) + (key & ((1 << a.shift) - 1))) * D;
 #pragma unroll
-      for (int k = 0; k < D / 4; ++k) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(c + 4 * k);
-        const uint32_t m = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-        mine[k >> 3] |= ((m & 1) | (m >> 7 & 2) | (m >> 14 & 4) | (m >> 21 & 8)) << ((k & 7) * 4);
-        any |= m;
-      }
-    }
-    for (uint32_t have = __ballot_sync(0xffffffffu, any != 0); have; have &= have - 1) {
-      const int from = __ffs(have) - 1;
+          for (int k = 0; k < D / 4; ++k) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(c + 4 * k);
+            const uint32_t m = (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+            mine[k >> 3] |= ((m & 1) | (m >> 7 & 2) | (m >> 14 & 4) | (m >> 21 & 8)) << ((k & 7) * 4);
+            any |= m;
+          }
+        }
+        for (uint32_t have = __ballot_sync(0xffffffffu, any != 0); have; have &= have - 1) {
+          const int from = __ffs(have) - 1;
 #pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        const uint32_t bits = __shfl_sync(0xffffffffu, mine[k], from);
-        if (k0 + from >= lo && k0 + from <= pos) nan[k] |= bits;
+          for (int k = 0; k < D / 32; ++k) {
+            const uint32_t bits = __shfl_sync(0xffffffffu, mine[k], from);
+            if (k0 + from >= lo && k0 + from <= pos) nan[k] |= bits;
+          }
+        }
       }
     }
   }
@@ -381,6 +392,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __shared__ int first_s[2], most_s, least_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  for (int i = threadIdx.x; i < kPieceRing * kMarks; i += kChunkThreads) smem[M::kNan + i] = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kMostK; ++s) {
       mbar_init(smem_u32(&bars->k_full[s]), 1);
@@ -398,7 +410,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     mbar_init(smem_u32(&bars->q_ready), kSoftWarps);
     mbar_init(smem_u32(&bars->mma_done), 1);
-    for (int s = 0; s < kScaleRing; ++s) scales[s * kScaleFloats + 25] = 0.f;
+    for (int s = 0; s < kPieceRing; ++s) bars->nan[s] = 0;
     most_s = 0;
     least_s = 1 << 30;
     fence_mbar_init();
@@ -760,8 +772,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const int t = threadIdx.x - kSoftWarps * 32;
     const int c4 = t & 3, half = D == 128 ? (t >> 2) & 1 : 0, rin = D == 128 ? t >> 3 : t >> 2;
     bool ok = true;
-    uint32_t jt = 0;
-    for (int b = b0; b < b1 && ok;) {
+    uint32_t jt = 0, pieces = 0;
+    for (int b = b0; b < b1 && ok; ++pieces) {
       const Piece p = piece_at(b);
       b = p.next;
 #pragma unroll 1
@@ -799,7 +811,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (!(__low2float(nan) == 0.f && __high2float(nan) == 0.f)) {
           // NaN codes: zero, and known to have been there
-          scales[(jt + 1) % kScaleRing * kScaleFloats + 25] = __uint_as_float(jt + 1);
+          bars->nan[pieces % kPieceRing] = pieces + 1;
+          smem[M::kNan + pieces % kPieceRing * kMarks + mark_of((k >> 1) - p.ja, p.jb - p.ja)] = stamp_of(pieces);
 #pragma unroll 1
           for (int i = 0; i < STEP_PASSES * 8; ++i) {
             const int row = (k & 1) * 64 + (i >> 3) * PASS + rin;
@@ -836,7 +849,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const unsigned pair = valid ? p.t.pair0 + x * 128 + r : 0u;
       const int token = (int)(pair / (unsigned)a.G), head = p.kh * a.G + (int)(pair % (unsigned)a.G);
       const int pos = valid ? p.len - p.rows + token : -1;  // keys (pos - window, pos] are seen
-      const int lo = oldest_seen(a, pos);
+      const int lo = a.window > 0 ? max(pos, -1) - a.window + 1 : 0;
       const float fac = chunk_queries<T, D>(args, q_reg(x) + (uint32_t)(qq * 32 * D), p.row0, p.kh, p.t.pair0 + x * 128 + qq * 32,
                                             p.t.pairs - x * 128 - qq * 32);
       {
@@ -846,11 +859,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars->q_ready));
       }
 
-      // A block with a NaN leaves its number in the place of the block behind it, whose turn it is
-      // once the product has landed.  The converting warps come to that place again at the
-      // fourth block on, which they reach only when all rows have been here (tile A
-      // ends a block before tile B at most).
-      auto nan_of = [&](int j) { nan_into<D>(a, ocol, p.seq, p.len, p.kh, p.ja + j, lo, pos); };
       float m_used = -INFINITY, l = 0.f;
       for (int j = 0; j < nb && alive; ++j) {
         // (every lane polls: a broadcast costs the chain of a block's steps its latency)
@@ -860,10 +868,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         // (loops that are not unrolled: six roles' code contends for the instruction cache)
         const int key0 = (p.ja + j) * kKeys;
         const uint32_t sc = sbase + (uint32_t)(M::kScales + ((base + j) % kScaleRing) * (kScaleFloats * 4));
-        const float4 marks = lds_f4(sc + 96);
-        const bool lost = marks.x != 0.f, nan = __float_as_uint(marks.y) == base + j && j > 0;
-        if (__any_sync(0xffffffffu, key0 + kKeys - 1 > pos || key0 < lo || lost || nan)) {
-          if (nan) nan_of(j - 1);
+        const bool lost = lds_f4(sc + 96).x != 0.f;
+        if (__any_sync(0xffffffffu, key0 + kKeys - 1 > pos || key0 < lo || lost)) {
           // keys that this row does not see, and pages out of range: -inf, in tensor memory
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -979,8 +985,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (alive) alive = warp_wait(&bars->mma_done, pieces & 1, a.err);
       if (alive && x * 128 < p.t.pairs) {
         tc_fence_after();
-        if (nb > 0 && __float_as_uint(*reinterpret_cast<volatile float*>(&scales[(base + nb) % kScaleRing * kScaleFloats + 25])) == base + nb)
-          nan_of(nb - 1);
+        // (the place is this piece's until the converting warps are four ahead, which wait for this one's rows)
+        if (nb > 0 && *reinterpret_cast<volatile uint32_t*>(&bars->nan[pieces % kPieceRing]) == pieces + 1)
+          nan_into<D>(a, ocol, smem + M::kNan + pieces % kPieceRing * kMarks, stamp_of(pieces), p.seq, p.len, p.kh, p.ja, p.jb - p.ja, lo, pos);
         __syncwarp();
         const int64_t slot = 2 * (int64_t)blockIdx.x + (pieces == 0 ? 0 : 1);
         // (a row that sees keys and has no sum is NaN)
