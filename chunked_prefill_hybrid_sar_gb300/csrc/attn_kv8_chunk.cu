@@ -26,6 +26,9 @@
 // those of their keys that they see (a NaN under 64 rows 200000 deep: 131 us; 2650 when
 // they looked through all of the piece's, 114 without a NaN).
 //
+// Value scales far apart would lose the weights of the smaller: pages far from most are passed
+// over by the loop and follow at the piece's end (8192 rows 495 us; 541 when they were taken in the loop).
+//
 // Units' blocks of 128 keys form one line.  Every CTA (one per SM) takes an equal stretch of
 // it, or every unit gets as many CTAs, or a CTA a whole unit, whichever should end first;
 // pieces of a unit are joined by the kernel behind (attn_kv8_join.cu).  With four or more
@@ -34,7 +37,7 @@
 // Bound by a tile's chain (its Q K^T, its softmax, its P V, and the handing over, about
 // 2 us for a block's two tiles), which the two tiles hide from one another in part, and by
 // a piece's queries and results, as long as some blocks.  8192 rows of 32 heads, bf16:
-// 510 us, 1.08 PFLOP/s; 512 rows 16384 deep, f16, beside five single tokens: 160 us, 0.84
+// 495 us, 1.11 PFLOP/s; 512 rows 16384 deep, f16, beside five single tokens: 162 us, 0.84
 // PFLOP/s; 25 chunks of up to 6 rows in a window of 1024 keys, beside seven: 34 us.
 // Taken at an earlier state: steps of 64 keys with two buffers of scores, so that a tile's
 // next product does not wait for its softmax (666 for 554 us and 195 for 172: products 64
@@ -42,7 +45,7 @@
 // more, with the blocks in turn (180 for 171 us; 42.5 for 43.7 with 25 short chunks).
 // The loop over blocks is sensitive to what else is in the function: with a piece's
 // results and the search for NaN out of line the first took 510 us, with all in line 554,
-// with the queries out of line too 669.
+// with the queries out of line too 669; with a warp of their own for the scales 623.
 #include <algorithm>
 
 #include "kv8.cuh"
@@ -58,14 +61,14 @@ constexpr int kChunkThreads = (kSoftWarps + kConvWarps + 4) * 32;  // (whole war
 constexpr int kTileRegion = 128 * 128;   // [128 rows][128 bytes]: 64 dims of 128 rows
 constexpr int kScaleRing = 4;             // blocks whose scales are kept: three K stages ahead, and the softmax's
 constexpr int kScaleFloats = 28;         // of a block: eight runs' factors, log2 and inverse of the value scales, a flag
-constexpr int kPieceRing = 4;            // pieces that are known at once: V's codes are turned two blocks ahead
+constexpr int kPieceRing = 4;            // pieces that are known at once: scales are fetched three blocks ahead, V's codes turned two
 constexpr int kMarks = 512;              // of a piece's blocks, for one or some of which each stands
 constexpr int kRawSteps = 3;              // steps of 64 keys of V whose codes are under way
 constexpr int kMostK = 3;                 // K stages
 constexpr int kLeastBlocks = 4;          // of a stretch
 constexpr int kPieceBlocks = 12;         // a CTA's second piece takes as long as so many blocks more (four chunks of up to
                                          // 512 rows 90 us; 106 where 8 or 5 are reckoned; others alike)
-constexpr float kGrowth = 8.f;           // log2 of a maximum's growth that O tolerates
+constexpr uint32_t kApartBits = 8u << 23; // of two numbers a factor of 1 / kApart from one another
 constexpr uint32_t kColsS = 128;         // S_x at x * 128; P over its last 64 columns
 constexpr uint32_t kColsO = 256;         // O_x at 256 + x * 128
 
@@ -77,6 +80,9 @@ struct ChunkBars {
   uint32_t tmem;
   uint32_t read[kScaleRing];  // runs of a block whose V was read
   uint32_t nan[kPieceRing];   // a piece's number + 1, where V has NaN codes
+  uint32_t apart[kPieceRing]; // ... where value scales lie far from most
+  uint32_t odd[kPieceRing];   // ... where either
+  float low[kPieceRing];      // the least scale of those that the loop over blocks weighs
 };
 
 struct ChunkArgs8 {
@@ -96,12 +102,12 @@ struct ChunkSmem {
   static constexpr int kRawStep = 64 * D;
   static constexpr int kK = 2 * kParts * kPart, kV = kK + kStagesK * kPart, kRaw = kV + 2 * kStageV;
   static constexpr int kBars = kRaw + kRawSteps * kRawStep;
-  static constexpr int kScales = kBars + 256;
+  static constexpr int kScales = kBars + 288;
   static constexpr int kTable = kScales + kScaleRing * kScaleFloats * 4;  // before [tiles + 1], seq, u
   static constexpr int kNan = kTable + (3 * kMostTiles + 1) * 4;  // [pieces][marks] bytes
   static constexpr int kBytes = 1024 + kNan + kPieceRing * kMarks;
 };
-static_assert(sizeof(ChunkBars) <= 256, "barrier area");
+static_assert(sizeof(ChunkBars) <= 288, "barrier area");
 static_assert(ChunkSmem<__half, 128>::kBytes <= 226 * 1024, "shared memory per CTA");
 
 // Instruction descriptor: fp32 sums, M = 128; both operands of format 0 (fp16 of
@@ -320,6 +326,118 @@ __device__ __noinline__ void nan_into(const Kv8Attn& a, uint32_t ocol, const uin
   }
   tmem_wait_st();
 }
+// The page of a run of 16 keys, -1 where the call reads none of the page's keys or it is out of range.
+__device__ __forceinline__ int run_page(const Kv8Attn& a, int seq, int len, int key, int oldest) {
+  const int ps = 1 << a.shift, first = key & ~(ps - 1);
+  const int page = first < len && first + ps > oldest ? a.bt[(int64_t)seq * a.bt_stride + (key >> a.shift)] : -1;
+  return page < a.num_pages ? page : -1;
+}
+// The least value scale of a piece that the loop over its blocks weighs, 2^-4 of the median of 32
+// pages' (its power of two; page: this lane's): one page of a large scale does not send all others
+// the slow way.  (Out of line: 512 rows 16384 deep 162 us, 174 with it in the loads' warp.)
+__device__ __noinline__ float usual_scales(const Kv8Attn& a, int page, int kh) {
+  const int ex = page >= 0 ? (int)(__float_as_uint(a.v_scales[(int64_t)page * a.kvh + kh]) >> 23) : -1;
+  const int half = (__popc(__ballot_sync(0xffffffffu, ex >= 0)) + 1) / 2;
+  int e = 0;  // the largest exponent that at least half of the pages reach
+#pragma unroll 1
+  for (int bit = 128; bit > 0; bit >>= 1)
+    if (half > 0 && __popc(__ballot_sync(0xffffffffu, ex >= (e | bit))) >= half) e |= bit;
+  return __uint_as_float((uint32_t)min(max(e - 4, 1), 246) << 23);
+}
+// Runs of 16 keys whose pages' value scales are far from most pages' (less than low, or more than
+// low / kApart): the loop over a piece's blocks passes over them, and here they follow, with weights
+// in fp32.  O has the products of all blocks; returns the row's maximum and sum with these keys'.
+// q: where the warp's queries lie, whose scores are to be multiplied by fac.  Slow (a run 23 us, a block of eight in the loop 2), for scales that a model's values hardly ever have.
+template <typename T, int D>
+__device__ __noinline__ float2 runs_apart(const Kv8Attn& a, uint32_t q, float fac, uint32_t ocol, float low, int seq, int len, int kh, int ja,
+                                          int jb, int oldest, int lo, int pos, float m, float l) {
+  using M = ChunkSmem<T, D>;
+  const int lane = threadIdx.x & 31, ps = 1 << a.shift;
+#pragma unroll 1
+  for (int j0 = ja; j0 < jb; j0 += 4) {  // a run of four blocks' to a lane
+    const int j = j0 + lane / 8, key = j * kKeys + lane % 8 * 16;
+    const int page = j < jb ? run_page(a, seq, len, key, oldest) : -1;
+    float ks = 0.f, vs = low;
+    if (page >= 0) ks = a.k_scales[(int64_t)page * a.kvh + kh], vs = a.v_scales[(int64_t)page * a.kvh + kh];
+#pragma unroll 1
+    for (uint32_t runs = __ballot_sync(0xffffffffu, __float_as_uint(vs) - __float_as_uint(low) > kApartBits); runs; runs &= runs - 1) {
+      const int from = __ffs(runs) - 1, k0 = __shfl_sync(0xffffffffu, key, from);
+      const int64_t unit = (int64_t)__shfl_sync(0xffffffffu, page, from) * a.kvh + kh;
+      const int64_t codes = ((unit << a.shift) + (k0 & (ps - 1))) * D;
+      const float f = fmaxf(__shfl_sync(0xffffffffu, ks, from) * fac, 1.2e-38f), v_scale = __shfl_sync(0xffffffffu, vs, from);
+      const float off = log2_fast(v_scale), iv = rcp_fast(v_scale);
+      float w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < D / 16; ++c) {
+        float x[16] = {};
+#pragma unroll
+        for (int k = 0; k < M::kParts; ++k) {
+          const uint4 v = lds_u4(chunk_at<T, D>(q, lane, c) + (uint32_t)(k * M::kPart));
+          const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 u = e4m3x2_floats(words[i >> 2] >> (8 * (i & 2)));
+            x[i] += u.x, x[i + 1] += u.y;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint4 v = *reinterpret_cast<const uint4*>(a.k_codes + codes + e * D + c * 16);
+          const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 u = e4m3x2_floats(words[i >> 2] >> (8 * (i & 2)));
+            w[e] = fmaf(x[i], u.x, fmaf(x[i + 1], u.y, w[e]));
+          }
+        }
+      }
+      float top_w = m;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        w[e] = k0 + e >= lo && k0 + e <= pos ? fmaf(w[e], f, off) : -INFINITY;
+        top_w = fmaxf(top_w, w[e]);
+      }
+      const float grown = top_w == -INFINITY ? 1.f : exp2_fast(m - top_w);  // (0 from -inf)
+      m = top_w;
+      const float ref = m == -INFINITY ? 0.f : m - kBias;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        w[e] = exp2_fast(w[e] - ref);
+        sum += w[e];
+      }
+      l = fmaf(sum, iv, l * grown);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t u[16];
+        float o[16];
+        tmem_ld16(ocol + c, u);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]) * grown;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const uint4 v = *reinterpret_cast<const uint4*>(a.v_codes + codes + e * D + c);
+          const uint32_t words[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float2 x = e4m3x2_floats(words[i >> 2] >> (8 * (i & 2)));
+            // (NaN codes as zero, as in the product)
+            o[i] = fmaf(w[e], x.x == x.x ? x.x : 0.f, o[i]);
+            o[i + 1] = fmaf(w[e], x.y == x.y ? x.y : 0.f, o[i + 1]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(o[i]);
+        tmem_st16(ocol + c, u);
+      }
+      tmem_wait_st();
+    }
+  }
+  return make_float2(m, l);
+}
 // A row of O times inv, in 16 bits, row by row through the place of the warp's own
 // queries' first two parts (other warps may be at the next piece already).
 template <typename T, int D>
@@ -410,7 +528,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
     mbar_init(smem_u32(&bars->q_ready), kSoftWarps);
     mbar_init(smem_u32(&bars->mma_done), 1);
-    for (int s = 0; s < kPieceRing; ++s) bars->nan[s] = 0;
+    for (int s = 0; s < kPieceRing; ++s) bars->nan[s] = bars->apart[s] = bars->odd[s] = 0;
     most_s = 0;
     least_s = 1 << 30;
     fence_mbar_init();
@@ -596,7 +714,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const uint32_t tmem = bars->tmem;
 
   // Registers: 512 threads start with 128 each; 56 for the products' and loads' warpgroup and
-  // 80 for the converting one leave 184 for the softmax (256 * 184 + 128 * 80 + 128 * 56 < 512 * 128).
+  // 72 for the converting one leave 192 for the softmax (256 * 192 + 128 * 72 + 128 * 56 = 512 * 128).
   if (warp >= kSoftWarps + kConvWarps) {
     // ---------------- products ----------------
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
@@ -667,9 +785,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       const int ps = 1 << a.shift, run = lane & 7;
       const uint32_t firsts = ps == 16 ? 0xffu : ps == 32 ? 0x55u : 0x11u;  // the runs that boxes begin with
       bool ok = true;
-      uint32_t jt = 0;
+      uint32_t jt = 0, pieces = 0;
       if (lane == 0) tma_prefetch_desc(map);
-      for (int b = b0; b < b1 && ok;) {
+      for (int b = b0; b < b1 && ok; ++pieces) {
         const Piece p = piece_at(b);
         const int nb = p.jb - p.ja;
         b = p.next;
@@ -683,6 +801,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         };
         // scales of the block behind the present one, pages of two: no load is waited for
         int next = look_up(0), next2 = look_up(1);
+        const int sample = is_k ? run_page(a, p.seq, p.len, (p.ja + (int)((int64_t)nb * lane / 32)) * kKeys + lane % 8 * 16, p.t.lo) : -1;
         float ks_next, vs_next;
         auto scales_of = [&](int g) {
           ks_next = vs_next = 1.f;
@@ -692,6 +811,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         };
         scales_of(next);
+        float low = 0.f;  // pages of value scales within [low, low / kApart] are weighed in the loop
+        if (is_k) low = usual_scales(a, sample, p.kh);
         for (int j = 0; j < nb && ok; ++j, ++jt) {
           int page = next;
           const float ks = ks_next, vs = vs_next;
@@ -704,7 +825,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           next2 = look_up(j + 2);
           scales_of(next);
           const uint32_t pages = __ballot_sync(0xffffffffu, page >= 0) & 0xffu, boxes = pages & firsts;
-          const uint32_t any_lost = __ballot_sync(0xffffffffu, lost);
           // (rows of the maps are as long as a key's)
           const int row = (int)(((int64_t)page * a.kvh + p.kh) << a.shift);
           int y[8];
@@ -712,14 +832,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(0xffffffffu, row, i);
           if (is_k) {
             const uint32_t s = jt % M::kStagesK, bar = smem_u32(&bars->k_full[s]);
+            // (few instructions: all roles' loops contend for the instruction cache)
+            const bool apart = page >= 0 && __float_as_uint(vs) - __float_as_uint(low) > kApartBits;
+            const bool over = __any_sync(0xffffffffu, lost || apart);
             ok = warp_wait(&bars->k_free[s], ((jt / M::kStagesK) & 1) ^ 1, a.err);
             if (!ok) break;
             if (lane < 8) {
               float* sc = scales + (jt % kScaleRing) * kScaleFloats + lane;
-              if (lane == 0) sc[24] = any_lost ? 1.f : 0.f;
-              sc[0] = lost ? -1.f : ks;  // negative: keys that are passed over
-              sc[8] = log2f(vs);
-              sc[16] = 1.f / vs;
+              if (lane == 0) sc[24] = over ? 1.f : 0.f;
+              if (apart) {
+                bars->apart[pieces % kPieceRing] = bars->odd[pieces % kPieceRing] = pieces + 1;
+                bars->low[pieces % kPieceRing] = low;
+              }
+              sc[0] = lost || apart ? -1.f : ks;  // negative: keys that are passed over
+              sc[8] = log2_fast(vs);
+              sc[16] = rcp_fast(vs);
             }
             __syncwarp();
             if (elect_one()) {
@@ -768,7 +895,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // Steps of 64 keys of V, 16 bytes of a key to a thread, consecutive bytes to
     // consecutive threads.  head_dim 128: lanes of the second half of a key write their
     // two chunks the other way round, so that eight lanes touch every bank once.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     const int t = threadIdx.x - kSoftWarps * 32;
     const int c4 = t & 3, half = D == 128 ? (t >> 2) & 1 : 0, rin = D == 128 ? t >> 3 : t >> 2;
     bool ok = true;
@@ -811,7 +938,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         if (!(__low2float(nan) == 0.f && __high2float(nan) == 0.f)) {
           // NaN codes: zero, and known to have been there
-          bars->nan[pieces % kPieceRing] = pieces + 1;
+          bars->nan[pieces % kPieceRing] = bars->odd[pieces % kPieceRing] = pieces + 1;
           smem[M::kNan + pieces % kPieceRing * kMarks + mark_of((k >> 1) - p.ja, p.jb - p.ja)] = stamp_of(pieces);
 #pragma unroll 1
           for (int i = 0; i < STEP_PASSES * 8; ++i) {
@@ -835,7 +962,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
   } else {
     // ---------------- softmax: a row to a thread ----------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int x = warp >> 2, qq = warp & 3;
     const int r = qq * 32 + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
@@ -945,7 +1072,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           l *= rs;
           if (need) m_used = m_new;
         }
-        const float ref = m_used == -INFINITY ? 0.f : m_used;
+        const float ref = m_used == -INFINITY ? 0.f : m_used - kBias;
         // P lies over the scores' upper half
         auto weigh = [&](const float* x, int c, const float4& k, const float4& lv) {
           const float4 iv = lds_f4(sc + 64 + c * 16);
@@ -985,9 +1112,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (alive) alive = warp_wait(&bars->mma_done, pieces & 1, a.err);
       if (alive && x * 128 < p.t.pairs) {
         tc_fence_after();
-        // (the place is this piece's until the converting warps are four ahead, which wait for this one's rows)
-        if (nb > 0 && *reinterpret_cast<volatile uint32_t*>(&bars->nan[pieces % kPieceRing]) == pieces + 1)
-          nan_into<D>(a, ocol, smem + M::kNan + pieces % kPieceRing * kMarks, stamp_of(pieces), p.seq, p.len, p.kh, p.ja, p.jb - p.ja, lo, pos);
+        // (the places are this piece's until the warps that write them are four ahead, and those wait for this one's rows)
+        const uint32_t place = pieces % kPieceRing;
+        if (nb > 0 && *reinterpret_cast<volatile uint32_t*>(&bars->odd[place]) == pieces + 1) {
+          if (*reinterpret_cast<volatile uint32_t*>(&bars->apart[place]) == pieces + 1) {
+            const float2 ml = runs_apart<T, D>(a, q_reg(x) + (uint32_t)(qq * 32 * D), fac, ocol, bars->low[place], p.seq, p.len, p.kh, p.ja, p.jb,
+                                               p.t.lo, lo, pos, m_used, l);
+            m_used = ml.x;
+            l = ml.y;
+          }
+          if (*reinterpret_cast<volatile uint32_t*>(&bars->nan[place]) == pieces + 1)
+            nan_into<D>(a, ocol, smem + M::kNan + place * kMarks, stamp_of(pieces), p.seq, p.len, p.kh, p.ja, p.jb - p.ja, lo, pos);
+        }
         __syncwarp();
         const int64_t slot = 2 * (int64_t)blockIdx.x + (pieces == 0 ? 0 : 1);
         // (a row that sees keys and has no sum is NaN)

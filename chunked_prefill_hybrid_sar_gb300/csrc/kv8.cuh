@@ -13,6 +13,14 @@ namespace sar {
 // 2^-49 become zero, those over 448 * 2^60 saturate.
 constexpr int kKv8Least = -40, kKv8Most = 60;
 
+// Attention weighs V's codes by 2^(t - m), t = S k_scale scale + log2(v_scale) and m near the
+// largest t so far (its growth by 2^kGrowth is tolerated before m follows), in fp16.  fp16's
+// subnormal numbers are off by 2^-25, so the weights lie 2^kBias higher: up to 2^15, where fp16 ends
+// at 2^16, and off by 2^-32 of 2^m.  A page of a small value scale beside larger ones
+// has small weights for large probabilities: pages whose scales lie within a factor of
+// 1 / kApart are weighed together (off by 2^-24 of the row's largest probability), others apart.
+constexpr float kGrowth = 8.f, kBias = 7.f, kApart = 1.f / 256.f;
+
 // The smallest power of two s within those exponents with a <= 448 s, for a finite
 // a >= 0: 448 = 1.75 * 2^8.
 __device__ __forceinline__ float kv8_scale(float a) {
@@ -38,6 +46,16 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float log2_fast(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {

@@ -276,7 +276,9 @@ int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream
  * nothing (p < 0) is zero; keys that it does not see do not touch it, whatever they
  * hold.  Single tokens and chunks may stand side by side in a call.  Codes are
  * multiplied as they are, sums are fp32; a query's elements are off by 2^-17 of the
- * largest of their row and head at most, probabilities are rounded to fp16.
+ * largest of their row and head at most, a key's probability by 2^-11 of itself or 2^-24 of
+ * its row's largest, whatever value scales lie beside one another (chunks of several rows
+ * take pages slowly whose scale is more than 2^4 from most others' of their sequence).
  * Rows are 16-bit, row r at q + r * ldq elements, heads of head_dim adjacent; out
  * likewise.  max_rows bounds a sequence's rows (1: single tokens alone); max_len
  * (0: unknown) is about the longest length and only guides how work is shared
