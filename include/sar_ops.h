@@ -289,8 +289,8 @@ int sar_qk_norm_rope(const sar_qk_rows* rows, const sar_kv8* cache, void* stream
  * holds nothing between calls) belongs to one call at a time.
  * Sequences whose offsets are out of range or fall, whose rows pass max_rows or
  * whose length passes its block table's bt_cols pages are left out, and keys of pages out of range
- * are passed over; sar_op_sync_status() reports either.  Rows of no sequence stay as they
- * are.  Async on `stream`; allocates nothing. */
+ * are passed over (a row that sees no others is NaN); sar_op_sync_status() reports either.
+ * Rows of no sequence stay as they are.  Async on `stream`; allocates nothing. */
 typedef struct sar_kv8_batch {
   const void* q;
   void* out;
