@@ -1,8 +1,8 @@
 // Attention of single tokens over the 8-bit paged cache.
 //
 // Bound by the cache's bytes: 2 D of them per key and KV head, for 4 D G flops.  128
-// sequences of up to 8192 keys (1.09 GB): 173 us with the join, 6.3 TB/s (170 without it);
-// four of up to 131072: 116.6 us, 5.8 TB/s; one of 500 keys: 10.3 us, latencies.
+// sequences of up to 8192 keys (1.09 GB): 174.5 us with the join, 6.2 TB/s (170 without it);
+// four of up to 131072: 117 us, 5.8 TB/s; one of 500 keys: 10.3 us, latencies.
 //
 // All (sequence, KV head) units' keys, in blocks of 32, form one line, of which every
 // CTA takes a stretch, whatever the lengths.  Where a stretch begins or ends

@@ -9,8 +9,8 @@
 namespace sar {
 
 // Exponents of a page's scale.  Between them attention's weights, which carry a
-// page's value scale in their exponent, stay inside fp32's range; magnitudes under
-// 2^-49 become zero, those over 448 * 2^60 saturate.
+// page's value scale in their exponent, stay inside fp32's range; magnitudes of at most
+// 2^-10 of a page's scale become zero (2^-50 under the least), those over 448 * 2^60 saturate.
 constexpr int kKv8Least = -40, kKv8Most = 60;
 
 // Attention weighs V's codes by 2^(t - m), t = S k_scale scale + log2(v_scale) and m near the
@@ -48,6 +48,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// A scale's logarithm and inverse by the SFU (relative error 2^-22): both are factors of a
+// weight that is rounded to fp16.
 __device__ __forceinline__ float log2_fast(float x) {
   float y;
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -14,9 +14,11 @@
 // maximum per run (whose order does not matter), and writes codes: the input is read once.
 //
 // Rows of queries are bound by memory (12288 x 56 heads of 128, bf16: 61 us, where a copy of
-// them takes 53), the cache's part by its instructions, about 200 to 32 lanes' rows (8 + 8
-// heads: 39 us; 45 where every row of a run searched the maxima of the others).
-// Both in one launch 100 us on inputs that are not in L2, against 63 for the bytes.  At an
+// them takes 53).  The cache's part (8 + 8 heads: 39 us; 45 where every row of a run searched the
+// maxima of the others) is bound by a CTA's chain of slots, rows, maxima, barrier and codes: issue
+// slots are 46% used and memory 18%, with 29 of 64 warps on an SM, which wait for loads,
+// shared memory, one another and the barrier in like parts.
+// Both in one launch 98 us on inputs that are not in L2, against 63 for the bytes.  At an
 // earlier state (98): their CTAs in turn instead of the cache's first, 98 too; a window's
 // tasks side by side, 105, as the longest then come last as well.
 #include <math.h>
