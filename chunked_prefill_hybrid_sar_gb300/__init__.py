@@ -691,7 +691,8 @@ def page_map(lens, new_lens, block_tables, free_pages, free_count, row_offsets, 
     ``new_lens`` more tokens of each request (-1: it has ended and gives its pages
     back) from the stack ``free_pages`` [pages of the cache], whose first
     ``free_count`` are free; ``row_offsets`` [n + 1], ``positions`` and ``slots``
-    [rows] of the step's rows.  ``lens_out`` and ``free_count_out`` default to ``lens``
+    [rows] of the step's rows.  ``block_tables`` may be columns of a wider tensor, whose
+    others stay as they are.  ``lens_out`` and ``free_count_out`` default to ``lens``
     and ``free_count``, in place; see ``sar_page_map``."""
     what, n = "page_map", lens.numel()
     _row_types()
